@@ -40,6 +40,16 @@
  *   rapid_lm_head_accept  LM head, alone or followed by rapid_accept (or, with
  *                      rapid_lm_head_accept_ex, by rapid_accept_ex).
  *
+ *   rapid_qkv_append   the rows of the query, key and value projections: norm
+ *                      of each head, rotation by position, queries into the
+ *                      layout of the attention calls, keys and values into
+ *                      the cache.
+ *
+ *   rapid_kv_seal      a history held in 8 bits: full blocks of cache rows
+ *   rapid_kv_seal_advance  become pages of e4m3 values with one scale for each
+ *   rapid_verify_attn_q8   block, head and side, and verify attention reads
+ *                      them, the rows not sealed yet and the step's rows.
+ *
  *   rapid_retrieval_scores  cosine scores of chunk embeddings against the
  *   rapid_retrieval_select  query, and the budgeted, thresholded choice of
  *                      chunks for the draft's retrieved context ("RAPID ...",
@@ -49,7 +59,8 @@
  *  - All tensor arguments are DEVICE pointers owned by the caller.  The library
  *    allocates nothing on these paths; scratch space is the caller's
  *    `workspace` (size from the matching *_workspace_size call, 256-byte
- *    aligned).  Only rapid_kv_commit writes to the KV cache.
+ *    aligned).  Only rapid_kv_commit, rapid_qkv_append and rapid_kv_seal
+ *    write to the KV cache.
  *  - Calls are asynchronous and stream-ordered on `stream` (a cudaStream_t
  *    passed as void*; NULL = the legacy default stream).  No call
  *    synchronises the device; results are valid once the stream reaches them.
@@ -344,9 +355,10 @@ int rapid_version(void);
  * (bit 0: a bounded wait for an asynchronous copy or a peer gave up, so the
  * outputs of that call are invalid; bit 1: a kernel found an invalid
  * device-side input -- a history length, parent, draft token or node count
- * out of range in rapid_verify_attn / rapid_accept*, or an input that
- * rapid_kv_commit, rapid_kv_advance or rapid_retrieval_select refused,
- * leaving that sequence alone).  Synchronises the device to read the word;
+ * out of range in rapid_verify_attn[_q8] / rapid_accept*, a page id outside
+ * the pool, or an input that rapid_kv_commit, rapid_kv_advance,
+ * rapid_qkv_append, rapid_kv_seal, rapid_kv_seal_advance or
+ * rapid_retrieval_select refused, leaving that sequence alone).  Synchronises the device to read the word;
  * clears it when `clear` is non-zero.  Returns -1 if the word could not be
  * read.
  */
@@ -581,6 +593,165 @@ rapid_status rapid_lm_head_accept_ex(const void* hidden, const void* W_lm, int h
                                      float* diag, void* workspace, size_t workspace_bytes,
                                      void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Projection rows into queries and cache rows                               */
+/* ------------------------------------------------------------------------ */
+
+/* Flags of rapid_qkv_append. */
+enum {
+    /* Rotate neighbouring elements (2i, 2i + 1); without it element i rotates
+     * with element i + rot_dim / 2. */
+    RAPID_ROPE_INTERLEAVED = 1u
+};
+
+/*
+ * One pass over the rows that a layer's query, key and value projections give
+ * for n tokens of every sequence (the n_q nodes of a verify step, or a chunk
+ * of a prefill, of any length):
+ *   y = x / sqrt(mean(x^2) + eps) * weight     per head of q and k, where a
+ *                                              weight is given;
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t), t = pos * inv_freq[pair],
+ *                                              over the first rot_dim elements
+ *                                              of every head of q and k;
+ *   Q[b, h, i, :] = the query; Kcache[b, g, prefix_len[b] + i, :] = the key;
+ *   Vcache[b, g, prefix_len[b] + i, :] = the value, unchanged,
+ * with pos = prefix_len[b] + pos_offset[b] + (row_offset[b][i], or i).  The
+ * arithmetic is fp32 with one rounding at the store; the angle is reduced
+ * modulo one turn exactly, at any position.  A verify step's Q and rows are
+ * then what rapid_verify_attn and rapid_verify_attn_q8 read.
+ *
+ *  q          rows of dtype: token i of sequence b starts at element
+ *             b * strides[0] + i * strides[1] and holds Hq heads of d elements
+ *             one after the other
+ *  k, v       the same with Hkv heads; strides[2], [3] and [4], [5]
+ *  strides    HOST array of six element strides (views of one fused projection
+ *             need no copy), or NULL: q, k and v packed [B, n, heads, d].  Every
+ *             stride a multiple of 16 bytes
+ *  q_weight, k_weight  device [d] of dtype, or NULL: no norm of that side
+ *  inv_freq   device float [rot_dim / 2]: radians per position of each pair
+ *             (element pair i, i + rot_dim / 2, or 2 i, 2 i + 1); unused when
+ *             rot_dim is 0.  An infinite or NaN entry does not rotate
+ *  rot_dim    a multiple of 16 in [0, d]
+ *  prefix_len device int32 [B]: cache rows before the new ones
+ *  pos_offset device int32 [B] or NULL (0): tokens before the cache's first
+ *             row (rapid_verify_attn_q8's sealed_len)
+ *  row_offset device int32 [B, n] or NULL (i): position of row i after the
+ *             first, the depth of a token tree's node
+ *  n_rows     device int32 [B] or NULL (n): sequence b has rows [0, n_rows[b]);
+ *             the rows behind them are neither read nor written, in Q and in
+ *             the caches
+ *  Q          [B, Hq, n, d], Kcache and Vcache [B, Hkv, kv_capacity, d], of
+ *             dtype, 16-byte aligned; none may overlap q, k or v
+ *  n          tokens per sequence, B * n <= 2^31
+ *
+ * Errors: RAPID_EINVAL for NULL pointers, bad sizes, a bad rot_dim, flag, eps
+ * (negative or not finite), dtype or alignment; RAPID_ECUDA on launch failure.
+ * A sequence whose n_rows is outside [0, n] or whose rows do not fit the cache
+ * (prefix_len < 0, prefix_len + n_rows > kv_capacity) is left alone, in Q too,
+ * and bit 1 of the device error word is set.
+ */
+rapid_status rapid_qkv_append(const void* q, const void* k, const void* v, const int64_t* strides,
+                              int dtype, int B, int n, int Hq, int Hkv, int d,
+                              const void* q_weight, const void* k_weight, float eps,
+                              const float* inv_freq, int rot_dim, uint32_t flags,
+                              const int32_t* prefix_len, const int32_t* pos_offset,
+                              const int32_t* row_offset, const int32_t* n_rows, void* Q,
+                              void* Kcache, void* Vcache, int64_t kv_capacity, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* A history held in 8 bits                                                  */
+/* ------------------------------------------------------------------------ */
+
+enum {
+    RAPID_Q8_PAGE_TOKENS = 64,     /* tokens of a page                         */
+    RAPID_Q8_MAX_PAGES = 1 << 24   /* pages of one sequence                    */
+};
+
+/*
+ * The cache.  The history of sequence b is its sealed_len[b] oldest tokens (a
+ * multiple of RAPID_Q8_PAGE_TOKENS), held in pages, followed by tail_len[b]
+ * tokens held as rows [0, tail_len[b]) of the tail caches, which are ordinary
+ * caches [B, Hkv, tail_capacity, d] of fp32 or bf16: a verify step writes its
+ * speculative rows behind the tail rows (rapid_qkv_append with pos_offset =
+ * sealed_len), and rapid_kv_commit and rapid_kv_advance work on them with
+ * tail_len as prefix_len.  rapid_kv_seal then moves whole blocks from the front
+ * of the tail into pages, so no 8-bit block is ever rewritten and speculative
+ * rows are never rounded to 8 bits.
+ *
+ *  pages      [n_pages, Hkv, 2, 64, d] e4m3 (K, then V, of one page and head)
+ *  scales     float [n_pages, Hkv, 2]: value = code * scale
+ *  page_table device int32 [B, max_pages]: page of block j of sequence b.  One
+ *             table serves every layer; each layer has its own pages and scales
+ *
+ * rapid_kv_seal seals n_b = max(0, tail_len[b] - keep_rows) / 64 blocks of
+ * every sequence on every layer: block j of them goes to page
+ * page_table[b][sealed_len[b] / 64 + j], each head and side with
+ *   scale = 2^ceil(log2(max|x| / 448)), code = e4m3(x / scale) to nearest even
+ * (an exponent below -64 becomes -64; an all-zero block has scale 1; a value
+ * that is not finite becomes NaN and does not count in the maximum), and the
+ * tail rows [64 n_b, tail_len[b]) move to the front.  Rows behind tail_len are
+ * dropped.  The lengths stay as they are until rapid_kv_seal_advance, called
+ * after the last layer with the same keep_rows and sizes: sealed_len += 64 n_b,
+ * tail_len -= 64 n_b.  Both calls work from device memory alone, so they can be
+ * captured with the step.  Pages given to several sequences must not be sealed
+ * into.
+ *
+ *  K_layers, V_layers, page_layers, scale_layers  HOST arrays of `layers`
+ *             device pointers (tails and pages 16-byte aligned)
+ *  keep_rows  newest rows that stay in the tail whatever happens, >= 0
+ *
+ * Errors: RAPID_EINVAL for NULL pointers, layers outside [1,
+ * RAPID_COMMIT_MAX_LAYERS], B < 1, Hkv < 1, B * Hkv > 65535, d not 64 or 128,
+ * tail_capacity or n_pages < 1, max_pages outside [1, RAPID_Q8_MAX_PAGES],
+ * keep_rows < 0, a bad dtype or alignment; RAPID_ECUDA on launch failure.  A
+ * sequence whose device inputs are invalid (tail_len outside [0,
+ * tail_capacity], sealed_len negative or no multiple of 64, more blocks than
+ * the page table has entries, a page id outside the pool) is left untouched by
+ * both calls and bit 1 of the device error word is set.
+ */
+rapid_status rapid_kv_seal(void* const* K_layers, void* const* V_layers, void* const* page_layers,
+                           float* const* scale_layers, int layers, int dtype, int B, int Hkv, int d,
+                           int64_t tail_capacity, int keep_rows, int n_pages,
+                           const int32_t* page_table, int max_pages, const int32_t* sealed_len,
+                           const int32_t* tail_len, void* stream);
+rapid_status rapid_kv_seal_advance(int32_t* sealed_len, int32_t* tail_len, const int32_t* page_table,
+                                   int B, int max_pages, int n_pages, int64_t tail_capacity,
+                                   int keep_rows, void* stream);
+
+/* Bytes of scratch that rapid_verify_attn_q8 needs; 0 for sizes it rejects. */
+size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_q,
+                                           int64_t tail_capacity, int max_pages, int dtype);
+
+/*
+ * rapid_verify_attn over such a cache: every query of sequence b sees its
+ * sealed pages and its tail rows, and the speculative rows [tail_len[b],
+ * tail_len[b] + n_q) of the tail caches as spec_mask says.
+ *
+ *  Q, O       [B, Hq, n_q, d] of dtype (RAPID_DTYPE_BF16 or RAPID_DTYPE_F32),
+ *             as the tail caches
+ *  scales     positive and finite
+ *  sealed_len, tail_len  device int32 [B].  A sealed_len that is negative, no
+ *             multiple of 64 or past max_pages, a tail_len outside [0,
+ *             tail_capacity - n_q] and a page id outside the pool are clamped,
+ *             and bit 1 of the device error word is set
+ *  spec_mask, softmax_scale, LSE, workspace  as for rapid_verify_attn
+ *
+ * Rows of the tail caches that a query does not see have no effect on it,
+ * whatever they hold.  With bf16 the products run on tensor cores with fp32
+ * sums; the codes are exact in the products' operand type, and the
+ * probabilities are rounded to it (fp16 over pages, bf16 over tail rows).
+ *
+ * Errors: those of rapid_verify_attn, and RAPID_EINVAL for n_pages < 1, n_pages
+ * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], scales
+ * or index arrays not 4-byte aligned.
+ */
+rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void* V_tail,
+                                  const void* pages, const float* scales, const int32_t* page_table,
+                                  int dtype, int B, int Hq, int Hkv, int d, int n_q,
+                                  int64_t tail_capacity, int n_pages, int max_pages,
+                                  const int32_t* sealed_len, const int32_t* tail_len,
+                                  const uint8_t* spec_mask, float softmax_scale, void* O, float* LSE,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,142 @@
+// Verify attention over an 8-bit history: shared parameter block, the split plan and kernel
+// entry points.
+//
+// The keys of a sequence are its sealed pages (64 tokens each, e4m3 values with one scale
+// for each page, KV head and side), then its tail rows, then the n_q speculative rows of the
+// step, which follow the tail rows in the tail caches.  A history kernel splits them over
+// CTAs that each leave an un-normalised partial (acc, m, l); a merge kernel combines the
+// partials by log-sum-exp.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "kv_seal.cuh"
+
+namespace rapid {
+
+constexpr int kQ8Tile = 128;                 // keys of a tile: two pages, or 128 tail rows
+
+struct AttnQ8Params {
+    const void* Q;               // [B, Hq, n_q, d]
+    const void* K;               // [B, Hkv, cap, d] tail caches
+    const void* V;
+    const uint8_t* pages;        // [n_pages, Hkv, 2, 64, d] e4m3
+    const float* scales;         // [n_pages, Hkv, 2]
+    const int32_t* page_table;   // [B, max_pages]
+    const int32_t* sealed_len;   // [B]
+    const int32_t* tail_len;     // [B]
+    const uint8_t* mask;         // [B, n_q, n_q] or nullptr (chain)
+    void* O;                     // [B, Hq, n_q, d]
+    float* LSE;                  // [B, Hq, n_q]
+    // Partials of (KV head, slot, group row): acc [.., d], (m, l) with m in the log2 domain.
+    // Sequence b's splits sit at slots part_first[b * Hkv + g] .. + part_count[..] - 1.
+    float* part_acc;             // [Hkv, S, R, d]
+    float* part_ml;              // [Hkv, S, R, 2]
+    int* part_first;             // [B * Hkv]
+    int* part_count;             // [B * Hkv]
+    unsigned int* err;
+    int64_t cap;                 // rows of a tail cache
+    int B, Hq, Hkv, d, n_q, G, R;
+    int max_pages, n_pages;
+    int S;                       // (sequence, split) slots per KV head, at least B
+    float scale_log2;            // softmax scale * log2(e)
+};
+
+// Lengths of one sequence, clamped so that every access stays in bounds (the merge kernel
+// flags a value that had to be clamped).
+struct Q8Keys {
+    int pages;                   // sealed pages
+    int64_t tail;                // tail rows
+    int page_tiles, tiles;
+};
+
+__device__ __forceinline__ Q8Keys q8_keys(const AttnQ8Params& p, int b) {
+    Q8Keys k;
+    int pages = p.sealed_len[b] / kPageTokens;
+    if (pages < 0) pages = 0;
+    k.pages = pages > p.max_pages ? p.max_pages : pages;
+    int64_t tail = p.tail_len[b];
+    if (tail < 0) tail = 0;
+    if (tail > p.cap - p.n_q) tail = p.cap - p.n_q;
+    k.tail = tail;
+    k.page_tiles = (k.pages + 1) / 2;
+    k.tiles = k.page_tiles + (int)((tail + p.n_q + kQ8Tile - 1) / kQ8Tile);
+    return k;
+}
+
+// Page id of block j of sequence b, clamped into the pool and flagged where it is outside.
+__device__ __forceinline__ int q8_page(const AttnQ8Params& p, int b, int j) {
+    const int id = p.page_table[(int64_t)b * p.max_pages + j];
+    if (id >= 0 && id < p.n_pages) return id;
+    if (p.err) atomicOr(p.err, kErrBadInput);
+    return 0;
+}
+
+struct Q8Split {
+    int b;               // sequence, or -1 where the slot has no work
+    int s, count;        // split s of count
+    int first;           // slot of the sequence's split 0
+};
+
+__device__ __forceinline__ int warp_sum_int(int v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The (sequence, split) of slot c, worked out by one whole warp from the device-side
+// lengths: the smallest number of tiles per split whose splits fit into the S slots, so
+// that short and long sequences of a ragged batch finish together.  Lanes take sequences
+// lane, lane + 32, ..., so a large batch costs B / 32 reads a round.
+__device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c) {
+    const int lane = threadIdx.x & 31;
+    int total = 0, longest = 1;
+    for (int b = lane; b < p.B; b += 32) {
+        const int t = q8_keys(p, b).tiles;
+        total += t;
+        longest = t > longest ? t : longest;
+    }
+    total = warp_sum_int(total);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    int lo = (total + p.S - 1) / p.S;
+    if (lo < 1) lo = 1;
+    int hi = longest > lo ? longest : lo;
+    if (p.B == 1) hi = lo;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        int used = 0;
+        for (int b = lane; b < p.B; b += 32) used += (q8_keys(p, b).tiles + mid - 1) / mid;
+        used = warp_sum_int(used);
+        if (used <= p.S) hi = mid; else lo = mid + 1;
+    }
+    int first = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b < p.B ? (q8_keys(p, b).tiles + lo - 1) / lo : 0;
+        int end = n;                                  // inclusive scan over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, c < first + end);
+        if (hit) {
+            const int w = __ffs(hit) - 1;
+            const int count = __shfl_sync(0xffffffffu, n, w);
+            const int f = first + __shfl_sync(0xffffffffu, end, w) - count;
+            return Q8Split{b0 + w, c - f, count, f};
+        }
+        first += __shfl_sync(0xffffffffu, end, 31);
+    }
+    return Q8Split{-1, 0, 0, 0};
+}
+
+// Group rows that one CTA of the history kernels takes.
+constexpr int kQ8SimtRows = 64;
+
+cudaError_t launch_attn_q8_simt(const AttnQ8Params& p, int dtype, cudaStream_t s);
+cudaError_t launch_attn_q8_merge(const AttnQ8Params& p, int dtype, cudaStream_t s);
+
+}  // namespace rapid

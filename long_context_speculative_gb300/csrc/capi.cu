@@ -17,14 +17,6 @@ namespace rapid {
 // [0] sticky error bits, [1] code of the first timed-out wait, [2..7] spare.
 __device__ unsigned int g_device_error[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
-namespace {
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 unsigned int* device_error_word() {
     void* ptr = nullptr;
     if (cudaGetSymbolAddress(&ptr, g_device_error) != cudaSuccess) {
@@ -41,6 +33,14 @@ int sm_count() {
         return 148;
     return n;
 }
+
+namespace {
+
+constexpr size_t kAlign = 256;
+
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct AttnPlan {
     bool tc;        // tensor-core history kernel

@@ -250,4 +250,8 @@ RAPID_DEVICE void bulk_prefetch_l2(const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+// Host helpers (capi.cu): address of the current device's error word, its SM count.
+unsigned int* device_error_word();
+int sm_count();
+
 }  // namespace rapid

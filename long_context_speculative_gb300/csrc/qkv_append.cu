@@ -1,0 +1,244 @@
+// Per-head norm, rotary positions and the append to the KV cache, in one pass over the
+// projection rows of a verify step or a prefill chunk.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w          (where a norm weight is given)
+//   (a, b) -> (a cos t - b sin t, b cos t + a sin t),   t = position * inv_freq[pair]
+//
+// Queries go to [B, Hq, n, d], the layout verify attention reads; keys and values to their
+// cache rows.  All arithmetic is in fp32 and rounded once, at the store.
+//
+// The angle is formed in fixed point: inv_freq / (2 pi) becomes a 64-bit fraction of a
+// turn, its product with the integer position wraps modulo one turn exactly, and the top
+// 32 bits go to sincospi.  An fp32 product would be off by 2^-24 of the angle, 0.008 rad at
+// position 131072.
+//
+// The work is copying: d elements in and out for each head row, no reuse.  A head row is
+// read by d / 16 lanes, each with the two 16-byte (bf16) pieces whose elements rotate into
+// each other, so a rotated pair never leaves its lane; a warp takes one token and some of
+// its heads, with the sines and cosines of its lanes' pairs kept in registers over all of
+// them.
+#include "common.cuh"
+#include "qkv_append.cuh"
+
+namespace rapid {
+
+namespace {
+
+constexpr int kAppendThreads = 128;
+constexpr int kAppendWarps = kAppendThreads / 32;
+
+// inv_freq / (2 pi) modulo one turn as a fraction of 2^64.  |f| = m 2^(e - 23) with m a
+// 24-bit integer, and 1 / (2 pi) = C 2^-66 to 64 bits, so the fraction is m C 2^(e - 25).
+__device__ __forceinline__ uint64_t turns_per_position(float f) {
+    constexpr uint64_t kInvTwoPi = 0xa2f9836e4e441529ull;   // 2^66 / (2 pi), rounded down
+    const uint32_t bits = __float_as_uint(f);
+    const int field = (int)((bits >> 23) & 0xff);
+    if (field == 0xff) return 0;                            // inf or NaN: no rotation is defined
+    const uint64_t m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u);
+    const int right = 25 - ((field ? field : 1) - 127);     // fraction = (hi : lo) >> right
+    const uint64_t lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+    uint64_t x;
+    if (right >= 128) x = 0;
+    else if (right >= 64) x = hi >> (right - 64);
+    else if (right > 0) x = (lo >> right) | (hi << (64 - right));
+    else x = right > -64 ? lo << -right : 0;
+    return (bits >> 31) ? 0 - x : x;
+}
+
+__device__ __forceinline__ void sincos_turn(uint64_t per_pos, int64_t pos, float* s, float* c) {
+    const uint64_t t = per_pos * (uint64_t)pos;             // modulo one turn
+    const int32_t top = (int32_t)((t + 0x80000000ull) >> 32);
+    sincospif((float)top * 4.656612873077392578125e-10f, s, c);   // top 2^-31 half turns
+}
+
+template <typename T> struct Piece;                         // 8 elements
+template <> struct Piece<__nv_bfloat16> { uint4 a; };
+template <> struct Piece<float> { float4 a, b; };
+
+__device__ __forceinline__ void load_piece(const __nv_bfloat16* p, Piece<__nv_bfloat16>& r) {
+    r.a = __ldg(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void load_piece(const float* p, Piece<float>& r) {
+    r.a = __ldg(reinterpret_cast<const float4*>(p));
+    r.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+}
+__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const Piece<__nv_bfloat16>& r) {
+    *reinterpret_cast<uint4*>(p) = r.a;
+}
+__device__ __forceinline__ void store_piece(float* p, const Piece<float>& r) {
+    reinterpret_cast<float4*>(p)[0] = r.a;
+    reinterpret_cast<float4*>(p)[1] = r.b;
+}
+__device__ __forceinline__ void unpack(const Piece<__nv_bfloat16>& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack(const Piece<float>& r, float (&x)[8]) {
+    x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+    x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Piece<__nv_bfloat16>& r) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Piece<float>& r) {
+    r.a = make_float4(x[0], x[1], x[2], x[3]);
+    r.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+template <typename T, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const QkvAppendParams p) {
+    constexpr int kLanes = D / 16;                  // lanes of one head row
+    constexpr int kRows = 32 / kLanes;              // head rows a warp handles at a time
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / kLanes, l = lane - sub * kLanes;
+    const int H = p.Hq + 2 * p.Hkv;
+    const int64_t unit = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const int64_t token = unit / p.slices;
+    const int slice = (int)(unit - token * p.slices);
+    if (token >= (int64_t)p.B * p.n) return;
+    const int b = (int)(token / p.n), i = (int)(token - (int64_t)b * p.n);
+
+    const int count = p.n_rows ? p.n_rows[b] : p.n;
+    const int64_t P = p.prefix_len[b];
+    if (count < 0 || count > p.n || P < 0 || P + count > p.cap) {   // refused: left alone
+        if (i == 0 && slice == 0 && lane == 0 && p.err) atomicOr(p.err, kErrBadInput);
+        return;
+    }
+    if (i >= count) return;
+    int64_t pos = P + (p.row_offset ? p.row_offset[(int64_t)b * p.n + i] : i);
+    if (p.pos_offset) pos += p.pos_offset[b];
+
+    // The lane's two pieces.  Rotated halves: piece c pairs with piece c + rot / 16; the
+    // pieces past rot are not rotated.  Interleaved pairs sit inside a piece.
+    const int half = p.rot / 16;
+    int c0, c1;
+    if (INTERLEAVED || l < half) { c0 = l; c1 = l + (INTERLEAVED ? kLanes : half); }
+    else { c0 = 2 * l; c1 = 2 * l + 1; }
+    const bool turn = !INTERLEAVED && l < half;
+    float sn[8], cs[8];
+    if (INTERLEAVED) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {               // u < 4: pairs of piece c0, else of c1
+            const int pair = (u < 4 ? c0 : c1) * 4 + (u & 3);
+            sn[u] = 0.f;
+            cs[u] = 1.f;
+            if (2 * pair < p.rot) sincos_turn(turns_per_position(__ldg(p.inv_freq + pair)), pos, &sn[u], &cs[u]);
+        }
+    } else if (turn) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            sincos_turn(turns_per_position(__ldg(p.inv_freq + 8 * c0 + u)), pos, &sn[u], &cs[u]);
+    }
+
+    const int steps = (H + kRows - 1) / kRows;
+    for (int it = slice; it < steps; it += p.slices) {
+        const int h = it * kRows + sub;
+        const bool live = h < H;
+        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+        const T* src;
+        T* dst;
+        if (is_q) {
+            src = static_cast<const T*>(p.q) + b * p.q_batch + i * p.q_token + (int64_t)h * D;
+            dst = static_cast<T*>(p.Q) + (((int64_t)b * p.Hq + h) * p.n + i) * D;
+        } else {
+            const int hk = h - p.Hq - (is_k ? 0 : p.Hkv);
+            src = is_k ? static_cast<const T*>(p.k) + b * p.k_batch + i * p.k_token + (int64_t)hk * D
+                       : static_cast<const T*>(p.v) + b * p.v_batch + i * p.v_token + (int64_t)hk * D;
+            dst = static_cast<T*>(is_k ? p.K : p.V) + (((int64_t)b * p.Hkv + hk) * p.cap + P + i) * D;
+        }
+        Piece<T> r0 = {}, r1 = {};
+        if (live) {
+            load_piece(src + 8 * c0, r0);
+            load_piece(src + 8 * c1, r1);
+        }
+        float x[8], y[8];
+        unpack(r0, x);
+        unpack(r1, y);
+        float ss = 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) ss = fmaf(x[u], x[u], fmaf(y[u], y[u], ss));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (!live) continue;
+        if (is_q || is_k) {
+            const T* w = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+            if (w) {
+                const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+                Piece<T> w0, w1;
+                load_piece(w + 8 * c0, w0);
+                load_piece(w + 8 * c1, w1);
+                float wx[8], wy[8];
+                unpack(w0, wx);
+                unpack(w1, wy);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    x[u] = x[u] * inv * wx[u];
+                    y[u] = y[u] * inv * wy[u];
+                }
+            }
+            if (INTERLEAVED) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float a = x[2 * u], c = x[2 * u + 1], e = y[2 * u], f = y[2 * u + 1];
+                    x[2 * u] = a * cs[u] - c * sn[u];
+                    x[2 * u + 1] = c * cs[u] + a * sn[u];
+                    y[2 * u] = e * cs[4 + u] - f * sn[4 + u];
+                    y[2 * u + 1] = f * cs[4 + u] + e * sn[4 + u];
+                }
+            } else if (turn) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float a = x[u], c = y[u];
+                    x[u] = a * cs[u] - c * sn[u];
+                    y[u] = c * cs[u] + a * sn[u];
+                }
+            }
+            pack(x, r0);
+            pack(y, r1);
+        }
+        store_piece(dst + 8 * c0, r0);
+        store_piece(dst + 8 * c1, r1);
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(QkvAppendParams p, cudaStream_t st) {
+    const int steps = (p.Hq + 2 * p.Hkv + 32 / (D / 16) - 1) / (32 / (D / 16));
+    const int64_t tokens = (int64_t)p.B * p.n;
+    // few tokens: spread each one's heads over several warps
+    int64_t slices = (152 * 32 + tokens - 1) / tokens;
+    if (slices > steps) slices = steps;
+    p.slices = (int)(slices < 1 ? 1 : slices);
+    const int64_t blocks = (tokens * p.slices + kAppendWarps - 1) / kAppendWarps;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks, 1, 1);
+    cfg.blockDim = dim3(kAppendThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return p.interleaved ? cudaLaunchKernelEx(&cfg, qkv_append_kernel<T, D, true>, p)
+                         : cudaLaunchKernelEx(&cfg, qkv_append_kernel<T, D, false>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_qkv_append(QkvAppendParams p, int dtype, cudaStream_t st) {
+    if (dtype == 1)
+        return p.d == 128 ? launch_typed<__nv_bfloat16, 128>(p, st) : launch_typed<__nv_bfloat16, 64>(p, st);
+    return p.d == 128 ? launch_typed<float, 128>(p, st) : launch_typed<float, 64>(p, st);
+}
+
+}  // namespace rapid

@@ -6,6 +6,7 @@ device pointers, sizes workspaces and passes the current CUDA stream.  There
 is no CPU or PyTorch fallback: if librapid.so is missing or cannot be loaded,
 every call raises.
 """
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -30,6 +31,9 @@ RAPID_COMMIT_MAX_LAYERS = 128
 RAPID_RETRIEVAL_MAX_CHUNKS = 8192
 RAPID_LM_HEAD_MAX_ROWS = 256
 RAPID_NOALLOC_MAX_NODES = 4096
+RAPID_ROPE_INTERLEAVED = 1
+RAPID_Q8_PAGE_TOKENS = 64
+RAPID_Q8_MAX_PAGES = 1 << 24
 
 _lib = None
 
@@ -98,6 +102,19 @@ def lib() -> ctypes.CDLL:
     L.rapid_lm_head_accept_ex.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, f32, f32,
                                           u64, vp, u32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
     L.rapid_lm_head_accept_ex.restype = i32
+    L.rapid_qkv_append.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, f32, vp,
+                                   i32, u32, vp, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.rapid_qkv_append.restype = i32
+    L.rapid_kv_seal.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i64, i32, i32, vp, i32,
+                                vp, vp, vp]
+    L.rapid_kv_seal.restype = i32
+    L.rapid_kv_seal_advance.argtypes = [vp, vp, vp, i32, i32, i32, i64, i32, vp]
+    L.rapid_kv_seal_advance.restype = i32
+    L.rapid_verify_attn_q8_workspace_size.argtypes = [i32, i32, i32, i32, i32, i64, i32, i32]
+    L.rapid_verify_attn_q8_workspace_size.restype = sz
+    L.rapid_verify_attn_q8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64,
+                                       i32, i32, vp, vp, vp, f32, vp, vp, vp, sz, vp]
+    L.rapid_verify_attn_q8.restype = i32
     _lib = L
     return L
 
@@ -395,6 +412,167 @@ def rapid_retrieval_select(scores, context_tokens, selected, n_selected, tokens_
     _check(st, "rapid_retrieval_select")
 
 
+def _head_rows(t, B, n, H, d, dtype, name):
+    """Batch and token stride of projection rows [B, n, H, d] whose heads lie one after the
+    other (a view of a fused projection will do)."""
+    if t.dim() != 4 or tuple(t.shape) != (B, n, H, d) or t.dtype != dtype:
+        raise RapidError(f"{name} must be a {dtype} tensor of shape {(B, n, H, d)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise RapidError("librapid works on CUDA tensors only (no CPU path)")
+    sb, sn, sh, se = t.stride()
+    if se != 1 or (H > 1 and sh != d):
+        raise RapidError(f"{name}: the heads of a token must be contiguous")
+    # the stride of a dimension of size 1 means nothing and may be anything
+    return (sb if B > 1 else 0), (sn if n > 1 else 0)
+
+
+def rapid_qkv_append(q, k, v, q_weight, k_weight, eps, inv_freq, flags, prefix_len, pos_offset,
+                     row_offset, n_rows, Q, Kcache, Vcache, stream=None):
+    """Norm and rotate the rows q [B, n, Hq, d] and k [B, n, Hkv, d], write queries to
+    Q [B, Hq, n, d] and keys and values to cache rows prefix_len + i; None for what is
+    optional.  q, k and v may be views of one fused projection."""
+    _need_cuda(q_weight, k_weight, inv_freq, prefix_len, pos_offset, row_offset, n_rows, Q,
+               Kcache, Vcache)
+    if Q.dim() != 4 or Kcache.dim() != 4:
+        raise RapidError("Q and the caches must have four dimensions")
+    B, Hq, n, d = Q.shape
+    Hkv, cap = Kcache.shape[1], Kcache.shape[2]
+    dt = Q.dtype
+    strides = (ctypes.c_int64 * 6)(*_head_rows(q, B, n, Hq, d, dt, "q"),
+                                   *_head_rows(k, B, n, Hkv, d, dt, "k"),
+                                   *_head_rows(v, B, n, Hkv, d, dt, "v"))
+    _need(Kcache, dt, (B, Hkv, cap, d), "Kcache")
+    _need(Vcache, dt, (B, Hkv, cap, d), "Vcache")
+    _need(q_weight, dt, (d,), "q_weight")
+    _need(k_weight, dt, (d,), "k_weight")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _need(inv_freq, torch.float32, (rot // 2,), "inv_freq")
+    _need(prefix_len, torch.int32, (B,), "prefix_len")
+    _need(pos_offset, torch.int32, (B,), "pos_offset")
+    _need(row_offset, torch.int32, (B, n), "row_offset")
+    _need(n_rows, torch.int32, (B,), "n_rows")
+    _need_same_device(q, k, v, q_weight, k_weight, inv_freq, prefix_len, pos_offset, row_offset,
+                      n_rows, Q, Kcache, Vcache)
+    st = lib().rapid_qkv_append(_ptr(q), _ptr(k), _ptr(v), strides, _dtype_code(Q), B, n, Hq, Hkv,
+                                d, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), rot,
+                                int(flags), _ptr(prefix_len), _ptr(pos_offset), _ptr(row_offset),
+                                _ptr(n_rows), _ptr(Q), _ptr(Kcache), _ptr(Vcache), cap,
+                                _stream(stream))
+    _check(st, "rapid_qkv_append")
+
+
+class Q8LayerTable:
+    """The device addresses of every layer's tail caches [B, Hkv, tail_capacity, d], pages
+    [n_pages, Hkv, 2, 64, d] (torch.float8_e4m3fn) and scales [n_pages, Hkv, 2] (float32),
+    checked and packed once for repeated rapid_kv_seal calls."""
+
+    def __init__(self, K_layers, V_layers, page_layers, scale_layers):
+        lists = [list(x) for x in (K_layers, V_layers, page_layers, scale_layers)]
+        if not lists[0] or len({len(x) for x in lists}) != 1:
+            raise RapidError("rapid_kv_seal needs matching, non-empty layer lists")
+        if len(lists[0]) > RAPID_COMMIT_MAX_LAYERS:
+            raise RapidError(f"at most {RAPID_COMMIT_MAX_LAYERS} layers per call")
+        for x in lists:
+            _need_cuda(*x)
+        K, V, pages, scales = lists
+        if K[0].dim() != 4 or pages[0].dim() != 5:
+            raise RapidError("tail caches are [B, Hkv, tail_capacity, d], pages [n_pages, Hkv, 2, 64, d]")
+        self.layers = len(K)
+        self.B, self.Hkv, self.cap, self.d = K[0].shape
+        self.n_pages = pages[0].shape[0]
+        self.dtype = _dtype_code(K[0])
+        for t in K + V:
+            _need(t, K[0].dtype, (self.B, self.Hkv, self.cap, self.d), "tail cache")
+        for t in pages:
+            _need(t, torch.float8_e4m3fn,
+                  (self.n_pages, self.Hkv, 2, RAPID_Q8_PAGE_TOKENS, self.d), "pages")
+        for t in scales:
+            _need(t, torch.float32, (self.n_pages, self.Hkv, 2), "scales")
+        _need_same_device(*K, *V, *pages, *scales)
+        self.device = K[0].device
+        self._ptrs = [(ctypes.c_void_p * self.layers)(*[t.data_ptr() for t in x]) for x in lists]
+        self._keep = lists                                # the tensors outlive the table
+
+    def _lengths(self, page_table, sealed_len, tail_len):
+        _need_cuda(page_table, sealed_len, tail_len)
+        if page_table.dim() != 2:
+            raise RapidError("page_table must be [B, max_pages]")
+        _need(page_table, torch.int32, (self.B, page_table.shape[1]), "page_table")
+        _need(sealed_len, torch.int32, (self.B,), "sealed_len")
+        _need(tail_len, torch.int32, (self.B,), "tail_len")
+        _need_same_device(page_table, sealed_len, tail_len, self._keep[0][0])
+
+    def seal(self, page_table, sealed_len, tail_len, keep_rows=0, stream=None):
+        """Seal (tail_len - keep_rows) // 64 blocks of every sequence on every layer and move
+        the tail rows that stay to the front; the lengths are left to seal_advance."""
+        self._lengths(page_table, sealed_len, tail_len)
+        st = lib().rapid_kv_seal(*self._ptrs, self.layers, self.dtype, self.B, self.Hkv, self.d,
+                                 self.cap, int(keep_rows), self.n_pages, _ptr(page_table),
+                                 page_table.shape[1], _ptr(sealed_len), _ptr(tail_len),
+                                 _stream(stream))
+        _check(st, "rapid_kv_seal")
+
+    def seal_advance(self, page_table, sealed_len, tail_len, keep_rows=0, stream=None):
+        """sealed_len += 64 n_b, tail_len -= 64 n_b (device, in place)."""
+        self._lengths(page_table, sealed_len, tail_len)
+        st = lib().rapid_kv_seal_advance(_ptr(sealed_len), _ptr(tail_len), _ptr(page_table),
+                                         self.B, page_table.shape[1], self.n_pages, self.cap,
+                                         int(keep_rows), _stream(stream))
+        _check(st, "rapid_kv_seal_advance")
+
+
+def rapid_kv_seal(table, page_table, sealed_len, tail_len, keep_rows=0, stream=None):
+    """Q8LayerTable.seal under the C call's name."""
+    table.seal(page_table, sealed_len, tail_len, keep_rows, stream)
+
+
+def rapid_kv_seal_advance(table, page_table, sealed_len, tail_len, keep_rows=0, stream=None):
+    """Q8LayerTable.seal_advance under the C call's name."""
+    table.seal_advance(page_table, sealed_len, tail_len, keep_rows, stream)
+
+
+def rapid_verify_attn_q8_workspace_size(B, Hq, Hkv, d, n_q, tail_capacity, max_pages, dtype) -> int:
+    return int(lib().rapid_verify_attn_q8_workspace_size(B, Hq, Hkv, d, n_q, tail_capacity,
+                                                         max_pages, dtype))
+
+
+def rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
+                         spec_mask, softmax_scale, O, LSE, workspace, stream=None):
+    """Verify attention over sealed 8-bit pages, tail rows and the speculative rows."""
+    _need_cuda(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len, spec_mask, O,
+               LSE, workspace)
+    if Q.dim() != 4 or K_tail.dim() != 4 or pages.dim() != 5 or page_table.dim() != 2:
+        raise RapidError("Q and the tails have 4 dimensions, pages 5, page_table 2")
+    B, Hq, n_q, d = Q.shape
+    Hkv, cap = K_tail.shape[1], K_tail.shape[2]
+    n_pages, max_pages = pages.shape[0], page_table.shape[1]
+    _need(K_tail, Q.dtype, (B, Hkv, cap, d), "K_tail")
+    _need(V_tail, Q.dtype, (B, Hkv, cap, d), "V_tail")
+    _need(pages, torch.float8_e4m3fn, (n_pages, Hkv, 2, RAPID_Q8_PAGE_TOKENS, d), "pages")
+    _need(scales, torch.float32, (n_pages, Hkv, 2), "scales")
+    _need(page_table, torch.int32, (B, max_pages), "page_table")
+    _need(sealed_len, torch.int32, (B,), "sealed_len")
+    _need(tail_len, torch.int32, (B,), "tail_len")
+    if spec_mask is not None and spec_mask.dtype != torch.bool:
+        _need(spec_mask, torch.uint8, (B, n_q, n_q), "spec_mask")
+    elif spec_mask is not None:
+        _need(spec_mask, torch.bool, (B, n_q, n_q), "spec_mask")
+    _need(O, Q.dtype, (B, Hq, n_q, d), "O")
+    _need(LSE, torch.float32, (B, Hq, n_q), "LSE")
+    _need_same_device(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
+                      spec_mask, O, LSE, workspace)
+    st = lib().rapid_verify_attn_q8(_ptr(Q), _ptr(K_tail), _ptr(V_tail), _ptr(pages), _ptr(scales),
+                                    _ptr(page_table), _dtype_code(Q), B, Hq, Hkv, d, n_q, cap,
+                                    n_pages, max_pages, _ptr(sealed_len), _ptr(tail_len),
+                                    _ptr(spec_mask), float(softmax_scale), _ptr(O), _ptr(LSE),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                    _stream(stream))
+    _check(st, "rapid_verify_attn_q8")
+
+
 def rapid_device_error(clear: bool = True) -> int:
     return int(lib().rapid_device_error(1 if clear else 0))
 
@@ -489,3 +667,49 @@ def lm_head_accept(hidden, W_lm, q, tokens, parent=None, T=1.0, eta=1.0, seed=0,
     rapid_lm_head_accept(hidden, W_lm, q, tokens, parent, T, eta, seed, flags, n_acc, nxt, path,
                          diag, workspace, stream)
     return dict(n_accepted=n_acc, next_token=nxt, path=path, diag=diag)
+
+
+def _on(stream):
+    """What a wrapper allocates belongs to the stream that its kernels run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def qkv_append(q, k, v, K, V, prefix_len, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6,
+               interleaved=False, pos_offset=None, row_offset=None, n_rows=None, out=None,
+               stream=None):
+    """Queries [B, Hq, n, d] of the projection rows q [B, n, Hq, d], k and v [B, n, Hkv, d], with
+    norm (where a weight is given) and rotation (where inv_freq is given); keys and values go to
+    rows prefix_len[b] + i of K and V [B, Hkv, capacity, d].
+
+    Where n_rows cuts a sequence short, its rows of `out` behind the count are left as they are
+    (unset memory in an `out` made here)."""
+    with _on(stream):
+        if out is None:
+            B, n, Hq, d = q.shape
+            out = torch.empty((B, Hq, n, d), dtype=q.dtype, device=q.device)
+        rapid_qkv_append(q, k, v, q_weight, k_weight, eps, inv_freq,
+                         RAPID_ROPE_INTERLEAVED if interleaved else 0, prefix_len, pos_offset,
+                         row_offset, n_rows, out, K, V, stream)
+    return out
+
+
+def verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
+                   spec_mask=None, softmax_scale=0.0, out=None, lse=None, workspace=None,
+                   stream=None):
+    """O [B,Hq,n_q,d] (dtype of Q) and LSE [B,Hq,n_q] float32 over an 8-bit history."""
+    B, Hq, n_q, d = Q.shape
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(Q)
+        if lse is None:
+            lse = torch.empty((B, Hq, n_q), dtype=torch.float32, device=Q.device)
+        if workspace is None:
+            nbytes = rapid_verify_attn_q8_workspace_size(B, Hq, K_tail.shape[1], d, n_q,
+                                                         K_tail.shape[2], page_table.shape[1],
+                                                         _dtype_code(Q))
+            if nbytes == 0:
+                raise RapidError("unsupported verify_attn_q8 shape")
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+        rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
+                             spec_mask, softmax_scale, out, lse, workspace, stream)
+    return out, lse
