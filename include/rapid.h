@@ -743,7 +743,7 @@ size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_
  *
  * Errors: those of rapid_verify_attn, and RAPID_EINVAL for n_pages < 1, n_pages
  * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], scales
- * or index arrays not 4-byte aligned.
+ * not 8-byte aligned, index arrays not 4-byte aligned.
  */
 rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void* V_tail,
                                   const void* pages, const float* scales, const int32_t* page_table,

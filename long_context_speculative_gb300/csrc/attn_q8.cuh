@@ -135,8 +135,11 @@ __device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c) {
 
 // Group rows that one CTA of the history kernels takes.
 constexpr int kQ8SimtRows = 64;
+constexpr int kQ8TcRows = 128;
+__host__ __device__ __forceinline__ int q8_row_blocks(int R) { return (R + kQ8TcRows - 1) / kQ8TcRows; }
 
-cudaError_t launch_attn_q8_simt(const AttnQ8Params& p, int dtype, cudaStream_t s);
+cudaError_t launch_attn_q8_tc(const AttnQ8Params& p, cudaStream_t s);   // bf16
+cudaError_t launch_attn_q8_simt(const AttnQ8Params& p, cudaStream_t s); // fp32
 cudaError_t launch_attn_q8_merge(const AttnQ8Params& p, int dtype, cudaStream_t s);
 
 }  // namespace rapid

@@ -44,22 +44,9 @@ __device__ __forceinline__ void load_row16(const float* src, float (&x)[16]) {
         x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
     }
 }
-__device__ __forceinline__ void load_row16(const __nv_bfloat16* src, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(src)[i];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            x[8 * i + 2 * u] = __uint_as_float(w[u] << 16);
-            x[8 * i + 2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
-        }
-    }
-}
-
 // CTA = (slot and block of up to 64 group rows, KV head).  Each lane owns one key of a
 // 32-key step for the scores and d / 32 output columns for the products with V.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8Params p) {
     constexpr int DP = D + 4;                 // padded K pitch: conflict-free float4 rows
     constexpr int NC = D / 32;                // output columns per lane
@@ -93,10 +80,10 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     const int r0 = rb * kQ8SimtRows;
     const int nrows = min(kQ8SimtRows, p.R - r0);
 
-    const T* Qg = static_cast<const T*>(p.Q) + ((int64_t)b * p.Hq + (int64_t)g * p.G) * p.n_q * D;
+    const float* Qg = static_cast<const float*>(p.Q) + ((int64_t)b * p.Hq + (int64_t)g * p.G) * p.n_q * D;
     for (int idx = threadIdx.x; idx < kQ8SimtRows * D; idx += kSimtThreads) {
         const int r = idx / D, k = idx - r * D;
-        sQ[idx] = r < nrows ? to_float(Qg[(int64_t)(r0 + r) * D + k]) * p.scale_log2 : 0.f;
+        sQ[idx] = r < nrows ? Qg[(int64_t)(r0 + r) * D + k] * p.scale_log2 : 0.f;
     }
     float acc[kRowsPerWarp][NC];
     float m[kRowsPerWarp], l[kRowsPerWarp];
@@ -107,8 +94,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
     }
-    const T* Kh = static_cast<const T*>(p.K) + bg * p.cap * D;
-    const T* Vh = static_cast<const T*>(p.V) + bg * p.cap * D;
+    const float* Kh = static_cast<const float*>(p.K) + bg * p.cap * D;
+    const float* Vh = static_cast<const float*>(p.V) + bg * p.cap * D;
     const int64_t tail_keys = keys.tail + p.n_q;
 
     for (int64_t step = (int64_t)t_begin * (kQ8Tile / kKeys); step < (int64_t)t_end * (kQ8Tile / kKeys); ++step) {
@@ -303,10 +290,10 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
     if (lane == 0) p.LSE[row] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t simt_typed(const AttnQ8Params& p, cudaStream_t st) {
     const int smem = (kQ8SimtRows * D + kKeys * (D + 4) + kKeys * D) * (int)sizeof(float);
-    auto kern = attn_q8_simt_kernel<T, D>;
+    auto kern = attn_q8_simt_kernel<D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int n_rb = (p.R + kQ8SimtRows - 1) / kQ8SimtRows;
@@ -331,10 +318,8 @@ cudaError_t merge_typed(const AttnQ8Params& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attn_q8_simt(const AttnQ8Params& p, int dtype, cudaStream_t s) {
-    if (dtype == 1)
-        return p.d == 128 ? simt_typed<__nv_bfloat16, 128>(p, s) : simt_typed<__nv_bfloat16, 64>(p, s);
-    return p.d == 128 ? simt_typed<float, 128>(p, s) : simt_typed<float, 64>(p, s);
+cudaError_t launch_attn_q8_simt(const AttnQ8Params& p, cudaStream_t s) {
+    return p.d == 128 ? simt_typed<128>(p, s) : simt_typed<64>(p, s);
 }
 
 cudaError_t launch_attn_q8_merge(const AttnQ8Params& p, int dtype, cudaStream_t s) {

@@ -1,0 +1,868 @@
+// Verify attention over an 8-bit history on tensor cores (bf16 queries and tails, head
+// dimension 64 or 128, any group size), written for sm_103a.
+//
+// Both products are formed transposed, with the keys (and then the head dimension) as the
+// M = 128 operand and the query rows of the KV-head group as N:
+//   S^T[key, row] = K Q^T            A = K (tensor memory), B = Q (shared memory)
+//   O^T[dim, row] += V^T P^T         A = V (shared memory, MN-major), B = P (shared memory)
+// A verify step has few rows (4 to 128 for a KV head), so rows in M would leave most of every
+// tensor instruction idle (44 of 128 rows for an 11-node chain); in N they cost what they
+// are, in steps of 16.  It also gives every softmax thread one key: the key's page scales are
+// two numbers of the thread, and the running maximum needs no reduction at all until some
+// score passes the reference by more than 2^8 (the reference of a row then moves, O is
+// rescaled, and the tile is taken again).
+//
+// The 8-bit codes become fp16 exactly, so K and V lose nothing.  Q is held as fp16 times one
+// power of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to
+// 2^-30 of that keep all 8 bits of a bf16).  P is fp16 of 2^(s - ref), 2^7 at the reference
+// and below 2^15, so it keeps 11 bits down to 2^-21 of the row's largest and fades out below
+// 2^-31.  The scale of V joins P relative to the largest scale of the CTA's pages, which
+// multiplies O at the end.  Tail rows and speculative rows are bf16 as they are: those tiles,
+// the last of a sequence, run the same way in bf16.
+//
+// CTA = (sequence and split, block of at most 128 group rows; KV head).  Tiles are 128 keys:
+// two pages, or 128 tail rows.  Warps:
+//   softmax     4 (up to 64 rows) or 8 (two groups with half the rows each); warp w owns the
+//               keys, later the output dimensions, of tensor-memory lane quadrant w % 4
+//   converters  4: codes -> fp16, K into tensor memory, V into swizzled shared memory
+//   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
+//               into a ring of raw stages by TMA
+//   issuer      1: the MMAs, in the order in which their inputs become ready
+// Every wait is bounded in wall-clock time; after a failed wait the kernel records an error
+// code, stops issuing, drains and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+
+#include <cstddef>
+
+#include "attn_q8.cuh"
+#include "common.cuh"
+#include "tcgen05.cuh"
+
+namespace rapid {
+
+namespace {
+
+constexpr int kMaxRawStages = 6;
+constexpr int kFlagged = 64;           // pieces of V remembered for an element that is not finite
+
+// Tensor-memory columns (512): K buffer u at 64 u, O^T at 128, S^T buffer u at 256 + 128 u.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemK = 0;
+constexpr uint32_t kTmemO = 128;
+constexpr uint32_t kTmemS = 256;
+
+constexpr float kRefShift = 7.f;       // P is 2^7 at the reference ...
+constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
+                                       // (fp16 ends at 65504)
+
+template <int D, int NCH, int GROUPS>
+struct Plan {
+    static constexpr int kCols = 16 * NCH;                  // group rows of one softmax group
+    static constexpr int kN = kCols * GROUPS;               // N of the products
+    static constexpr int kSoftmaxWarps = 4 * GROUPS;
+    static constexpr int kConvWarp = kSoftmaxWarps;         // first of four
+    static constexpr int kProducerWarp = kConvWarp + 4;
+    static constexpr int kMmaWarp = kConvWarp + 7;
+    static constexpr int kThreads = 32 * (kSoftmaxWarps + 8);
+    static constexpr int kPageBytes = 2 * kPageTokens * D;  // K and V of one page and head
+    static constexpr int kRawBytes = 2 * kPageBytes;        // one stage: two pages
+    static constexpr int kVBlock = kQ8Tile * 128;           // 64 dimensions of a V tile
+    static constexpr int kVBytes = (D / 64) * kVBlock;
+    static constexpr int kPBlocks = (kN + 63) / 64;
+    static constexpr int kPBytes = kPBlocks * kQ8Tile * 128;
+    static constexpr int kQBlock = kN * 128;                // 64 dimensions of Q
+    static constexpr int kQBytes = (D / 64) * kQBlock;
+    // V comes first: at D = 64 the M = 128 operand's second half reads on into what follows
+    static constexpr int kOffV = 0;
+    static constexpr int kOffP = kOffV + 2 * kVBytes;
+    static constexpr int kOffQ = kOffP + kPBytes;
+    static constexpr int kOffRaw = (kOffQ + kQBytes + 1023) / 1024 * 1024;
+    static constexpr int kScalarBytes = 4096;
+    static constexpr int kFit = (232448 - 1024 - kScalarBytes - kOffRaw) / kRawBytes;
+    static constexpr int kStages = kFit < kMaxRawStages ? kFit : kMaxRawStages;
+    static constexpr int kOffScalar = kOffRaw + kStages * kRawBytes;
+    static constexpr int kSmemBytes = kOffScalar + kScalarBytes + 1024;
+    static_assert(D == 64 || D == 128, "head dimension 64 or 128");
+    static_assert(kN <= 128 && kCols <= 64, "at most 128 rows, 64 in a group");
+    static_assert(kStages >= 2, "too few stages");
+    static_assert(kOffRaw + kStages * kRawBytes >= kOffV + 2 * kVBytes + kVBlock, "V operand in bounds");
+};
+
+struct Scalars {
+    uint64_t raw_full[kMaxRawStages];
+    uint64_t raw_free[kMaxRawStages];
+    uint64_t k_full[2];      // K in tensor memory
+    uint64_t s_full[2];      // S^T done (and K's buffer free)
+    uint64_t s_free[2];      // S^T loaded by the softmax warps
+    uint64_t v_full[2];
+    uint64_t pv_done[2];     // O^T += V^T P^T of a tile done (V's buffer and P free)
+    uint64_t p_full;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    Q8Split split;
+    alignas(16) float neg_ref[128];   // -(reference) of every row: P = 2^(s + neg_ref); +inf before the first key
+    alignas(16) float corr[128];
+    float part[2][4][64];    // per softmax group and warp: a number for each of its rows
+    float wmax[16];
+    int flagged;             // pieces of tail rows whose V is not finite in some element
+    int64_t flagged_piece[kFlagged];   // row * (d / 8) + piece of 8 elements
+};
+static_assert(sizeof(Scalars) <= 4096, "scalar block too small");
+static_assert(offsetof(Scalars, neg_ref) % 16 == 0 && offsetof(Scalars, corr) % 16 == 0,
+              "rows' references are read four at a time");
+
+enum : unsigned int {
+    kRoleProducer = 0x11u << 24, kRoleMma = 0x12u << 24, kRoleSoftmax = 0x13u << 24,
+    kRoleConvert = 0x14u << 24,
+    kBarRawFull = 1u << 16, kBarRawFree = 2u << 16, kBarS = 3u << 16, kBarPv = 4u << 16,
+    kBarAny = 5u << 16, kBarDrain = 6u << 16
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float warp_max_redux(float x) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+// Four e4m3 codes to four fp16 values (exact).
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
+    uint2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(r.x), "=r"(r.y)
+        : "r"(w));
+    return r;
+}
+
+// Barrier of one softmax group with an OR over its 128 threads.
+__device__ __forceinline__ bool group_any(int gr, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(1 + gr)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int gr) {
+    asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + gr) : "memory");
+}
+
+// Instruction descriptor: fp32 sums, A and B fp16 or bf16, A / B MN-major, M = 128.
+constexpr uint32_t idesc(bool bf16, bool a_mn, bool b_mn, int n) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+           (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int D, int NCH, int GROUPS>
+__global__ void __launch_bounds__(Plan<D, NCH, GROUPS>::kThreads, 1)
+attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p, const int n_rb,
+                  const int rows_per_block) {
+    using L = Plan<D, NCH, GROUPS>;
+    constexpr int kStages = L::kStages;
+    constexpr int kN = L::kN;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Scalars* sc = reinterpret_cast<Scalars*>(smem + L::kOffScalar);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int slot_idx = blockIdx.x / n_rb, rb = blockIdx.x - slot_idx * n_rb;
+    const int g = blockIdx.y;
+    const int r0 = rb * rows_per_block;                 // first group row of this CTA
+    const int Rb = min(rows_per_block, p.R - r0);       // its rows
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sc->raw_full[i], 1);
+            mbar_init(&sc->raw_free[i], 4);
+        }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(&sc->k_full[u], 128);
+            mbar_init(&sc->s_full[u], 1);
+            mbar_init(&sc->s_free[u], L::kSoftmaxWarps);
+            mbar_init(&sc->v_full[u], 128);
+            mbar_init(&sc->pv_done[u], 1);
+        }
+        mbar_init(&sc->p_full, 128 * GROUPS);
+        mbar_init(&sc->drain, 1);
+        sc->abort = 0;
+        sc->flagged = 0;
+        fence_mbar_init();
+    }
+    if (tid < 128) sc->neg_ref[tid] = INFINITY;
+    if (warp == L::kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sc->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    griddep_wait();
+    if (warp == 0) {
+        const Q8Split sp0 = q8_split_of(p, slot_idx);
+        if (lane == 0) {
+            sc->split = sp0;
+            if (sp0.b >= 0 && sp0.s == 0 && rb == 0) {
+                p.part_first[sp0.b * p.Hkv + g] = sp0.first;
+                p.part_count[sp0.b * p.Hkv + g] = sp0.count;
+            }
+        }
+    }
+    tc_fence_before();   // the allocation, before its address is read
+    __syncthreads();
+    tc_fence_after();
+
+    const Q8Split sp = sc->split;
+    const bool has_work = sp.b >= 0;
+    const int b = has_work ? sp.b : 0;
+    const int64_t bg = (int64_t)b * p.Hkv + g;
+    const Q8Keys keys = q8_keys(p, b);
+    const int t_begin = has_work ? (int)((int64_t)sp.s * keys.tiles / sp.count) : 0;
+    const int t_end = has_work ? (int)((int64_t)(sp.s + 1) * keys.tiles / sp.count) : 0;
+    const int n = t_end - t_begin;
+    const int n_page = min(max(keys.page_tiles - t_begin, 0), n);   // the first n_page tiles are pages
+    const int64_t tail_keys = keys.tail + p.n_q;
+    const __nv_bfloat16* Kh = static_cast<const __nv_bfloat16*>(p.K) + bg * p.cap * D;
+    const __nv_bfloat16* Vh = static_cast<const __nv_bfloat16*>(p.V) + bg * p.cap * D;
+    const uint4* Qg = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(p.Q) +
+        (((int64_t)b * p.Hq + (int64_t)g * p.G) * p.n_q + r0) * D);
+    const int64_t slot = ((int64_t)g * p.S + slot_idx) * p.R + r0;   // this CTA's partial rows
+
+    // Q into shared memory: K-major, 128-byte swizzle, blocks of 64 dimensions; piece i is 8
+    // elements of row i / (D / 8).  Rows past the CTA's are zero.
+    auto q_address = [&](int i) -> uint4* {
+        const int r = i / (D / 8), j = i - r * (D / 8);
+        return reinterpret_cast<uint4*>(smem + L::kOffQ + (j >> 3) * L::kQBlock + r * 128 +
+                                        (((j & 7) ^ (r & 7)) << 4));
+    };
+    float q_unit = 1.f;                                 // Q = unit * (its fp16 form)
+    if (n_page > 0) {
+        float top = 0.f;
+        for (int i = tid; i < Rb * (D / 8); i += L::kThreads) {
+            const uint4 v = Qg[i];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float x = fabsf(__uint_as_float(w[u] << 16)), y = fabsf(__uint_as_float(w[u] & 0xffff0000u));
+                if (x < INFINITY) top = fmaxf(top, x);
+                if (y < INFINITY) top = fmaxf(top, y);
+            }
+        }
+        top = warp_max(top);
+        if (lane == 0) sc->wmax[warp] = top;
+        __syncthreads();
+        top = 0.f;
+        for (int i = 0; i < L::kThreads / 32; ++i) top = fmaxf(top, sc->wmax[i]);
+        // top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
+        const int k = (int)(__float_as_uint(top) >> 23) - 127;
+        const int up = min(14 - k, 100);
+        const float mul = __uint_as_float((uint32_t)(127 + max(up, -126)) << 23);
+        q_unit = 1.f / mul;
+        for (int i = tid; i < kN * (D / 8); i += L::kThreads) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i < Rb * (D / 8)) {
+                v = Qg[i];
+                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    w[u] = f16x2(__uint_as_float(w[u] << 16) * mul, __uint_as_float(w[u] & 0xffff0000u) * mul);
+            }
+            *q_address(i) = v;
+        }
+    } else if (n > 0) {
+        for (int i = tid; i < kN * (D / 8); i += L::kThreads)
+            *q_address(i) = i < Rb * (D / 8) ? Qg[i] : make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sc->tmem_base;
+    const uint32_t smem_base = smem_u32(smem);
+
+    if (n <= 0) {
+        // nothing to do
+    } else if (warp == L::kProducerWarp) {
+        // ------------------------------ producer ------------------------------
+        // lane i holds the id of page 32 k + i of the split
+        const uint64_t policy = l2_policy_evict_first();
+        const bool once = n_rb == 1;                    // else the other row blocks read it again
+        const int first_page = 2 * t_begin, last_page = keys.pages;
+        int id = 0, issued = 0;
+        bool ok = true;
+        for (int i = 0; i < n_page && ok; ++i) {
+            if ((i & 15) == 0) {
+                const int j = first_page + 2 * i + lane;
+                id = j < last_page ? q8_page(p, b, j) : 0;
+            }
+            const int id0 = __shfl_sync(0xffffffffu, id, (2 * i) & 31);
+            const int id1 = __shfl_sync(0xffffffffu, id, (2 * i + 1) & 31);
+            const int st = i % kStages;
+            if (lane == 0) {
+                if (i >= kStages)
+                    ok = mbar_wait_sleep(&sc->raw_free[st], ((i / kStages) + 1) & 1, p.err,
+                                         kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff));
+                if (*((volatile int*)&sc->abort)) ok = false;
+                if (ok) {
+                    uint8_t* dst = smem + L::kOffRaw + st * L::kRawBytes;
+                    const bool two = first_page + 2 * i + 1 < last_page;
+                    mbar_arrive_expect_tx(&sc->raw_full[st], two ? L::kRawBytes : L::kPageBytes);
+                    const int y0 = (id0 * p.Hkv + g) * D, y1 = (id1 * p.Hkv + g) * D;
+                    if (once) {
+                        tma_load_2d_hint(dst, &pool, 0, y0, &sc->raw_full[st], policy);
+                        if (two) tma_load_2d_hint(dst + L::kPageBytes, &pool, 0, y1, &sc->raw_full[st], policy);
+                    } else {
+                        tma_load_2d(dst, &pool, 0, y0, &sc->raw_full[st]);
+                        if (two) tma_load_2d(dst + L::kPageBytes, &pool, 0, y1, &sc->raw_full[st]);
+                    }
+                    ++issued;
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        if (!ok && lane == 0) {
+            sc->abort = 1;
+            // let the copies still in flight land before the CTA exits
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(&sc->raw_full[i % kStages], (i / kStages) & 1, p.err,
+                          kRoleProducer | kBarRawFull | (unsigned)(i & 0xffff));
+        }
+    } else if (warp >= L::kConvWarp && warp < L::kConvWarp + 4) {
+        // ------------------------------ converters ----------------------------
+        const int t = tid - 32 * L::kConvWarp, q4 = t >> 5;
+        const uint32_t k_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kTmemK;
+        bool ok = true;
+        for (int i = 0; i < n && ok; ++i) {
+            const int u = i & 1;
+            const uint32_t par = (uint32_t)((i >> 1) & 1);
+            const bool paged = i < n_page;
+            const int st = i % kStages;
+            const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
+            const uint8_t* raw = smem + L::kOffRaw + st * L::kRawBytes;
+            const bool two = 2 * (t_begin + i) + 1 < keys.pages;
+            const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
+            if (paged)
+                ok = mbar_wait_sleep(&sc->raw_full[st], (i / kStages) & 1, p.err, code | kBarRawFull);
+            // S of tile i - 2 has read this K buffer
+            if (ok && i >= 2) ok = mbar_wait_sleep(&sc->s_full[u], par ^ 1, p.err, code | kBarS);
+            if (ok && !paged && i == n_page && i > 0) {
+                // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
+                ok = mbar_wait_sleep(&sc->s_full[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
+                if (ok) {
+                    for (int x = t; x < kN * (D / 8); x += 128)
+                        *q_address(x) = x < Rb * (D / 8) ? Qg[x] : make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            // K: one key to a thread, its row into the thread's lane of tensor memory
+            if (paged) {
+                const int r = t & 63;
+                const uint8_t* page = raw + (t >> 6) * L::kPageBytes;
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = 4 * h + j;                 // 16 elements
+                        const int row = D == 128 ? r : r >> 1;   // row of 128 bytes and piece in it
+                        const int cc = D == 128 ? c : 4 * (r & 1) + c;
+                        const uint4 v = *reinterpret_cast<const uint4*>(page + row * 128 + ((cc ^ (row & 7)) << 4));
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint2 y = e4m3x4_to_f16x4(x[e]);
+                            w[8 * j + 2 * e] = y.x;
+                            w[8 * j + 2 * e + 1] = y.y;
+                        }
+                    }
+                    tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
+                }
+            } else {
+                const bool live = k0 + t < tail_keys;
+                const uint4* row = reinterpret_cast<const uint4*>(Kh + (k0 + t) * D);
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = live ? row[8 * h + j] : make_uint4(0, 0, 0, 0);
+                        w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+                    }
+                    tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sc->k_full[u]);
+            // V: rows of 64 dimensions, 128-byte swizzle; the product of tile i - 2 has read it
+            if (i >= 2) ok = mbar_wait_sleep(&sc->pv_done[u], par ^ 1, p.err, code | kBarPv);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            uint8_t* vt = smem + L::kOffV + u * L::kVBytes;
+            if (paged) {
+                constexpr int kIters = kQ8Tile * D / 16 / 128;
+#pragma unroll 4
+                for (int it = 0; it < kIters; ++it) {
+                    // 8 lanes take one 128-byte row of codes
+                    const int row8 = it * 16 + (t >> 3);           // row of the tile's V codes
+                    const int half = row8 / (D / 2), row = row8 - half * (D / 2);
+                    const int cc = t & 7;
+                    const int key = half * 64 + (D == 128 ? row : 2 * row + (cc >> 2));
+                    const int c = D == 128 ? cc : cc & 3;          // 16 dimensions of that key
+                    uint4 a = make_uint4(0, 0, 0, 0), e = a;
+                    if (half == 0 || two) {                        // a page that is not there reads as zeros
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            raw + half * L::kPageBytes + kPageTokens * D + row * 128 + ((cc ^ (row & 7)) << 4));
+                        const uint2 x0 = e4m3x4_to_f16x4(v.x), x1 = e4m3x4_to_f16x4(v.y);
+                        const uint2 x2 = e4m3x4_to_f16x4(v.z), x3 = e4m3x4_to_f16x4(v.w);
+                        a = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                        e = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                    }
+                    uint8_t* dst = vt + (c >> 2) * L::kVBlock + key * 128;
+                    // lanes of the second block start with their second piece: no bank twice
+                    const int s = (c >> 2) & 1;
+                    const int p0 = 2 * (c & 3) + s, p1 = p0 ^ 1;
+                    *reinterpret_cast<uint4*>(dst + ((p0 ^ (key & 7)) << 4)) = s ? e : a;
+                    *reinterpret_cast<uint4*>(dst + ((p1 ^ (key & 7)) << 4)) = s ? a : e;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc->raw_free[st]);
+            } else {
+                // V elements that are not finite would turn hidden keys' zero probabilities
+                // into NaN: they are zero here and join the rows that see them at the end
+                for (int x = t; x < kQ8Tile * (D / 8); x += 128) {
+                    const int key = x / (D / 8), j = x - key * (D / 8);
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (k0 + key < tail_keys) {
+                        v = reinterpret_cast<const uint4*>(Vh + (k0 + key) * D)[j];
+                        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                        bool odd = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd = true; }
+                            if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd = true; }
+                        }
+                        if (odd) {
+                            const int at = atomicAdd(&sc->flagged, 1);
+                            if (at < kFlagged) sc->flagged_piece[at] = (k0 + key) * (D / 8) + j;
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(vt + (j >> 3) * L::kVBlock + key * 128 +
+                                              (((j & 7) ^ (key & 7)) << 4)) = v;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&sc->v_full[u]);
+        }
+        if (!ok) sc->abort = 1;
+    } else if (warp == L::kMmaWarp) {
+        // ------------------------------ issuer --------------------------------
+        if (lane == 0) {
+            constexpr uint32_t kS16 = idesc(false, false, false, kN), kSb = idesc(true, false, false, kN);
+            constexpr uint32_t kO16 = idesc(false, true, true, kN), kOb = idesc(true, true, true, kN);
+            const uint64_t qd = sdesc(smem_base + L::kOffQ, 16, 1024);
+            const uint64_t vd = sdesc(smem_base + L::kOffV, L::kVBlock, 1024);
+            const uint64_t pd = sdesc(smem_base + L::kOffP, kQ8Tile * 128, 1024);
+            int ns = 0, npv = 0;
+            bool ok = true;
+            uint64_t t_last = global_timer_ns();
+            while (npv < n) {
+                bool progressed = false;
+                if (ns < n && mbar_try_wait(&sc->k_full[ns & 1], (ns >> 1) & 1) &&
+                    (ns < 2 || mbar_try_wait(&sc->s_free[ns & 1], ((ns >> 1) - 1) & 1))) {
+                    tc_fence_after();
+                    const uint32_t dS = tmem + kTmemS + (uint32_t)((ns & 1) * 128);
+                    const uint32_t aK = tmem + kTmemK + (uint32_t)((ns & 1) * 64);
+                    const uint32_t id = ns < n_page ? kS16 : kSb;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_bf16_ta(dS, aK + (uint32_t)(8 * k),
+                                    qd + (uint64_t)(((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), id,
+                                    k > 0 ? 1u : 0u);
+                    mma_commit(&sc->s_full[ns & 1]);
+                    ++ns;
+                    progressed = true;
+                }
+                if (npv < ns && mbar_try_wait(&sc->p_full, npv & 1) &&
+                    mbar_try_wait(&sc->v_full[npv & 1], (npv >> 1) & 1)) {
+                    tc_fence_after();
+                    const uint64_t va = vd + (uint64_t)((npv & 1) * (L::kVBytes >> 4));
+                    const uint32_t id = npv < n_page ? kO16 : kOb;
+#pragma unroll
+                    for (int k = 0; k < kQ8Tile / 16; ++k)
+                        mma_bf16(tmem + kTmemO, va + (uint64_t)(k * (2048 >> 4)),
+                                 pd + (uint64_t)(k * (2048 >> 4)), id, (npv > 0 || k > 0) ? 1u : 0u);
+                    mma_commit(&sc->pv_done[npv & 1]);
+                    ++npv;
+                    progressed = true;
+                }
+                if (progressed) {
+                    t_last = global_timer_ns();
+                } else if (global_timer_ns() - t_last <= kWaitLimitNs) {
+                    if (npv < ns)
+                        (void)mbar_try_wait_sleep(&sc->p_full, npv & 1, 200u);
+                    else
+                        (void)mbar_try_wait_sleep(&sc->k_full[ns & 1], (ns >> 1) & 1, 200u);
+                } else {
+                    atomicOr(p.err, kErrWaitTimeout);
+                    atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarAny | (unsigned)(npv & 0xffff));
+                    ok = false;
+                    break;
+                }
+            }
+            if (!ok) sc->abort = 1;
+            mma_commit(&sc->drain);
+            mbar_wait_sleep(&sc->drain, 0, p.err, kRoleMma | kBarDrain);
+        }
+    } else if (warp < L::kSoftmaxWarps) {
+        // ------------------------------ softmax -------------------------------
+        const int gr = warp >> 2, q4 = warp & 3;
+        const int t = tid & 127;                        // this thread's key of every tile
+        const int c0 = gr * L::kCols;                   // first row (column of S^T) of the group
+        const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
+        float* neg_ref = sc->neg_ref + c0;
+        float* corr = sc->corr + c0;
+        const int half = t >> 6;
+
+        // largest scale of V among the split's pages: the unit of O^T
+        float unit = 0.f;
+#pragma unroll 1
+        for (int j = 2 * t_begin + t; j < min(keys.pages, 2 * (t_begin + n_page)); j += 128)
+            unit = fmaxf(unit, __ldg(p.scales + ((int64_t)q8_page(p, b, j) * p.Hkv + g) * 2 + 1));
+        unit = warp_max(unit);
+        if (lane == 0) sc->part[gr][q4][0] = unit;
+        group_sync(gr);
+        unit = fmaxf(fmaxf(sc->part[gr][0][0], sc->part[gr][1][0]), fmaxf(sc->part[gr][2][0], sc->part[gr][3][0]));
+        if (!(unit > 0.f)) unit = 1.f;
+        group_sync(gr);
+        const float inv_unit = 1.f / unit;
+
+        // (scale of K, scale of V) of this thread's key in page tile i, fetched a tile ahead
+        auto page_of = [&](int i) -> int {
+            const int j = 2 * (t_begin + i) + half;
+            return i < n_page && j < keys.pages ? q8_page(p, b, j) : -1;
+        };
+        auto scales_of = [&](int page) -> float2 {
+            return page >= 0 ? __ldg(reinterpret_cast<const float2*>(p.scales + ((int64_t)page * p.Hkv + g) * 2))
+                             : make_float2(0.f, 0.f);
+        };
+        float2 scale_now = scales_of(page_of(0));
+        int page_next = page_of(1);
+
+        float2 l2[L::kCols / 2];                        // this thread's part of the rows' sums
+#pragma unroll
+        for (int c = 0; c < L::kCols / 2; ++c) l2[c] = make_float2(0.f, 0.f);
+        bool fail = false;
+        for (int i = 0; i < n; ++i) {
+            const int u = i & 1;
+            const bool paged = i < n_page;
+            const unsigned code = kRoleSoftmax | (unsigned)(i & 0xffff);
+            const float2 scale_next = scales_of(page_next);
+            const int page_after = page_of(i + 2);
+            // which of the rows see this thread's key
+            uint64_t seen;
+            float a, vmul;                              // s = a * S^T; the factor of V in P
+            if (paged) {
+                seen = 2 * (t_begin + i) + half < keys.pages ? ~0ull : 0ull;
+                a = scale_now.x * (p.scale_log2 * q_unit);
+                vmul = scale_now.y * inv_unit;
+            } else {
+                const int64_t key = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile + t;
+                const int64_t node = key - keys.tail;
+                seen = key < tail_keys ? ~0ull : 0ull;
+                if (node >= 0 && key < tail_keys) {
+                    seen = 0;
+#pragma unroll 1
+                    for (int c = 0; c < L::kCols; ++c) {
+                        const int iq = (r0 + c0 + c) % p.n_q;
+                        const bool vis = p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0
+                                                : node <= iq;
+                        seen |= (vis ? 1ull : 0ull) << c;
+                    }
+                }
+                a = p.scale_log2;
+                vmul = inv_unit;
+            }
+            fail |= !mbar_wait_sleep(&sc->s_full[u], (uint32_t)((i >> 1) & 1), p.err, code | kBarS);
+            fail = __any_sync(0xffffffffu, fail);
+            tc_fence_after();
+            float x[L::kCols];
+            const uint32_t s_addr = lanes + kTmemS + (uint32_t)(u * 128 + c0);
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch) {
+                uint32_t r[16];
+                tmem_ld16(s_addr + 16 * ch, r);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) x[16 * ch + c] = __uint_as_float(r[c]);
+            }
+            tmem_wait_ld();
+            bool over = false;                          // some score passed its reference by too much
+#pragma unroll
+            for (int c = 0; c < L::kCols; c += 4) {
+                const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
+                const float2 aa = make_float2(a, a);
+                const float2 y0 = fma2(make_float2(x[c], x[c + 1]), aa, make_float2(nr.x, nr.y));
+                const float2 y1 = fma2(make_float2(x[c + 2], x[c + 3]), aa, make_float2(nr.z, nr.w));
+                x[c] = y0.x; x[c + 1] = y0.y; x[c + 2] = y1.x; x[c + 3] = y1.y;
+            }
+            if (seen != ~0ull) {
+                uint64_t bits = seen;
+#pragma unroll
+                for (int c = 0; c < L::kCols; ++c) {
+                    if (!(bits & 1ull)) x[c] = -INFINITY;
+                    bits >>= 1;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < L::kCols; ++c) over |= !(x[c] <= kMaxLog2P);   // NaN too
+            if (group_any(gr, over || fail)) {
+                if (group_any(gr, fail)) { fail = true; break; }   // the same answer in every warp
+                // ---- the references of the rows that need it move ----
+                uint64_t bits = seen;
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    uint32_t r[16];
+                    tmem_ld16(s_addr + 16 * ch, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float m = warp_max_redux((bits & 1ull) ? __uint_as_float(r[c]) * a : -INFINITY);
+                        if (lane == 0) sc->part[gr][q4][16 * ch + c] = m;
+                        bits >>= 1;
+                    }
+                }
+                group_sync(gr);
+                if (t < L::kCols) {
+                    const float m = fmaxf(fmaxf(sc->part[gr][0][t], sc->part[gr][1][t]),
+                                          fmaxf(sc->part[gr][2][t], sc->part[gr][3][t]));
+                    const float old = neg_ref[t];
+                    float f = 1.f;
+                    if (m > -INFINITY && m + old > kMaxLog2P) {
+                        neg_ref[t] = kRefShift - m;
+                        f = ex2(kRefShift - m - old);   // 0 for the first key of the row
+                    }
+                    corr[t] = f;
+                }
+                group_sync(gr);
+                if (i > 0) {
+                    fail |= !mbar_wait_sleep(&sc->pv_done[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarPv);
+                    fail = __any_sync(0xffffffffu, fail);
+                    tc_fence_after();
+#pragma unroll
+                    for (int ch = 0; ch < NCH; ++ch) {
+                        uint32_t o[16];
+                        tmem_ld16(lanes + kTmemO + (uint32_t)(c0 + 16 * ch), o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * corr[16 * ch + c]);
+                        tmem_st16(lanes + kTmemO + (uint32_t)(c0 + 16 * ch), o);
+                    }
+                    tmem_wait_st();
+                }
+                bits = seen;
+#pragma unroll
+                for (int ch = 0; ch < NCH; ++ch) {
+                    uint32_t r[16];
+                    tmem_ld16(s_addr + 16 * ch, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const int col = 16 * ch + c;
+                        if (c & 1) l2[col >> 1].y *= corr[col]; else l2[col >> 1].x *= corr[col];
+                        // a row whose visible scores are all -inf so far keeps p = 0
+                        const float nr = neg_ref[col] == INFINITY ? 0.f : neg_ref[col];
+                        x[col] = (bits & 1ull) ? fmaf(__uint_as_float(r[c]), a, nr) : -INFINITY;
+                        bits >>= 1;
+                    }
+                }
+            }
+            // S^T is in registers: the buffer is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sc->s_free[u]);
+            uint32_t pk[L::kCols / 2];
+            const float2 vm = make_float2(vmul, vmul);
+#pragma unroll
+            for (int c = 0; c < L::kCols / 2; ++c) {
+                const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
+                l2[c] = add2(l2[c], e);
+                const float2 w = mul2(e, vm);
+                pk[c] = paged ? f16x2(w.x, w.y) : bf16x2(w.x, w.y);
+            }
+            // P's buffer is free once the previous product has read it
+            if (i > 0) {
+                fail |= !mbar_wait_sleep(&sc->pv_done[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarPv);
+                fail = __any_sync(0xffffffffu, fail);
+            }
+            if (!fail) {
+                uint8_t* row = smem + L::kOffP + (c0 >> 6) * (kQ8Tile * 128) + t * 128;
+                const int j0 = (c0 & 63) >> 3;          // first 16-byte piece of the group's rows
+#pragma unroll
+                for (int j = 0; j < L::kCols / 8; ++j) {
+                    const int jj = j0 + j;
+                    *reinterpret_cast<uint4*>(row + (jj >> 3) * (kQ8Tile * 128) + (((jj & 7) ^ (t & 7)) << 4)) =
+                        make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(&sc->p_full);
+            }
+            scale_now = scale_next;
+            page_next = page_after;
+        }
+        if (tid == 0) griddep_launch_dependents();
+        // O^T of the last product
+        if (!fail)
+            fail = !mbar_wait_sleep(&sc->pv_done[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1), p.err,
+                                    kRoleSoftmax | kBarPv | 0xffffu);
+        fail = group_any(gr, fail);
+        // the rows' sums over this warp's keys
+#pragma unroll
+        for (int c = 0; c < L::kCols; ++c) {
+            const float s = warp_sum(c & 1 ? l2[c >> 1].y : l2[c >> 1].x);
+            if (lane == 0) sc->part[gr][q4][c] = s;
+        }
+        group_sync(gr);
+        if (fail) {
+            sc->abort = 1;
+        } else {
+            tc_fence_after();
+            if (t < L::kCols && c0 + t < Rb) {
+                const float s = (sc->part[gr][0][t] + sc->part[gr][1][t]) + (sc->part[gr][2][t] + sc->part[gr][3][t]);
+                const float nr = neg_ref[t];
+                *reinterpret_cast<float2*>(p.part_ml + (slot + c0 + t) * 2) =
+                    nr == INFINITY && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
+            }
+            const int dim = 32 * q4 + lane;
+#pragma unroll
+            for (int ch = 0; ch < NCH; ++ch) {
+                uint32_t o[16];
+                tmem_ld16(lanes + kTmemO + (uint32_t)(c0 + 16 * ch), o);
+                tmem_wait_ld();
+                if (dim >= D) continue;                 // warp-uniform: D is 64 or 128
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const int r = c0 + 16 * ch + c;
+                    if (r < Rb) p.part_acc[(slot + r) * D + dim] = __uint_as_float(o[c]) * unit;
+                }
+            }
+            const int flagged = sc->flagged;
+            if (flagged > 0 && dim < D) {
+                // V elements left out of the products reach the rows that see them
+                const int64_t first = (int64_t)max(t_begin - keys.page_tiles, 0) * kQ8Tile;
+                const int64_t last = min((int64_t)(t_end - keys.page_tiles) * kQ8Tile, tail_keys);
+                const bool listed = flagged <= kFlagged;
+                const int64_t m = listed ? flagged : last - first;
+#pragma unroll 1
+                for (int64_t f = 0; f < m; ++f) {
+                    int64_t key = first + f;
+                    if (listed) {
+                        key = sc->flagged_piece[f] / (D / 8);
+                        if (sc->flagged_piece[f] % (D / 8) != dim / 8) continue;
+                    }
+                    const float v = __bfloat162float(Vh[key * D + dim]);
+                    if (fabsf(v) < INFINITY) continue;
+                    const int64_t node = key - keys.tail;
+#pragma unroll 1
+                    for (int r = c0; r < min(c0 + L::kCols, Rb); ++r) {
+                        const int iq = (r0 + r) % p.n_q;
+                        if (node < 0 || (p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0
+                                                : node <= iq))
+                            p.part_acc[(slot + r) * D + dim] += v;
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == L::kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sc->tmem_base),
+                     "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+// The pool as rows of 128 bytes; a page and head (K, then V) is d of them.
+bool make_pool_map(CUtensorMap* m, const AttnQ8Params& p) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {128, (cuuint64_t)p.n_pages * p.Hkv * p.d};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, (cuuint32_t)p.d};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.pages), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NCH, int GROUPS>
+cudaError_t launch_shape(const CUtensorMap& pool, const AttnQ8Params& p, int n_rb, int rows, cudaStream_t st) {
+    using L = Plan<D, NCH, GROUPS>;
+    auto kern = attn_q8_tc_kernel<D, NCH, GROUPS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.S * n_rb, p.Hkv, 1);
+    cfg.blockDim = dim3(L::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = L::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, pool, p, n_rb, rows);
+}
+
+template <int D>
+cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStream_t st) {
+    const int n_rb = q8_row_blocks(p.R);
+    const int rows = (p.R + n_rb - 1) / n_rb;
+    switch (rows <= 64 ? (rows + 15) / 16 : 4 + (rows + 31) / 32) {
+        case 1: return launch_shape<D, 1, 1>(pool, p, n_rb, rows, st);
+        case 2: return launch_shape<D, 2, 1>(pool, p, n_rb, rows, st);
+        case 3: return launch_shape<D, 3, 1>(pool, p, n_rb, rows, st);
+        case 4: return launch_shape<D, 4, 1>(pool, p, n_rb, rows, st);
+        case 7: return launch_shape<D, 3, 2>(pool, p, n_rb, rows, st);
+        default: return launch_shape<D, 4, 2>(pool, p, n_rb, rows, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_q8_tc(const AttnQ8Params& p, cudaStream_t st) {
+    CUtensorMap pool;
+    if (!make_pool_map(&pool, p)) return cudaErrorInvalidValue;
+    return p.d == 128 ? launch_rows<128>(pool, p, st) : launch_rows<64>(pool, p, st);
+}
+
+}  // namespace rapid

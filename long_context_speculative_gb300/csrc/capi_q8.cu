@@ -34,10 +34,19 @@ bool attn_q8_args_ok(int B, int Hq, int Hkv, int d, int n_q, int64_t cap, int ma
 
 Q8Plan plan_attn_q8(int B, int Hq, int Hkv, int d, int n_q, int dtype) {
     const int64_t R = (int64_t)(Hq / Hkv) * n_q;
-    const int64_t rbs = (R + kQ8SimtRows - 1) / kQ8SimtRows;
-    // enough slots for four CTAs on every SM; a slot for every sequence
-    int64_t S = 4 * (int64_t)sm_count() / (Hkv * rbs);
-    if (S > 512) S = 512;
+    const int64_t sms = sm_count();
+    int64_t S;
+    if (dtype == RAPID_DTYPE_BF16) {
+        // tensor cores: one CTA on every SM, and as many whole waves of them as give every
+        // sequence a slot
+        const int64_t per_slot = (int64_t)Hkv * q8_row_blocks((int)R);
+        const int64_t waves = (B * per_slot + sms - 1) / sms;
+        S = waves * sms / per_slot;
+    } else {
+        // CUDA cores: four CTAs on every SM
+        S = 4 * sms / (Hkv * ((R + kQ8SimtRows - 1) / kQ8SimtRows));
+        if (S > 512) S = 512;
+    }
     if (S < B) S = B;
     Q8Plan pl;
     pl.S = (int)S;
@@ -168,9 +177,10 @@ rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void*
     const void* rows16[] = {Q, K_tail, V_tail, pages, O, workspace};
     for (const void* x : rows16)
         if (!aligned(x, 16)) return RAPID_EINVAL;
-    const void* words[] = {scales, page_table, sealed_len, tail_len, LSE};
+    const void* words[] = {page_table, sealed_len, tail_len, LSE};
     for (const void* x : words)
         if (!aligned(x, 4)) return RAPID_EINVAL;
+    if (!aligned(scales, 8)) return RAPID_EINVAL;
     if (!std::isfinite(softmax_scale)) return RAPID_EINVAL;
     const Q8Plan pl = plan_attn_q8(B, Hq, Hkv, d, n_q, dtype);
     if (workspace_bytes < pl.bytes) return RAPID_ENOMEM;
@@ -194,7 +204,8 @@ rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void*
     ws += align_up((size_t)B * Hkv * sizeof(int));
     p.part_count = reinterpret_cast<int*>(ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_attn_q8_simt(p, dtype, st) != cudaSuccess) return RAPID_ECUDA;
+    const cudaError_t e = dtype == RAPID_DTYPE_BF16 ? launch_attn_q8_tc(p, st) : launch_attn_q8_simt(p, st);
+    if (e != cudaSuccess) return RAPID_ECUDA;
     return launch_attn_q8_merge(p, dtype, st) == cudaSuccess ? RAPID_OK : RAPID_ECUDA;
 }
 

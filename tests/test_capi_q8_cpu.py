@@ -84,7 +84,7 @@ def test_verify_attn_q8(lib):
              [(0, None), (1, None), (2, None), (3, None), (4, None), (5, None), (15, None), (16, None),
               (19, None), (20, None), (21, None), (6, 2), (7, 0), (10, 32), (11, 0), (11, 65), (12, 10),
               (13, 0), (13, 1 << 22), (14, 0), (0, ODD), (1, ODD), (2, ODD), (3, ODD), (19, ODD),
-              (21, ODD), (4, BYTE), (5, BYTE), (15, BYTE), (16, BYTE), (20, BYTE),
+              (21, ODD), (4, ctypes.c_void_p(260)), (5, BYTE), (15, BYTE), (16, BYTE), (20, BYTE),
               (18, f(float("inf"))), (18, f(float("nan")))])
     _refused(lib.rapid_verify_attn_q8, good, [(22, need - 1)], status=-3)
 
