@@ -54,6 +54,8 @@ constexpr uint32_t kTmemO = 128;
 constexpr uint32_t kTmemS = 256;
 
 constexpr float kRefShift = 7.f;       // P is 2^7 at the reference ...
+constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no key: any finite
+                                       // score passes it
 constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
                                        // (fp16 ends at 65504)
 
@@ -62,10 +64,19 @@ struct Plan {
     static constexpr int kCols = 16 * NCH;                  // group rows of one softmax group
     static constexpr int kN = kCols * GROUPS;               // N of the products
     static constexpr int kSoftmaxWarps = 4 * GROUPS;
-    static constexpr int kConvWarp = kSoftmaxWarps;         // first of four
-    static constexpr int kProducerWarp = kConvWarp + 4;
-    static constexpr int kMmaWarp = kConvWarp + 7;
-    static constexpr int kThreads = 32 * (kSoftmaxWarps + 8);
+    // one group of four converter warps for K and one for V, or one for both beside two
+    // softmax groups
+    static constexpr int kConvGroups = GROUPS == 1 ? 2 : 1;
+    static constexpr int kConvWarp = kSoftmaxWarps;
+    static constexpr int kProducerWarp = kConvWarp + 4 * kConvGroups;
+    static constexpr int kMmaWarp = kProducerWarp + 3;
+    static constexpr int kThreads = 32 * (kProducerWarp + 4);
+    // 512 threads start with 128 registers each; the four warpgroups share them out anew
+    static constexpr int kSoftmaxRegs = GROUPS == 1 ? 200 : 176;
+    static constexpr int kConvRegs = 104;
+    static constexpr int kLastRegs = 56;
+    static_assert(kThreads == 512 && GROUPS * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= 512,
+                  "registers of a block");
     static constexpr int kPageBytes = 2 * kPageTokens * D;  // K and V of one page and head
     static constexpr int kRawBytes = 2 * kPageBytes;        // one stage: two pages
     static constexpr int kVBlock = kQ8Tile * 128;           // 64 dimensions of a V tile
@@ -103,7 +114,7 @@ struct Scalars {
     uint32_t tmem_base;
     int abort;
     Q8Split split;
-    alignas(16) float neg_ref[128];   // -(reference) of every row: P = 2^(s + neg_ref); +inf before the first key
+    alignas(16) float neg_ref[128];   // -(reference) of every row: P = 2^(s + neg_ref)
     alignas(16) float corr[128];
     float part[2][4][64];    // per softmax group and warp: a number for each of its rows
     float wmax[16];
@@ -125,6 +136,17 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+template <int N> __device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
@@ -196,7 +218,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sc->raw_full[i], 1);
-            mbar_init(&sc->raw_free[i], 4);
+            mbar_init(&sc->raw_free[i], 4 * L::kConvGroups);
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(&sc->k_full[u], 128);
@@ -211,7 +233,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         sc->flagged = 0;
         fence_mbar_init();
     }
-    if (tid < 128) sc->neg_ref[tid] = INFINITY;
+    if (tid < 128) sc->neg_ref[tid] = kNoKey;
     if (warp == L::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sc->tmem_base)),
@@ -305,55 +327,138 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 
     if (n <= 0) {
         // nothing to do
-    } else if (warp == L::kProducerWarp) {
-        // ------------------------------ producer ------------------------------
-        // lane i holds the id of page 32 k + i of the split
-        const uint64_t policy = l2_policy_evict_first();
-        const bool once = n_rb == 1;                    // else the other row blocks read it again
-        const int first_page = 2 * t_begin, last_page = keys.pages;
-        int id = 0, issued = 0;
-        bool ok = true;
-        for (int i = 0; i < n_page && ok; ++i) {
-            if ((i & 15) == 0) {
-                const int j = first_page + 2 * i + lane;
-                id = j < last_page ? q8_page(p, b, j) : 0;
-            }
-            const int id0 = __shfl_sync(0xffffffffu, id, (2 * i) & 31);
-            const int id1 = __shfl_sync(0xffffffffu, id, (2 * i + 1) & 31);
-            const int st = i % kStages;
-            if (lane == 0) {
-                if (i >= kStages)
-                    ok = mbar_wait_sleep(&sc->raw_free[st], ((i / kStages) + 1) & 1, p.err,
-                                         kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff));
-                if (*((volatile int*)&sc->abort)) ok = false;
-                if (ok) {
-                    uint8_t* dst = smem + L::kOffRaw + st * L::kRawBytes;
-                    const bool two = first_page + 2 * i + 1 < last_page;
-                    mbar_arrive_expect_tx(&sc->raw_full[st], two ? L::kRawBytes : L::kPageBytes);
-                    const int y0 = (id0 * p.Hkv + g) * D, y1 = (id1 * p.Hkv + g) * D;
-                    if (once) {
-                        tma_load_2d_hint(dst, &pool, 0, y0, &sc->raw_full[st], policy);
-                        if (two) tma_load_2d_hint(dst + L::kPageBytes, &pool, 0, y1, &sc->raw_full[st], policy);
-                    } else {
-                        tma_load_2d(dst, &pool, 0, y0, &sc->raw_full[st]);
-                        if (two) tma_load_2d(dst + L::kPageBytes, &pool, 0, y1, &sc->raw_full[st]);
-                    }
-                    ++issued;
+    } else if (warp >= L::kProducerWarp) {
+        regs_down<L::kLastRegs>();
+        if (warp == L::kProducerWarp) {
+            // ------------------------------ producer ------------------------------
+            // lane i holds the id of page 32 k + i of the split
+            const uint64_t policy = l2_policy_evict_first();
+            const bool once = n_rb == 1;                    // else the other row blocks read it again
+            const int first_page = 2 * t_begin, last_page = keys.pages;
+            int id = 0, issued = 0;
+            bool ok = true;
+            for (int i = 0; i < n_page && ok; ++i) {
+                if ((i & 15) == 0) {
+                    const int j = first_page + 2 * i + lane;
+                    id = j < last_page ? q8_page(p, b, j) : 0;
                 }
+                const int id0 = __shfl_sync(0xffffffffu, id, (2 * i) & 31);
+                const int id1 = __shfl_sync(0xffffffffu, id, (2 * i + 1) & 31);
+                const int st = i % kStages;
+                if (lane == 0) {
+                    if (i >= kStages)
+                        ok = mbar_wait_sleep(&sc->raw_free[st], ((i / kStages) + 1) & 1, p.err,
+                                             kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff));
+                    if (*((volatile int*)&sc->abort)) ok = false;
+                    if (ok) {
+                        uint8_t* dst = smem + L::kOffRaw + st * L::kRawBytes;
+                        const bool two = first_page + 2 * i + 1 < last_page;
+                        mbar_arrive_expect_tx(&sc->raw_full[st], two ? L::kRawBytes : L::kPageBytes);
+                        const int y0 = (id0 * p.Hkv + g) * D, y1 = (id1 * p.Hkv + g) * D;
+                        if (once) {
+                            tma_load_2d_hint(dst, &pool, 0, y0, &sc->raw_full[st], policy);
+                            if (two) tma_load_2d_hint(dst + L::kPageBytes, &pool, 0, y1, &sc->raw_full[st], policy);
+                        } else {
+                            tma_load_2d(dst, &pool, 0, y0, &sc->raw_full[st]);
+                            if (two) tma_load_2d(dst + L::kPageBytes, &pool, 0, y1, &sc->raw_full[st]);
+                        }
+                        ++issued;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!ok && lane == 0) {
+                sc->abort = 1;
+                // let the copies still in flight land before the CTA exits
+                for (int i = max(0, issued - kStages); i < issued; ++i)
+                    mbar_wait(&sc->raw_full[i % kStages], (i / kStages) & 1, p.err,
+                              kRoleProducer | kBarRawFull | (unsigned)(i & 0xffff));
+            }
+        } else if (warp == L::kMmaWarp) {
+            // ------------------------------ issuer --------------------------------
+            if (lane == 0) {
+                constexpr uint32_t kS16 = idesc(false, false, false, kN), kSb = idesc(true, false, false, kN);
+                constexpr uint32_t kO16 = idesc(false, true, true, kN), kOb = idesc(true, true, true, kN);
+                const uint64_t qd = sdesc(smem_base + L::kOffQ, 16, 1024);
+                const uint64_t vd = sdesc(smem_base + L::kOffV, L::kVBlock, 1024);
+                const uint64_t pd = sdesc(smem_base + L::kOffP, kQ8Tile * 128, 1024);
+                int ns = 0, npv = 0;
+                bool ok = true;
+                uint64_t t_last = global_timer_ns();
+                while (npv < n) {
+                    bool progressed = false;
+                    if (ns < n && mbar_try_wait(&sc->k_full[ns & 1], (ns >> 1) & 1) &&
+                        (ns < 2 || mbar_try_wait(&sc->s_free[ns & 1], ((ns >> 1) - 1) & 1))) {
+                        tc_fence_after();
+                        const uint32_t dS = tmem + kTmemS + (uint32_t)((ns & 1) * 128);
+                        const uint32_t aK = tmem + kTmemK + (uint32_t)((ns & 1) * 64);
+                        const uint32_t id = ns < n_page ? kS16 : kSb;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_bf16_ta(dS, aK + (uint32_t)(8 * k),
+                                        qd + (uint64_t)(((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), id,
+                                        k > 0 ? 1u : 0u);
+                        mma_commit(&sc->s_full[ns & 1]);
+                        ++ns;
+                        progressed = true;
+                    }
+                    if (npv < ns && mbar_try_wait(&sc->p_full, npv & 1) &&
+                        mbar_try_wait(&sc->v_full[npv & 1], (npv >> 1) & 1)) {
+                        tc_fence_after();
+                        const uint64_t va = vd + (uint64_t)((npv & 1) * (L::kVBytes >> 4));
+                        const uint32_t id = npv < n_page ? kO16 : kOb;
+#pragma unroll
+                        for (int k = 0; k < kQ8Tile / 16; ++k)
+                            mma_bf16(tmem + kTmemO, va + (uint64_t)(k * (2048 >> 4)),
+                                     pd + (uint64_t)(k * (2048 >> 4)), id, (npv > 0 || k > 0) ? 1u : 0u);
+                        mma_commit(&sc->pv_done[npv & 1]);
+                        ++npv;
+                        progressed = true;
+                    }
+                    if (progressed) {
+                        t_last = global_timer_ns();
+                    } else if (global_timer_ns() - t_last <= kWaitLimitNs) {
+                        if (npv < ns)
+                            (void)mbar_try_wait_sleep(&sc->p_full, npv & 1, 200u);
+                        else
+                            (void)mbar_try_wait_sleep(&sc->k_full[ns & 1], (ns >> 1) & 1, 200u);
+                    } else {
+                        atomicOr(p.err, kErrWaitTimeout);
+                        atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarAny | (unsigned)(npv & 0xffff));
+                        ok = false;
+                        break;
+                    }
+                }
+                if (!ok) sc->abort = 1;
+                mma_commit(&sc->drain);
+                mbar_wait_sleep(&sc->drain, 0, p.err, kRoleMma | kBarDrain);
+            }
         }
-        if (!ok && lane == 0) {
-            sc->abort = 1;
-            // let the copies still in flight land before the CTA exits
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait(&sc->raw_full[i % kStages], (i / kStages) & 1, p.err,
-                          kRoleProducer | kBarRawFull | (unsigned)(i & 0xffff));
-        }
-    } else if (warp >= L::kConvWarp && warp < L::kConvWarp + 4) {
+    } else if (warp >= L::kConvWarp) {
         // ------------------------------ converters ----------------------------
-        const int t = tid - 32 * L::kConvWarp, q4 = t >> 5;
+        regs_down<L::kConvRegs>();
+        const int t = tid & 127, q4 = t >> 5;
+        const bool do_k = L::kConvGroups == 1 || warp < L::kConvWarp + 4;
+        const bool do_v = L::kConvGroups == 1 || !do_k;
         const uint32_t k_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kTmemK;
+        // K codes: thread t's key is row t % 64 of page t / 64, 128 / (128 / d) bytes of a
+        // 128-byte line
+        const int k_line = D == 128 ? t & 63 : (t & 63) >> 1;
+        const uint8_t* k_src = smem + L::kOffRaw + (t >> 6) * L::kPageBytes + k_line * 128;
+        const int k_piece = D == 128 ? 0 : 4 * (t & 1);
+        // V codes: 8 threads to a 128-byte line, so thread t takes piece t % 8 of the lines
+        // t / 8, t / 8 + 16, ... of a page: the same 16 dimensions of keys 16 (or 32) apart
+        const int v_piece = t & 7, v_line = t >> 3;
+        const uint8_t* v_src = smem + L::kOffRaw + kPageTokens * D + v_line * 128 +
+                               ((v_piece ^ (v_line & 7)) << 4);
+        const int v_dim = D == 128 ? v_piece : v_piece & 3;             // 16 dimensions
+        const int v_key = D == 128 ? v_line : 2 * v_line + (v_piece >> 2);
+        // the two 16-byte pieces it writes; threads of the second block of dimensions start
+        // with their second piece, so that 8 threads never meet in a bank
+        const int v_odd = (v_dim >> 2) & 1;
+        const uint32_t v_dst = L::kOffV + (v_dim >> 2) * L::kVBlock + v_key * 128;
+        const uint32_t v_p0 = ((2 * (v_dim & 3) + v_odd) ^ (v_key & 7)) << 4;
+        const uint32_t v_p1 = ((2 * (v_dim & 3) + (v_odd ^ 1)) ^ (v_key & 7)) << 4;
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
             const int u = i & 1;
@@ -361,186 +466,128 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const bool paged = i < n_page;
             const int st = i % kStages;
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
-            const uint8_t* raw = smem + L::kOffRaw + st * L::kRawBytes;
-            const bool two = 2 * (t_begin + i) + 1 < keys.pages;
             const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
             if (paged)
                 ok = mbar_wait_sleep(&sc->raw_full[st], (i / kStages) & 1, p.err, code | kBarRawFull);
-            // S of tile i - 2 has read this K buffer
-            if (ok && i >= 2) ok = mbar_wait_sleep(&sc->s_full[u], par ^ 1, p.err, code | kBarS);
-            if (ok && !paged && i == n_page && i > 0) {
-                // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
-                ok = mbar_wait_sleep(&sc->s_full[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
-                if (ok) {
-                    for (int x = t; x < kN * (D / 8); x += 128)
-                        *q_address(x) = x < Rb * (D / 8) ? Qg[x] : make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
+            if (do_k) {
+                // S of tile i - 2 has read this K buffer
+                if (ok && i >= 2) ok = mbar_wait_sleep(&sc->s_full[u], par ^ 1, p.err, code | kBarS);
+                if (ok && !paged && i == n_page && i > 0) {
+                    // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
+                    ok = mbar_wait_sleep(&sc->s_full[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
+                    if (ok) {
+                        for (int x = t; x < kN * (D / 8); x += 128)
+                            *q_address(x) = x < Rb * (D / 8) ? Qg[x] : make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
                 }
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (paged) {
+                    const uint8_t* line = k_src + st * L::kRawBytes;
+                    uint4 v[D / 16];
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j)
+                        v[j] = *reinterpret_cast<const uint4*>(line + (((k_piece + j) ^ (k_line & 7)) << 4));
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t x[4] = {v[4 * h + j].x, v[4 * h + j].y, v[4 * h + j].z, v[4 * h + j].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint2 y = e4m3x4_to_f16x4(x[e]);
+                                w[8 * j + 2 * e] = y.x;
+                                w[8 * j + 2 * e + 1] = y.y;
+                            }
+                        }
+                        tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
+                    }
+                } else {
+                    const bool live = k0 + t < tail_keys;
+                    const uint4* row = reinterpret_cast<const uint4*>(Kh + (k0 + t) * D);
+#pragma unroll
+                    for (int h = 0; h < D / 64; ++h) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint4 v = live ? row[8 * h + j] : make_uint4(0, 0, 0, 0);
+                            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+                        }
+                        tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sc->k_full[u]);
             }
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            // K: one key to a thread, its row into the thread's lane of tensor memory
-            if (paged) {
-                const int r = t & 63;
-                const uint8_t* page = raw + (t >> 6) * L::kPageBytes;
+            if (do_v) {
+                // V: lines of 64 dimensions, 128-byte swizzle; the product of tile i - 2 has read it
+                if (ok && i >= 2) ok = mbar_wait_sleep(&sc->pv_done[u], par ^ 1, p.err, code | kBarPv);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (paged) {
+                    constexpr int kSteps = D / 32;                      // 16 lines of a page at a time
+                    const bool two = 2 * (t_begin + i) + 1 < keys.pages;
+                    const uint8_t* src = v_src + st * L::kRawBytes;
+                    uint8_t* dst = smem + v_dst + u * L::kVBytes;
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    uint32_t w[32];
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 v[kSteps];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c = 4 * h + j;                 // 16 elements
-                        const int row = D == 128 ? r : r >> 1;   // row of 128 bytes and piece in it
-                        const int cc = D == 128 ? c : 4 * (r & 1) + c;
-                        const uint4 v = *reinterpret_cast<const uint4*>(page + row * 128 + ((cc ^ (row & 7)) << 4));
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        for (int j = 0; j < kSteps; ++j)                // a page that is not there reads as zeros
+                            v[j] = half == 0 || two
+                                       ? *reinterpret_cast<const uint4*>(src + half * L::kPageBytes + j * 2048)
+                                       : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint2 y = e4m3x4_to_f16x4(x[e]);
-                            w[8 * j + 2 * e] = y.x;
-                            w[8 * j + 2 * e + 1] = y.y;
+                        for (int j = 0; j < kSteps; ++j) {
+                            const uint2 x0 = e4m3x4_to_f16x4(v[j].x), x1 = e4m3x4_to_f16x4(v[j].y);
+                            const uint2 x2 = e4m3x4_to_f16x4(v[j].z), x3 = e4m3x4_to_f16x4(v[j].w);
+                            const uint4 a = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                            const uint4 e = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                            uint8_t* to = dst + (half * 64 + j * (D == 128 ? 16 : 32)) * 128;
+                            *reinterpret_cast<uint4*>(to + v_p0) = v_odd ? e : a;
+                            *reinterpret_cast<uint4*>(to + v_p1) = v_odd ? a : e;
                         }
                     }
-                    tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
-                }
-            } else {
-                const bool live = k0 + t < tail_keys;
-                const uint4* row = reinterpret_cast<const uint4*>(Kh + (k0 + t) * D);
+                } else {
+                    // V elements that are not finite would turn hidden keys' zero probabilities
+                    // into NaN: they are zero here and join the rows that see them at the end
+                    uint8_t* vt = smem + L::kOffV + u * L::kVBytes;
+                    for (int x = t; x < kQ8Tile * (D / 8); x += 128) {
+                        const int key = x / (D / 8), j = x - key * (D / 8);
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (k0 + key < tail_keys) {
+                            v = reinterpret_cast<const uint4*>(Vh + (k0 + key) * D)[j];
+                            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                            bool odd = false;
 #pragma unroll
-                for (int h = 0; h < D / 64; ++h) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint4 v = live ? row[8 * h + j] : make_uint4(0, 0, 0, 0);
-                        w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
+                            for (int e = 0; e < 4; ++e) {
+                                if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd = true; }
+                                if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd = true; }
+                            }
+                            if (odd) {
+                                const int at = atomicAdd(&sc->flagged, 1);
+                                if (at < kFlagged) sc->flagged_piece[at] = (k0 + key) * (D / 8) + j;
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(vt + (j >> 3) * L::kVBlock + key * 128 +
+                                                  (((j & 7) ^ (key & 7)) << 4)) = v;
                     }
-                    tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
                 }
+                fence_proxy_async_smem();
+                mbar_arrive(&sc->v_full[u]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&sc->k_full[u]);
-            // V: rows of 64 dimensions, 128-byte swizzle; the product of tile i - 2 has read it
-            if (i >= 2) ok = mbar_wait_sleep(&sc->pv_done[u], par ^ 1, p.err, code | kBarPv);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            uint8_t* vt = smem + L::kOffV + u * L::kVBytes;
-            if (paged) {
-                constexpr int kIters = kQ8Tile * D / 16 / 128;
-#pragma unroll 4
-                for (int it = 0; it < kIters; ++it) {
-                    // 8 lanes take one 128-byte row of codes
-                    const int row8 = it * 16 + (t >> 3);           // row of the tile's V codes
-                    const int half = row8 / (D / 2), row = row8 - half * (D / 2);
-                    const int cc = t & 7;
-                    const int key = half * 64 + (D == 128 ? row : 2 * row + (cc >> 2));
-                    const int c = D == 128 ? cc : cc & 3;          // 16 dimensions of that key
-                    uint4 a = make_uint4(0, 0, 0, 0), e = a;
-                    if (half == 0 || two) {                        // a page that is not there reads as zeros
-                        const uint4 v = *reinterpret_cast<const uint4*>(
-                            raw + half * L::kPageBytes + kPageTokens * D + row * 128 + ((cc ^ (row & 7)) << 4));
-                        const uint2 x0 = e4m3x4_to_f16x4(v.x), x1 = e4m3x4_to_f16x4(v.y);
-                        const uint2 x2 = e4m3x4_to_f16x4(v.z), x3 = e4m3x4_to_f16x4(v.w);
-                        a = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                        e = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                    }
-                    uint8_t* dst = vt + (c >> 2) * L::kVBlock + key * 128;
-                    // lanes of the second block start with their second piece: no bank twice
-                    const int s = (c >> 2) & 1;
-                    const int p0 = 2 * (c & 3) + s, p1 = p0 ^ 1;
-                    *reinterpret_cast<uint4*>(dst + ((p0 ^ (key & 7)) << 4)) = s ? e : a;
-                    *reinterpret_cast<uint4*>(dst + ((p1 ^ (key & 7)) << 4)) = s ? a : e;
-                }
+            if (paged) {                                                // this group has read the raw stage
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc->raw_free[st]);
-            } else {
-                // V elements that are not finite would turn hidden keys' zero probabilities
-                // into NaN: they are zero here and join the rows that see them at the end
-                for (int x = t; x < kQ8Tile * (D / 8); x += 128) {
-                    const int key = x / (D / 8), j = x - key * (D / 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (k0 + key < tail_keys) {
-                        v = reinterpret_cast<const uint4*>(Vh + (k0 + key) * D)[j];
-                        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-                        bool odd = false;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd = true; }
-                            if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd = true; }
-                        }
-                        if (odd) {
-                            const int at = atomicAdd(&sc->flagged, 1);
-                            if (at < kFlagged) sc->flagged_piece[at] = (k0 + key) * (D / 8) + j;
-                        }
-                    }
-                    *reinterpret_cast<uint4*>(vt + (j >> 3) * L::kVBlock + key * 128 +
-                                              (((j & 7) ^ (key & 7)) << 4)) = v;
-                }
             }
-            fence_proxy_async_smem();
-            mbar_arrive(&sc->v_full[u]);
         }
         if (!ok) sc->abort = 1;
-    } else if (warp == L::kMmaWarp) {
-        // ------------------------------ issuer --------------------------------
-        if (lane == 0) {
-            constexpr uint32_t kS16 = idesc(false, false, false, kN), kSb = idesc(true, false, false, kN);
-            constexpr uint32_t kO16 = idesc(false, true, true, kN), kOb = idesc(true, true, true, kN);
-            const uint64_t qd = sdesc(smem_base + L::kOffQ, 16, 1024);
-            const uint64_t vd = sdesc(smem_base + L::kOffV, L::kVBlock, 1024);
-            const uint64_t pd = sdesc(smem_base + L::kOffP, kQ8Tile * 128, 1024);
-            int ns = 0, npv = 0;
-            bool ok = true;
-            uint64_t t_last = global_timer_ns();
-            while (npv < n) {
-                bool progressed = false;
-                if (ns < n && mbar_try_wait(&sc->k_full[ns & 1], (ns >> 1) & 1) &&
-                    (ns < 2 || mbar_try_wait(&sc->s_free[ns & 1], ((ns >> 1) - 1) & 1))) {
-                    tc_fence_after();
-                    const uint32_t dS = tmem + kTmemS + (uint32_t)((ns & 1) * 128);
-                    const uint32_t aK = tmem + kTmemK + (uint32_t)((ns & 1) * 64);
-                    const uint32_t id = ns < n_page ? kS16 : kSb;
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_bf16_ta(dS, aK + (uint32_t)(8 * k),
-                                    qd + (uint64_t)(((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), id,
-                                    k > 0 ? 1u : 0u);
-                    mma_commit(&sc->s_full[ns & 1]);
-                    ++ns;
-                    progressed = true;
-                }
-                if (npv < ns && mbar_try_wait(&sc->p_full, npv & 1) &&
-                    mbar_try_wait(&sc->v_full[npv & 1], (npv >> 1) & 1)) {
-                    tc_fence_after();
-                    const uint64_t va = vd + (uint64_t)((npv & 1) * (L::kVBytes >> 4));
-                    const uint32_t id = npv < n_page ? kO16 : kOb;
-#pragma unroll
-                    for (int k = 0; k < kQ8Tile / 16; ++k)
-                        mma_bf16(tmem + kTmemO, va + (uint64_t)(k * (2048 >> 4)),
-                                 pd + (uint64_t)(k * (2048 >> 4)), id, (npv > 0 || k > 0) ? 1u : 0u);
-                    mma_commit(&sc->pv_done[npv & 1]);
-                    ++npv;
-                    progressed = true;
-                }
-                if (progressed) {
-                    t_last = global_timer_ns();
-                } else if (global_timer_ns() - t_last <= kWaitLimitNs) {
-                    if (npv < ns)
-                        (void)mbar_try_wait_sleep(&sc->p_full, npv & 1, 200u);
-                    else
-                        (void)mbar_try_wait_sleep(&sc->k_full[ns & 1], (ns >> 1) & 1, 200u);
-                } else {
-                    atomicOr(p.err, kErrWaitTimeout);
-                    atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarAny | (unsigned)(npv & 0xffff));
-                    ok = false;
-                    break;
-                }
-            }
-            if (!ok) sc->abort = 1;
-            mma_commit(&sc->drain);
-            mbar_wait_sleep(&sc->drain, 0, p.err, kRoleMma | kBarDrain);
-        }
-    } else if (warp < L::kSoftmaxWarps) {
+    } else {
+        regs_up<L::kSoftmaxRegs>();
         // ------------------------------ softmax -------------------------------
         const int gr = warp >> 2, q4 = warp & 3;
         const int t = tid & 127;                        // this thread's key of every tile
@@ -564,13 +611,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const float inv_unit = 1.f / unit;
 
         // (scale of K, scale of V) of this thread's key in page tile i, fetched a tile ahead
-        auto page_of = [&](int i) -> int {
-            const int j = 2 * (t_begin + i) + half;
-            return i < n_page && j < keys.pages ? q8_page(p, b, j) : -1;
-        };
+        // (its page id, two tiles ahead: neither load is waited for; the producer flags an id
+        // that is outside the pool)
+        const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin + half;
+        const int my_pages = min(keys.pages - 2 * t_begin - half, 2 * n_page);   // ids[0, my_pages) exist
+        auto page_of = [&](int i) -> int { return 2 * i < my_pages ? __ldg(ids + 2 * i) : 0; };
         auto scales_of = [&](int page) -> float2 {
-            return page >= 0 ? __ldg(reinterpret_cast<const float2*>(p.scales + ((int64_t)page * p.Hkv + g) * 2))
-                             : make_float2(0.f, 0.f);
+            const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
+            return __ldg(reinterpret_cast<const float2*>(p.scales + ((int64_t)id * p.Hkv + g) * 2));
         };
         float2 scale_now = scales_of(page_of(0));
         int page_next = page_of(1);
@@ -591,7 +639,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (paged) {
                 seen = 2 * (t_begin + i) + half < keys.pages ? ~0ull : 0ull;
                 a = scale_now.x * (p.scale_log2 * q_unit);
-                vmul = scale_now.y * inv_unit;
+                vmul = seen ? scale_now.y * inv_unit : 0.f;   // no page: no scale to trust
             } else {
                 const int64_t key = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile + t;
                 const int64_t node = key - keys.tail;
@@ -622,7 +670,6 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 for (int c = 0; c < 16; ++c) x[16 * ch + c] = __uint_as_float(r[c]);
             }
             tmem_wait_ld();
-            bool over = false;                          // some score passed its reference by too much
 #pragma unroll
             for (int c = 0; c < L::kCols; c += 4) {
                 const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
@@ -639,8 +686,13 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     bits >>= 1;
                 }
             }
+            float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < L::kCols; ++c) over |= !(x[c] <= kMaxLog2P);   // NaN too
+            for (int c = 0; c < L::kCols; c += 4) {
+                top0 = fmax3(top0, x[c], x[c + 1]);
+                top1 = fmax3(top1, x[c + 2], x[c + 3]);
+            }
+            const bool over = fmaxf(top0, top1) > kMaxLog2P;
             if (group_any(gr, over || fail)) {
                 if (group_any(gr, fail)) { fail = true; break; }   // the same answer in every warp
                 // ---- the references of the rows that need it move ----
@@ -663,7 +715,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                                           fmaxf(sc->part[gr][2][t], sc->part[gr][3][t]));
                     const float old = neg_ref[t];
                     float f = 1.f;
-                    if (m > -INFINITY && m + old > kMaxLog2P) {
+                    if (m + old > kMaxLog2P) {
                         neg_ref[t] = kRefShift - m;
                         f = ex2(kRefShift - m - old);   // 0 for the first key of the row
                     }
@@ -696,9 +748,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     for (int c = 0; c < 16; ++c) {
                         const int col = 16 * ch + c;
                         if (c & 1) l2[col >> 1].y *= corr[col]; else l2[col >> 1].x *= corr[col];
-                        // a row whose visible scores are all -inf so far keeps p = 0
-                        const float nr = neg_ref[col] == INFINITY ? 0.f : neg_ref[col];
-                        x[col] = (bits & 1ull) ? fmaf(__uint_as_float(r[c]), a, nr) : -INFINITY;
+                        x[col] = (bits & 1ull) ? fmaf(__uint_as_float(r[c]), a, neg_ref[col]) : -INFINITY;
                         bits >>= 1;
                     }
                 }
@@ -758,7 +808,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const float s = (sc->part[gr][0][t] + sc->part[gr][1][t]) + (sc->part[gr][2][t] + sc->part[gr][3][t]);
                 const float nr = neg_ref[t];
                 *reinterpret_cast<float2*>(p.part_ml + (slot + c0 + t) * 2) =
-                    nr == INFINITY && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
+                    nr == kNoKey && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
             }
             const int dim = 32 * q4 + lane;
 #pragma unroll

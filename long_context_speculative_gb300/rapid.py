@@ -156,6 +156,45 @@ def _need(t, dtype, shape, name):
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
+def _refuse(t, dev, dtype, shape, name):
+    """The reason why _arg turned a tensor away."""
+    if not isinstance(t, torch.Tensor):
+        raise RapidError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise RapidError(f"{name}: librapid works on CUDA tensors only (no CPU path)")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise RapidError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise RapidError(f"{name}: librapid needs contiguous tensors")
+    raise RapidError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _arg(t, dev, dtype, shape, name):
+    """The address of a contiguous tensor of this type and shape on device `dev` (one test
+    of each, a few hundred nanoseconds: a short kernel waits for the host)."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, dev, dtype, shape, name)
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    """The current device, which `t` has to be on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise RapidError(f"{name}: librapid works on CUDA tensors only (no CPU path)")
+    cur = torch.cuda.current_device()
+    if dev != cur:
+        raise RapidError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
+    return dev
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _check_accept_tensors(z_target, q_draft, draft_tokens, parent, n_accepted, next_token, path,
                           diag, n_nodes=None):
     """The sizes the kernels will index by: z and q float32 [B, n_q, V]; tokens,
@@ -412,19 +451,16 @@ def rapid_retrieval_select(scores, context_tokens, selected, n_selected, tokens_
     _check(st, "rapid_retrieval_select")
 
 
-def _head_rows(t, B, n, H, d, dtype, name):
-    """Batch and token stride of projection rows [B, n, H, d] whose heads lie one after the
-    other (a view of a fused projection will do)."""
-    if t.dim() != 4 or tuple(t.shape) != (B, n, H, d) or t.dtype != dtype:
-        raise RapidError(f"{name} must be a {dtype} tensor of shape {(B, n, H, d)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise RapidError("librapid works on CUDA tensors only (no CPU path)")
+def _head_rows(t, dev, B, n, H, d, dtype, name):
+    """Address, batch and token stride of projection rows [B, n, H, d] whose heads lie one
+    after the other (a view of a fused projection will do)."""
+    if t.shape != (B, n, H, d) or t.dtype != dtype or t.get_device() != dev:
+        _refuse(t, dev, dtype, (B, n, H, d), name)
     sb, sn, sh, se = t.stride()
     if se != 1 or (H > 1 and sh != d):
         raise RapidError(f"{name}: the heads of a token must be contiguous")
     # the stride of a dimension of size 1 means nothing and may be anything
-    return (sb if B > 1 else 0), (sn if n > 1 else 0)
+    return t.data_ptr(), (sb if B > 1 else 0), (sn if n > 1 else 0)
 
 
 def rapid_qkv_append(q, k, v, q_weight, k_weight, eps, inv_freq, flags, prefix_len, pos_offset,
@@ -432,35 +468,27 @@ def rapid_qkv_append(q, k, v, q_weight, k_weight, eps, inv_freq, flags, prefix_l
     """Norm and rotate the rows q [B, n, Hq, d] and k [B, n, Hkv, d], write queries to
     Q [B, Hq, n, d] and keys and values to cache rows prefix_len + i; None for what is
     optional.  q, k and v may be views of one fused projection."""
-    _need_cuda(q_weight, k_weight, inv_freq, prefix_len, pos_offset, row_offset, n_rows, Q,
-               Kcache, Vcache)
+    dev = _device_of(Q, "Q")
     if Q.dim() != 4 or Kcache.dim() != 4:
         raise RapidError("Q and the caches must have four dimensions")
     B, Hq, n, d = Q.shape
     Hkv, cap = Kcache.shape[1], Kcache.shape[2]
     dt = Q.dtype
-    strides = (ctypes.c_int64 * 6)(*_head_rows(q, B, n, Hq, d, dt, "q"),
-                                   *_head_rows(k, B, n, Hkv, d, dt, "k"),
-                                   *_head_rows(v, B, n, Hkv, d, dt, "v"))
-    _need(Kcache, dt, (B, Hkv, cap, d), "Kcache")
-    _need(Vcache, dt, (B, Hkv, cap, d), "Vcache")
-    _need(q_weight, dt, (d,), "q_weight")
-    _need(k_weight, dt, (d,), "k_weight")
-    rot = 0
-    if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _need(inv_freq, torch.float32, (rot // 2,), "inv_freq")
-    _need(prefix_len, torch.int32, (B,), "prefix_len")
-    _need(pos_offset, torch.int32, (B,), "pos_offset")
-    _need(row_offset, torch.int32, (B, n), "row_offset")
-    _need(n_rows, torch.int32, (B,), "n_rows")
-    _need_same_device(q, k, v, q_weight, k_weight, inv_freq, prefix_len, pos_offset, row_offset,
-                      n_rows, Q, Kcache, Vcache)
-    st = lib().rapid_qkv_append(_ptr(q), _ptr(k), _ptr(v), strides, _dtype_code(Q), B, n, Hq, Hkv,
-                                d, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(inv_freq), rot,
-                                int(flags), _ptr(prefix_len), _ptr(pos_offset), _ptr(row_offset),
-                                _ptr(n_rows), _ptr(Q), _ptr(Kcache), _ptr(Vcache), cap,
-                                _stream(stream))
+    i32 = torch.int32
+    q_ptr, qb, qt = _head_rows(q, dev, B, n, Hq, d, dt, "q")
+    k_ptr, kb, kt = _head_rows(k, dev, B, n, Hkv, d, dt, "k")
+    v_ptr, vb, vt = _head_rows(v, dev, B, n, Hkv, d, dt, "v")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    st = lib().rapid_qkv_append(
+        q_ptr, k_ptr, v_ptr, (ctypes.c_int64 * 6)(qb, qt, kb, kt, vb, vt), _dtype_code(Q), B, n,
+        Hq, Hkv, d, _arg(q_weight, dev, dt, (d,), "q_weight"),
+        _arg(k_weight, dev, dt, (d,), "k_weight"), eps,
+        _arg(inv_freq, dev, torch.float32, (rot // 2,), "inv_freq"), rot, flags,
+        _arg(prefix_len, dev, i32, (B,), "prefix_len"),
+        _arg(pos_offset, dev, i32, (B,), "pos_offset"),
+        _arg(row_offset, dev, i32, (B, n), "row_offset"), _arg(n_rows, dev, i32, (B,), "n_rows"),
+        _arg(Q, dev, dt, (B, Hq, n, d), "Q"), _arg(Kcache, dev, dt, (B, Hkv, cap, d), "Kcache"),
+        _arg(Vcache, dev, dt, (B, Hkv, cap, d), "Vcache"), cap, _raw_stream(stream, dev))
     _check(st, "rapid_qkv_append")
 
 
@@ -497,30 +525,28 @@ class Q8LayerTable:
         self._keep = lists                                # the tensors outlive the table
 
     def _lengths(self, page_table, sealed_len, tail_len):
-        _need_cuda(page_table, sealed_len, tail_len)
+        dev = _device_of(self._keep[0][0], "tail cache")
         if page_table.dim() != 2:
             raise RapidError("page_table must be [B, max_pages]")
-        _need(page_table, torch.int32, (self.B, page_table.shape[1]), "page_table")
-        _need(sealed_len, torch.int32, (self.B,), "sealed_len")
-        _need(tail_len, torch.int32, (self.B,), "tail_len")
-        _need_same_device(page_table, sealed_len, tail_len, self._keep[0][0])
+        max_pages, i32 = page_table.shape[1], torch.int32
+        return (dev, max_pages, _arg(page_table, dev, i32, (self.B, max_pages), "page_table"),
+                _arg(sealed_len, dev, i32, (self.B,), "sealed_len"),
+                _arg(tail_len, dev, i32, (self.B,), "tail_len"))
 
     def seal(self, page_table, sealed_len, tail_len, keep_rows=0, stream=None):
         """Seal (tail_len - keep_rows) // 64 blocks of every sequence on every layer and move
         the tail rows that stay to the front; the lengths are left to seal_advance."""
-        self._lengths(page_table, sealed_len, tail_len)
+        dev, max_pages, table, sealed, tail = self._lengths(page_table, sealed_len, tail_len)
         st = lib().rapid_kv_seal(*self._ptrs, self.layers, self.dtype, self.B, self.Hkv, self.d,
-                                 self.cap, int(keep_rows), self.n_pages, _ptr(page_table),
-                                 page_table.shape[1], _ptr(sealed_len), _ptr(tail_len),
-                                 _stream(stream))
+                                 self.cap, keep_rows, self.n_pages, table, max_pages, sealed, tail,
+                                 _raw_stream(stream, dev))
         _check(st, "rapid_kv_seal")
 
     def seal_advance(self, page_table, sealed_len, tail_len, keep_rows=0, stream=None):
         """sealed_len += 64 n_b, tail_len -= 64 n_b (device, in place)."""
-        self._lengths(page_table, sealed_len, tail_len)
-        st = lib().rapid_kv_seal_advance(_ptr(sealed_len), _ptr(tail_len), _ptr(page_table),
-                                         self.B, page_table.shape[1], self.n_pages, self.cap,
-                                         int(keep_rows), _stream(stream))
+        dev, max_pages, table, sealed, tail = self._lengths(page_table, sealed_len, tail_len)
+        st = lib().rapid_kv_seal_advance(sealed, tail, table, self.B, max_pages, self.n_pages,
+                                         self.cap, keep_rows, _raw_stream(stream, dev))
         _check(st, "rapid_kv_seal_advance")
 
 
@@ -542,34 +568,27 @@ def rapid_verify_attn_q8_workspace_size(B, Hq, Hkv, d, n_q, tail_capacity, max_p
 def rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
                          spec_mask, softmax_scale, O, LSE, workspace, stream=None):
     """Verify attention over sealed 8-bit pages, tail rows and the speculative rows."""
-    _need_cuda(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len, spec_mask, O,
-               LSE, workspace)
+    dev = _device_of(Q, "Q")
     if Q.dim() != 4 or K_tail.dim() != 4 or pages.dim() != 5 or page_table.dim() != 2:
         raise RapidError("Q and the tails have 4 dimensions, pages 5, page_table 2")
-    B, Hq, n_q, d = Q.shape
-    Hkv, cap = K_tail.shape[1], K_tail.shape[2]
+    B, Hq, n_q, d = shape = Q.shape
+    _, Hkv, cap, _ = K_tail.shape
     n_pages, max_pages = pages.shape[0], page_table.shape[1]
-    _need(K_tail, Q.dtype, (B, Hkv, cap, d), "K_tail")
-    _need(V_tail, Q.dtype, (B, Hkv, cap, d), "V_tail")
-    _need(pages, torch.float8_e4m3fn, (n_pages, Hkv, 2, RAPID_Q8_PAGE_TOKENS, d), "pages")
-    _need(scales, torch.float32, (n_pages, Hkv, 2), "scales")
-    _need(page_table, torch.int32, (B, max_pages), "page_table")
-    _need(sealed_len, torch.int32, (B,), "sealed_len")
-    _need(tail_len, torch.int32, (B,), "tail_len")
-    if spec_mask is not None and spec_mask.dtype != torch.bool:
-        _need(spec_mask, torch.uint8, (B, n_q, n_q), "spec_mask")
-    elif spec_mask is not None:
-        _need(spec_mask, torch.bool, (B, n_q, n_q), "spec_mask")
-    _need(O, Q.dtype, (B, Hq, n_q, d), "O")
-    _need(LSE, torch.float32, (B, Hq, n_q), "LSE")
-    _need_same_device(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
-                      spec_mask, O, LSE, workspace)
-    st = lib().rapid_verify_attn_q8(_ptr(Q), _ptr(K_tail), _ptr(V_tail), _ptr(pages), _ptr(scales),
-                                    _ptr(page_table), _dtype_code(Q), B, Hq, Hkv, d, n_q, cap,
-                                    n_pages, max_pages, _ptr(sealed_len), _ptr(tail_len),
-                                    _ptr(spec_mask), float(softmax_scale), _ptr(O), _ptr(LSE),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                    _stream(stream))
+    dt, i32 = Q.dtype, torch.int32
+    tail_shape = (B, Hkv, cap, d)
+    mask_dt = torch.bool if spec_mask is not None and spec_mask.dtype == torch.bool else torch.uint8
+    st = lib().rapid_verify_attn_q8(
+        _arg(Q, dev, dt, shape, "Q"), _arg(K_tail, dev, dt, tail_shape, "K_tail"),
+        _arg(V_tail, dev, dt, tail_shape, "V_tail"),
+        _arg(pages, dev, torch.float8_e4m3fn, (n_pages, Hkv, 2, RAPID_Q8_PAGE_TOKENS, d), "pages"),
+        _arg(scales, dev, torch.float32, (n_pages, Hkv, 2), "scales"),
+        _arg(page_table, dev, i32, (B, max_pages), "page_table"), _dtype_code(Q), B, Hq, Hkv, d,
+        n_q, cap, n_pages, max_pages, _arg(sealed_len, dev, i32, (B,), "sealed_len"),
+        _arg(tail_len, dev, i32, (B,), "tail_len"),
+        _arg(spec_mask, dev, mask_dt, (B, n_q, n_q), "spec_mask"), softmax_scale,
+        _arg(O, dev, dt, shape, "O"), _arg(LSE, dev, torch.float32, (B, Hq, n_q), "LSE"),
+        _arg(workspace, dev, torch.uint8, (workspace.numel(),), "workspace"), workspace.numel(),
+        _raw_stream(stream, dev))
     _check(st, "rapid_verify_attn_q8")
 
 
@@ -683,13 +702,13 @@ def qkv_append(q, k, v, K, V, prefix_len, inv_freq=None, q_weight=None, k_weight
 
     Where n_rows cuts a sequence short, its rows of `out` behind the count are left as they are
     (unset memory in an `out` made here)."""
-    with _on(stream):
-        if out is None:
-            B, n, Hq, d = q.shape
+    if out is None:
+        B, n, Hq, d = q.shape
+        with _on(stream):
             out = torch.empty((B, Hq, n, d), dtype=q.dtype, device=q.device)
-        rapid_qkv_append(q, k, v, q_weight, k_weight, eps, inv_freq,
-                         RAPID_ROPE_INTERLEAVED if interleaved else 0, prefix_len, pos_offset,
-                         row_offset, n_rows, out, K, V, stream)
+    rapid_qkv_append(q, k, v, q_weight, k_weight, eps, inv_freq,
+                     RAPID_ROPE_INTERLEAVED if interleaved else 0, prefix_len, pos_offset,
+                     row_offset, n_rows, out, K, V, stream)
     return out
 
 
@@ -697,19 +716,20 @@ def verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tai
                    spec_mask=None, softmax_scale=0.0, out=None, lse=None, workspace=None,
                    stream=None):
     """O [B,Hq,n_q,d] (dtype of Q) and LSE [B,Hq,n_q] float32 over an 8-bit history."""
-    B, Hq, n_q, d = Q.shape
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(Q)
-        if lse is None:
-            lse = torch.empty((B, Hq, n_q), dtype=torch.float32, device=Q.device)
-        if workspace is None:
-            nbytes = rapid_verify_attn_q8_workspace_size(B, Hq, K_tail.shape[1], d, n_q,
-                                                         K_tail.shape[2], page_table.shape[1],
-                                                         _dtype_code(Q))
-            if nbytes == 0:
-                raise RapidError("unsupported verify_attn_q8 shape")
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
-        rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
-                             spec_mask, softmax_scale, out, lse, workspace, stream)
+    if out is None or lse is None or workspace is None:
+        B, Hq, n_q, d = Q.shape
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(Q)
+            if lse is None:
+                lse = Q.new_empty((B, Hq, n_q), dtype=torch.float32)
+            if workspace is None:
+                nbytes = rapid_verify_attn_q8_workspace_size(
+                    B, Hq, K_tail.shape[1], d, n_q, K_tail.shape[2], page_table.shape[1],
+                    _dtype_code(Q))
+                if nbytes == 0:
+                    raise RapidError("unsupported verify_attn_q8 shape")
+                workspace = Q.new_empty((nbytes,), dtype=torch.uint8)
+    rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
+                         spec_mask, softmax_scale, out, lse, workspace, stream)
     return out, lse
