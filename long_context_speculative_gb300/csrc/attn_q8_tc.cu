@@ -4,7 +4,7 @@
 // Both products are formed transposed, with the keys (and then the head dimension) as the
 // M = 128 operand and the query rows of the KV-head group as N:
 //   S^T[key, row] = K Q^T            A = K (tensor memory), B = Q (shared memory)
-//   O^T[dim, row] += V^T P^T         A = V (shared memory, MN-major), B = P (shared memory)
+//   O^T[dim, row] += V^T P^T         A = V^T (tensor memory), B = P (shared memory, MN-major)
 // A verify step has few rows (4 to 128 for a KV head), so rows in M would leave most of every
 // tensor instruction idle (44 of 128 rows for an 11-node chain); in N they cost what they
 // are, in steps of 16.  It also gives every softmax thread one key: the key's page scales are
@@ -20,11 +20,17 @@
 // multiplies O at the end.  Tail rows and speculative rows are bf16 as they are: those tiles,
 // the last of a sequence, run the same way in bf16.
 //
+// Both operands that come from the cache are converted in registers on their way from the raw
+// stages to tensor memory, K by rows and V through transposing 8-bit ldmatrix loads, so a
+// code byte crosses shared memory twice (copy in, read out).  With V as a shared-memory
+// operand in fp16 it would be written and read there once more at twice the width, and
+// shared-memory bandwidth (128 B a clock), not HBM, bounded that version.
+//
 // CTA = (sequence and split, block of at most 128 group rows; KV head).  Tiles are 128 keys:
 // two pages, or 128 tail rows.  Warps:
-//   softmax     4 (up to 64 rows) or 8 (two groups with half the rows each); warp w owns the
-//               keys, later the output dimensions, of tensor-memory lane quadrant w % 4
-//   converters  4: codes -> fp16, K into tensor memory, V into swizzled shared memory
+//   softmax     8, two groups with half the rows each; warp w owns the keys, later the output
+//               dimensions, of tensor-memory lane quadrant w % 4
+//   converters  4 for K and 4 for V (4 for both with more than 96 rows)
 //   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
 //               into a ring of raw stages by TMA
 //   issuer      1: the MMAs, in the order in which their inputs become ready
@@ -45,13 +51,8 @@ namespace rapid {
 namespace {
 
 constexpr int kMaxRawStages = 6;
-constexpr int kFlagged = 64;           // pieces of V remembered for an element that is not finite
-
-// Tensor-memory columns (512): K buffer u at 64 u, O^T at 128, S^T buffer u at 256 + 128 u.
+constexpr int kFlagged = 64;           // elements of V remembered for not being finite
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemK = 0;
-constexpr uint32_t kTmemO = 128;
-constexpr uint32_t kTmemS = 256;
 
 constexpr float kRefShift = 7.f;       // P is 2^7 at the reference ...
 constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no key: any finite
@@ -59,55 +60,56 @@ constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no
 constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
                                        // (fp16 ends at 65504)
 
-template <int D, int NCH, int GROUPS>
+// COLS: group rows of one of the two softmax groups (a multiple of 8, at most 64).
+template <int D, int COLS>
 struct Plan {
-    static constexpr int kCols = 16 * NCH;                  // group rows of one softmax group
-    static constexpr int kN = kCols * GROUPS;               // N of the products
-    static constexpr int kSoftmaxWarps = 4 * GROUPS;
-    // one group of four converter warps for K and one for V, or one for both beside two
-    // softmax groups
-    static constexpr int kConvGroups = GROUPS == 1 ? 2 : 1;
-    static constexpr int kConvWarp = kSoftmaxWarps;
+    static constexpr int kN = 2 * COLS;                     // N of the products
+    static constexpr int kConvGroups = kN <= 96 ? 2 : 1;
+    static constexpr int kConvWarp = 8;
     static constexpr int kProducerWarp = kConvWarp + 4 * kConvGroups;
     static constexpr int kMmaWarp = kProducerWarp + 3;
     static constexpr int kThreads = 32 * (kProducerWarp + 4);
-    // 512 threads start with 128 registers each; the four warpgroups share them out anew
-    static constexpr int kSoftmaxRegs = GROUPS == 1 ? 200 : 176;
-    static constexpr int kConvRegs = 104;
-    static constexpr int kLastRegs = 56;
-    static_assert(kThreads == 512 && GROUPS * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= 512,
+    // A block starts with kLaunchRegs registers a thread; its warpgroups share them out anew.
+    static constexpr int kLaunchRegs = kThreads == 640 ? 96 : 128;
+    static constexpr int kSoftmaxRegs = kThreads == 512 ? 176 : COLS <= 32 ? 112 : 136;
+    static constexpr int kConvRegs = kThreads == 512 ? 104 : COLS <= 32 ? 96 : 80;
+    static constexpr int kLastRegs = COLS == 48 ? 48 : 56;
+    static_assert(2 * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
                   "registers of a block");
+    // Tensor-memory columns: K and V tiles (64 each), O^T, two S^T buffers.
+    static constexpr int kKBufs = kN <= 64 ? 2 : 1;
+    static constexpr int kVBufs = kN <= 96 ? 2 : 1;
+    static constexpr uint32_t kNCols = kN < 32 ? 32 : kN;
+    static constexpr uint32_t kTmemK = 0;
+    static constexpr uint32_t kTmemV = 64 * kKBufs;
+    static constexpr uint32_t kTmemO = kTmemV + 64 * kVBufs;
+    static constexpr uint32_t kTmemS = kTmemO + kNCols;
+    static_assert(kTmemS + 2 * kNCols <= kTmemCols, "tensor memory");
     static constexpr int kPageBytes = 2 * kPageTokens * D;  // K and V of one page and head
     static constexpr int kRawBytes = 2 * kPageBytes;        // one stage: two pages
-    static constexpr int kVBlock = kQ8Tile * 128;           // 64 dimensions of a V tile
-    static constexpr int kVBytes = (D / 64) * kVBlock;
-    static constexpr int kPBlocks = (kN + 63) / 64;
-    static constexpr int kPBytes = kPBlocks * kQ8Tile * 128;
+    static constexpr int kPBytes = (kN + 63) / 64 * (kQ8Tile * 128);
     static constexpr int kQBlock = kN * 128;                // 64 dimensions of Q
-    static constexpr int kQBytes = (D / 64) * kQBlock;
-    // V comes first: at D = 64 the M = 128 operand's second half reads on into what follows
-    static constexpr int kOffV = 0;
-    static constexpr int kOffP = kOffV + 2 * kVBytes;
+    static constexpr int kOffP = 0;
     static constexpr int kOffQ = kOffP + kPBytes;
-    static constexpr int kOffRaw = (kOffQ + kQBytes + 1023) / 1024 * 1024;
+    static constexpr int kOffRaw = kOffQ + (D / 64) * kQBlock;
     static constexpr int kScalarBytes = 4096;
     static constexpr int kFit = (232448 - 1024 - kScalarBytes - kOffRaw) / kRawBytes;
     static constexpr int kStages = kFit < kMaxRawStages ? kFit : kMaxRawStages;
     static constexpr int kOffScalar = kOffRaw + kStages * kRawBytes;
     static constexpr int kSmemBytes = kOffScalar + kScalarBytes + 1024;
     static_assert(D == 64 || D == 128, "head dimension 64 or 128");
-    static_assert(kN <= 128 && kCols <= 64, "at most 128 rows, 64 in a group");
-    static_assert(kStages >= 2, "too few stages");
-    static_assert(kOffRaw + kStages * kRawBytes >= kOffV + 2 * kVBytes + kVBlock, "V operand in bounds");
+    static_assert(COLS % 8 == 0 && COLS <= 64, "at most 64 rows in a group, in steps of 8");
+    static_assert(kOffRaw % 1024 == 0 && kStages >= 3, "raw stages");
 };
 
 struct Scalars {
     uint64_t raw_full[kMaxRawStages];
     uint64_t raw_free[kMaxRawStages];
+    uint64_t q_full;         // Q in shared memory
     uint64_t k_full[2];      // K in tensor memory
     uint64_t s_full[2];      // S^T done (and K's buffer free)
     uint64_t s_free[2];      // S^T loaded by the softmax warps
-    uint64_t v_full[2];
+    uint64_t v_full[2];      // V^T in tensor memory
     uint64_t pv_done[2];     // O^T += V^T P^T of a tile done (V's buffer and P free)
     uint64_t p_full;
     uint64_t drain;
@@ -117,9 +119,9 @@ struct Scalars {
     alignas(16) float neg_ref[128];   // -(reference) of every row: P = 2^(s + neg_ref)
     alignas(16) float corr[128];
     float part[2][4][64];    // per softmax group and warp: a number for each of its rows
-    float wmax[16];
-    int flagged;             // pieces of tail rows whose V is not finite in some element
-    int64_t flagged_piece[kFlagged];   // row * (d / 8) + piece of 8 elements
+    float wmax[8];
+    int flagged;             // elements of the tail rows' V that are not finite
+    int64_t flagged_at[kFlagged];      // row * d + dimension
 };
 static_assert(sizeof(Scalars) <= 4096, "scalar block too small");
 static_assert(offsetof(Scalars, neg_ref) % 16 == 0 && offsetof(Scalars, corr) % 16 == 0,
@@ -129,7 +131,7 @@ enum : unsigned int {
     kRoleProducer = 0x11u << 24, kRoleMma = 0x12u << 24, kRoleSoftmax = 0x13u << 24,
     kRoleConvert = 0x14u << 24,
     kBarRawFull = 1u << 16, kBarRawFree = 2u << 16, kBarS = 3u << 16, kBarPv = 4u << 16,
-    kBarAny = 5u << 16, kBarDrain = 6u << 16
+    kBarAny = 5u << 16, kBarDrain = 6u << 16, kBarQ = 7u << 16
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -192,19 +194,42 @@ __device__ __forceinline__ void group_sync(int gr) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + gr) : "memory");
 }
 
-// Instruction descriptor: fp32 sums, A and B fp16 or bf16, A / B MN-major, M = 128.
-constexpr uint32_t idesc(bool bf16, bool a_mn, bool b_mn, int n) {
-    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
-           (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+// Instruction descriptor: fp32 sums, A and B fp16 or bf16, A K-major, B K- or MN-major, M = 128.
+constexpr uint32_t idesc(bool bf16, bool b_mn, int n) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-template <int D, int NCH, int GROUPS>
-__global__ void __launch_bounds__(Plan<D, NCH, GROUPS>::kThreads, 1)
+// Two transposed 16 x 16 byte matrices; lanes 0..15 and 16..31 give the addresses of their rows.
+__device__ __forceinline__ void ldmatrix_t_b8_x2(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Sums of v[0..7] over the warp; lane l returns the one of column l / 4 (halving the columns
+// a lane carries at each of the first three exchanges: 9 shuffles instead of 40).
+__device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
+    float a[4], c[2];
+    const bool h4 = lane & 16, h2 = lane & 8, h1 = lane & 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        a[e] = (h4 ? v[4 + e] : v[e]) + __shfl_xor_sync(0xffffffffu, h4 ? v[e] : v[4 + e], 16);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        c[e] = (h2 ? a[2 + e] : a[e]) + __shfl_xor_sync(0xffffffffu, h2 ? a[e] : a[2 + e], 8);
+    float s = (h1 ? c[1] : c[0]) + __shfl_xor_sync(0xffffffffu, h1 ? c[0] : c[1], 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    return s + __shfl_xor_sync(0xffffffffu, s, 1);
+}
+
+template <int D, int COLS>
+__global__ void __launch_bounds__(Plan<D, COLS>::kThreads, 1)
 attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p, const int n_rb,
                   const int rows_per_block) {
-    using L = Plan<D, NCH, GROUPS>;
-    constexpr int kStages = L::kStages;
-    constexpr int kN = L::kN;
+    using L = Plan<D, COLS>;
+    constexpr int kStages = L::kStages, kN = L::kN, KB = L::kKBufs, VB = L::kVBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Scalars* sc = reinterpret_cast<Scalars*>(smem + L::kOffScalar);
@@ -220,14 +245,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             mbar_init(&sc->raw_full[i], 1);
             mbar_init(&sc->raw_free[i], 4 * L::kConvGroups);
         }
+        mbar_init(&sc->q_full, 256);
         for (int u = 0; u < 2; ++u) {
             mbar_init(&sc->k_full[u], 128);
             mbar_init(&sc->s_full[u], 1);
-            mbar_init(&sc->s_free[u], L::kSoftmaxWarps);
+            mbar_init(&sc->s_free[u], 8);
             mbar_init(&sc->v_full[u], 128);
             mbar_init(&sc->pv_done[u], 1);
         }
-        mbar_init(&sc->p_full, 128 * GROUPS);
+        mbar_init(&sc->p_full, 256);
         mbar_init(&sc->drain, 1);
         sc->abort = 0;
         sc->flagged = 0;
@@ -266,74 +292,27 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     const int n = t_end - t_begin;
     const int n_page = min(max(keys.page_tiles - t_begin, 0), n);   // the first n_page tiles are pages
     const int64_t tail_keys = keys.tail + p.n_q;
-    const __nv_bfloat16* Kh = static_cast<const __nv_bfloat16*>(p.K) + bg * p.cap * D;
-    const __nv_bfloat16* Vh = static_cast<const __nv_bfloat16*>(p.V) + bg * p.cap * D;
     const uint4* Qg = reinterpret_cast<const uint4*>(
         static_cast<const __nv_bfloat16*>(p.Q) +
         (((int64_t)b * p.Hq + (int64_t)g * p.G) * p.n_q + r0) * D);
-    const int64_t slot = ((int64_t)g * p.S + slot_idx) * p.R + r0;   // this CTA's partial rows
-
-    // Q into shared memory: K-major, 128-byte swizzle, blocks of 64 dimensions; piece i is 8
+    const uint32_t tmem = sc->tmem_base;
+    // Q in shared memory: K-major, 128-byte swizzle, blocks of 64 dimensions; piece i is 8
     // elements of row i / (D / 8).  Rows past the CTA's are zero.
     auto q_address = [&](int i) -> uint4* {
         const int r = i / (D / 8), j = i - r * (D / 8);
         return reinterpret_cast<uint4*>(smem + L::kOffQ + (j >> 3) * L::kQBlock + r * 128 +
                                         (((j & 7) ^ (r & 7)) << 4));
     };
-    float q_unit = 1.f;                                 // Q = unit * (its fp16 form)
-    if (n_page > 0) {
-        float top = 0.f;
-        for (int i = tid; i < Rb * (D / 8); i += L::kThreads) {
-            const uint4 v = Qg[i];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float x = fabsf(__uint_as_float(w[u] << 16)), y = fabsf(__uint_as_float(w[u] & 0xffff0000u));
-                if (x < INFINITY) top = fmaxf(top, x);
-                if (y < INFINITY) top = fmaxf(top, y);
-            }
-        }
-        top = warp_max(top);
-        if (lane == 0) sc->wmax[warp] = top;
-        __syncthreads();
-        top = 0.f;
-        for (int i = 0; i < L::kThreads / 32; ++i) top = fmaxf(top, sc->wmax[i]);
-        // top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
-        const int k = (int)(__float_as_uint(top) >> 23) - 127;
-        const int up = min(14 - k, 100);
-        const float mul = __uint_as_float((uint32_t)(127 + max(up, -126)) << 23);
-        q_unit = 1.f / mul;
-        for (int i = tid; i < kN * (D / 8); i += L::kThreads) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i < Rb * (D / 8)) {
-                v = Qg[i];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    w[u] = f16x2(__uint_as_float(w[u] << 16) * mul, __uint_as_float(w[u] & 0xffff0000u) * mul);
-            }
-            *q_address(i) = v;
-        }
-    } else if (n > 0) {
-        for (int i = tid; i < kN * (D / 8); i += L::kThreads)
-            *q_address(i) = i < Rb * (D / 8) ? Qg[i] : make_uint4(0, 0, 0, 0);
-    }
-    fence_proxy_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sc->tmem_base;
-    const uint32_t smem_base = smem_u32(smem);
 
     if (n <= 0) {
         // nothing to do
     } else if (warp >= L::kProducerWarp) {
         regs_down<L::kLastRegs>();
         if (warp == L::kProducerWarp) {
-            // ------------------------------ producer ------------------------------
+            // ------------------------------ producer --------------------------
             // lane i holds the id of page 32 k + i of the split
             const uint64_t policy = l2_policy_evict_first();
-            const bool once = n_rb == 1;                    // else the other row blocks read it again
+            const bool once = n_rb == 1;                // else the other row blocks read it again
             const int first_page = 2 * t_begin, last_page = keys.pages;
             int id = 0, issued = 0;
             bool ok = true;
@@ -375,23 +354,23 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                               kRoleProducer | kBarRawFull | (unsigned)(i & 0xffff));
             }
         } else if (warp == L::kMmaWarp) {
-            // ------------------------------ issuer --------------------------------
+            // ------------------------------ issuer ----------------------------
             if (lane == 0) {
-                constexpr uint32_t kS16 = idesc(false, false, false, kN), kSb = idesc(true, false, false, kN);
-                constexpr uint32_t kO16 = idesc(false, true, true, kN), kOb = idesc(true, true, true, kN);
-                const uint64_t qd = sdesc(smem_base + L::kOffQ, 16, 1024);
-                const uint64_t vd = sdesc(smem_base + L::kOffV, L::kVBlock, 1024);
-                const uint64_t pd = sdesc(smem_base + L::kOffP, kQ8Tile * 128, 1024);
+                constexpr uint32_t kS16 = idesc(false, false, kN), kSb = idesc(true, false, kN);
+                constexpr uint32_t kO16 = idesc(false, true, kN), kOb = idesc(true, true, kN);
+                const uint32_t base = smem_u32(smem);
+                const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
+                const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
                 int ns = 0, npv = 0;
-                bool ok = true;
+                bool ok = mbar_wait_sleep(&sc->q_full, 0, p.err, kRoleMma | kBarQ);
                 uint64_t t_last = global_timer_ns();
-                while (npv < n) {
+                while (ok && npv < n) {
                     bool progressed = false;
-                    if (ns < n && mbar_try_wait(&sc->k_full[ns & 1], (ns >> 1) & 1) &&
+                    if (ns < n && mbar_try_wait(&sc->k_full[ns % KB], (ns / KB) & 1) &&
                         (ns < 2 || mbar_try_wait(&sc->s_free[ns & 1], ((ns >> 1) - 1) & 1))) {
                         tc_fence_after();
-                        const uint32_t dS = tmem + kTmemS + (uint32_t)((ns & 1) * 128);
-                        const uint32_t aK = tmem + kTmemK + (uint32_t)((ns & 1) * 64);
+                        const uint32_t dS = tmem + L::kTmemS + (uint32_t)(ns & 1) * L::kNCols;
+                        const uint32_t aK = tmem + L::kTmemK + (uint32_t)(64 * (ns % KB));
                         const uint32_t id = ns < n_page ? kS16 : kSb;
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k)
@@ -403,14 +382,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         progressed = true;
                     }
                     if (npv < ns && mbar_try_wait(&sc->p_full, npv & 1) &&
-                        mbar_try_wait(&sc->v_full[npv & 1], (npv >> 1) & 1)) {
+                        mbar_try_wait(&sc->v_full[npv % VB], (npv / VB) & 1)) {
                         tc_fence_after();
-                        const uint64_t va = vd + (uint64_t)((npv & 1) * (L::kVBytes >> 4));
+                        const uint32_t aV = tmem + L::kTmemV + (uint32_t)(64 * (npv % VB));
                         const uint32_t id = npv < n_page ? kO16 : kOb;
 #pragma unroll
                         for (int k = 0; k < kQ8Tile / 16; ++k)
-                            mma_bf16(tmem + kTmemO, va + (uint64_t)(k * (2048 >> 4)),
-                                     pd + (uint64_t)(k * (2048 >> 4)), id, (npv > 0 || k > 0) ? 1u : 0u);
+                            mma_bf16_ta(tmem + L::kTmemO, aV + (uint32_t)(8 * k),
+                                        pd + (uint64_t)(k * (2048 >> 4)), id, (npv > 0 || k > 0) ? 1u : 0u);
                         mma_commit(&sc->pv_done[npv & 1]);
                         ++npv;
                         progressed = true;
@@ -421,12 +400,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         if (npv < ns)
                             (void)mbar_try_wait_sleep(&sc->p_full, npv & 1, 200u);
                         else
-                            (void)mbar_try_wait_sleep(&sc->k_full[ns & 1], (ns >> 1) & 1, 200u);
+                            (void)mbar_try_wait_sleep(&sc->k_full[ns % KB], (ns / KB) & 1, 200u);
                     } else {
                         atomicOr(p.err, kErrWaitTimeout);
                         atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarAny | (unsigned)(npv & 0xffff));
                         ok = false;
-                        break;
                     }
                 }
                 if (!ok) sc->abort = 1;
@@ -440,29 +418,22 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const int t = tid & 127, q4 = t >> 5;
         const bool do_k = L::kConvGroups == 1 || warp < L::kConvWarp + 4;
         const bool do_v = L::kConvGroups == 1 || !do_k;
-        const uint32_t k_addr = tmem + ((uint32_t)(q4 * 32) << 16) + kTmemK;
-        // K codes: thread t's key is row t % 64 of page t / 64, 128 / (128 / d) bytes of a
-        // 128-byte line
+        const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
+        const __nv_bfloat16* Kh = static_cast<const __nv_bfloat16*>(p.K) + bg * p.cap * D;
+        const __nv_bfloat16* Vh = static_cast<const __nv_bfloat16*>(p.V) + bg * p.cap * D;
+        // K codes: thread t's key is row t % 64 of page t / 64.  A line of 128 bytes holds
+        // 128 / d keys.
         const int k_line = D == 128 ? t & 63 : (t & 63) >> 1;
         const uint8_t* k_src = smem + L::kOffRaw + (t >> 6) * L::kPageBytes + k_line * 128;
         const int k_piece = D == 128 ? 0 : 4 * (t & 1);
-        // V codes: 8 threads to a 128-byte line, so thread t takes piece t % 8 of the lines
-        // t / 8, t / 8 + 16, ... of a page: the same 16 dimensions of keys 16 (or 32) apart
-        const int v_piece = t & 7, v_line = t >> 3;
-        const uint8_t* v_src = smem + L::kOffRaw + kPageTokens * D + v_line * 128 +
-                               ((v_piece ^ (v_line & 7)) << 4);
-        const int v_dim = D == 128 ? v_piece : v_piece & 3;             // 16 dimensions
-        const int v_key = D == 128 ? v_line : 2 * v_line + (v_piece >> 2);
-        // the two 16-byte pieces it writes; threads of the second block of dimensions start
-        // with their second piece, so that 8 threads never meet in a bank
-        const int v_odd = (v_dim >> 2) & 1;
-        const uint32_t v_dst = L::kOffV + (v_dim >> 2) * L::kVBlock + v_key * 128;
-        const uint32_t v_p0 = ((2 * (v_dim & 3) + v_odd) ^ (v_key & 7)) << 4;
-        const uint32_t v_p1 = ((2 * (v_dim & 3) + (v_odd ^ 1)) ^ (v_key & 7)) << 4;
+        // V codes: a transposing load takes 32 keys x 16 dimensions, lane l giving the address
+        // of key l's 16 bytes; lane l then holds dimensions l / 4 and l / 4 + 8, keys
+        // 4 (l % 4) .. + 3 of each half, which as fp16 pairs are the 16x256b tensor-memory layout
+        const int v_line = D == 128 ? lane : lane >> 1;               // line of the load's key
+        const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
+        const uint32_t v_src = smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128);
         bool ok = true;
         for (int i = 0; i < n && ok; ++i) {
-            const int u = i & 1;
-            const uint32_t par = (uint32_t)((i >> 1) & 1);
             const bool paged = i < n_page;
             const int st = i % kStages;
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
@@ -470,11 +441,12 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (paged)
                 ok = mbar_wait_sleep(&sc->raw_full[st], (i / kStages) & 1, p.err, code | kBarRawFull);
             if (do_k) {
-                // S of tile i - 2 has read this K buffer
-                if (ok && i >= 2) ok = mbar_wait_sleep(&sc->s_full[u], par ^ 1, p.err, code | kBarS);
+                // S of tile i - KB has read this K buffer
+                if (ok && i >= KB)
+                    ok = mbar_wait_sleep(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), p.err, code | kBarS);
                 if (ok && !paged && i == n_page && i > 0) {
                     // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
-                    ok = mbar_wait_sleep(&sc->s_full[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
+                    ok = mbar_wait_sleep(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
                     if (ok) {
                         for (int x = t; x < kN * (D / 8); x += 128)
                             *q_address(x) = x < Rb * (D / 8) ? Qg[x] : make_uint4(0, 0, 0, 0);
@@ -484,18 +456,19 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t dst = lanes + L::kTmemK + (uint32_t)(64 * (i % KB));
                 if (paged) {
                     const uint8_t* line = k_src + st * L::kRawBytes;
-                    uint4 v[D / 16];
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        v[j] = *reinterpret_cast<const uint4*>(line + (((k_piece + j) ^ (k_line & 7)) << 4));
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = *reinterpret_cast<const uint4*>(line + (((k_piece + 4 * h + j) ^ (k_line & 7)) << 4));
                         uint32_t w[32];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint32_t x[4] = {v[4 * h + j].x, v[4 * h + j].y, v[4 * h + j].z, v[4 * h + j].w};
+                            const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const uint2 y = e4m3x4_to_f16x4(x[e]);
@@ -503,7 +476,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                                 w[8 * j + 2 * e + 1] = y.y;
                             }
                         }
-                        tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
+                        tmem_st32(dst + (uint32_t)(32 * h), w);
                     }
                 } else {
                     const bool live = k0 + t < tail_keys;
@@ -516,129 +489,186 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                             const uint4 v = live ? row[8 * h + j] : make_uint4(0, 0, 0, 0);
                             w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
                         }
-                        tmem_st32(k_addr + (uint32_t)(u * 64 + 32 * h), w);
+                        tmem_st32(dst + (uint32_t)(32 * h), w);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sc->k_full[u]);
+                mbar_arrive(&sc->k_full[i % KB]);
             }
             if (do_v) {
-                // V: lines of 64 dimensions, 128-byte swizzle; the product of tile i - 2 has read it
-                if (ok && i >= 2) ok = mbar_wait_sleep(&sc->pv_done[u], par ^ 1, p.err, code | kBarPv);
+                // the product of tile i - VB has read this V buffer
+                if (ok && i >= VB)
+                    ok = mbar_wait_sleep(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), p.err, code | kBarPv);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                tc_fence_after();
+                const uint32_t dst = lanes + L::kTmemV + (uint32_t)(64 * (i % VB));
                 if (paged) {
-                    constexpr int kSteps = D / 32;                      // 16 lines of a page at a time
                     const bool two = 2 * (t_begin + i) + 1 < keys.pages;
-                    const uint8_t* src = v_src + st * L::kRawBytes;
-                    uint8_t* dst = smem + v_dst + u * L::kVBytes;
+                    const uint32_t src = v_src + (uint32_t)(st * L::kRawBytes);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint4 v[kSteps];
+                    for (int h = 0; h < D / 64; ++h) {
+                        // 16 dimensions of the quadrant into 16 of its lanes
+                        const uint32_t piece = (uint32_t)(((v_piece + (D == 128 ? 2 * q4 + h : q4)) ^ (v_line & 7)) << 4);
+                        uint32_t w[32];
 #pragma unroll
-                        for (int j = 0; j < kSteps; ++j)                // a page that is not there reads as zeros
-                            v[j] = half == 0 || two
-                                       ? *reinterpret_cast<const uint4*>(src + half * L::kPageBytes + j * 2048)
-                                       : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < kSteps; ++j) {
-                            const uint2 x0 = e4m3x4_to_f16x4(v[j].x), x1 = e4m3x4_to_f16x4(v[j].y);
-                            const uint2 x2 = e4m3x4_to_f16x4(v[j].z), x3 = e4m3x4_to_f16x4(v[j].w);
-                            const uint4 a = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                            const uint4 e = make_uint4(x2.x, x2.y, x3.x, x3.y);
-                            uint8_t* to = dst + (half * 64 + j * (D == 128 ? 16 : 32)) * 128;
-                            *reinterpret_cast<uint4*>(to + v_p0) = v_odd ? e : a;
-                            *reinterpret_cast<uint4*>(to + v_p1) = v_odd ? a : e;
-                        }
-                    }
-                } else {
-                    // V elements that are not finite would turn hidden keys' zero probabilities
-                    // into NaN: they are zero here and join the rows that see them at the end
-                    uint8_t* vt = smem + L::kOffV + u * L::kVBytes;
-                    for (int x = t; x < kQ8Tile * (D / 8); x += 128) {
-                        const int key = x / (D / 8), j = x - key * (D / 8);
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (k0 + key < tail_keys) {
-                            v = reinterpret_cast<const uint4*>(Vh + (k0 + key) * D)[j];
-                            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-                            bool odd = false;
+                        for (int m = 0; m < 4; ++m) {                 // 32 keys, two loads to a page
+                            uint32_t r[4] = {0, 0, 0, 0};             // a page that is not there reads as zeros
+                            if (m < 2 || two)
+                                ldmatrix_t_b8_x2(src + (uint32_t)((m >> 1) * L::kPageBytes + (m & 1) * 32 * D) + piece, r);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; odd = true; }
-                                if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; odd = true; }
-                            }
-                            if (odd) {
-                                const int at = atomicAdd(&sc->flagged, 1);
-                                if (at < kFlagged) sc->flagged_piece[at] = (k0 + key) * (D / 8) + j;
+                                const uint2 y = e4m3x4_to_f16x4(r[e]);
+                                w[8 * m + 2 * e] = y.x;
+                                w[8 * m + 2 * e + 1] = y.y;
                             }
                         }
-                        *reinterpret_cast<uint4*>(vt + (j >> 3) * L::kVBlock + key * 128 +
-                                                  (((j & 7) ^ (key & 7)) << 4)) = v;
+                        tmem_st_16x256b_x8(dst + ((uint32_t)(16 * h) << 16), w);
+                    }
+                } else {
+                    // One dimension to a thread.  Elements that are not finite would turn hidden
+                    // keys' zero probabilities into NaN: they are zero here and join the rows
+                    // that see them at the end.
+                    const int dim = D == 128 ? 32 * q4 + lane : 16 * q4 + lane;
+                    const bool mine = D == 128 || lane < 16;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            uint32_t two[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int64_t key = k0 + 64 * h + 2 * j + e;
+                                two[e] = 0;
+                                if (mine && key < tail_keys)
+                                    two[e] = reinterpret_cast<const uint16_t*>(Vh)[key * D + dim];
+                            }
+                            w[j] = two[0] | two[1] << 16;
+                        }
+                        bool odd = false;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; odd = true; }
+                            if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0xffffu; odd = true; }
+                        }
+                        if (odd) {
+#pragma unroll 1
+                            for (int j = 0; j < 64; ++j) {
+                                const int64_t key = k0 + 64 * h + j;
+                                if (key >= tail_keys) break;
+                                if ((reinterpret_cast<const uint16_t*>(Vh)[key * D + dim] & 0x7f80u) != 0x7f80u) continue;
+                                const int at = atomicAdd(&sc->flagged, 1);
+                                if (at < kFlagged) sc->flagged_at[at] = key * D + dim;
+                            }
+                        }
+                        __syncwarp();
+                        tmem_st32(dst + (uint32_t)(32 * h), w);
                     }
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&sc->v_full[u]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sc->v_full[i % VB]);
             }
-            if (paged) {                                                // this group has read the raw stage
+            if (paged) {                                              // this group has read the raw stage
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc->raw_free[st]);
             }
         }
         if (!ok) sc->abort = 1;
     } else {
-        regs_up<L::kSoftmaxRegs>();
         // ------------------------------ softmax -------------------------------
+        regs_up<L::kSoftmaxRegs>();
         const int gr = warp >> 2, q4 = warp & 3;
         const int t = tid & 127;                        // this thread's key of every tile
-        const int c0 = gr * L::kCols;                   // first row (column of S^T) of the group
+        const int c0 = gr * COLS;                       // first row (column of S^T) of the group
         const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
+        const int64_t slot = ((int64_t)g * p.S + slot_idx) * p.R + r0;   // this CTA's partial rows
         float* neg_ref = sc->neg_ref + c0;
         float* corr = sc->corr + c0;
         const int half = t >> 6;
 
-        // largest scale of V among the split's pages: the unit of O^T
-        float unit = 0.f;
-#pragma unroll 1
-        for (int j = 2 * t_begin + t; j < min(keys.pages, 2 * (t_begin + n_page)); j += 128)
-            unit = fmaxf(unit, __ldg(p.scales + ((int64_t)q8_page(p, b, j) * p.Hkv + g) * 2 + 1));
-        unit = warp_max(unit);
-        if (lane == 0) sc->part[gr][q4][0] = unit;
-        group_sync(gr);
-        unit = fmaxf(fmaxf(sc->part[gr][0][0], sc->part[gr][1][0]), fmaxf(sc->part[gr][2][0], sc->part[gr][3][0]));
-        if (!(unit > 0.f)) unit = 1.f;
-        group_sync(gr);
-        const float inv_unit = 1.f / unit;
-
         // (scale of K, scale of V) of this thread's key in page tile i, fetched a tile ahead
         // (its page id, two tiles ahead: neither load is waited for; the producer flags an id
         // that is outside the pool)
-        const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin + half;
-        const int my_pages = min(keys.pages - 2 * t_begin - half, 2 * n_page);   // ids[0, my_pages) exist
-        auto page_of = [&](int i) -> int { return 2 * i < my_pages ? __ldg(ids + 2 * i) : 0; };
+        const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
+        const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
+        auto page_of = [&](int j) -> int { return j < my_pages ? __ldg(ids + j) : 0; };
         auto scales_of = [&](int page) -> float2 {
             const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
             return __ldg(reinterpret_cast<const float2*>(p.scales + ((int64_t)id * p.Hkv + g) * 2));
         };
-        float2 scale_now = scales_of(page_of(0));
-        int page_next = page_of(1);
-
-        float2 l2[L::kCols / 2];                        // this thread's part of the rows' sums
+        const int page_first = page_of(half);
+        int page_next = page_of(2 + half);
+        // largest scale of V among the split's pages: the unit of O^T
+        float unit = 0.f;
+#pragma unroll 1
+        for (int j = t; j < my_pages; j += 128) unit = fmaxf(unit, scales_of(page_of(j)).y);
+        float2 scale_now = scales_of(page_first);
+        // Q into shared memory
+        float q_top = 0.f;
+        if (n_page > 0) {
+            for (int i = tid; i < Rb * (D / 8); i += 256) {
+                const uint4 v = Qg[i];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int c = 0; c < L::kCols / 2; ++c) l2[c] = make_float2(0.f, 0.f);
+                for (int e = 0; e < 4; ++e) {
+                    const float x = fabsf(__uint_as_float(w[e] << 16)), y = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+                    if (x < INFINITY) q_top = fmaxf(q_top, x);
+                    if (y < INFINITY) q_top = fmaxf(q_top, y);
+                }
+            }
+        }
+        unit = warp_max(unit);
+        q_top = warp_max(q_top);
+        if (lane == 0) {
+            sc->part[gr][q4][0] = unit;
+            sc->wmax[warp] = q_top;
+        }
+        asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+        unit = fmaxf(fmaxf(sc->part[gr][0][0], sc->part[gr][1][0]), fmaxf(sc->part[gr][2][0], sc->part[gr][3][0]));
+        if (!(unit > 0.f)) unit = 1.f;
+        const float inv_unit = 1.f / unit;
+        q_top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q_top = fmaxf(q_top, sc->wmax[i]);
+        // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
+        const int q_exp = max(min(14 - ((int)(__float_as_uint(q_top) >> 23) - 127), 100), -126);
+        const float q_mul = __uint_as_float((uint32_t)(127 + q_exp) << 23);
+        for (int i = tid; i < kN * (D / 8); i += 256) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i < Rb * (D / 8)) {
+                v = Qg[i];
+                if (n_page > 0) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = f16x2(__uint_as_float(w[e] << 16) * q_mul, __uint_as_float(w[e] & 0xffff0000u) * q_mul);
+                }
+            }
+            *q_address(i) = v;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sc->q_full);
+        const float a_page = p.scale_log2 * (1.f / q_mul);
+
+        float2 l2[COLS / 2];                            // this thread's part of the rows' sums
+#pragma unroll
+        for (int c = 0; c < COLS / 2; ++c) l2[c] = make_float2(0.f, 0.f);
         bool fail = false;
         for (int i = 0; i < n; ++i) {
             const int u = i & 1;
             const bool paged = i < n_page;
             const unsigned code = kRoleSoftmax | (unsigned)(i & 0xffff);
             const float2 scale_next = scales_of(page_next);
-            const int page_after = page_of(i + 2);
+            const int page_after = page_of(2 * (i + 2) + half);
             // which of the rows see this thread's key
             uint64_t seen;
             float a, vmul;                              // s = a * S^T; the factor of V in P
             if (paged) {
                 seen = 2 * (t_begin + i) + half < keys.pages ? ~0ull : 0ull;
-                a = scale_now.x * (p.scale_log2 * q_unit);
+                a = scale_now.x * a_page;
                 vmul = seen ? scale_now.y * inv_unit : 0.f;   // no page: no scale to trust
             } else {
                 const int64_t key = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile + t;
@@ -647,7 +677,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 if (node >= 0 && key < tail_keys) {
                     seen = 0;
 #pragma unroll 1
-                    for (int c = 0; c < L::kCols; ++c) {
+                    for (int c = 0; c < COLS; ++c) {
                         const int iq = (r0 + c0 + c) % p.n_q;
                         const bool vis = p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0
                                                 : node <= iq;
@@ -660,18 +690,19 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             fail |= !mbar_wait_sleep(&sc->s_full[u], (uint32_t)((i >> 1) & 1), p.err, code | kBarS);
             fail = __any_sync(0xffffffffu, fail);
             tc_fence_after();
-            float x[L::kCols];
-            const uint32_t s_addr = lanes + kTmemS + (uint32_t)(u * 128 + c0);
+            float x[COLS];
+            const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                uint32_t r[16];
-                tmem_ld16(s_addr + 16 * ch, r);
+            for (int ch = 0; ch < COLS / 8; ++ch) {
+                uint32_t r[8];
+                tmem_ld8(s_addr + 8 * ch, r);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) x[16 * ch + c] = __uint_as_float(r[c]);
+                for (int c = 0; c < 8; ++c) x[8 * ch + c] = __uint_as_float(r[c]);
             }
             tmem_wait_ld();
+            float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < L::kCols; c += 4) {
+            for (int c = 0; c < COLS; c += 4) {
                 const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
                 const float2 aa = make_float2(a, a);
                 const float2 y0 = fma2(make_float2(x[c], x[c + 1]), aa, make_float2(nr.x, nr.y));
@@ -681,36 +712,35 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (seen != ~0ull) {
                 uint64_t bits = seen;
 #pragma unroll
-                for (int c = 0; c < L::kCols; ++c) {
+                for (int c = 0; c < COLS; ++c) {
                     if (!(bits & 1ull)) x[c] = -INFINITY;
                     bits >>= 1;
                 }
             }
-            float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < L::kCols; c += 4) {
+            for (int c = 0; c < COLS; c += 4) {
                 top0 = fmax3(top0, x[c], x[c + 1]);
                 top1 = fmax3(top1, x[c + 2], x[c + 3]);
             }
-            const bool over = fmaxf(top0, top1) > kMaxLog2P;
+            const bool over = fmaxf(top0, top1) > kMaxLog2P;   // some score passed its reference by too much
             if (group_any(gr, over || fail)) {
                 if (group_any(gr, fail)) { fail = true; break; }   // the same answer in every warp
                 // ---- the references of the rows that need it move ----
                 uint64_t bits = seen;
 #pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    uint32_t r[16];
-                    tmem_ld16(s_addr + 16 * ch, r);
+                for (int ch = 0; ch < COLS / 8; ++ch) {
+                    uint32_t r[8];
+                    tmem_ld8(s_addr + 8 * ch, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         const float m = warp_max_redux((bits & 1ull) ? __uint_as_float(r[c]) * a : -INFINITY);
-                        if (lane == 0) sc->part[gr][q4][16 * ch + c] = m;
+                        if (lane == 0) sc->part[gr][q4][8 * ch + c] = m;
                         bits >>= 1;
                     }
                 }
                 group_sync(gr);
-                if (t < L::kCols) {
+                if (t < COLS) {
                     const float m = fmaxf(fmaxf(sc->part[gr][0][t], sc->part[gr][1][t]),
                                           fmaxf(sc->part[gr][2][t], sc->part[gr][3][t]));
                     const float old = neg_ref[t];
@@ -727,26 +757,27 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     fail = __any_sync(0xffffffffu, fail);
                     tc_fence_after();
 #pragma unroll
-                    for (int ch = 0; ch < NCH; ++ch) {
-                        uint32_t o[16];
-                        tmem_ld16(lanes + kTmemO + (uint32_t)(c0 + 16 * ch), o);
+                    for (int ch = 0; ch < COLS / 8; ++ch) {
+                        uint32_t o[8];
+                        const uint32_t o_addr = lanes + L::kTmemO + (uint32_t)(c0 + 8 * ch);
+                        tmem_ld8(o_addr, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            o[c] = __float_as_uint(__uint_as_float(o[c]) * corr[16 * ch + c]);
-                        tmem_st16(lanes + kTmemO + (uint32_t)(c0 + 16 * ch), o);
+                        for (int c = 0; c < 8; ++c)
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * corr[8 * ch + c]);
+                        tmem_st8(o_addr, o);
                     }
                     tmem_wait_st();
                 }
                 bits = seen;
 #pragma unroll
-                for (int ch = 0; ch < NCH; ++ch) {
-                    uint32_t r[16];
-                    tmem_ld16(s_addr + 16 * ch, r);
+                for (int ch = 0; ch < COLS / 8; ++ch) {
+                    uint32_t r[8];
+                    tmem_ld8(s_addr + 8 * ch, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int col = 16 * ch + c;
+                    for (int c = 0; c < 8; ++c) {
+                        const int col = 8 * ch + c;
                         if (c & 1) l2[col >> 1].y *= corr[col]; else l2[col >> 1].x *= corr[col];
                         x[col] = (bits & 1ull) ? fmaf(__uint_as_float(r[c]), a, neg_ref[col]) : -INFINITY;
                         bits >>= 1;
@@ -757,10 +788,10 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sc->s_free[u]);
-            uint32_t pk[L::kCols / 2];
+            uint32_t pk[COLS / 2];
             const float2 vm = make_float2(vmul, vmul);
 #pragma unroll
-            for (int c = 0; c < L::kCols / 2; ++c) {
+            for (int c = 0; c < COLS / 2; ++c) {
                 const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
                 l2[c] = add2(l2[c], e);
                 const float2 w = mul2(e, vm);
@@ -772,12 +803,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 fail = __any_sync(0xffffffffu, fail);
             }
             if (!fail) {
-                uint8_t* row = smem + L::kOffP + (c0 >> 6) * (kQ8Tile * 128) + t * 128;
-                const int j0 = (c0 & 63) >> 3;          // first 16-byte piece of the group's rows
 #pragma unroll
-                for (int j = 0; j < L::kCols / 8; ++j) {
-                    const int jj = j0 + j;
-                    *reinterpret_cast<uint4*>(row + (jj >> 3) * (kQ8Tile * 128) + (((jj & 7) ^ (t & 7)) << 4)) =
+                for (int j = 0; j < COLS / 8; ++j) {
+                    const int jj = c0 / 8 + j;          // 16-byte piece: 8 rows
+                    *reinterpret_cast<uint4*>(smem + L::kOffP + (jj >> 3) * (kQ8Tile * 128) + t * 128 +
+                                              (((jj & 7) ^ (t & 7)) << 4)) =
                         make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
                 }
                 fence_proxy_async_smem();
@@ -788,44 +818,47 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             page_next = page_after;
         }
         if (tid == 0) griddep_launch_dependents();
+        // the rows' sums over this warp's keys
+#pragma unroll
+        for (int c = 0; c < COLS; c += 8) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { v[2 * e] = l2[c / 2 + e].x; v[2 * e + 1] = l2[c / 2 + e].y; }
+            const float s = warp_sum8(v, lane);
+            if ((lane & 3) == 0) sc->part[gr][q4][c + (lane >> 2)] = s;
+        }
         // O^T of the last product
         if (!fail)
             fail = !mbar_wait_sleep(&sc->pv_done[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1), p.err,
                                     kRoleSoftmax | kBarPv | 0xffffu);
         fail = group_any(gr, fail);
-        // the rows' sums over this warp's keys
-#pragma unroll
-        for (int c = 0; c < L::kCols; ++c) {
-            const float s = warp_sum(c & 1 ? l2[c >> 1].y : l2[c >> 1].x);
-            if (lane == 0) sc->part[gr][q4][c] = s;
-        }
-        group_sync(gr);
         if (fail) {
             sc->abort = 1;
         } else {
             tc_fence_after();
-            if (t < L::kCols && c0 + t < Rb) {
+            if (t < COLS && c0 + t < Rb) {
                 const float s = (sc->part[gr][0][t] + sc->part[gr][1][t]) + (sc->part[gr][2][t] + sc->part[gr][3][t]);
                 const float nr = neg_ref[t];
                 *reinterpret_cast<float2*>(p.part_ml + (slot + c0 + t) * 2) =
                     nr == kNoKey && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
             }
-            const int dim = 32 * q4 + lane;
+            const int dim = D == 128 ? 32 * q4 + lane : 16 * q4 + lane;
+            const bool mine = D == 128 || lane < 16;
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-                uint32_t o[16];
-                tmem_ld16(lanes + kTmemO + (uint32_t)(c0 + 16 * ch), o);
+            for (int ch = 0; ch < COLS / 8; ++ch) {
+                uint32_t o[8];
+                tmem_ld8(lanes + L::kTmemO + (uint32_t)(c0 + 8 * ch), o);
                 tmem_wait_ld();
-                if (dim >= D) continue;                 // warp-uniform: D is 64 or 128
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    const int r = c0 + 16 * ch + c;
-                    if (r < Rb) p.part_acc[(slot + r) * D + dim] = __uint_as_float(o[c]) * unit;
+                for (int c = 0; c < 8; ++c) {
+                    const int r = c0 + 8 * ch + c;
+                    if (mine && r < Rb) p.part_acc[(slot + r) * D + dim] = __uint_as_float(o[c]) * unit;
                 }
             }
             const int flagged = sc->flagged;
-            if (flagged > 0 && dim < D) {
+            if (flagged > 0 && mine) {
                 // V elements left out of the products reach the rows that see them
+                const __nv_bfloat16* Vh = static_cast<const __nv_bfloat16*>(p.V) + bg * p.cap * D;
                 const int64_t first = (int64_t)max(t_begin - keys.page_tiles, 0) * kQ8Tile;
                 const int64_t last = min((int64_t)(t_end - keys.page_tiles) * kQ8Tile, tail_keys);
                 const bool listed = flagged <= kFlagged;
@@ -834,14 +867,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 for (int64_t f = 0; f < m; ++f) {
                     int64_t key = first + f;
                     if (listed) {
-                        key = sc->flagged_piece[f] / (D / 8);
-                        if (sc->flagged_piece[f] % (D / 8) != dim / 8) continue;
+                        key = sc->flagged_at[f] / D;
+                        if (sc->flagged_at[f] % D != dim) continue;
                     }
                     const float v = __bfloat162float(Vh[key * D + dim]);
                     if (fabsf(v) < INFINITY) continue;
                     const int64_t node = key - keys.tail;
 #pragma unroll 1
-                    for (int r = c0; r < min(c0 + L::kCols, Rb); ++r) {
+                    for (int r = c0; r < min(c0 + COLS, Rb); ++r) {
                         const int iq = (r0 + r) % p.n_q;
                         if (node < 0 || (p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0
                                                 : node <= iq))
@@ -855,8 +888,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     __syncthreads();
     if (warp == L::kMmaWarp) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sc->tmem_base),
-                     "r"(kTmemCols)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                      : "memory");
     }
 }
@@ -874,10 +906,10 @@ bool make_pool_map(CUtensorMap* m, const AttnQ8Params& p) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NCH, int GROUPS>
+template <int D, int COLS>
 cudaError_t launch_shape(const CUtensorMap& pool, const AttnQ8Params& p, int n_rb, int rows, cudaStream_t st) {
-    using L = Plan<D, NCH, GROUPS>;
-    auto kern = attn_q8_tc_kernel<D, NCH, GROUPS>;
+    using L = Plan<D, COLS>;
+    auto kern = attn_q8_tc_kernel<D, COLS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -893,18 +925,17 @@ cudaError_t launch_shape(const CUtensorMap& pool, const AttnQ8Params& p, int n_r
     return cudaLaunchKernelEx(&cfg, kern, pool, p, n_rb, rows);
 }
 
+// Rows of a CTA in steps of 16 up to 64, then of 32.
 template <int D>
 cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStream_t st) {
     const int n_rb = q8_row_blocks(p.R);
     const int rows = (p.R + n_rb - 1) / n_rb;
-    switch (rows <= 64 ? (rows + 15) / 16 : 4 + (rows + 31) / 32) {
-        case 1: return launch_shape<D, 1, 1>(pool, p, n_rb, rows, st);
-        case 2: return launch_shape<D, 2, 1>(pool, p, n_rb, rows, st);
-        case 3: return launch_shape<D, 3, 1>(pool, p, n_rb, rows, st);
-        case 4: return launch_shape<D, 4, 1>(pool, p, n_rb, rows, st);
-        case 7: return launch_shape<D, 3, 2>(pool, p, n_rb, rows, st);
-        default: return launch_shape<D, 4, 2>(pool, p, n_rb, rows, st);
-    }
+    if (rows <= 16) return launch_shape<D, 8>(pool, p, n_rb, rows, st);
+    if (rows <= 32) return launch_shape<D, 16>(pool, p, n_rb, rows, st);
+    if (rows <= 48) return launch_shape<D, 24>(pool, p, n_rb, rows, st);
+    if (rows <= 64) return launch_shape<D, 32>(pool, p, n_rb, rows, st);
+    if (rows <= 96) return launch_shape<D, 48>(pool, p, n_rb, rows, st);
+    return launch_shape<D, 64>(pool, p, n_rb, rows, st);
 }
 
 }  // namespace
