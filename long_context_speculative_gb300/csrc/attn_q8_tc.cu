@@ -28,8 +28,10 @@
 //
 // CTA = (sequence and split, block of at most 128 group rows; KV head).  Tiles are 128 keys:
 // two pages, or 128 tail rows.  Warps:
-//   softmax     8, two groups with half the rows each; warp w owns the keys, later the output
-//               dimensions, of tensor-memory lane quadrant w % 4
+//   softmax     8 in two groups; warp w owns the keys, later the output dimensions, of
+//               tensor-memory lane quadrant w % 4.  Up to 64 rows the groups take the tiles in
+//               turn, each with its own references and O^T, joined at the end; above, both
+//               take every tile and half of its rows
 //   converters  4 for K and 4 for V (4 for both with more than 96 rows)
 //   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
 //               into a ring of raw stages by TMA
@@ -51,6 +53,7 @@ namespace rapid {
 namespace {
 
 constexpr int kMaxRawStages = 6;
+constexpr int kConvNap = 60;           // ns between tests of the converters' and the producer's waits
 constexpr int kFlagged = 64;           // elements of V remembered for not being finite
 constexpr uint32_t kTmemCols = 512;
 
@@ -60,10 +63,11 @@ constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no
 constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
                                        // (fp16 ends at 65504)
 
-// COLS: group rows of one of the two softmax groups (a multiple of 8, at most 64).
-template <int D, int COLS>
+// COLS: rows of one softmax group (a multiple of 8, at most 64).  ALT: the groups take tiles in
+// turn (all rows each); else every tile, half of the rows each.
+template <int D, int COLS, bool ALT>
 struct Plan {
-    static constexpr int kN = 2 * COLS;                     // N of the products
+    static constexpr int kN = ALT ? COLS : 2 * COLS;        // N of the products
     static constexpr int kConvGroups = kN <= 96 ? 2 : 1;
     static constexpr int kConvWarp = 8;
     static constexpr int kProducerWarp = kConvWarp + 4 * kConvGroups;
@@ -71,23 +75,24 @@ struct Plan {
     static constexpr int kThreads = 32 * (kProducerWarp + 4);
     // A block starts with kLaunchRegs registers a thread; its warpgroups share them out anew.
     static constexpr int kLaunchRegs = kThreads == 640 ? 96 : 128;
-    static constexpr int kSoftmaxRegs = kThreads == 512 ? 176 : COLS <= 32 ? 112 : 136;
-    static constexpr int kConvRegs = kThreads == 512 ? 104 : COLS <= 32 ? 96 : 80;
-    static constexpr int kLastRegs = COLS == 48 ? 48 : 56;
+    static constexpr int kSoftmaxRegs = kThreads == 512 ? 176 : COLS <= 32 ? 112 : COLS <= 48 ? 136 : 152;
+    static constexpr int kConvRegs = kThreads == 512 ? 104 : COLS <= 32 ? 96 : COLS <= 48 ? 80 : 64;
+    static constexpr int kLastRegs = kThreads == 512 || COLS <= 32 ? 56 : COLS <= 48 ? 48 : 40;
     static_assert(2 * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
                   "registers of a block");
-    // Tensor-memory columns: K and V tiles (64 each), O^T, two S^T buffers.
+    // Tensor-memory columns: K and V tiles (64 each), O^T (of each group), two S^T buffers.
     static constexpr int kKBufs = kN <= 64 ? 2 : 1;
     static constexpr int kVBufs = kN <= 96 ? 2 : 1;
     static constexpr uint32_t kNCols = kN < 32 ? 32 : kN;
     static constexpr uint32_t kTmemK = 0;
     static constexpr uint32_t kTmemV = 64 * kKBufs;
     static constexpr uint32_t kTmemO = kTmemV + 64 * kVBufs;
-    static constexpr uint32_t kTmemS = kTmemO + kNCols;
+    static constexpr uint32_t kTmemS = kTmemO + (ALT ? 2 : 1) * kNCols;
     static_assert(kTmemS + 2 * kNCols <= kTmemCols, "tensor memory");
     static constexpr int kPageBytes = 2 * kPageTokens * D;  // K and V of one page and head
     static constexpr int kRawBytes = 2 * kPageBytes;        // one stage: two pages
-    static constexpr int kPBytes = (kN + 63) / 64 * (kQ8Tile * 128);
+    static constexpr int kPBuf = (kN + 63) / 64 * (kQ8Tile * 128);
+    static constexpr int kPBytes = (ALT ? 2 : 1) * kPBuf;   // one for each group in ALT
     static constexpr int kQBlock = kN * 128;                // 64 dimensions of Q
     static constexpr int kOffP = 0;
     static constexpr int kOffQ = kOffP + kPBytes;
@@ -111,12 +116,12 @@ struct Scalars {
     uint64_t s_free[2];      // S^T loaded by the softmax warps
     uint64_t v_full[2];      // V^T in tensor memory
     uint64_t pv_done[2];     // O^T += V^T P^T of a tile done (V's buffer and P free)
-    uint64_t p_full;
+    uint64_t p_full[2];      // P of a tile in shared memory (of each group in ALT)
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
     Q8Split split;
-    alignas(16) float neg_ref[128];   // -(reference) of every row: P = 2^(s + neg_ref)
+    alignas(16) float neg_ref[128];   // -(reference) of every row (64 g + row in ALT): P = 2^(s + neg_ref)
     alignas(16) float corr[128];
     float part[2][4][64];    // per softmax group and warp: a number for each of its rows
     float wmax[8];
@@ -131,7 +136,7 @@ enum : unsigned int {
     kRoleProducer = 0x11u << 24, kRoleMma = 0x12u << 24, kRoleSoftmax = 0x13u << 24,
     kRoleConvert = 0x14u << 24,
     kBarRawFull = 1u << 16, kBarRawFree = 2u << 16, kBarS = 3u << 16, kBarPv = 4u << 16,
-    kBarAny = 5u << 16, kBarDrain = 6u << 16, kBarQ = 7u << 16
+    kBarK = 5u << 16, kBarDrain = 6u << 16, kBarQ = 7u << 16, kBarP = 8u << 16, kBarV = 9u << 16
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -177,19 +182,22 @@ __device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w) {
     return r;
 }
 
-// Barrier of one softmax group with an OR over its 128 threads.
-__device__ __forceinline__ bool group_any(int gr, bool x) {
+// Barrier `id` of N threads with an OR over them: the same answer in each.
+template <int N>
+__device__ __forceinline__ bool barrier_any(int id, bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)x), "r"(1 + gr)
+        : "r"((uint32_t)x), "r"(id), "n"(N)
         : "memory");
     return r != 0;
 }
+// ... of one softmax group.
+__device__ __forceinline__ bool group_any(int gr, bool x) { return barrier_any<128>(1 + gr, x); }
 __device__ __forceinline__ void group_sync(int gr) {
     asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + gr) : "memory");
 }
@@ -198,6 +206,31 @@ __device__ __forceinline__ void group_sync(int gr) {
 constexpr uint32_t idesc(bool bf16, bool b_mn, int n) {
     return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+// mma_bf16_ta and mma_commit, issued by the lane with `leader` set.
+__device__ __forceinline__ void mma_ta_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit_if(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)), "r"(leader)
+        : "memory");
 }
 
 // Two transposed 16 x 16 byte matrices; lanes 0..15 and 16..31 give the addresses of their rows.
@@ -224,17 +257,19 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
     return s + __shfl_xor_sync(0xffffffffu, s, 1);
 }
 
-template <int D, int COLS>
-__global__ void __launch_bounds__(Plan<D, COLS>::kThreads, 1)
+template <int D, int COLS, bool ALT>
+__global__ void __launch_bounds__(Plan<D, COLS, ALT>::kThreads, 1)
 attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p, const int n_rb,
                   const int rows_per_block) {
-    using L = Plan<D, COLS>;
+    using L = Plan<D, COLS, ALT>;
     constexpr int kStages = L::kStages, kN = L::kN, KB = L::kKBufs, VB = L::kVBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Scalars* sc = reinterpret_cast<Scalars*>(smem + L::kOffScalar);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp index through a shuffle: known to be the same in all lanes, so that the roles'
+    // branches, addresses and descriptors stay on the uniform path
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int slot_idx = blockIdx.x / n_rb, rb = blockIdx.x - slot_idx * n_rb;
     const int g = blockIdx.y;
     const int r0 = rb * rows_per_block;                 // first group row of this CTA
@@ -249,11 +284,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         for (int u = 0; u < 2; ++u) {
             mbar_init(&sc->k_full[u], 128);
             mbar_init(&sc->s_full[u], 1);
-            mbar_init(&sc->s_free[u], 8);
+            mbar_init(&sc->s_free[u], ALT ? 4 : 8);
+            mbar_init(&sc->p_full[u], ALT ? 128 : 256);
             mbar_init(&sc->v_full[u], 128);
             mbar_init(&sc->pv_done[u], 1);
         }
-        mbar_init(&sc->p_full, 256);
         mbar_init(&sc->drain, 1);
         sc->abort = 0;
         sc->flagged = 0;
@@ -326,7 +361,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const int st = i % kStages;
                 if (lane == 0) {
                     if (i >= kStages)
-                        ok = mbar_wait_sleep(&sc->raw_free[st], ((i / kStages) + 1) & 1, p.err,
+                        ok = mbar_wait_lean<kConvNap>(&sc->raw_free[st], ((i / kStages) + 1) & 1, p.err,
                                              kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff));
                     if (*((volatile int*)&sc->abort)) ok = false;
                     if (ok) {
@@ -355,62 +390,64 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             }
         } else if (warp == L::kMmaWarp) {
             // ------------------------------ issuer ----------------------------
-            if (lane == 0) {
-                constexpr uint32_t kS16 = idesc(false, false, kN), kSb = idesc(true, false, kN);
-                constexpr uint32_t kO16 = idesc(false, true, kN), kOb = idesc(true, true, kN);
-                const uint32_t base = smem_u32(smem);
-                const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
-                const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
-                int ns = 0, npv = 0;
-                bool ok = mbar_wait_sleep(&sc->q_full, 0, p.err, kRoleMma | kBarQ);
-                uint64_t t_last = global_timer_ns();
-                while (ok && npv < n) {
-                    bool progressed = false;
-                    if (ns < n && mbar_try_wait(&sc->k_full[ns % KB], (ns / KB) & 1) &&
-                        (ns < 2 || mbar_try_wait(&sc->s_free[ns & 1], ((ns >> 1) - 1) & 1))) {
-                        tc_fence_after();
-                        const uint32_t dS = tmem + L::kTmemS + (uint32_t)(ns & 1) * L::kNCols;
-                        const uint32_t aK = tmem + L::kTmemK + (uint32_t)(64 * (ns % KB));
-                        const uint32_t id = ns < n_page ? kS16 : kSb;
+            // The whole warp runs the loop, so that addresses and descriptors stay in uniform
+            // registers, and one elected lane issues.  The order is fixed, S of tile i + 2
+            // (its buffer is free once S of tile i is loaded) before the product of tile i:
+            // that is the order in which the inputs come.  Converters that do K and V in turn
+            // reach K of tile i + 2 only after the product of tile i, so there it is S of i + 1.
+            constexpr int kAhead = L::kConvGroups == 1 ? 1 : 2;
+            constexpr uint32_t kS16 = idesc(false, false, kN), kSb = idesc(true, false, kN);
+            constexpr uint32_t kO16 = idesc(false, true, kN), kOb = idesc(true, true, kN);
+            const uint32_t base = smem_u32(smem);
+            // warp reductions of values that are the same in every lane, into uniform registers
+            const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+            const int tiles = __reduce_max_sync(0xffffffffu, n), page_tiles = __reduce_max_sync(0xffffffffu, n_page);
+            const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
+            const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
+            const uint32_t leader = elect_one();
+            auto wait = [&](uint64_t* bar, uint32_t par, unsigned code) {
+                return __all_sync(0xffffffffu, mbar_wait_lean<0>(bar, par, p.err, kRoleMma | code)) != 0;
+            };
+            auto scores = [&](int j) -> bool {
+                if (!wait(&sc->k_full[j % KB], (uint32_t)((j / KB) & 1), kBarK | (unsigned)(j & 0xffff))) return false;
+                if (j >= 2 && !wait(&sc->s_free[j & 1], (uint32_t)(((j >> 1) - 1) & 1), kBarS | (unsigned)(j & 0xffff)))
+                    return false;
+                tc_fence_after();
+                const uint32_t dS = tm + L::kTmemS + (uint32_t)(j & 1) * L::kNCols;
+                const uint32_t aK = tm + L::kTmemK + (uint32_t)(64 * (j % KB));
+                const uint32_t id = j < page_tiles ? kS16 : kSb;
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            mma_bf16_ta(dS, aK + (uint32_t)(8 * k),
-                                        qd + (uint64_t)(((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), id,
-                                        k > 0 ? 1u : 0u);
-                        mma_commit(&sc->s_full[ns & 1]);
-                        ++ns;
-                        progressed = true;
-                    }
-                    if (npv < ns && mbar_try_wait(&sc->p_full, npv & 1) &&
-                        mbar_try_wait(&sc->v_full[npv % VB], (npv / VB) & 1)) {
-                        tc_fence_after();
-                        const uint32_t aV = tmem + L::kTmemV + (uint32_t)(64 * (npv % VB));
-                        const uint32_t id = npv < n_page ? kO16 : kOb;
+                for (int k = 0; k < D / 16; ++k)
+                    mma_ta_if(leader, dS, aK + (uint32_t)(8 * k),
+                              qd + (uint64_t)(((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), id, k > 0 ? 1u : 0u);
+                mma_commit_if(leader, &sc->s_full[j & 1]);
+                return true;
+            };
+            bool ok = wait(&sc->q_full, 0, kBarQ);
+            ok = ok && scores(0);
+            if (kAhead > 1 && tiles > 1) ok = ok && scores(1);
+            for (int i = 0; ok && i < tiles; ++i) {
+                if (i + kAhead < tiles) ok = scores(i + kAhead);
+                // ALT: group i & 1 and its tile i >> 1
+                const int pb = ALT ? i & 1 : 0;
+                ok = ok && wait(&sc->p_full[pb], (uint32_t)((ALT ? i >> 1 : i) & 1), kBarP | (unsigned)(i & 0xffff));
+                ok = ok && wait(&sc->v_full[i % VB], (uint32_t)((i / VB) & 1), kBarV | (unsigned)(i & 0xffff));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dO = tm + L::kTmemO + (uint32_t)pb * L::kNCols;
+                const uint32_t aV = tm + L::kTmemV + (uint32_t)(64 * (i % VB));
+                const uint64_t bP = pd + (uint64_t)(pb * (L::kPBuf >> 4));
+                const uint32_t id = i < page_tiles ? kO16 : kOb;
+                const uint32_t add = i < (ALT ? 2 : 1) ? 0u : 1u;   // the group's first product starts O^T
 #pragma unroll
-                        for (int k = 0; k < kQ8Tile / 16; ++k)
-                            mma_bf16_ta(tmem + L::kTmemO, aV + (uint32_t)(8 * k),
-                                        pd + (uint64_t)(k * (2048 >> 4)), id, (npv > 0 || k > 0) ? 1u : 0u);
-                        mma_commit(&sc->pv_done[npv & 1]);
-                        ++npv;
-                        progressed = true;
-                    }
-                    if (progressed) {
-                        t_last = global_timer_ns();
-                    } else if (global_timer_ns() - t_last <= kWaitLimitNs) {
-                        if (npv < ns)
-                            (void)mbar_try_wait_sleep(&sc->p_full, npv & 1, 200u);
-                        else
-                            (void)mbar_try_wait_sleep(&sc->k_full[ns % KB], (ns / KB) & 1, 200u);
-                    } else {
-                        atomicOr(p.err, kErrWaitTimeout);
-                        atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarAny | (unsigned)(npv & 0xffff));
-                        ok = false;
-                    }
-                }
-                if (!ok) sc->abort = 1;
-                mma_commit(&sc->drain);
-                mbar_wait_sleep(&sc->drain, 0, p.err, kRoleMma | kBarDrain);
+                for (int k = 0; k < kQ8Tile / 16; ++k)
+                    mma_ta_if(leader, dO, aV + (uint32_t)(8 * k), bP + (uint64_t)(k * (2048 >> 4)), id,
+                              k > 0 ? 1u : add);
+                mma_commit_if(leader, &sc->pv_done[i & 1]);
             }
+            if (!ok) sc->abort = 1;
+            mma_commit_if(leader, &sc->drain);
+            mbar_wait_lean<0>(&sc->drain, 0, p.err, kRoleMma | kBarDrain);
         }
     } else if (warp >= L::kConvWarp) {
         // ------------------------------ converters ----------------------------
@@ -439,14 +476,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
             const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
             if (paged)
-                ok = mbar_wait_sleep(&sc->raw_full[st], (i / kStages) & 1, p.err, code | kBarRawFull);
+                ok = mbar_wait_lean<kConvNap>(&sc->raw_full[st], (i / kStages) & 1, p.err, code | kBarRawFull);
             if (do_k) {
                 // S of tile i - KB has read this K buffer
                 if (ok && i >= KB)
-                    ok = mbar_wait_sleep(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), p.err, code | kBarS);
+                    ok = mbar_wait_lean<kConvNap>(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), p.err, code | kBarS);
                 if (ok && !paged && i == n_page && i > 0) {
                     // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
-                    ok = mbar_wait_sleep(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
+                    ok = mbar_wait_lean<kConvNap>(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
                     if (ok) {
                         for (int x = t; x < kN * (D / 8); x += 128)
                             *q_address(x) = x < Rb * (D / 8) ? Qg[x] : make_uint4(0, 0, 0, 0);
@@ -499,7 +536,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (do_v) {
                 // the product of tile i - VB has read this V buffer
                 if (ok && i >= VB)
-                    ok = mbar_wait_sleep(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), p.err, code | kBarPv);
+                    ok = mbar_wait_lean<kConvNap>(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), p.err, code | kBarPv);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -582,11 +619,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         regs_up<L::kSoftmaxRegs>();
         const int gr = warp >> 2, q4 = warp & 3;
         const int t = tid & 127;                        // this thread's key of every tile
-        const int c0 = gr * COLS;                       // first row (column of S^T) of the group
+        const int c0 = ALT ? 0 : gr * COLS;             // first row (column of S^T) of the group
+        const int first_tile = ALT ? gr : 0;
+        constexpr int kStep = ALT ? 2 : 1;              // tiles from one of the group's to its next
         const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
         const int64_t slot = ((int64_t)g * p.S + slot_idx) * p.R + r0;   // this CTA's partial rows
-        float* neg_ref = sc->neg_ref + c0;
-        float* corr = sc->corr + c0;
+        float* neg_ref = sc->neg_ref + (ALT ? 64 * gr : c0);
+        float* corr = sc->corr + (ALT ? 64 * gr : c0);
+        const uint32_t o_base = lanes + L::kTmemO + (ALT ? (uint32_t)gr * L::kNCols : (uint32_t)c0);
         const int half = t >> 6;
 
         // (scale of K, scale of V) of this thread's key in page tile i, fetched a tile ahead
@@ -599,8 +639,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
             return __ldg(reinterpret_cast<const float2*>(p.scales + ((int64_t)id * p.Hkv + g) * 2));
         };
-        const int page_first = page_of(half);
-        int page_next = page_of(2 + half);
+        const int page_first = page_of(2 * first_tile + half);
+        int page_next = page_of(2 * (first_tile + kStep) + half);
         // largest scale of V among the split's pages: the unit of O^T
         float unit = 0.f;
 #pragma unroll 1
@@ -657,12 +697,13 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll
         for (int c = 0; c < COLS / 2; ++c) l2[c] = make_float2(0.f, 0.f);
         bool fail = false;
-        for (int i = 0; i < n; ++i) {
+        for (int i = first_tile; i < n; i += kStep) {
             const int u = i & 1;
+            const int prev = i - kStep;                 // the product that used this group's P and O^T last
             const bool paged = i < n_page;
             const unsigned code = kRoleSoftmax | (unsigned)(i & 0xffff);
             const float2 scale_next = scales_of(page_next);
-            const int page_after = page_of(2 * (i + 2) + half);
+            const int page_after = page_of(2 * (i + 2 * kStep) + half);
             // which of the rows see this thread's key
             uint64_t seen;
             float a, vmul;                              // s = a * S^T; the factor of V in P
@@ -687,8 +728,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 a = p.scale_log2;
                 vmul = inv_unit;
             }
-            fail |= !mbar_wait_sleep(&sc->s_full[u], (uint32_t)((i >> 1) & 1), p.err, code | kBarS);
-            fail = __any_sync(0xffffffffu, fail);
+            fail |= !mbar_wait_lean<0>(&sc->s_full[u], (uint32_t)((i >> 1) & 1), p.err, code | kBarS);
             tc_fence_after();
             float x[COLS];
             const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
@@ -752,14 +792,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     corr[t] = f;
                 }
                 group_sync(gr);
-                if (i > 0) {
-                    fail |= !mbar_wait_sleep(&sc->pv_done[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarPv);
-                    fail = __any_sync(0xffffffffu, fail);
+                if (prev >= 0) {
+                    fail |= !mbar_wait_lean<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), p.err, code | kBarPv);
+                    __syncwarp();
                     tc_fence_after();
 #pragma unroll
                     for (int ch = 0; ch < COLS / 8; ++ch) {
                         uint32_t o[8];
-                        const uint32_t o_addr = lanes + L::kTmemO + (uint32_t)(c0 + 8 * ch);
+                        const uint32_t o_addr = o_base + (uint32_t)(8 * ch);
                         tmem_ld8(o_addr, o);
                         tmem_wait_ld();
 #pragma unroll
@@ -790,30 +830,33 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (lane == 0) mbar_arrive(&sc->s_free[u]);
             uint32_t pk[COLS / 2];
             const float2 vm = make_float2(vmul, vmul);
+            auto exps = [&](auto pack) {
 #pragma unroll
-            for (int c = 0; c < COLS / 2; ++c) {
-                const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
-                l2[c] = add2(l2[c], e);
-                const float2 w = mul2(e, vm);
-                pk[c] = paged ? f16x2(w.x, w.y) : bf16x2(w.x, w.y);
-            }
+                for (int c = 0; c < COLS / 2; ++c) {
+                    const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
+                    l2[c] = add2(l2[c], e);
+                    const float2 w = mul2(e, vm);
+                    pk[c] = pack(w.x, w.y);
+                }
+            };
+            if (paged) exps([](float lo, float hi) { return f16x2(lo, hi); });
+            else exps([](float lo, float hi) { return bf16x2(lo, hi); });
             // P's buffer is free once the previous product has read it
-            if (i > 0) {
-                fail |= !mbar_wait_sleep(&sc->pv_done[u ^ 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarPv);
-                fail = __any_sync(0xffffffffu, fail);
-            }
+            if (prev >= 0)
+                fail |= !mbar_wait_lean<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), p.err, code | kBarPv);
             if (!fail) {
+                uint8_t* pt = smem + L::kOffP + (ALT ? gr * L::kPBuf : 0) + t * 128;
 #pragma unroll
                 for (int j = 0; j < COLS / 8; ++j) {
                     const int jj = c0 / 8 + j;          // 16-byte piece: 8 rows
-                    *reinterpret_cast<uint4*>(smem + L::kOffP + (jj >> 3) * (kQ8Tile * 128) + t * 128 +
-                                              (((jj & 7) ^ (t & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(pt + (jj >> 3) * (kQ8Tile * 128) + (((jj & 7) ^ (t & 7)) << 4)) =
                         make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&sc->p_full);
+                mbar_arrive(&sc->p_full[ALT ? gr : 0]);
             }
+            __syncwarp();
             scale_now = scale_next;
             page_next = page_after;
         }
@@ -827,32 +870,69 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const float s = warp_sum8(v, lane);
             if ((lane & 3) == 0) sc->part[gr][q4][c + (lane >> 2)] = s;
         }
-        // O^T of the last product
-        if (!fail)
-            fail = !mbar_wait_sleep(&sc->pv_done[(n - 1) & 1], (uint32_t)(((n - 1) >> 1) & 1), p.err,
-                                    kRoleSoftmax | kBarPv | 0xffffu);
-        fail = group_any(gr, fail);
-        if (fail) {
+        // O^T of the last products (in ALT of both groups)
+        for (int i = max(n - kStep, 0); i < n; ++i)
+            fail |= !mbar_wait_lean<0>(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), p.err,
+                                     kRoleSoftmax | kBarPv | 0xffffu);
+        if (barrier_any<256>(3, fail)) {                // sums and references of both groups are there
             sc->abort = 1;
         } else {
             tc_fence_after();
-            if (t < COLS && c0 + t < Rb) {
-                const float s = (sc->part[gr][0][t] + sc->part[gr][1][t]) + (sc->part[gr][2][t] + sc->part[gr][3][t]);
-                const float nr = neg_ref[t];
-                *reinterpret_cast<float2*>(p.part_ml + (slot + c0 + t) * 2) =
-                    nr == kNoKey && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
-            }
             const int dim = D == 128 ? 32 * q4 + lane : 16 * q4 + lane;
             const bool mine = D == 128 || lane < 16;
+            auto row_sum = [&](int group, int r) {
+                const float(*s)[64] = sc->part[group];
+                return (s[0][r] + s[1][r]) + (s[2][r] + s[3][r]);
+            };
+            if constexpr (ALT) {
+                // Weights of the two groups' parts of a row; this group writes half of the rows.
+                // A group that took no tile has nothing in O^T.
+                constexpr int kHalf = COLS / 2;
+                if (t < kHalf) {
+                    const int r = gr * kHalf + t;
+                    const float s0 = row_sum(0, r), s1 = row_sum(1, r);
+                    const float m0 = -sc->neg_ref[r], m1 = -sc->neg_ref[64 + r];
+                    const float m = fmaxf(s0 != 0.f ? m0 : -kNoKey, s1 != 0.f ? m1 : -kNoKey);
+                    const float w0 = s0 != 0.f ? ex2(m0 - m) : 0.f, w1 = s1 != 0.f ? ex2(m1 - m) : 0.f;
+                    const float s = s0 * w0 + s1 * w1;
+                    sc->corr[r] = w0 * unit;
+                    sc->corr[64 + r] = w1 * unit;
+                    if (r < Rb)
+                        *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) =
+                            make_float2(m == -kNoKey && s == 0.f ? -INFINITY : m, s);
+                }
+                group_sync(gr);
 #pragma unroll
-            for (int ch = 0; ch < COLS / 8; ++ch) {
-                uint32_t o[8];
-                tmem_ld8(lanes + L::kTmemO + (uint32_t)(c0 + 8 * ch), o);
-                tmem_wait_ld();
+                for (int ch = 0; ch < kHalf / 8; ++ch) {
+                    uint32_t o0[8], o1[8];
+                    const int base = gr * kHalf + 8 * ch;
+                    tmem_ld8(lanes + L::kTmemO + (uint32_t)base, o0);
+                    tmem_ld8(lanes + L::kTmemO + L::kNCols + (uint32_t)base, o1);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int r = c0 + 8 * ch + c;
-                    if (mine && r < Rb) p.part_acc[(slot + r) * D + dim] = __uint_as_float(o[c]) * unit;
+                    for (int c = 0; c < 8; ++c) {
+                        const int r = base + c;
+                        const float w0 = sc->corr[r], w1 = sc->corr[64 + r];
+                        const float y = __uint_as_float(o0[c]) * w0 + (n > 1 ? __uint_as_float(o1[c]) * w1 : 0.f);
+                        if (mine && r < Rb) p.part_acc[(slot + r) * D + dim] = y;
+                    }
+                }
+            } else {
+                if (t < COLS && c0 + t < Rb) {
+                    const float s = row_sum(gr, t), nr = neg_ref[t];
+                    *reinterpret_cast<float2*>(p.part_ml + (slot + c0 + t) * 2) =
+                        nr == kNoKey && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
+                }
+#pragma unroll
+                for (int ch = 0; ch < COLS / 8; ++ch) {
+                    uint32_t o[8];
+                    tmem_ld8(o_base + (uint32_t)(8 * ch), o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const int r = c0 + 8 * ch + c;
+                        if (mine && r < Rb) p.part_acc[(slot + r) * D + dim] = __uint_as_float(o[c]) * unit;
+                    }
                 }
             }
             const int flagged = sc->flagged;
@@ -874,7 +954,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     if (fabsf(v) < INFINITY) continue;
                     const int64_t node = key - keys.tail;
 #pragma unroll 1
-                    for (int r = c0; r < min(c0 + COLS, Rb); ++r) {
+                    for (int r = ALT ? gr * (COLS / 2) : c0; r < min(ALT ? (gr + 1) * (COLS / 2) : c0 + COLS, Rb); ++r) {
                         const int iq = (r0 + r) % p.n_q;
                         if (node < 0 || (p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0
                                                 : node <= iq))
@@ -906,10 +986,10 @@ bool make_pool_map(CUtensorMap* m, const AttnQ8Params& p) {
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int COLS>
+template <int D, int COLS, bool ALT>
 cudaError_t launch_shape(const CUtensorMap& pool, const AttnQ8Params& p, int n_rb, int rows, cudaStream_t st) {
-    using L = Plan<D, COLS>;
-    auto kern = attn_q8_tc_kernel<D, COLS>;
+    using L = Plan<D, COLS, ALT>;
+    auto kern = attn_q8_tc_kernel<D, COLS, ALT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -930,12 +1010,12 @@ template <int D>
 cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStream_t st) {
     const int n_rb = q8_row_blocks(p.R);
     const int rows = (p.R + n_rb - 1) / n_rb;
-    if (rows <= 16) return launch_shape<D, 8>(pool, p, n_rb, rows, st);
-    if (rows <= 32) return launch_shape<D, 16>(pool, p, n_rb, rows, st);
-    if (rows <= 48) return launch_shape<D, 24>(pool, p, n_rb, rows, st);
-    if (rows <= 64) return launch_shape<D, 32>(pool, p, n_rb, rows, st);
-    if (rows <= 96) return launch_shape<D, 48>(pool, p, n_rb, rows, st);
-    return launch_shape<D, 64>(pool, p, n_rb, rows, st);
+    if (rows <= 16) return launch_shape<D, 16, true>(pool, p, n_rb, rows, st);
+    if (rows <= 32) return launch_shape<D, 32, true>(pool, p, n_rb, rows, st);
+    if (rows <= 48) return launch_shape<D, 48, true>(pool, p, n_rb, rows, st);
+    if (rows <= 64) return launch_shape<D, 64, true>(pool, p, n_rb, rows, st);
+    if (rows <= 96) return launch_shape<D, 48, false>(pool, p, n_rb, rows, st);
+    return launch_shape<D, 64, false>(pool, p, n_rb, rows, st);
 }
 
 }  // namespace
