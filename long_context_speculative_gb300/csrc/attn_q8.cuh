@@ -90,11 +90,14 @@ __device__ __forceinline__ int warp_sum_int(int v) {
 // lengths: the smallest number of tiles per split whose splits fit into the S slots, so
 // that short and long sequences of a ragged batch finish together.  Lanes take sequences
 // lane, lane + 32, ..., so a large batch costs B / 32 reads a round.
-__device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c) {
+static __device__ __noinline__ Q8Split q8_split_of_many(const AttnQ8Params& p, int c) {
     const int lane = threadIdx.x & 31;
+    const int mine = lane < p.B ? q8_keys(p, lane).tiles : 0;   // of the first 32 sequences
+    auto tiles_of = [&](int b) { return b == lane ? mine : q8_keys(p, b).tiles; };
     int total = 0, longest = 1;
+#pragma unroll 1
     for (int b = lane; b < p.B; b += 32) {
-        const int t = q8_keys(p, b).tiles;
+        const int t = tiles_of(b);
         total += t;
         longest = t > longest ? t : longest;
     }
@@ -103,18 +106,20 @@ __device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c) {
     int lo = (total + p.S - 1) / p.S;
     if (lo < 1) lo = 1;
     int hi = longest > lo ? longest : lo;
-    if (p.B == 1) hi = lo;
+#pragma unroll 1
     while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
         int used = 0;
-        for (int b = lane; b < p.B; b += 32) used += (q8_keys(p, b).tiles + mid - 1) / mid;
+#pragma unroll 1
+        for (int b = lane; b < p.B; b += 32) used += (tiles_of(b) + mid - 1) / mid;
         used = warp_sum_int(used);
         if (used <= p.S) hi = mid; else lo = mid + 1;
     }
     int first = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const int n = b < p.B ? (q8_keys(p, b).tiles + lo - 1) / lo : 0;
+        const int n = b < p.B ? (tiles_of(b) + lo - 1) / lo : 0;
         int end = n;                                  // inclusive scan over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -131,6 +136,19 @@ __device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c) {
         first += __shfl_sync(0xffffffffu, end, 31);
     }
     return Q8Split{-1, 0, 0, 0};
+}
+
+// The same with the sequence's lengths; one sequence needs no search.
+__device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c, Q8Keys* keys) {
+    Q8Split sp{0, c, 0, 0};
+    if (p.B > 1) sp = q8_split_of_many(p, c);
+    *keys = q8_keys(p, sp.b < 0 ? 0 : sp.b);
+    if (p.B == 1) {
+        const int budget = (keys->tiles + p.S - 1) / p.S;
+        sp.count = (keys->tiles + budget - 1) / budget;
+        if (c >= sp.count) sp.b = -1;
+    }
+    return sp;
 }
 
 // Group rows that one CTA of the history kernels takes.

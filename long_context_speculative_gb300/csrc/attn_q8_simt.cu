@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     float* sK = sQ + kQ8SimtRows * D;                // [32][DP]
     float* sV = sK + kKeys * DP;                     // [32][D]
     __shared__ Q8Split s_split;
+    __shared__ Q8Keys s_keys;
 
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -62,8 +63,12 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     const int slot_idx = blockIdx.x / n_rb, rb = blockIdx.x - slot_idx * n_rb;
     const int g = blockIdx.y;
     if (warp == 0) {
-        const Q8Split sp = q8_split_of(p, slot_idx);
-        if (lane == 0) s_split = sp;
+        Q8Keys k;
+        const Q8Split sp = q8_split_of(p, slot_idx, &k);
+        if (lane == 0) {
+            s_split = sp;
+            s_keys = k;
+        }
     }
     __syncthreads();
     const Q8Split sp = s_split;
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
         p.part_first[bg] = sp.first;
         p.part_count[bg] = sp.count;
     }
-    const Q8Keys keys = q8_keys(p, b);
+    const Q8Keys keys = s_keys;
     const int t_begin = (int)((int64_t)sp.s * keys.tiles / sp.count);
     const int t_end = (int)((int64_t)(sp.s + 1) * keys.tiles / sp.count);
     const int r0 = rb * kQ8SimtRows;

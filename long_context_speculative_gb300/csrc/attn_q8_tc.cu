@@ -16,8 +16,8 @@
 // power of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to
 // 2^-30 of that keep all 8 bits of a bf16).  P is fp16 of 2^(s - ref), 2^7 at the reference
 // and below 2^15, so it keeps 11 bits down to 2^-21 of the row's largest and fades out below
-// 2^-31.  The scale of V joins P relative to the largest scale of the CTA's pages, which
-// multiplies O at the end.  Tail rows and speculative rows are bf16 as they are: those tiles,
+// 2^-31.  V takes its page's scale relative to the largest scale of the CTA's pages (exact for
+// powers of two down to 2^-15), which multiplies O at the end.  Tail rows and speculative rows are bf16 as they are: those tiles,
 // the last of a sequence, run the same way in bf16.
 //
 // Both operands that come from the cache are converted in registers on their way from the raw
@@ -53,7 +53,10 @@ namespace rapid {
 namespace {
 
 constexpr int kMaxRawStages = 6;
-constexpr int kConvNap = 60;           // ns between tests of the converters' and the producer's waits
+#ifndef KNAP
+#define KNAP 40
+#endif
+constexpr int kConvNap = KNAP;          // ns between tests of the converters' and the producer's waits
 constexpr int kFlagged = 64;           // elements of V remembered for not being finite
 constexpr uint32_t kTmemCols = 512;
 
@@ -121,10 +124,12 @@ struct Scalars {
     uint32_t tmem_base;
     int abort;
     Q8Split split;
+    Q8Keys keys;
     alignas(16) float neg_ref[128];   // -(reference) of every row (64 g + row in ALT): P = 2^(s + neg_ref)
     alignas(16) float corr[128];
     float part[2][4][64];    // per softmax group and warp: a number for each of its rows
-    float wmax[8];
+    float wmax[8], wunit[8];
+    float unit;              // largest scale of V among the split's pages: O = unit * O^T
     int flagged;             // elements of the tail rows' V that are not finite
     int64_t flagged_at[kFlagged];      // row * d + dimension
 };
@@ -208,6 +213,39 @@ constexpr uint32_t idesc(bool bf16, bool b_mn, int n) {
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// Waits, bounded by a number of tests (a test takes 20 clocks or more, so 2^25 of them are the
+// better part of a second; legitimate waits last microseconds).  A role keeps the code of the
+// wait that gave up and records it once, at its end: a wait has to be a few instructions,
+// because the roles' loops share a small instruction cache and a launch fetches them anew.
+template <int NAP>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned code, unsigned& failed) {
+    constexpr unsigned kTests = NAP > 0 ? 1u << 23 : 1u << 25;
+#pragma unroll 1
+    for (unsigned i = 0; i < kTests; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (NAP > 0) __nanosleep(NAP);
+    }
+    failed = code;
+    return false;
+}
+__device__ __forceinline__ void record(unsigned int* err, unsigned failed) {
+    if (failed && err) {
+        atomicOr(err, kErrWaitTimeout);
+        atomicCAS(err + 1, 0u, failed | 0x80000000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Scale of V of a page (an id outside the pool, which the producer flags, reads as page 0).
+__device__ __forceinline__ float v_scale(const AttnQ8Params& p, int page, int g) {
+    const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
+    return __ldg(p.scales + ((int64_t)id * p.Hkv + g) * 2 + 1);
+}
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -275,12 +313,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     const int r0 = rb * rows_per_block;                 // first group row of this CTA
     const int Rb = min(rows_per_block, p.R - r0);       // its rows
 
-    if (tid == 0) {
+    if (tid == 32) {
+#pragma unroll 1
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sc->raw_full[i], 1);
             mbar_init(&sc->raw_free[i], 4 * L::kConvGroups);
         }
         mbar_init(&sc->q_full, 256);
+#pragma unroll 1
         for (int u = 0; u < 2; ++u) {
             mbar_init(&sc->k_full[u], 128);
             mbar_init(&sc->s_full[u], 1);
@@ -294,7 +334,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         sc->flagged = 0;
         fence_mbar_init();
     }
-    if (tid < 128) sc->neg_ref[tid] = kNoKey;
+    if (tid >= 64 && tid < 192) sc->neg_ref[tid - 64] = kNoKey;
     if (warp == L::kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&sc->tmem_base)),
@@ -304,9 +344,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     }
     griddep_wait();
     if (warp == 0) {
-        const Q8Split sp0 = q8_split_of(p, slot_idx);
+        Q8Keys k;
+        const Q8Split sp0 = q8_split_of(p, slot_idx, &k);
         if (lane == 0) {
             sc->split = sp0;
+            sc->keys = k;
             if (sp0.b >= 0 && sp0.s == 0 && rb == 0) {
                 p.part_first[sp0.b * p.Hkv + g] = sp0.first;
                 p.part_count[sp0.b * p.Hkv + g] = sp0.count;
@@ -321,7 +363,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     const bool has_work = sp.b >= 0;
     const int b = has_work ? sp.b : 0;
     const int64_t bg = (int64_t)b * p.Hkv + g;
-    const Q8Keys keys = q8_keys(p, b);
+    const Q8Keys keys = sc->keys;
     const int t_begin = has_work ? (int)((int64_t)sp.s * keys.tiles / sp.count) : 0;
     const int t_end = has_work ? (int)((int64_t)(sp.s + 1) * keys.tiles / sp.count) : 0;
     const int n = t_end - t_begin;
@@ -343,14 +385,17 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         // nothing to do
     } else if (warp >= L::kProducerWarp) {
         regs_down<L::kLastRegs>();
+        unsigned failed = 0;                            // code of a wait that gave up
         if (warp == L::kProducerWarp) {
             // ------------------------------ producer --------------------------
             // lane i holds the id of page 32 k + i of the split
             const uint64_t policy = l2_policy_evict_first();
             const bool once = n_rb == 1;                // else the other row blocks read it again
             const int first_page = 2 * t_begin, last_page = keys.pages;
-            int id = 0, issued = 0;
+            int id = 0, issued = 0, st = 0;
+            uint32_t lap = 0;                           // parity of the ring's current lap
             bool ok = true;
+#pragma unroll 1
             for (int i = 0; i < n_page && ok; ++i) {
                 if ((i & 15) == 0) {
                     const int j = first_page + 2 * i + lane;
@@ -358,11 +403,10 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 const int id0 = __shfl_sync(0xffffffffu, id, (2 * i) & 31);
                 const int id1 = __shfl_sync(0xffffffffu, id, (2 * i + 1) & 31);
-                const int st = i % kStages;
                 if (lane == 0) {
                     if (i >= kStages)
-                        ok = mbar_wait_lean<kConvNap>(&sc->raw_free[st], ((i / kStages) + 1) & 1, p.err,
-                                             kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff));
+                        ok = wait_for<kConvNap>(&sc->raw_free[st], lap ^ 1u,
+                                                kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff), failed);
                     if (*((volatile int*)&sc->abort)) ok = false;
                     if (ok) {
                         uint8_t* dst = smem + L::kOffRaw + st * L::kRawBytes;
@@ -380,9 +424,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (++st == kStages) { st = 0; lap ^= 1u; }
             }
             if (!ok && lane == 0) {
                 sc->abort = 1;
+#pragma unroll 1
                 // let the copies still in flight land before the CTA exits
                 for (int i = max(0, issued - kStages); i < issued; ++i)
                     mbar_wait(&sc->raw_full[i % kStages], (i / kStages) & 1, p.err,
@@ -406,7 +452,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
             const uint32_t leader = elect_one();
             auto wait = [&](uint64_t* bar, uint32_t par, unsigned code) {
-                return __all_sync(0xffffffffu, mbar_wait_lean<0>(bar, par, p.err, kRoleMma | code)) != 0;
+                return __all_sync(0xffffffffu, wait_for<0>(bar, par, kRoleMma | code, failed)) != 0;
             };
             auto scores = [&](int j) -> bool {
                 if (!wait(&sc->k_full[j % KB], (uint32_t)((j / KB) & 1), kBarK | (unsigned)(j & 0xffff))) return false;
@@ -426,6 +472,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             bool ok = wait(&sc->q_full, 0, kBarQ);
             ok = ok && scores(0);
             if (kAhead > 1 && tiles > 1) ok = ok && scores(1);
+#pragma unroll 1
             for (int i = 0; ok && i < tiles; ++i) {
                 if (i + kAhead < tiles) ok = scores(i + kAhead);
                 // ALT: group i & 1 and its tile i >> 1
@@ -447,8 +494,9 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             }
             if (!ok) sc->abort = 1;
             mma_commit_if(leader, &sc->drain);
-            mbar_wait_lean<0>(&sc->drain, 0, p.err, kRoleMma | kBarDrain);
+            wait_for<0>(&sc->drain, 0, kRoleMma | kBarDrain, failed);
         }
+        if (lane == 0) record(p.err, failed);
     } else if (warp >= L::kConvWarp) {
         // ------------------------------ converters ----------------------------
         regs_down<L::kConvRegs>();
@@ -469,22 +517,49 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const int v_line = D == 128 ? lane : lane >> 1;               // line of the load's key
         const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
         const uint32_t v_src = smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128);
+        // page ids of the split, and the scales of V of a tile's two pages as fp16 pairs relative
+        // to the largest of the split (the unit of O^T), fetched ahead like the softmax warps'
+        const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
+        const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
+        float inv_unit = 1.f;
+        auto page_ids = [&](int i) -> int2 {
+            return make_int2(2 * i < my_pages ? __ldg(ids + 2 * i) : 0,
+                             2 * i + 1 < my_pages ? __ldg(ids + 2 * i + 1) : 0);
+        };
+        auto v_units = [&](int i, int2 id) -> uint2 {                 // 0 where there is no page
+            const float x = 2 * i < my_pages ? v_scale(p, id.x, g) * inv_unit : 0.f;
+            const float y = 2 * i + 1 < my_pages ? v_scale(p, id.y, g) * inv_unit : 0.f;
+            return make_uint2(f16x2(x, x), f16x2(y, y));
+        };
+        int2 id_next = make_int2(0, 0);
+        uint2 unit_now = make_uint2(0, 0);
         bool ok = true;
+        unsigned failed = 0;
+        if (do_v && n_page > 0) {
+            const int2 id0 = page_ids(0);
+            id_next = page_ids(1);
+            ok = wait_for<kConvNap>(&sc->q_full, 0, kRoleConvert | kBarQ, failed);   // the unit is there
+            inv_unit = 1.f / sc->unit;
+            unit_now = v_units(0, id0);
+        }
+        int st = 0;
+        uint32_t lap = 0;
+#pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
             const bool paged = i < n_page;
-            const int st = i % kStages;
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
             const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
             if (paged)
-                ok = mbar_wait_lean<kConvNap>(&sc->raw_full[st], (i / kStages) & 1, p.err, code | kBarRawFull);
+                ok = wait_for<kConvNap>(&sc->raw_full[st], lap, code | kBarRawFull, failed);
             if (do_k) {
                 // S of tile i - KB has read this K buffer
                 if (ok && i >= KB)
-                    ok = mbar_wait_lean<kConvNap>(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), p.err, code | kBarS);
+                    ok = wait_for<kConvNap>(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), code | kBarS, failed);
                 if (ok && !paged && i == n_page && i > 0) {
                     // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
-                    ok = mbar_wait_lean<kConvNap>(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), p.err, code | kBarS);
+                    ok = wait_for<kConvNap>(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), code | kBarS, failed);
                     if (ok) {
+#pragma unroll 1
                         for (int x = t; x < kN * (D / 8); x += 128)
                             *q_address(x) = x < Rb * (D / 8) ? Qg[x] : make_uint4(0, 0, 0, 0);
                         fence_proxy_async_smem();
@@ -494,9 +569,9 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t dst = lanes + L::kTmemK + (uint32_t)(64 * (i % KB));
-                if (paged) {
+                if (__builtin_expect(paged, 1)) {
                     const uint8_t* line = k_src + st * L::kRawBytes;
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < D / 64; ++h) {
                         uint4 v[4];
 #pragma unroll
@@ -518,15 +593,12 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 } else {
                     const bool live = k0 + t < tail_keys;
                     const uint4* row = reinterpret_cast<const uint4*>(Kh + (k0 + t) * D);
-#pragma unroll
-                    for (int h = 0; h < D / 64; ++h) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint4 v = live ? row[8 * h + j] : make_uint4(0, 0, 0, 0);
-                            w[4 * j] = v.x; w[4 * j + 1] = v.y; w[4 * j + 2] = v.z; w[4 * j + 3] = v.w;
-                        }
-                        tmem_st32(dst + (uint32_t)(32 * h), w);
+#pragma unroll 1
+                    for (int j = 0; j < D / 16; ++j) {                // 16 elements: 8 columns
+                        const uint4 v0 = live ? row[2 * j] : make_uint4(0, 0, 0, 0);
+                        const uint4 v1 = live ? row[2 * j + 1] : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                        tmem_st8(dst + (uint32_t)(8 * j), w);
                     }
                 }
                 tmem_wait_st();
@@ -534,17 +606,22 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 mbar_arrive(&sc->k_full[i % KB]);
             }
             if (do_v) {
+                const uint32_t unit0 = unit_now.x, unit1 = unit_now.y;   // of the tile's two pages
+                if (paged) {
+                    unit_now = v_units(i + 1, id_next);
+                    id_next = page_ids(i + 2);
+                }
                 // the product of tile i - VB has read this V buffer
                 if (ok && i >= VB)
-                    ok = mbar_wait_lean<kConvNap>(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), p.err, code | kBarPv);
+                    ok = wait_for<kConvNap>(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), code | kBarPv, failed);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t dst = lanes + L::kTmemV + (uint32_t)(64 * (i % VB));
-                if (paged) {
-                    const bool two = 2 * (t_begin + i) + 1 < keys.pages;
+                if (__builtin_expect(paged, 1)) {
+                    const bool two = 2 * i + 1 < my_pages;
                     const uint32_t src = v_src + (uint32_t)(st * L::kRawBytes);
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < D / 64; ++h) {
                         // 16 dimensions of the quadrant into 16 of its lanes
                         const uint32_t piece = (uint32_t)(((v_piece + (D == 128 ? 2 * q4 + h : q4)) ^ (v_line & 7)) << 4);
@@ -557,8 +634,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const uint2 y = e4m3x4_to_f16x4(r[e]);
-                                w[8 * m + 2 * e] = y.x;
-                                w[8 * m + 2 * e + 1] = y.y;
+                                w[8 * m + 2 * e] = mul_f16x2(y.x, m < 2 ? unit0 : unit1);
+                                w[8 * m + 2 * e + 1] = mul_f16x2(y.y, m < 2 ? unit0 : unit1);
                             }
                         }
                         tmem_st_16x256b_x8(dst + ((uint32_t)(16 * h) << 16), w);
@@ -569,39 +646,28 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     // that see them at the end.
                     const int dim = D == 128 ? 32 * q4 + lane : 16 * q4 + lane;
                     const bool mine = D == 128 || lane < 16;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            uint32_t two[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int64_t key = k0 + 64 * h + 2 * j + e;
-                                two[e] = 0;
-                                if (mine && key < tail_keys)
-                                    two[e] = reinterpret_cast<const uint16_t*>(Vh)[key * D + dim];
-                            }
-                            w[j] = two[0] | two[1] << 16;
-                        }
-                        bool odd = false;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; odd = true; }
-                            if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0xffffu; odd = true; }
-                        }
-                        if (odd) {
+                    const uint16_t* col = reinterpret_cast<const uint16_t*>(Vh) + dim;
 #pragma unroll 1
-                            for (int j = 0; j < 64; ++j) {
-                                const int64_t key = k0 + 64 * h + j;
-                                if (key >= tail_keys) break;
-                                if ((reinterpret_cast<const uint16_t*>(Vh)[key * D + dim] & 0x7f80u) != 0x7f80u) continue;
-                                const int at = atomicAdd(&sc->flagged, 1);
-                                if (at < kFlagged) sc->flagged_at[at] = key * D + dim;
-                            }
+                    for (int j = 0; j < kQ8Tile / 16; ++j) {          // 16 keys: 8 columns
+                        uint32_t x[16], w[8];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int64_t key = k0 + 16 * j + e;
+                            x[e] = mine && key < tail_keys ? col[key * D] : 0u;
                         }
+                        uint32_t odd = 0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if ((x[e] & 0x7f80u) == 0x7f80u) { x[e] = 0; odd |= 1u << e; }
+#pragma unroll 1
+                        for (; odd; odd &= odd - 1) {
+                            const int at = atomicAdd(&sc->flagged, 1);
+                            if (at < kFlagged) sc->flagged_at[at] = (k0 + 16 * j + __ffs(odd) - 1) * D + dim;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = x[2 * e] | x[2 * e + 1] << 16;
                         __syncwarp();
-                        tmem_st32(dst + (uint32_t)(32 * h), w);
+                        tmem_st8(dst + (uint32_t)(8 * j), w);
                     }
                 }
                 tmem_wait_st();
@@ -611,9 +677,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (paged) {                                              // this group has read the raw stage
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sc->raw_free[st]);
+                if (++st == kStages) { st = 0; lap ^= 1u; }
             }
         }
         if (!ok) sc->abort = 1;
+        record(p.err, failed);
     } else {
         // ------------------------------ softmax -------------------------------
         regs_up<L::kSoftmaxRegs>();
@@ -629,65 +697,63 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const uint32_t o_base = lanes + L::kTmemO + (ALT ? (uint32_t)gr * L::kNCols : (uint32_t)c0);
         const int half = t >> 6;
 
-        // (scale of K, scale of V) of this thread's key in page tile i, fetched a tile ahead
-        // (its page id, two tiles ahead: neither load is waited for; the producer flags an id
-        // that is outside the pool)
+        // scale of K of this thread's key in page tile i, fetched a tile ahead (its page id, two
+        // tiles ahead: neither load is waited for; the producer flags an id outside the pool)
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
         auto page_of = [&](int j) -> int { return j < my_pages ? __ldg(ids + j) : 0; };
-        auto scales_of = [&](int page) -> float2 {
+        auto scale_of = [&](int page) -> float {
             const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
-            return __ldg(reinterpret_cast<const float2*>(p.scales + ((int64_t)id * p.Hkv + g) * 2));
+            return __ldg(p.scales + ((int64_t)id * p.Hkv + g) * 2);
         };
         const int page_first = page_of(2 * first_tile + half);
         int page_next = page_of(2 * (first_tile + kStep) + half);
-        // largest scale of V among the split's pages: the unit of O^T
-        float unit = 0.f;
+        float scale_now = scale_of(page_first);
+        // One pass over Q (into shared memory as it is) and over the scales of V: what the CTA's
+        // fp16 forms are relative to.
+        float unit = 0.f, q_top = 0.f;
 #pragma unroll 1
-        for (int j = t; j < my_pages; j += 128) unit = fmaxf(unit, scales_of(page_of(j)).y);
-        float2 scale_now = scales_of(page_first);
-        // Q into shared memory
-        float q_top = 0.f;
-        if (n_page > 0) {
-            for (int i = tid; i < Rb * (D / 8); i += 256) {
-                const uint4 v = Qg[i];
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = tid; j < my_pages; j += 256) unit = fmaxf(unit, v_scale(p, __ldg(ids + j), g));
+#pragma unroll 4
+        for (int i = tid; i < kN * (D / 8); i += 256) {
+            const uint4 v = i < Rb * (D / 8) ? Qg[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = fabsf(__uint_as_float(w[e] << 16)), y = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-                    if (x < INFINITY) q_top = fmaxf(q_top, x);
-                    if (y < INFINITY) q_top = fmaxf(q_top, y);
-                }
+            for (int e = 0; e < 4; ++e) {
+                const float x = fabsf(__uint_as_float(w[e] << 16)), y = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+                if (x < INFINITY) q_top = fmaxf(q_top, x);
+                if (y < INFINITY) q_top = fmaxf(q_top, y);
             }
+            *q_address(i) = v;
         }
         unit = warp_max(unit);
         q_top = warp_max(q_top);
         if (lane == 0) {
-            sc->part[gr][q4][0] = unit;
             sc->wmax[warp] = q_top;
+            sc->wunit[warp] = unit;
         }
         asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
-        unit = fmaxf(fmaxf(sc->part[gr][0][0], sc->part[gr][1][0]), fmaxf(sc->part[gr][2][0], sc->part[gr][3][0]));
-        if (!(unit > 0.f)) unit = 1.f;
-        const float inv_unit = 1.f / unit;
-        q_top = 0.f;
+        unit = q_top = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q_top = fmaxf(q_top, sc->wmax[i]);
+        for (int i = 0; i < 8; ++i) {
+            q_top = fmaxf(q_top, sc->wmax[i]);
+            unit = fmaxf(unit, sc->wunit[i]);
+        }
+        if (!(unit > 0.f)) unit = 1.f;
+        if (tid == 0) sc->unit = unit;
         // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
         const int q_exp = max(min(14 - ((int)(__float_as_uint(q_top) >> 23) - 127), 100), -126);
         const float q_mul = __uint_as_float((uint32_t)(127 + q_exp) << 23);
-        for (int i = tid; i < kN * (D / 8); i += 256) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (i < Rb * (D / 8)) {
-                v = Qg[i];
-                if (n_page > 0) {
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+        if (n_page > 0) {
+#pragma unroll 2
+            for (int i = tid; i < Rb * (D / 8); i += 256) {   // this thread's own pieces
+                uint4 v = *q_address(i);
+                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = f16x2(__uint_as_float(w[e] << 16) * q_mul, __uint_as_float(w[e] & 0xffff0000u) * q_mul);
-                }
+                for (int e = 0; e < 4; ++e)
+                    w[e] = f16x2(__uint_as_float(w[e] << 16) * q_mul, __uint_as_float(w[e] & 0xffff0000u) * q_mul);
+                *q_address(i) = v;
             }
-            *q_address(i) = v;
         }
         fence_proxy_async_smem();
         mbar_arrive(&sc->q_full);
@@ -697,20 +763,21 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll
         for (int c = 0; c < COLS / 2; ++c) l2[c] = make_float2(0.f, 0.f);
         bool fail = false;
+        unsigned failed = 0;
+#pragma unroll 1
         for (int i = first_tile; i < n; i += kStep) {
             const int u = i & 1;
             const int prev = i - kStep;                 // the product that used this group's P and O^T last
             const bool paged = i < n_page;
             const unsigned code = kRoleSoftmax | (unsigned)(i & 0xffff);
-            const float2 scale_next = scales_of(page_next);
+            const float scale_next = scale_of(page_next);
             const int page_after = page_of(2 * (i + 2 * kStep) + half);
             // which of the rows see this thread's key
             uint64_t seen;
-            float a, vmul;                              // s = a * S^T; the factor of V in P
-            if (paged) {
-                seen = 2 * (t_begin + i) + half < keys.pages ? ~0ull : 0ull;
-                a = scale_now.x * a_page;
-                vmul = seen ? scale_now.y * inv_unit : 0.f;   // no page: no scale to trust
+            float a;                                    // s = a * S^T
+            if (__builtin_expect(paged, 1)) {
+                seen = 2 * i + half < my_pages ? ~0ull : 0ull;
+                a = scale_now * a_page;
             } else {
                 const int64_t key = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile + t;
                 const int64_t node = key - keys.tail;
@@ -726,48 +793,56 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     }
                 }
                 a = p.scale_log2;
-                vmul = inv_unit;
             }
-            fail |= !mbar_wait_lean<0>(&sc->s_full[u], (uint32_t)((i >> 1) & 1), p.err, code | kBarS);
+            fail |= !wait_for<0>(&sc->s_full[u], (uint32_t)((i >> 1) & 1), code | kBarS, failed);
             tc_fence_after();
             float x[COLS];
             const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
+#pragma unroll 1
+            for (int pass = 0;; ++pass) {
 #pragma unroll
-            for (int ch = 0; ch < COLS / 8; ++ch) {
-                uint32_t r[8];
-                tmem_ld8(s_addr + 8 * ch, r);
+                for (int ch = 0; ch < COLS / 8; ++ch) {
+                    uint32_t r[8];
+                    tmem_ld8(s_addr + 8 * ch, r);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) x[8 * ch + c] = __uint_as_float(r[c]);
-            }
-            tmem_wait_ld();
-            float top0 = -INFINITY, top1 = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < COLS; c += 4) {
-                const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
-                const float2 aa = make_float2(a, a);
-                const float2 y0 = fma2(make_float2(x[c], x[c + 1]), aa, make_float2(nr.x, nr.y));
-                const float2 y1 = fma2(make_float2(x[c + 2], x[c + 3]), aa, make_float2(nr.z, nr.w));
-                x[c] = y0.x; x[c + 1] = y0.y; x[c + 2] = y1.x; x[c + 3] = y1.y;
-            }
-            if (seen != ~0ull) {
-                uint64_t bits = seen;
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) {
-                    if (!(bits & 1ull)) x[c] = -INFINITY;
-                    bits >>= 1;
+                    for (int c = 0; c < 8; ++c) x[8 * ch + c] = __uint_as_float(r[c]);
                 }
-            }
+                tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < COLS; c += 4) {
-                top0 = fmax3(top0, x[c], x[c + 1]);
-                top1 = fmax3(top1, x[c + 2], x[c + 3]);
-            }
-            const bool over = fmaxf(top0, top1) > kMaxLog2P;   // some score passed its reference by too much
-            if (group_any(gr, over || fail)) {
-                if (group_any(gr, fail)) { fail = true; break; }   // the same answer in every warp
-                // ---- the references of the rows that need it move ----
+                for (int c = 0; c < COLS; c += 4) {
+                    const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
+                    const float2 aa = make_float2(a, a);
+                    const float2 y0 = fma2(make_float2(x[c], x[c + 1]), aa, make_float2(nr.x, nr.y));
+                    const float2 y1 = fma2(make_float2(x[c + 2], x[c + 3]), aa, make_float2(nr.z, nr.w));
+                    x[c] = y0.x; x[c + 1] = y0.y; x[c + 2] = y1.x; x[c + 3] = y1.y;
+                }
+                if (__builtin_expect(seen != ~0ull, 0)) {
+                    uint64_t bits = seen;
+#pragma unroll
+                    for (int c = 0; c < COLS; ++c) {
+                        if (!(bits & 1ull)) x[c] = -INFINITY;
+                        bits >>= 1;
+                    }
+                }
+                float top0 = -INFINITY, top1 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 4) {
+                    top0 = fmax3(top0, x[c], x[c + 1]);
+                    top1 = fmax3(top1, x[c + 2], x[c + 3]);
+                }
+                const bool over = fmaxf(top0, top1) > kMaxLog2P;   // some score passed its reference by too much
+                if (__builtin_expect(!group_any(gr, over || fail), 1)) break;
+                fail = group_any(gr, fail);             // the same answer in every warp
+                if (fail) break;
+                if (pass > 0) {
+                    // scores past 2^26, whose own rounding is that coarse: hold them at the limit
+#pragma unroll
+                    for (int c = 0; c < COLS; ++c) x[c] = x[c] > kMaxLog2P ? kMaxLog2P : x[c];
+                    break;
+                }
+                // ---- the references of the rows that need it move; then S^T is taken again ----
                 uint64_t bits = seen;
-#pragma unroll
+#pragma unroll 1
                 for (int ch = 0; ch < COLS / 8; ++ch) {
                     uint32_t r[8];
                     tmem_ld8(s_addr + 8 * ch, r);
@@ -793,10 +868,10 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 group_sync(gr);
                 if (prev >= 0) {
-                    fail |= !mbar_wait_lean<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), p.err, code | kBarPv);
+                    fail |= !wait_for<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
                     __syncwarp();
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < COLS / 8; ++ch) {
                         uint32_t o[8];
                         const uint32_t o_addr = o_base + (uint32_t)(8 * ch);
@@ -809,41 +884,39 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     }
                     tmem_wait_st();
                 }
-                bits = seen;
 #pragma unroll
-                for (int ch = 0; ch < COLS / 8; ++ch) {
-                    uint32_t r[8];
-                    tmem_ld8(s_addr + 8 * ch, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int col = 8 * ch + c;
-                        if (c & 1) l2[col >> 1].y *= corr[col]; else l2[col >> 1].x *= corr[col];
-                        x[col] = (bits & 1ull) ? fmaf(__uint_as_float(r[c]), a, neg_ref[col]) : -INFINITY;
-                        bits >>= 1;
-                    }
+                for (int c = 0; c < COLS; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(corr + c);
+                    l2[c / 2] = mul2(l2[c / 2], make_float2(f.x, f.y));
+                    l2[c / 2 + 1] = mul2(l2[c / 2 + 1], make_float2(f.z, f.w));
                 }
             }
+            if (fail) break;                            // the same in the whole group
             // S^T is in registers: the buffer is free
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sc->s_free[u]);
             uint32_t pk[COLS / 2];
-            const float2 vm = make_float2(vmul, vmul);
-            auto exps = [&](auto pack) {
+            if (__builtin_expect(paged, 1)) {
+#pragma unroll
+                for (int c = 0; c < COLS / 2; ++c) {
+                    const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
+                    l2[c] = add2(l2[c], e);
+                    pk[c] = f16x2(e.x, e.y);
+                }
+            } else {
+                const float2 vm = make_float2(1.f / unit, 1.f / unit);   // V as it is: P takes the unit
 #pragma unroll
                 for (int c = 0; c < COLS / 2; ++c) {
                     const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
                     l2[c] = add2(l2[c], e);
                     const float2 w = mul2(e, vm);
-                    pk[c] = pack(w.x, w.y);
+                    pk[c] = bf16x2(w.x, w.y);
                 }
-            };
-            if (paged) exps([](float lo, float hi) { return f16x2(lo, hi); });
-            else exps([](float lo, float hi) { return bf16x2(lo, hi); });
+            }
             // P's buffer is free once the previous product has read it
             if (prev >= 0)
-                fail |= !mbar_wait_lean<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), p.err, code | kBarPv);
+                fail |= !wait_for<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
             if (!fail) {
                 uint8_t* pt = smem + L::kOffP + (ALT ? gr * L::kPBuf : 0) + t * 128;
 #pragma unroll
@@ -872,8 +945,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         }
         // O^T of the last products (in ALT of both groups)
         for (int i = max(n - kStep, 0); i < n; ++i)
-            fail |= !mbar_wait_lean<0>(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), p.err,
-                                     kRoleSoftmax | kBarPv | 0xffffu);
+            fail |= !wait_for<0>(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), kRoleSoftmax | kBarPv | 0xffffu, failed);
+        record(p.err, failed);
         if (barrier_any<256>(3, fail)) {                // sums and references of both groups are there
             sc->abort = 1;
         } else {
@@ -902,8 +975,9 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                             make_float2(m == -kNoKey && s == 0.f ? -INFINITY : m, s);
                 }
                 group_sync(gr);
-#pragma unroll
-                for (int ch = 0; ch < kHalf / 8; ++ch) {
+                float* dst = p.part_acc + (slot + gr * kHalf) * D + dim;
+#pragma unroll 1
+                for (int ch = 0; ch < kHalf / 8; ++ch, dst += 8 * D) {
                     uint32_t o0[8], o1[8];
                     const int base = gr * kHalf + 8 * ch;
                     tmem_ld8(lanes + L::kTmemO + (uint32_t)base, o0);
@@ -914,7 +988,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         const int r = base + c;
                         const float w0 = sc->corr[r], w1 = sc->corr[64 + r];
                         const float y = __uint_as_float(o0[c]) * w0 + (n > 1 ? __uint_as_float(o1[c]) * w1 : 0.f);
-                        if (mine && r < Rb) p.part_acc[(slot + r) * D + dim] = y;
+                        if (mine && r < Rb) dst[c * D] = y;
                     }
                 }
             } else {
@@ -923,16 +997,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     *reinterpret_cast<float2*>(p.part_ml + (slot + c0 + t) * 2) =
                         nr == kNoKey && s == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(-nr, s);
                 }
-#pragma unroll
-                for (int ch = 0; ch < COLS / 8; ++ch) {
+                float* dst = p.part_acc + (slot + c0) * D + dim;
+#pragma unroll 1
+                for (int ch = 0; ch < COLS / 8; ++ch, dst += 8 * D) {
                     uint32_t o[8];
                     tmem_ld8(o_base + (uint32_t)(8 * ch), o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int r = c0 + 8 * ch + c;
-                        if (mine && r < Rb) p.part_acc[(slot + r) * D + dim] = __uint_as_float(o[c]) * unit;
-                    }
+                    for (int c = 0; c < 8; ++c)
+                        if (mine && c0 + 8 * ch + c < Rb) dst[c * D] = __uint_as_float(o[c]) * unit;
                 }
             }
             const int flagged = sc->flagged;

@@ -216,28 +216,6 @@ RAPID_DEVICE bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, unsigned int* 
     return false;
 }
 
-// Bounded wait like mbar_wait for warps that have few instructions to spare: the clock is read
-// every 32 tests only, and NAP > 0 sleeps that many nanoseconds between tests (for a warp
-// that runs ahead of the ones it feeds; every test takes issue slots from the others).
-template <int NAP>
-RAPID_DEVICE bool mbar_wait_lean(uint64_t* bar, uint32_t parity, unsigned int* err,
-                                 unsigned int code = 0, uint64_t limit_ns = kWaitLimitNs) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    do {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i) {
-            if (NAP > 0) __nanosleep(NAP);
-            if (mbar_try_wait(bar, parity)) return true;
-        }
-    } while (global_timer_ns() - t0 <= limit_ns);
-    if (err) {
-        atomicOr(err, kErrWaitTimeout);
-        atomicCAS(err + 1, 0u, code | 0x80000000u);
-    }
-    return false;
-}
-
 // 1-D bulk copy global -> shared memory of this CTA, completing on `bar`.
 // dst, src 16-byte aligned; bytes a multiple of 16.
 RAPID_DEVICE void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
