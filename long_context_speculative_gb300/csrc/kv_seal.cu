@@ -47,34 +47,67 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// 16 consecutive elements as floats.
-__device__ __forceinline__ void load_unit(const __nv_bfloat16* p, float (&x)[16]) {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0], c = reinterpret_cast<const uint4*>(p)[1];
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+// A unit is 16 consecutive elements, held as they are: 2 (bf16) or 4 (fp32) 16-byte pieces.
+// Magnitudes are compared as integers, which order finite values as floats do and put what
+// is not finite above them.
+template <typename T> struct Unit;
+template <> struct Unit<__nv_bfloat16> {
+    static constexpr uint32_t kFirstOdd = 0x7f80u;      // least magnitude that is not finite
+    uint4 v[2];
+    __device__ __forceinline__ void top(uint32_t& m) const {   // two running maxima in m
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
     }
-}
-__device__ __forceinline__ void load_unit(const float* p, float (&x)[16]) {
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m << 16; }   // as fp32
+    __device__ __forceinline__ void to_float(float (&x)[16]) const {
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(p)[i];
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        for (int i = 0; i < 8; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
     }
+};
+template <> struct Unit<float> {
+    static constexpr uint32_t kFirstOdd = 0x7f800000u;
+    uint4 v[4];
+    __device__ __forceinline__ void top(uint32_t& m) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m = max(max(max(m, v[i].x & 0x7fffffffu), max(v[i].y & 0x7fffffffu, v[i].z & 0x7fffffffu)),
+                    v[i].w & 0x7fffffffu);
+    }
+    static __device__ __forceinline__ uint32_t join(uint32_t m) { return m; }
+    static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
+    __device__ __forceinline__ void to_float(float (&x)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[4 * i] = __uint_as_float(v[i].x); x[4 * i + 1] = __uint_as_float(v[i].y);
+            x[4 * i + 2] = __uint_as_float(v[i].z); x[4 * i + 3] = __uint_as_float(v[i].w);
+        }
+    }
+};
+
+// Maximum over the four warps of a side.
+__device__ __forceinline__ uint32_t side_max(uint32_t m, uint32_t (&s)[4], int warp, int lane) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) s[warp] = m;
+    __syncthreads();
+    return max(max(s[0], s[1]), max(s[2], s[3]));
 }
 
 // grid: (parts, B * Hkv, layers).  Part 0 seals the blocks that the rows which stay will
 // overwrite and then moves those rows to the front; the other blocks are shared out over
 // the parts.  So no row is overwritten before its one reader has read it.
 template <typename T, int D>
-__global__ void __launch_bounds__(kSealThreads) kv_seal_kernel(const __grid_constant__ SealParams p) {
+__global__ void __launch_bounds__(kSealThreads, sizeof(T) == 2 ? 4 : 2) kv_seal_kernel(const __grid_constant__ SealParams p) {
     constexpr int kUnits = kPageTokens * D / 16 / kSideThreads;   // 16-element units a thread holds
     constexpr int kPiece = 16 / sizeof(T);                        // elements of 16 bytes
     constexpr int kRowPieces = D / kPiece;
     constexpr int kMovePieces = kPageTokens * kRowPieces / kSideThreads;   // 64 rows at a time
-    __shared__ float s_max[2][4];
+    __shared__ uint32_t s_max[2][4];
     griddep_wait();
     const int part = blockIdx.x;
     const int b = blockIdx.y / p.Hkv, g = blockIdx.y - b * p.Hkv;
@@ -98,25 +131,34 @@ __global__ void __launch_bounds__(kSealThreads) kv_seal_kernel(const __grid_cons
     for (int j = 0; j < n_b; ++j) {
         const int owner = j < first ? 0 : (j - first + 1) % p.parts;
         if (owner != part) continue;
-        float x[kUnits][16];
+        Unit<T> held[kUnits];
         const T* src = rows + (int64_t)j * kPageTokens * D;
-        float top = 0.f;
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) load_unit(src + (u * kSideThreads + t) * 16, x[u]);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
+            const uint4* from = reinterpret_cast<const uint4*>(src + (u * kSideThreads + t) * 16);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float a = fabsf(x[u][e]);
-                if (a < INFINITY) top = fmaxf(top, a);
-                else x[u][e] = __int_as_float(0x7fffffff);
-            }
+            for (int e = 0; e < (int)sizeof(T); ++e) held[u].v[e] = from[e];
         }
-        top = warp_max(top);
-        if (lane == 0) s_max[side][warp] = top;
-        __syncthreads();
-        top = fmaxf(fmaxf(s_max[side][0], s_max[side][1]), fmaxf(s_max[side][2], s_max[side][3]));
-        __syncthreads();   // s_max is free for the next block
+        uint32_t m = 0;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) held[u].top(m);
+        m = side_max(Unit<T>::join(m), s_max[side], warp, lane);
+        const bool odd = m >= Unit<T>::kFirstOdd;       // something is not finite (the same in the side)
+        if (__syncthreads_or(odd)) {                    // the maximum again, of what is finite
+            float f = 0.f;
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                float x[16];
+                held[u].to_float(x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (fabsf(x[e]) < INFINITY) f = fmaxf(f, fabsf(x[e]));
+            }
+            const uint32_t g2 = side_max(__float_as_uint(f), s_max[side], warp, lane);
+            if (odd) m = sizeof(T) == 2 ? g2 >> 16 : g2;
+            __syncthreads();
+        }
+        const float top = __uint_as_float(Unit<T>::bits(m));
         // 448 = 1.75 * 2^8: top = 1.f 2^k needs exponent k - 8, one more above 1.75
         const uint32_t bits = __float_as_uint(top);
         int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
@@ -127,11 +169,18 @@ __global__ void __launch_bounds__(kSealThreads) kv_seal_kernel(const __grid_cons
         uint8_t* dst = layer.pages + slot * kPageTokens * D;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
+            float x[16];
+            held[u].to_float(x);
+            if (odd) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (!(fabsf(x[e]) < INFINITY)) x[e] = __int_as_float(0x7fffffff);
+            }
             uint32_t w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                w[q] = (uint32_t)e4m3x2(x[u][4 * q] * inv, x[u][4 * q + 1] * inv) |
-                       (uint32_t)e4m3x2(x[u][4 * q + 2] * inv, x[u][4 * q + 3] * inv) << 16;
+                w[q] = (uint32_t)e4m3x2(x[4 * q] * inv, x[4 * q + 1] * inv) |
+                       (uint32_t)e4m3x2(x[4 * q + 2] * inv, x[4 * q + 3] * inv) << 16;
             *reinterpret_cast<uint4*>(dst + (u * kSideThreads + t) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         if (t == 0) layer.scales[slot] = __uint_as_float((uint32_t)(127 + e) << 23);

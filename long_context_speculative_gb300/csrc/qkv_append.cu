@@ -93,14 +93,16 @@ __device__ __forceinline__ void pack(const float (&x)[8], Piece<float>& r) {
     r.b = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// CTAs of an SM: 28 warps (bf16) or 16 (fp32) with two head rows a lane group in flight.
+template <typename T> constexpr int kAppendCtas = sizeof(T) == 2 ? 7 : 4;
+
 template <typename T, int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const QkvAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas<T>) qkv_append_kernel(const QkvAppendParams p) {
     constexpr int kLanes = D / 16;                  // lanes of one head row
     constexpr int kRows = 32 / kLanes;              // head rows a warp handles at a time
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int sub = lane / kLanes, l = lane - sub * kLanes;
-    const int H = p.Hq + 2 * p.Hkv;
     const int64_t unit = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int64_t token = unit / p.slices;
     const int slice = (int)(unit - token * p.slices);
@@ -124,65 +126,78 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const QkvApp
     if (INTERLEAVED || l < half) { c0 = l; c1 = l + (INTERLEAVED ? kLanes : half); }
     else { c0 = 2 * l; c1 = 2 * l + 1; }
     const bool turn = !INTERLEAVED && l < half;
-    float sn[8], cs[8];
-    if (INTERLEAVED) {
+    // Sines and cosines of the lane's 8 pairs.  The lanes of a token's other rows need the same
+    // ones, so each row's lanes work out their share and the rest comes by shuffles.
+    constexpr int kShare = 8 / kRows;
+    float my_sn[kShare], my_cs[kShare], sn[8], cs[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {               // u < 4: pairs of piece c0, else of c1
-            const int pair = (u < 4 ? c0 : c1) * 4 + (u & 3);
-            sn[u] = 0.f;
-            cs[u] = 1.f;
-            if (2 * pair < p.rot) sincos_turn(turns_per_position(__ldg(p.inv_freq + pair)), pos, &sn[u], &cs[u]);
-        }
-    } else if (turn) {
+    for (int e = 0; e < kShare; ++e) {
+        const int u = sub * kShare + e;             // interleaved: u < 4 pairs of piece c0, else of c1
+        const int pair = INTERLEAVED ? (u < 4 ? c0 : c1) * 4 + (u & 3) : 8 * c0 + u;
+        my_sn[e] = 0.f;
+        my_cs[e] = 1.f;
+        if (INTERLEAVED ? 2 * pair < p.rot : turn)
+            sincos_turn(turns_per_position(__ldg(p.inv_freq + pair)), pos, &my_sn[e], &my_cs[e]);
+    }
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            sincos_turn(turns_per_position(__ldg(p.inv_freq + 8 * c0 + u)), pos, &sn[u], &cs[u]);
+    for (int u = 0; u < 8; ++u) {
+        sn[u] = __shfl_sync(0xffffffffu, my_sn[u % kShare], u / kShare * kLanes + l);
+        cs[u] = __shfl_sync(0xffffffffu, my_cs[u % kShare], u / kShare * kLanes + l);
     }
 
-    const int steps = (H + kRows - 1) / kRows;
-    for (int it = slice; it < steps; it += p.slices) {
-        const int h = it * kRows + sub;
-        const bool live = h < H;
-        const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-        const T* src;
-        T* dst;
-        if (is_q) {
-            src = static_cast<const T*>(p.q) + b * p.q_batch + i * p.q_token + (int64_t)h * D;
-            dst = static_cast<T*>(p.Q) + (((int64_t)b * p.Hq + h) * p.n + i) * D;
-        } else {
-            const int hk = h - p.Hq - (is_k ? 0 : p.Hkv);
-            src = is_k ? static_cast<const T*>(p.k) + b * p.k_batch + i * p.k_token + (int64_t)hk * D
-                       : static_cast<const T*>(p.v) + b * p.v_batch + i * p.v_token + (int64_t)hk * D;
-            dst = static_cast<T*>(is_k ? p.K : p.V) + (((int64_t)b * p.Hkv + hk) * p.cap + P + i) * D;
-        }
-        Piece<T> r0 = {}, r1 = {};
-        if (live) {
-            load_piece(src + 8 * c0, r0);
-            load_piece(src + 8 * c1, r1);
-        }
-        float x[8], y[8];
-        unpack(r0, x);
-        unpack(r1, y);
-        float ss = 0.f;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) ss = fmaf(x[u], x[u], fmaf(y[u], y[u], ss));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (!live) continue;
-        if (is_q || is_k) {
+    // Steps of kRows heads: first the queries', then the keys', then the values'.  Rows of
+    // queries and of the caches are q_step and kv_step elements apart.
+    const int q_steps = (p.Hq + kRows - 1) / kRows, kv_steps = (p.Hkv + kRows - 1) / kRows;
+    const int steps = q_steps + 2 * kv_steps;
+    const T* q = static_cast<const T*>(p.q) + b * p.q_batch + i * p.q_token;
+    const T* k = static_cast<const T*>(p.k) + b * p.k_batch + i * p.k_token;
+    const T* v = static_cast<const T*>(p.v) + b * p.v_batch + i * p.v_token;
+    T* Q = static_cast<T*>(p.Q) + ((int64_t)b * p.Hq * p.n + i) * D;
+    const int64_t cache = ((int64_t)b * p.Hkv * p.cap + P + i) * D;
+    const int64_t q_step = (int64_t)p.n * D, kv_step = p.cap * D;
+
+    auto load_step = [&](int it, Piece<T>& r0, Piece<T>& r1) {
+        const bool is_q = it < q_steps, is_k = it < q_steps + kv_steps;
+        const int h = (is_q ? it : is_k ? it - q_steps : it - q_steps - kv_steps) * kRows + sub;
+        r0 = {};
+        r1 = {};
+        if (h >= (is_q ? p.Hq : p.Hkv)) return;
+        const T* src = (is_q ? q : is_k ? k : v) + h * D;
+        load_piece(src + 8 * c0, r0);
+        load_piece(src + 8 * c1, r1);
+    };
+    auto finish_step = [&](int it, Piece<T>& r0, Piece<T>& r1) {
+        const bool is_q = it < q_steps, is_k = it < q_steps + kv_steps;   // one kind for the warp
+        const int h = (is_q ? it : is_k ? it - q_steps : it - q_steps - kv_steps) * kRows + sub;
+        if (is_k) {                                 // a query or a key
+            float x[8], y[8];
+            unpack(r0, x);
+            unpack(r1, y);
             const T* w = static_cast<const T*>(is_q ? p.q_weight : p.k_weight);
             if (w) {
-                const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
                 Piece<T> w0, w1;
                 load_piece(w + 8 * c0, w0);
                 load_piece(w + 8 * c1, w1);
+                float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < 8; u += 2) {
+                    const float2 a = make_float2(x[u], x[u + 1]), c = make_float2(y[u], y[u + 1]);
+                    s2 = fma2(a, a, fma2(c, c, s2));
+                }
+                float ss = s2.x + s2.y;
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+                const float2 i2 = make_float2(inv, inv);
                 float wx[8], wy[8];
                 unpack(w0, wx);
                 unpack(w1, wy);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    x[u] = x[u] * inv * wx[u];
-                    y[u] = y[u] * inv * wy[u];
+                for (int u = 0; u < 8; u += 2) {
+                    const float2 a = mul2(mul2(make_float2(x[u], x[u + 1]), i2), make_float2(wx[u], wx[u + 1]));
+                    const float2 c = mul2(mul2(make_float2(y[u], y[u + 1]), i2), make_float2(wy[u], wy[u + 1]));
+                    x[u] = a.x; x[u + 1] = a.y;
+                    y[u] = c.x; y[u + 1] = c.y;
                 }
             }
             if (INTERLEAVED) {
@@ -205,14 +220,27 @@ __global__ void __launch_bounds__(kAppendThreads) qkv_append_kernel(const QkvApp
             pack(x, r0);
             pack(y, r1);
         }
-        store_piece(dst + 8 * c0, r0);
-        store_piece(dst + 8 * c1, r1);
+        if (h < (is_q ? p.Hq : p.Hkv)) {
+            T* dst = is_q ? Q + h * q_step : static_cast<T*>(is_k ? p.K : p.V) + cache + h * kv_step;
+            store_piece(dst + 8 * c0, r0);
+            store_piece(dst + 8 * c1, r1);
+        }
+    };
+    // two steps at a time, both on their way before the first is worked on
+    for (int it = slice; it < steps; it += 2 * p.slices) {
+        const int next = it + p.slices;
+        Piece<T> r0, r1, n0, n1;
+        load_step(it, r0, r1);
+        if (next < steps) load_step(next, n0, n1);
+        finish_step(it, r0, r1);
+        if (next < steps) finish_step(next, n0, n1);
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(QkvAppendParams p, cudaStream_t st) {
-    const int steps = (p.Hq + 2 * p.Hkv + 32 / (D / 16) - 1) / (32 / (D / 16));
+    constexpr int kRows = 32 / (D / 16);
+    const int steps = (p.Hq + kRows - 1) / kRows + 2 * ((p.Hkv + kRows - 1) / kRows);
     const int64_t tokens = (int64_t)p.B * p.n;
     // few tokens: spread each one's heads over several warps
     int64_t slices = (152 * 32 + tokens - 1) / tokens;

@@ -8,7 +8,9 @@ every call raises.
 """
 import contextlib
 import ctypes
+import functools
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -712,24 +714,49 @@ def qkv_append(q, k, v, K, V, prefix_len, inv_freq=None, q_weight=None, k_weight
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_q8_bytes(device, *sizes):
+    nbytes = rapid_verify_attn_q8_workspace_size(*sizes)
+    if nbytes == 0:
+        raise RapidError("unsupported verify_attn_q8 shape")
+    return nbytes
+
+
+_held = threading.local()
+
+
+def _scratch(dev, nbytes):
+    """Scratch for one call on the current stream.  It is kept for the next call that the same
+    host thread makes on the same stream, which the stream orders behind this one; a call that
+    is being captured gets memory of its own, because its graph may run on any stream."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+    held = _held.__dict__
+    t = held.get(key)
+    if t is None or t.numel() < nbytes:
+        t = held[key] = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
+    return t
+
+
 def verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
                    spec_mask=None, softmax_scale=0.0, out=None, lse=None, workspace=None,
                    stream=None):
     """O [B,Hq,n_q,d] (dtype of Q) and LSE [B,Hq,n_q] float32 over an 8-bit history."""
-    if out is None or lse is None or workspace is None:
-        B, Hq, n_q, d = Q.shape
-        with _on(stream):
-            if out is None:
-                out = torch.empty_like(Q)
-            if lse is None:
-                lse = Q.new_empty((B, Hq, n_q), dtype=torch.float32)
-            if workspace is None:
-                nbytes = rapid_verify_attn_q8_workspace_size(
-                    B, Hq, K_tail.shape[1], d, n_q, K_tail.shape[2], page_table.shape[1],
-                    _dtype_code(Q))
-                if nbytes == 0:
-                    raise RapidError("unsupported verify_attn_q8 shape")
-                workspace = Q.new_empty((nbytes,), dtype=torch.uint8)
+    if stream is not None:
+        with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
+            return verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len,
+                                  tail_len, spec_mask, softmax_scale, out, lse, workspace)
+    B, Hq, n_q, d = Q.shape
+    dev = Q.device
+    if out is None:
+        out = torch.empty_like(Q)
+    if lse is None:
+        lse = torch.empty((B, Hq, n_q), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _scratch(_device_of(Q, "Q"), _attn_q8_bytes(
+            dev.index, B, Hq, K_tail.shape[1], d, n_q, K_tail.shape[2], page_table.shape[1],
+            _dtype_code(Q)))
     rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
-                         spec_mask, softmax_scale, out, lse, workspace, stream)
+                         spec_mask, softmax_scale, out, lse, workspace)
     return out, lse
