@@ -28,10 +28,11 @@
 //
 // CTA = (sequence and split, block of at most 128 group rows; KV head).  Tiles are 128 keys:
 // two pages, or 128 tail rows.  Warps:
-//   softmax     8 in two groups; warp w owns the keys, later the output dimensions, of
-//               tensor-memory lane quadrant w % 4.  Up to 64 rows the groups take the tiles in
-//               turn, each with its own references and O^T, joined at the end; above, both
-//               take every tile and half of its rows
+//   softmax     groups of 4; warp w owns the keys, later the output dimensions, of
+//               tensor-memory lane quadrant w % 4.  Up to 64 rows two groups take the tiles in
+//               turn, each with its own references and O^T, joined at the end; above, four
+//               groups take every tile and a quarter of its rows.  Either way the chain of a
+//               tile (load S, compare, exponentials, store P) overlaps another's
 //   converters  4 for K and 4 for V (4 for both with more than 96 rows)
 //   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
 //               into a ring of raw stages by TMA
@@ -53,10 +54,7 @@ namespace rapid {
 namespace {
 
 constexpr int kMaxRawStages = 6;
-#ifndef KNAP
-#define KNAP 40
-#endif
-constexpr int kConvNap = KNAP;          // ns between tests of the converters' and the producer's waits
+constexpr int kConvNap = 40;           // ns between tests of the converters' and the producer's waits
 constexpr int kFlagged = 64;           // elements of V remembered for not being finite
 constexpr uint32_t kTmemCols = 512;
 
@@ -66,22 +64,24 @@ constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no
 constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
                                        // (fp16 ends at 65504)
 
-// COLS: rows of one softmax group (a multiple of 8, at most 64).  ALT: the groups take tiles in
-// turn (all rows each); else every tile, half of the rows each.
+// COLS: rows of one softmax group (a multiple of 8).  ALT: two groups take tiles in turn (all
+// rows each); else four take every tile, a quarter of the rows each.
 template <int D, int COLS, bool ALT>
 struct Plan {
-    static constexpr int kN = ALT ? COLS : 2 * COLS;        // N of the products
+    static constexpr int kGroups = ALT ? 2 : 4;
+    static constexpr int kN = ALT ? COLS : 4 * COLS;        // N of the products
     static constexpr int kConvGroups = kN <= 96 ? 2 : 1;
-    static constexpr int kConvWarp = 8;
+    static constexpr int kConvWarp = 4 * kGroups;
+    static constexpr int kSoftmaxThreads = 128 * kGroups;
     static constexpr int kProducerWarp = kConvWarp + 4 * kConvGroups;
     static constexpr int kMmaWarp = kProducerWarp + 3;
     static constexpr int kThreads = 32 * (kProducerWarp + 4);
     // A block starts with kLaunchRegs registers a thread; its warpgroups share them out anew.
-    static constexpr int kLaunchRegs = kThreads == 640 ? 96 : 128;
-    static constexpr int kSoftmaxRegs = kThreads == 512 ? 176 : COLS <= 32 ? 112 : COLS <= 48 ? 136 : 152;
-    static constexpr int kConvRegs = kThreads == 512 ? 104 : COLS <= 32 ? 96 : COLS <= 48 ? 80 : 64;
-    static constexpr int kLastRegs = kThreads == 512 || COLS <= 32 ? 56 : COLS <= 48 ? 48 : 40;
-    static_assert(2 * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
+    static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+    static constexpr int kSoftmaxRegs = ALT ? (COLS <= 32 ? 112 : COLS <= 48 ? 136 : 152) : 88;
+    static constexpr int kConvRegs = ALT ? (COLS <= 32 ? 96 : COLS <= 48 ? 80 : 64) : kConvGroups == 2 ? 56 : 88;
+    static constexpr int kLastRegs = ALT ? (COLS <= 32 ? 56 : COLS <= 48 ? 48 : 40) : 40;
+    static_assert(kGroups * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
                   "registers of a block");
     // Tensor-memory columns: K and V tiles (64 each), O^T (of each group), two S^T buffers.
     static constexpr int kKBufs = kN <= 64 ? 2 : 1;
@@ -106,7 +106,8 @@ struct Plan {
     static constexpr int kOffScalar = kOffRaw + kStages * kRawBytes;
     static constexpr int kSmemBytes = kOffScalar + kScalarBytes + 1024;
     static_assert(D == 64 || D == 128, "head dimension 64 or 128");
-    static_assert(COLS % 8 == 0 && COLS <= 64, "at most 64 rows in a group, in steps of 8");
+    static constexpr int kPart = ALT ? 64 : 32;             // numbers of a warp in Scalars::part
+    static_assert(COLS % 8 == 0 && COLS <= kPart, "rows of a group");
     static_assert(kOffRaw % 1024 == 0 && kStages >= 3, "raw stages");
 };
 
@@ -127,8 +128,9 @@ struct Scalars {
     Q8Keys keys;
     alignas(16) float neg_ref[128];   // -(reference) of every row (64 g + row in ALT): P = 2^(s + neg_ref)
     alignas(16) float corr[128];
-    float part[2][4][64];    // per softmax group and warp: a number for each of its rows
-    float wmax[8], wunit[8];
+    float part[512];         // per softmax warp: a number for each of its rows
+    float wmax[16], wunit[16];
+    int fail[4];             // a softmax group's failed wait
     float unit;              // largest scale of V among the split's pages: O = unit * O^T
     int flagged;             // elements of the tail rows' V that are not finite
     int64_t flagged_at[kFlagged];      // row * d + dimension
@@ -154,11 +156,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-template <int N> __device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// This warpgroup's registers a thread from NOW to N.  An increase waits for registers that the
+// others release; a decrease to more than there are is an illegal instruction.
+template <int NOW, int N> __device__ __forceinline__ void set_regs() {
+    static_assert(N >= 24 && N <= 256 && N % 8 == 0 && NOW % 8 == 0, "registers in steps of 8");
+    if constexpr (N > NOW) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    if constexpr (N < NOW) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t r;
@@ -319,19 +322,20 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             mbar_init(&sc->raw_full[i], 1);
             mbar_init(&sc->raw_free[i], 4 * L::kConvGroups);
         }
-        mbar_init(&sc->q_full, 256);
+        mbar_init(&sc->q_full, L::kSoftmaxThreads);
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
             mbar_init(&sc->k_full[u], 128);
             mbar_init(&sc->s_full[u], 1);
-            mbar_init(&sc->s_free[u], ALT ? 4 : 8);
-            mbar_init(&sc->p_full[u], ALT ? 128 : 256);
+            mbar_init(&sc->s_free[u], ALT ? 4 : 4 * L::kGroups);
+            mbar_init(&sc->p_full[u], ALT ? 128 : L::kSoftmaxThreads);
             mbar_init(&sc->v_full[u], 128);
             mbar_init(&sc->pv_done[u], 1);
         }
         mbar_init(&sc->drain, 1);
         sc->abort = 0;
         sc->flagged = 0;
+        for (int i = 0; i < 4; ++i) sc->fail[i] = 0;
         fence_mbar_init();
     }
     if (tid >= 64 && tid < 192) sc->neg_ref[tid - 64] = kNoKey;
@@ -384,7 +388,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     if (n <= 0) {
         // nothing to do
     } else if (warp >= L::kProducerWarp) {
-        regs_down<L::kLastRegs>();
+        set_regs<L::kLaunchRegs, L::kLastRegs>();
         unsigned failed = 0;                            // code of a wait that gave up
         if (warp == L::kProducerWarp) {
             // ------------------------------ producer --------------------------
@@ -499,7 +503,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         if (lane == 0) record(p.err, failed);
     } else if (warp >= L::kConvWarp) {
         // ------------------------------ converters ----------------------------
-        regs_down<L::kConvRegs>();
+        set_regs<L::kLaunchRegs, L::kConvRegs>();
         const int t = tid & 127, q4 = t >> 5;
         const bool do_k = L::kConvGroups == 1 || warp < L::kConvWarp + 4;
         const bool do_v = L::kConvGroups == 1 || !do_k;
@@ -684,7 +688,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         record(p.err, failed);
     } else {
         // ------------------------------ softmax -------------------------------
-        regs_up<L::kSoftmaxRegs>();
+        set_regs<L::kLaunchRegs, L::kSoftmaxRegs>();
         const int gr = warp >> 2, q4 = warp & 3;
         const int t = tid & 127;                        // this thread's key of every tile
         const int c0 = ALT ? 0 : gr * COLS;             // first row (column of S^T) of the group
@@ -692,6 +696,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         constexpr int kStep = ALT ? 2 : 1;              // tiles from one of the group's to its next
         const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
         const int64_t slot = ((int64_t)g * p.S + slot_idx) * p.R + r0;   // this CTA's partial rows
+        float* my_part = sc->part + warp * L::kPart;
+        const float* group_part = sc->part + 4 * gr * L::kPart;
         float* neg_ref = sc->neg_ref + (ALT ? 64 * gr : c0);
         float* corr = sc->corr + (ALT ? 64 * gr : c0);
         const uint32_t o_base = lanes + L::kTmemO + (ALT ? (uint32_t)gr * L::kNCols : (uint32_t)c0);
@@ -706,36 +712,41 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
             return __ldg(p.scales + ((int64_t)id * p.Hkv + g) * 2);
         };
-        const int page_first = page_of(2 * first_tile + half);
-        int page_next = page_of(2 * (first_tile + kStep) + half);
-        float scale_now = scale_of(page_first);
         // One pass over Q (into shared memory as it is) and over the scales of V: what the CTA's
-        // fp16 forms are relative to.
-        float unit = 0.f, q_top = 0.f;
-#pragma unroll 1
-        for (int j = tid; j < my_pages; j += 256) unit = fmaxf(unit, v_scale(p, __ldg(ids + j), g));
-#pragma unroll 4
-        for (int i = tid; i < kN * (D / 8); i += 256) {
-            const uint4 v = i < Rb * (D / 8) ? Qg[i] : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        // fp16 forms are relative to.  All loads that wait for nothing go out first.
+        constexpr int T = L::kSoftmaxThreads;
+        constexpr int kQPieces = (kN * (D / 8) + T - 1) / T;
+        const int page_unit = page_of(tid), page_first = page_of(2 * first_tile + half);
+        int page_next = page_of(2 * (first_tile + kStep) + half);
+        uint4 qv[kQPieces];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float x = fabsf(__uint_as_float(w[e] << 16)), y = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-                if (x < INFINITY) q_top = fmaxf(q_top, x);
-                if (y < INFINITY) q_top = fmaxf(q_top, y);
+        for (int e = 0; e < kQPieces; ++e)
+            qv[e] = tid + e * T < Rb * (D / 8) ? Qg[tid + e * T] : make_uint4(0, 0, 0, 0);
+        float unit = tid < my_pages ? v_scale(p, page_unit, g) : 0.f;
+        float scale_now = scale_of(page_first);
+#pragma unroll 1
+        for (int j = tid + T; j < my_pages; j += T) unit = fmaxf(unit, v_scale(p, __ldg(ids + j), g));
+        uint32_t q_bits = 0;                            // largest finite magnitude (bits order as values)
+#pragma unroll
+        for (int e = 0; e < kQPieces; ++e) {
+            const uint32_t w[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = w[j] & 0x7fffu, y = w[j] >> 16 & 0x7fffu;
+                q_bits = max(q_bits, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
             }
-            *q_address(i) = v;
         }
+        float q_top = __uint_as_float(q_bits << 16);
         unit = warp_max(unit);
         q_top = warp_max(q_top);
         if (lane == 0) {
             sc->wmax[warp] = q_top;
             sc->wunit[warp] = unit;
         }
-        asm volatile("barrier.cta.sync 3, 256;" ::: "memory");
+        asm volatile("barrier.cta.sync 5, %0;" ::"n"(T) : "memory");
         unit = q_top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+#pragma unroll 4
+        for (int i = 0; i < 4 * L::kGroups; ++i) {
             q_top = fmaxf(q_top, sc->wmax[i]);
             unit = fmaxf(unit, sc->wunit[i]);
         }
@@ -744,16 +755,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
         const int q_exp = max(min(14 - ((int)(__float_as_uint(q_top) >> 23) - 127), 100), -126);
         const float q_mul = __uint_as_float((uint32_t)(127 + q_exp) << 23);
-        if (n_page > 0) {
-#pragma unroll 2
-            for (int i = tid; i < Rb * (D / 8); i += 256) {   // this thread's own pieces
-                uint4 v = *q_address(i);
-                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = f16x2(__uint_as_float(w[e] << 16) * q_mul, __uint_as_float(w[e] & 0xffff0000u) * q_mul);
-                *q_address(i) = v;
+        for (int e = 0; e < kQPieces; ++e) {
+            if (n_page > 0) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(&qv[e]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = f16x2(__uint_as_float(w[j] << 16) * q_mul, __uint_as_float(w[j] & 0xffff0000u) * q_mul);
             }
+            if (tid + e * T < kN * (D / 8)) *q_address(tid + e * T) = qv[e];
         }
         fence_proxy_async_smem();
         mbar_arrive(&sc->q_full);
@@ -798,6 +808,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             tc_fence_after();
             float x[COLS];
             const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
+            bool quit = false;                          // a wait failed in the group
 #pragma unroll 1
             for (int pass = 0;; ++pass) {
 #pragma unroll
@@ -831,18 +842,21 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     top1 = fmax3(top1, x[c + 2], x[c + 3]);
                 }
                 const bool over = fmaxf(top0, top1) > kMaxLog2P;   // some score passed its reference by too much
+                if (fail) sc->fail[gr] = 1;
                 if (__builtin_expect(!group_any(gr, over || fail), 1)) break;
-                fail = group_any(gr, fail);             // the same answer in every warp
-                if (fail) break;
                 if (pass > 0) {
                     // scores past 2^26, whose own rounding is that coarse: hold them at the limit
 #pragma unroll
                     for (int c = 0; c < COLS; ++c) x[c] = x[c] > kMaxLog2P ? kMaxLog2P : x[c];
                     break;
                 }
+                // set before the barrier above, and again at the earliest after the ones below:
+                // the whole group reads the same
+                quit = *((volatile int*)&sc->fail[gr]) != 0;
+                if (quit) break;
                 // ---- the references of the rows that need it move; then S^T is taken again ----
                 uint64_t bits = seen;
-#pragma unroll 1
+#pragma unroll 2
                 for (int ch = 0; ch < COLS / 8; ++ch) {
                     uint32_t r[8];
                     tmem_ld8(s_addr + 8 * ch, r);
@@ -850,14 +864,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         const float m = warp_max_redux((bits & 1ull) ? __uint_as_float(r[c]) * a : -INFINITY);
-                        if (lane == 0) sc->part[gr][q4][8 * ch + c] = m;
+                        if (lane == 0) my_part[8 * ch + c] = m;
                         bits >>= 1;
                     }
                 }
                 group_sync(gr);
                 if (t < COLS) {
-                    const float m = fmaxf(fmaxf(sc->part[gr][0][t], sc->part[gr][1][t]),
-                                          fmaxf(sc->part[gr][2][t], sc->part[gr][3][t]));
+                    const float* m4 = group_part + t;
+                    const float m = fmaxf(fmaxf(m4[0], m4[L::kPart]), fmaxf(m4[2 * L::kPart], m4[3 * L::kPart]));
                     const float old = neg_ref[t];
                     float f = 1.f;
                     if (m + old > kMaxLog2P) {
@@ -883,15 +897,18 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         tmem_st8(o_addr, o);
                     }
                     tmem_wait_st();
-                }
 #pragma unroll
-                for (int c = 0; c < COLS; c += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(corr + c);
-                    l2[c / 2] = mul2(l2[c / 2], make_float2(f.x, f.y));
-                    l2[c / 2 + 1] = mul2(l2[c / 2 + 1], make_float2(f.z, f.w));
+                    for (int c = 0; c < COLS; c += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(corr + c);
+                        l2[c / 2] = mul2(l2[c / 2], make_float2(f.x, f.y));
+                        l2[c / 2 + 1] = mul2(l2[c / 2 + 1], make_float2(f.z, f.w));
+                    }
                 }
             }
-            if (fail) break;                            // the same in the whole group
+            if (quit) {
+                fail = true;
+                break;
+            }
             // S^T is in registers: the buffer is free
             tc_fence_before();
             __syncwarp();
@@ -941,21 +958,21 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll
             for (int e = 0; e < 4; ++e) { v[2 * e] = l2[c / 2 + e].x; v[2 * e + 1] = l2[c / 2 + e].y; }
             const float s = warp_sum8(v, lane);
-            if ((lane & 3) == 0) sc->part[gr][q4][c + (lane >> 2)] = s;
+            if ((lane & 3) == 0) my_part[c + (lane >> 2)] = s;
         }
         // O^T of the last products (in ALT of both groups)
         for (int i = max(n - kStep, 0); i < n; ++i)
             fail |= !wait_for<0>(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), kRoleSoftmax | kBarPv | 0xffffu, failed);
         record(p.err, failed);
-        if (barrier_any<256>(3, fail)) {                // sums and references of both groups are there
+        if (barrier_any<L::kSoftmaxThreads>(5, fail)) { // sums and references of all groups are there
             sc->abort = 1;
         } else {
             tc_fence_after();
             const int dim = D == 128 ? 32 * q4 + lane : 16 * q4 + lane;
             const bool mine = D == 128 || lane < 16;
             auto row_sum = [&](int group, int r) {
-                const float(*s)[64] = sc->part[group];
-                return (s[0][r] + s[1][r]) + (s[2][r] + s[3][r]);
+                const float* s = sc->part + 4 * group * L::kPart + r;
+                return (s[0] + s[L::kPart]) + (s[2 * L::kPart] + s[3 * L::kPart]);
             };
             if constexpr (ALT) {
                 // Weights of the two groups' parts of a row; this group writes half of the rows.
@@ -1087,8 +1104,8 @@ cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStre
     if (rows <= 32) return launch_shape<D, 32, true>(pool, p, n_rb, rows, st);
     if (rows <= 48) return launch_shape<D, 48, true>(pool, p, n_rb, rows, st);
     if (rows <= 64) return launch_shape<D, 64, true>(pool, p, n_rb, rows, st);
-    if (rows <= 96) return launch_shape<D, 48, false>(pool, p, n_rb, rows, st);
-    return launch_shape<D, 64, false>(pool, p, n_rb, rows, st);
+    if (rows <= 96) return launch_shape<D, 24, false>(pool, p, n_rb, rows, st);
+    return launch_shape<D, 32, false>(pool, p, n_rb, rows, st);
 }
 
 }  // namespace
