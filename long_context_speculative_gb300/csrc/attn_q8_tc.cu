@@ -54,7 +54,6 @@ namespace rapid {
 namespace {
 
 constexpr int kMaxRawStages = 6;
-constexpr int kConvNap = 40;           // ns between tests of the converters' and the producer's waits
 constexpr int kFlagged = 64;           // elements of V remembered for not being finite
 constexpr uint32_t kTmemCols = 512;
 
@@ -216,18 +215,34 @@ constexpr uint32_t idesc(bool bf16, bool b_mn, int n) {
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// Waits, bounded by a number of tests (a test takes 20 clocks or more, so 2^25 of them are the
-// better part of a second; legitimate waits last microseconds).  A role keeps the code of the
-// wait that gave up and records it once, at its end: a wait has to be a few instructions,
-// because the roles' loops share a small instruction cache and a launch fetches them anew.
-template <int NAP>
+__device__ __forceinline__ uint32_t timer_low() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+// Test of a phase that the hardware suspends for a while (a system-dependent time, after which
+// it is false): a waiting warp takes few issue slots from the others.
+__device__ __forceinline__ bool try_suspended(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits, bounded in time by the low word of the nanosecond clock (2^30 of them, about a second;
+// legitimate waits last microseconds).  A role keeps the code of the wait that gave up and
+// records it once, at its end: a wait has to be a few instructions, because the roles' loops
+// share a small instruction cache and a launch fetches them anew.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned code, unsigned& failed) {
-    constexpr unsigned kTests = NAP > 0 ? 1u << 23 : 1u << 25;
-#pragma unroll 1
-    for (unsigned i = 0; i < kTests; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (NAP > 0) __nanosleep(NAP);
-    }
+    if (try_suspended(bar, parity)) return true;
+    const uint32_t t0 = timer_low();
+    do {
+        if (try_suspended(bar, parity)) return true;
+    } while (timer_low() - t0 < 1u << 30);
     failed = code;
     return false;
 }
@@ -254,16 +269,35 @@ __device__ __forceinline__ uint32_t elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
     return r;
 }
-// mma_bf16_ta and mma_commit, issued by the lane with `leader` set.
-__device__ __forceinline__ void mma_ta_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                          uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
-        : "memory");
+// STEPS products of 16 in a row, issued by the lane with `leader` set: A in tensor memory, 8
+// columns a step; B's descriptor low word grows by B_STEP a step, by B_JUMP more after four
+// steps.  The first one starts the sum where `accumulate` is 0.
+template <int STEPS, int B_STEP, int B_JUMP>
+__device__ __forceinline__ void mma_chain_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                             uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+    for (int k = 0; k < STEPS; k += 4) {
+        asm volatile(
+            "{\n\t.reg .pred p, q, t;\n\t"
+            ".reg .b64 b1, b2, b3;\n\t"
+            ".reg .b32 a1, a2, a3;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "setp.eq.b32 t, 0, 0;\n\t"
+            "add.u32 a1, %1, 8;\n\t"
+            "add.u32 a2, %1, 16;\n\t"
+            "add.u32 a3, %1, 24;\n\t"
+            "add.u64 b1, %2, %6;\n\t"
+            "add.u64 b2, %2, %7;\n\t"
+            "add.u64 b3, %2, %8;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+            "r"(a_tmem + (uint32_t)(8 * k)), "l"(b + (uint64_t)(k * B_STEP + (k >> 2) * B_JUMP)), "r"(idesc),
+            "r"(k > 0 ? 1u : accumulate), "r"(leader), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+            : "memory");
+    }
 }
 __device__ __forceinline__ void mma_commit_if(uint32_t leader, uint64_t* bar) {
     asm volatile(
@@ -409,7 +443,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const int id1 = __shfl_sync(0xffffffffu, id, (2 * i + 1) & 31);
                 if (lane == 0) {
                     if (i >= kStages)
-                        ok = wait_for<kConvNap>(&sc->raw_free[st], lap ^ 1u,
+                        ok = wait_for(&sc->raw_free[st], lap ^ 1u,
                                                 kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff), failed);
                     if (*((volatile int*)&sc->abort)) ok = false;
                     if (ok) {
@@ -456,7 +490,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
             const uint32_t leader = elect_one();
             auto wait = [&](uint64_t* bar, uint32_t par, unsigned code) {
-                return __all_sync(0xffffffffu, wait_for<0>(bar, par, kRoleMma | code, failed)) != 0;
+                return __all_sync(0xffffffffu, wait_for(bar, par, kRoleMma | code, failed)) != 0;
             };
             auto scores = [&](int j) -> bool {
                 if (!wait(&sc->k_full[j % KB], (uint32_t)((j / KB) & 1), kBarK | (unsigned)(j & 0xffff))) return false;
@@ -466,10 +500,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const uint32_t dS = tm + L::kTmemS + (uint32_t)(j & 1) * L::kNCols;
                 const uint32_t aK = tm + L::kTmemK + (uint32_t)(64 * (j % KB));
                 const uint32_t id = j < page_tiles ? kS16 : kSb;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_ta_if(leader, dS, aK + (uint32_t)(8 * k),
-                              qd + (uint64_t)(((k >> 2) * L::kQBlock + (k & 3) * 32) >> 4), id, k > 0 ? 1u : 0u);
+                mma_chain_if<D / 16, 2, L::kQBlock / 16 - 8>(leader, dS, aK, qd, id, 0u);
                 mma_commit_if(leader, &sc->s_full[j & 1]);
                 return true;
             };
@@ -490,15 +521,12 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const uint64_t bP = pd + (uint64_t)(pb * (L::kPBuf >> 4));
                 const uint32_t id = i < page_tiles ? kO16 : kOb;
                 const uint32_t add = i < (ALT ? 2 : 1) ? 0u : 1u;   // the group's first product starts O^T
-#pragma unroll
-                for (int k = 0; k < kQ8Tile / 16; ++k)
-                    mma_ta_if(leader, dO, aV + (uint32_t)(8 * k), bP + (uint64_t)(k * (2048 >> 4)), id,
-                              k > 0 ? 1u : add);
+                mma_chain_if<kQ8Tile / 16, 128, 0>(leader, dO, aV, bP, id, add);
                 mma_commit_if(leader, &sc->pv_done[i & 1]);
             }
             if (!ok) sc->abort = 1;
             mma_commit_if(leader, &sc->drain);
-            wait_for<0>(&sc->drain, 0, kRoleMma | kBarDrain, failed);
+            wait_for(&sc->drain, 0, kRoleMma | kBarDrain, failed);
         }
         if (lane == 0) record(p.err, failed);
     } else if (warp >= L::kConvWarp) {
@@ -542,7 +570,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         if (do_v && n_page > 0) {
             const int2 id0 = page_ids(0);
             id_next = page_ids(1);
-            ok = wait_for<kConvNap>(&sc->q_full, 0, kRoleConvert | kBarQ, failed);   // the unit is there
+            ok = wait_for(&sc->q_full, 0, kRoleConvert | kBarQ, failed);   // the unit is there
             inv_unit = 1.f / sc->unit;
             unit_now = v_units(0, id0);
         }
@@ -554,14 +582,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
             const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
             if (paged)
-                ok = wait_for<kConvNap>(&sc->raw_full[st], lap, code | kBarRawFull, failed);
+                ok = wait_for(&sc->raw_full[st], lap, code | kBarRawFull, failed);
             if (do_k) {
                 // S of tile i - KB has read this K buffer
                 if (ok && i >= KB)
-                    ok = wait_for<kConvNap>(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), code | kBarS, failed);
+                    ok = wait_for(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), code | kBarS, failed);
                 if (ok && !paged && i == n_page && i > 0) {
                     // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
-                    ok = wait_for<kConvNap>(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), code | kBarS, failed);
+                    ok = wait_for(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), code | kBarS, failed);
                     if (ok) {
 #pragma unroll 1
                         for (int x = t; x < kN * (D / 8); x += 128)
@@ -617,7 +645,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 // the product of tile i - VB has read this V buffer
                 if (ok && i >= VB)
-                    ok = wait_for<kConvNap>(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), code | kBarPv, failed);
+                    ok = wait_for(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), code | kBarPv, failed);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -804,7 +832,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 a = p.scale_log2;
             }
-            fail |= !wait_for<0>(&sc->s_full[u], (uint32_t)((i >> 1) & 1), code | kBarS, failed);
+            fail |= !wait_for(&sc->s_full[u], (uint32_t)((i >> 1) & 1), code | kBarS, failed);
             tc_fence_after();
             float x[COLS];
             const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
@@ -882,7 +910,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 group_sync(gr);
                 if (prev >= 0) {
-                    fail |= !wait_for<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
+                    fail |= !wait_for(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -933,7 +961,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             }
             // P's buffer is free once the previous product has read it
             if (prev >= 0)
-                fail |= !wait_for<0>(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
+                fail |= !wait_for(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
             if (!fail) {
                 uint8_t* pt = smem + L::kOffP + (ALT ? gr * L::kPBuf : 0) + t * 128;
 #pragma unroll
@@ -962,7 +990,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         }
         // O^T of the last products (in ALT of both groups)
         for (int i = max(n - kStep, 0); i < n; ++i)
-            fail |= !wait_for<0>(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), kRoleSoftmax | kBarPv | 0xffffu, failed);
+            fail |= !wait_for(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), kRoleSoftmax | kBarPv | 0xffffu, failed);
         record(p.err, failed);
         if (barrier_any<L::kSoftmaxThreads>(5, fail)) { // sums and references of all groups are there
             sc->abort = 1;
