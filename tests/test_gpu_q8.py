@@ -304,6 +304,25 @@ def test_attn_large_batch():
     _run_attn(c, _queries(B, 2, 2, 64, BF16, seed=9))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G,n", [(1, 7), (1, 20), (1, 43), (1, 60), (2, 44), (2, 60), (3, 50)])
+def test_attn_many_tiles_to_a_block(d, G, n):
+    # so many KV heads that every block takes a whole sequence: 13 to 15 tiles one after the
+    # other at every number of rows a block can have, an odd number of pages at the end
+    Hkv = 152
+    c = _q8.cache(1, 2, d, BF16, [25], [150], n, seed=G + n, scale_spread=2)
+    c["scales"][c["page_table"][0, 20].long(), :, 0] *= 64   # a late block whose keys outweigh the rest
+    Q = _queries(1, 2 * G, n, d, BF16, seed=n)
+    ref = _q8.attn(Q, c["K"], c["V"], c["pages"], c["scales"], c["page_table"], c["sealed_len"],
+                   c["tail_len"])
+    rep = Hkv // 2
+    wide = dict(c, K=c["K"].repeat(1, rep, 1, 1), V=c["V"].repeat(1, rep, 1, 1),
+                pages=c["pages"].view(torch.uint8).repeat(1, rep, 1, 1, 1).view(torch.float8_e4m3fn),
+                scales=c["scales"].repeat(1, rep, 1).contiguous())
+    ref = [x.repeat(1, rep, *([1] * (x.dim() - 2))) for x in ref]
+    _run_attn(wide, Q.repeat(1, rep, 1, 1), ref=ref)
+
+
 def test_attn_long_history():
     c = _q8.cache(1, 1, 128, BF16, [300], [37], 11, seed=10, scale_spread=2)
     _run_attn(c, _queries(1, 4, 11, 128, BF16, seed=11))
