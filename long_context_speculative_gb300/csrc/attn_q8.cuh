@@ -16,7 +16,10 @@
 
 namespace rapid {
 
-constexpr int kQ8Tile = 128;                 // keys of a tile: two pages, or 128 tail rows
+// Keys of a tile, the unit of the split plan: two pages or 128 tail rows on tensor cores, half a
+// page or 32 tail rows on CUDA cores.
+constexpr int kQ8Tile = 128;
+constexpr int kQ8SimtTile = 32;
 
 struct AttnQ8Params {
     const void* Q;               // [B, Hq, n_q, d]
@@ -52,6 +55,7 @@ struct Q8Keys {
     int page_tiles, tiles;
 };
 
+template <int TILE>
 __device__ __forceinline__ Q8Keys q8_keys(const AttnQ8Params& p, int b) {
     Q8Keys k;
     int pages = p.sealed_len[b] / kPageTokens;
@@ -61,8 +65,9 @@ __device__ __forceinline__ Q8Keys q8_keys(const AttnQ8Params& p, int b) {
     if (tail < 0) tail = 0;
     if (tail > p.cap - p.n_q) tail = p.cap - p.n_q;
     k.tail = tail;
-    k.page_tiles = (k.pages + 1) / 2;
-    k.tiles = k.page_tiles + (int)((tail + p.n_q + kQ8Tile - 1) / kQ8Tile);
+    k.page_tiles = TILE >= kPageTokens ? (k.pages + TILE / kPageTokens - 1) / (TILE / kPageTokens)
+                                       : k.pages * (kPageTokens / TILE);
+    k.tiles = k.page_tiles + (int)((tail + p.n_q + TILE - 1) / TILE);
     return k;
 }
 
@@ -90,10 +95,11 @@ __device__ __forceinline__ int warp_sum_int(int v) {
 // lengths: the smallest number of tiles per split whose splits fit into the S slots, so
 // that short and long sequences of a ragged batch finish together.  Lanes take sequences
 // lane, lane + 32, ..., so a large batch costs B / 32 reads a round.
+template <int TILE>
 static __device__ __noinline__ Q8Split q8_split_of_many(const AttnQ8Params& p, int c) {
     const int lane = threadIdx.x & 31;
-    const int mine = lane < p.B ? q8_keys(p, lane).tiles : 0;   // of the first 32 sequences
-    auto tiles_of = [&](int b) { return b == lane ? mine : q8_keys(p, b).tiles; };
+    const int mine = lane < p.B ? q8_keys<TILE>(p, lane).tiles : 0;   // of the first 32 sequences
+    auto tiles_of = [&](int b) { return b == lane ? mine : q8_keys<TILE>(p, b).tiles; };
     int total = 0, longest = 1;
 #pragma unroll 1
     for (int b = lane; b < p.B; b += 32) {
@@ -139,10 +145,11 @@ static __device__ __noinline__ Q8Split q8_split_of_many(const AttnQ8Params& p, i
 }
 
 // The same with the sequence's lengths; one sequence needs no search.
+template <int TILE>
 __device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c, Q8Keys* keys) {
     Q8Split sp{0, c, 0, 0};
-    if (p.B > 1) sp = q8_split_of_many(p, c);
-    *keys = q8_keys(p, sp.b < 0 ? 0 : sp.b);
+    if (p.B > 1) sp = q8_split_of_many<TILE>(p, c);
+    *keys = q8_keys<TILE>(p, sp.b < 0 ? 0 : sp.b);
     if (p.B == 1) {
         const int budget = (keys->tiles + p.S - 1) / p.S;
         sp.count = (keys->tiles + budget - 1) / budget;

@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kSimtThreads = 128;                   // 4 warps
 constexpr int kRowsPerWarp = kQ8SimtRows / 4;
-constexpr int kKeys = 32;                           // keys of a shared-memory step, one per lane
+constexpr int kKeys = kQ8SimtTile;                  // keys of a tile, one per lane
 
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     uint32_t h;
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     const int g = blockIdx.y;
     if (warp == 0) {
         Q8Keys k;
-        const Q8Split sp = q8_split_of(p, slot_idx, &k);
+        const Q8Split sp = q8_split_of<kQ8SimtTile>(p, slot_idx, &k);
         if (lane == 0) {
             s_split = sp;
             s_keys = k;
@@ -103,15 +103,13 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     const float* Vh = static_cast<const float*>(p.V) + bg * p.cap * D;
     const int64_t tail_keys = keys.tail + p.n_q;
 
-    for (int64_t step = (int64_t)t_begin * (kQ8Tile / kKeys); step < (int64_t)t_end * (kQ8Tile / kKeys); ++step) {
+    for (int tile = t_begin; tile < t_end; ++tile) {
         // key of lane 0: a page key, or a tail row once the page tiles are through
-        const bool paged = step < (int64_t)keys.page_tiles * (kQ8Tile / kKeys);
-        const int64_t k0 = paged ? step * kKeys
-                                 : step * kKeys - (int64_t)keys.page_tiles * kQ8Tile;
+        const bool paged = tile < keys.page_tiles;
+        const int64_t k0 = (int64_t)(paged ? tile : tile - keys.page_tiles) * kKeys;
         const int64_t k_end = paged ? (int64_t)keys.pages * kPageTokens : tail_keys;
-        if (k0 >= k_end) continue;             // CTA-uniform
         const int nk = (int)(k_end - k0 < kKeys ? k_end - k0 : kKeys);
-        int64_t head = 0;                      // (page, head): one page holds the whole step
+        int64_t head = 0;                      // (page, head): one page holds the whole tile
         if (paged) head = (int64_t)q8_page(p, b, (int)(k0 / kPageTokens)) * p.Hkv + g;
         __syncthreads();
         for (int idx = threadIdx.x; idx < kKeys * (D / 16); idx += kSimtThreads) {
@@ -182,6 +180,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
             for (int c = 0; c < NC; ++c) vv[c] = sV[j * D + lane + 32 * c];
 #pragma unroll
             for (int i = 0; i < kRowsPerWarp; ++i) {
+                if (warp + 4 * i >= nrows) break;
                 const float pj = __shfl_sync(0xffffffffu, sc[i], j);
                 if (pj == 0.f) continue;       // a hidden row's V may hold anything
 #pragma unroll

@@ -383,7 +383,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     griddep_wait();
     if (warp == 0) {
         Q8Keys k;
-        const Q8Split sp0 = q8_split_of(p, slot_idx, &k);
+        const Q8Split sp0 = q8_split_of<kQ8Tile>(p, slot_idx, &k);
         if (lane == 0) {
             sc->split = sp0;
             sc->keys = k;
