@@ -33,7 +33,7 @@
 //               turn, each with its own references and O^T, joined at the end; above, four
 //               groups take every tile and a quarter of its rows.  Either way the chain of a
 //               tile (load S, compare, exponentials, store P) overlaps another's
-//   converters  4 for K and 4 for V (4 for both with more than 96 rows)
+//   converters  4 for K and 4 for V
 //   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
 //               into a ring of raw stages by TMA
 //   issuer      1: the MMAs, in the order in which their inputs become ready
@@ -69,18 +69,17 @@ template <int D, int COLS, bool ALT>
 struct Plan {
     static constexpr int kGroups = ALT ? 2 : 4;
     static constexpr int kN = ALT ? COLS : 4 * COLS;        // N of the products
-    static constexpr int kConvGroups = kN <= 96 ? 2 : 1;
     static constexpr int kConvWarp = 4 * kGroups;
     static constexpr int kSoftmaxThreads = 128 * kGroups;
-    static constexpr int kProducerWarp = kConvWarp + 4 * kConvGroups;
+    static constexpr int kProducerWarp = kConvWarp + 8;              // 4 for K, 4 for V
     static constexpr int kMmaWarp = kProducerWarp + 3;
     static constexpr int kThreads = 32 * (kProducerWarp + 4);
     // A block starts with kLaunchRegs registers a thread; its warpgroups share them out anew.
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
     static constexpr int kSoftmaxRegs = ALT ? (COLS <= 32 ? 112 : COLS <= 48 ? 136 : 152) : 88;
-    static constexpr int kConvRegs = ALT ? (COLS <= 32 ? 96 : COLS <= 48 ? 80 : 64) : kConvGroups == 2 ? 56 : 88;
+    static constexpr int kConvRegs = ALT ? (COLS <= 32 ? 96 : COLS <= 48 ? 80 : 64) : 56;
     static constexpr int kLastRegs = ALT ? (COLS <= 32 ? 56 : COLS <= 48 ? 48 : 40) : 40;
-    static_assert(kGroups * kSoftmaxRegs + kConvGroups * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
+    static_assert(kGroups * kSoftmaxRegs + 2 * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
                   "registers of a block");
     // Tensor-memory columns: K and V tiles (64 each), O^T (of each group), two S^T buffers.
     static constexpr int kKBufs = kN <= 64 ? 2 : 1;
@@ -354,7 +353,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll 1
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sc->raw_full[i], 1);
-            mbar_init(&sc->raw_free[i], 4 * L::kConvGroups);
+            mbar_init(&sc->raw_free[i], 8);
         }
         mbar_init(&sc->q_full, L::kSoftmaxThreads);
 #pragma unroll 1
@@ -477,9 +476,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             // The whole warp runs the loop, so that addresses and descriptors stay in uniform
             // registers, and one elected lane issues.  The order is fixed, S of tile i + 2
             // (its buffer is free once S of tile i is loaded) before the product of tile i:
-            // that is the order in which the inputs come.  Converters that do K and V in turn
-            // reach K of tile i + 2 only after the product of tile i, so there it is S of i + 1.
-            constexpr int kAhead = L::kConvGroups == 1 ? 1 : 2;
+            // that is the order in which the inputs come.
             constexpr uint32_t kS16 = idesc(false, false, kN), kSb = idesc(true, false, kN);
             constexpr uint32_t kO16 = idesc(false, true, kN), kOb = idesc(true, true, kN);
             const uint32_t base = smem_u32(smem);
@@ -506,10 +503,10 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             };
             bool ok = wait(&sc->q_full, 0, kBarQ);
             ok = ok && scores(0);
-            if (kAhead > 1 && tiles > 1) ok = ok && scores(1);
+            if (tiles > 1) ok = ok && scores(1);
 #pragma unroll 1
             for (int i = 0; ok && i < tiles; ++i) {
-                if (i + kAhead < tiles) ok = scores(i + kAhead);
+                if (i + 2 < tiles) ok = scores(i + 2);
                 // ALT: group i & 1 and its tile i >> 1
                 const int pb = ALT ? i & 1 : 0;
                 ok = ok && wait(&sc->p_full[pb], (uint32_t)((ALT ? i >> 1 : i) & 1), kBarP | (unsigned)(i & 0xffff));
@@ -533,8 +530,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         // ------------------------------ converters ----------------------------
         set_regs<L::kLaunchRegs, L::kConvRegs>();
         const int t = tid & 127, q4 = t >> 5;
-        const bool do_k = L::kConvGroups == 1 || warp < L::kConvWarp + 4;
-        const bool do_v = L::kConvGroups == 1 || !do_k;
+        const bool do_k = warp < L::kConvWarp + 4, do_v = !do_k;
         const uint32_t lanes = tmem + ((uint32_t)(q4 * 32) << 16);
         const __nv_bfloat16* Kh = static_cast<const __nv_bfloat16*>(p.K) + bg * p.cap * D;
         const __nv_bfloat16* Vh = static_cast<const __nv_bfloat16*>(p.V) + bg * p.cap * D;
