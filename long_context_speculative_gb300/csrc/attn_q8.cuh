@@ -85,12 +85,6 @@ struct Q8Split {
     int first;           // slot of the sequence's split 0
 };
 
-__device__ __forceinline__ int warp_sum_int(int v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 // The (sequence, split) of slot c, worked out by one whole warp from the device-side
 // lengths: the smallest number of tiles per split whose splits fit into the S slots, so
 // that short and long sequences of a ragged batch finish together.  Lanes take sequences
@@ -107,18 +101,23 @@ static __device__ __noinline__ Q8Split q8_split_of_many(const AttnQ8Params& p, i
         total += t;
         longest = t > longest ? t : longest;
     }
-    total = warp_sum_int(total);
+    total = __reduce_add_sync(0xffffffffu, total);
     longest = __reduce_max_sync(0xffffffffu, longest);
     int lo = (total + p.S - 1) / p.S;
     if (lo < 1) lo = 1;
+    // sum of ceil(t / m) <= (total - B) / m + B, so this many tiles are enough
     int hi = longest > lo ? longest : lo;
+    if (p.S > p.B) {
+        const int enough = (total - p.B + p.S - p.B - 1) / (p.S - p.B);
+        hi = enough < lo ? lo : enough < hi ? enough : hi;
+    }
 #pragma unroll 1
     while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
         int used = 0;
 #pragma unroll 1
         for (int b = lane; b < p.B; b += 32) used += (tiles_of(b) + mid - 1) / mid;
-        used = warp_sum_int(used);
+        used = __reduce_add_sync(0xffffffffu, used);
         if (used <= p.S) hi = mid; else lo = mid + 1;
     }
     int first = 0;

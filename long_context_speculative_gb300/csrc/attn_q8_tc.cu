@@ -830,40 +830,36 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             }
             fail |= !wait_for(&sc->s_full[u], (uint32_t)((i >> 1) & 1), code | kBarS, failed);
             tc_fence_after();
-            float x[COLS];
+            float2 x[COLS / 2];
             const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
             bool quit = false;                          // a wait failed in the group
 #pragma unroll 1
             for (int pass = 0;; ++pass) {
+                uint32_t r[COLS];
 #pragma unroll
-                for (int ch = 0; ch < COLS / 8; ++ch) {
-                    uint32_t r[8];
-                    tmem_ld8(s_addr + 8 * ch, r);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) x[8 * ch + c] = __uint_as_float(r[c]);
-                }
+                for (int ch = 0; ch < COLS; ch += 8) tmem_ld8(s_addr + ch, reinterpret_cast<uint32_t(&)[8]>(r[ch]));
                 tmem_wait_ld();
+                const float2 aa = make_float2(a, a);
 #pragma unroll
                 for (int c = 0; c < COLS; c += 4) {
                     const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
-                    const float2 aa = make_float2(a, a);
-                    const float2 y0 = fma2(make_float2(x[c], x[c + 1]), aa, make_float2(nr.x, nr.y));
-                    const float2 y1 = fma2(make_float2(x[c + 2], x[c + 3]), aa, make_float2(nr.z, nr.w));
-                    x[c] = y0.x; x[c + 1] = y0.y; x[c + 2] = y1.x; x[c + 3] = y1.y;
+                    x[c / 2] = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), aa, make_float2(nr.x, nr.y));
+                    x[c / 2 + 1] = fma2(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), aa, make_float2(nr.z, nr.w));
                 }
                 if (__builtin_expect(seen != ~0ull, 0)) {
                     uint64_t bits = seen;
 #pragma unroll
-                    for (int c = 0; c < COLS; ++c) {
-                        if (!(bits & 1ull)) x[c] = -INFINITY;
-                        bits >>= 1;
+                    for (int c = 0; c < COLS / 2; ++c) {
+                        if (!(bits & 1ull)) x[c].x = -INFINITY;
+                        if (!(bits & 2ull)) x[c].y = -INFINITY;
+                        bits >>= 2;
                     }
                 }
                 float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < COLS; c += 4) {
-                    top0 = fmax3(top0, x[c], x[c + 1]);
-                    top1 = fmax3(top1, x[c + 2], x[c + 3]);
+                for (int c = 0; c < COLS / 2; c += 2) {
+                    top0 = fmax3(top0, x[c].x, x[c].y);
+                    top1 = fmax3(top1, x[c + 1].x, x[c + 1].y);
                 }
                 const bool over = fmaxf(top0, top1) > kMaxLog2P;   // some score passed its reference by too much
                 if (fail) sc->fail[gr] = 1;
@@ -871,7 +867,10 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 if (pass > 0) {
                     // scores past 2^26, whose own rounding is that coarse: hold them at the limit
 #pragma unroll
-                    for (int c = 0; c < COLS; ++c) x[c] = x[c] > kMaxLog2P ? kMaxLog2P : x[c];
+                    for (int c = 0; c < COLS / 2; ++c) {
+                        x[c].x = x[c].x > kMaxLog2P ? kMaxLog2P : x[c].x;
+                        x[c].y = x[c].y > kMaxLog2P ? kMaxLog2P : x[c].y;
+                    }
                     break;
                 }
                 // set before the barrier above, and again at the earliest after the ones below:
@@ -941,7 +940,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (__builtin_expect(paged, 1)) {
 #pragma unroll
                 for (int c = 0; c < COLS / 2; ++c) {
-                    const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
+                    const float2 e = make_float2(ex2(x[c].x), ex2(x[c].y));
                     l2[c] = add2(l2[c], e);
                     pk[c] = f16x2(e.x, e.y);
                 }
@@ -949,7 +948,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const float2 vm = make_float2(1.f / unit, 1.f / unit);   // V as it is: P takes the unit
 #pragma unroll
                 for (int c = 0; c < COLS / 2; ++c) {
-                    const float2 e = make_float2(ex2(x[2 * c]), ex2(x[2 * c + 1]));
+                    const float2 e = make_float2(ex2(x[c].x), ex2(x[c].y));
                     l2[c] = add2(l2[c], e);
                     const float2 w = mul2(e, vm);
                     pk[c] = bf16x2(w.x, w.y);

@@ -323,6 +323,20 @@ def test_attn_many_tiles_to_a_block(d, G, n):
     _run_attn(wide, Q.repeat(1, rep, 1, 1), ref=ref)
 
 
+@pytest.mark.parametrize("B,Hkv", [(20, 8), (38, 8), (41, 16)])
+def test_attn_more_sequences_than_fit_on_the_machine_at_once(B, Hkv):
+    # more blocks than SMs even with one to a sequence; several splits of some, none of others
+    blocks = [(5 * b) % 13 for b in range(B)]
+    c = _q8.cache(B, Hkv, 64, BF16, blocks, [(7 * b) % 60 for b in range(B)], 1, seed=40)
+    _run_attn(c, _queries(B, 2 * Hkv, 1, 64, BF16, seed=41))
+
+
+def test_attn_more_row_blocks_than_sms():
+    # one sequence whose heads and blocks of rows alone are more than the SMs
+    c = _q8.cache(1, 40, 64, BF16, [9], [33], 64, seed=42)
+    _run_attn(c, _queries(1, 320, 64, 64, BF16, seed=43))
+
+
 def test_attn_long_history():
     c = _q8.cache(1, 1, 128, BF16, [300], [37], 11, seed=10, scale_spread=2)
     _run_attn(c, _queries(1, 4, 11, 128, BF16, seed=11))
