@@ -219,16 +219,42 @@ __device__ __forceinline__ uint32_t timer_low() {
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     return t;
 }
+// Shared addresses of the loops, as numbers that the compiler does not see through: it would
+// otherwise work an address out again from the CTA's window at every use (four instructions
+// and a special register: 14 such reads for a tile and softmax warp).
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+    asm volatile("mov.b32 %0, %0;" : "+r"(x));
+    return x;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_u4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
 // Test of a phase that the hardware suspends for a while (a system-dependent time, after which
 // it is false): a waiting warp takes few issue slots from the others.
-__device__ __forceinline__ bool try_suspended(uint64_t* bar, uint32_t parity) {
+__device__ __forceinline__ bool try_suspended(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
@@ -236,7 +262,7 @@ __device__ __forceinline__ bool try_suspended(uint64_t* bar, uint32_t parity) {
 // legitimate waits last microseconds).  A role keeps the code of the wait that gave up and
 // records it once, at its end: a wait has to be a few instructions, because the roles' loops
 // share a small instruction cache and a launch fetches them anew.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, unsigned code, unsigned& failed) {
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, unsigned code, unsigned& failed) {
     if (try_suspended(bar, parity)) return true;
     const uint32_t t0 = timer_low();
     do {
@@ -298,12 +324,12 @@ __device__ __forceinline__ void mma_chain_if(uint32_t leader, uint32_t d_tmem, u
             : "memory");
     }
 }
-__device__ __forceinline__ void mma_commit_if(uint32_t leader, uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_if(uint32_t leader, uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
         "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-            smem_u32(bar)), "r"(leader)
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
         : "memory");
 }
 
@@ -418,6 +444,9 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                                         (((j & 7) ^ (r & 7)) << 4));
     };
 
+    const uint32_t sb = opaque(smem_u32(sc));
+    auto at = [&](size_t offset, int i = 0) -> uint32_t { return sb + (uint32_t)offset + 8u * (uint32_t)i; };
+
     if (n <= 0) {
         // nothing to do
     } else if (warp >= L::kProducerWarp) {
@@ -442,7 +471,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const int id1 = __shfl_sync(0xffffffffu, id, (2 * i + 1) & 31);
                 if (lane == 0) {
                     if (i >= kStages)
-                        ok = wait_for(&sc->raw_free[st], lap ^ 1u,
+                        ok = wait_for(at(offsetof(Scalars, raw_free), st), lap ^ 1u,
                                                 kRoleProducer | kBarRawFree | (unsigned)(i & 0xffff), failed);
                     if (*((volatile int*)&sc->abort)) ok = false;
                     if (ok) {
@@ -486,22 +515,22 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
             const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
             const uint32_t leader = elect_one();
-            auto wait = [&](uint64_t* bar, uint32_t par, unsigned code) {
+            auto wait = [&](uint32_t bar, uint32_t par, unsigned code) {
                 return __all_sync(0xffffffffu, wait_for(bar, par, kRoleMma | code, failed)) != 0;
             };
             auto scores = [&](int j) -> bool {
-                if (!wait(&sc->k_full[j % KB], (uint32_t)((j / KB) & 1), kBarK | (unsigned)(j & 0xffff))) return false;
-                if (j >= 2 && !wait(&sc->s_free[j & 1], (uint32_t)(((j >> 1) - 1) & 1), kBarS | (unsigned)(j & 0xffff)))
+                if (!wait(at(offsetof(Scalars, k_full), j % KB), (uint32_t)((j / KB) & 1), kBarK | (unsigned)(j & 0xffff))) return false;
+                if (j >= 2 && !wait(at(offsetof(Scalars, s_free), j & 1), (uint32_t)(((j >> 1) - 1) & 1), kBarS | (unsigned)(j & 0xffff)))
                     return false;
                 tc_fence_after();
                 const uint32_t dS = tm + L::kTmemS + (uint32_t)(j & 1) * L::kNCols;
                 const uint32_t aK = tm + L::kTmemK + (uint32_t)(64 * (j % KB));
                 const uint32_t id = j < page_tiles ? kS16 : kSb;
                 mma_chain_if<D / 16, 2, L::kQBlock / 16 - 8>(leader, dS, aK, qd, id, 0u);
-                mma_commit_if(leader, &sc->s_full[j & 1]);
+                mma_commit_if(leader, at(offsetof(Scalars, s_full), j & 1));
                 return true;
             };
-            bool ok = wait(&sc->q_full, 0, kBarQ);
+            bool ok = wait(at(offsetof(Scalars, q_full)), 0, kBarQ);
             ok = ok && scores(0);
             if (tiles > 1) ok = ok && scores(1);
 #pragma unroll 1
@@ -509,8 +538,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 if (i + 2 < tiles) ok = scores(i + 2);
                 // ALT: group i & 1 and its tile i >> 1
                 const int pb = ALT ? i & 1 : 0;
-                ok = ok && wait(&sc->p_full[pb], (uint32_t)((ALT ? i >> 1 : i) & 1), kBarP | (unsigned)(i & 0xffff));
-                ok = ok && wait(&sc->v_full[i % VB], (uint32_t)((i / VB) & 1), kBarV | (unsigned)(i & 0xffff));
+                ok = ok && wait(at(offsetof(Scalars, p_full), pb), (uint32_t)((ALT ? i >> 1 : i) & 1), kBarP | (unsigned)(i & 0xffff));
+                ok = ok && wait(at(offsetof(Scalars, v_full), i % VB), (uint32_t)((i / VB) & 1), kBarV | (unsigned)(i & 0xffff));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t dO = tm + L::kTmemO + (uint32_t)pb * L::kNCols;
@@ -519,11 +548,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const uint32_t id = i < page_tiles ? kO16 : kOb;
                 const uint32_t add = i < (ALT ? 2 : 1) ? 0u : 1u;   // the group's first product starts O^T
                 mma_chain_if<kQ8Tile / 16, 128, 0>(leader, dO, aV, bP, id, add);
-                mma_commit_if(leader, &sc->pv_done[i & 1]);
+                mma_commit_if(leader, at(offsetof(Scalars, pv_done), i & 1));
             }
             if (!ok) sc->abort = 1;
-            mma_commit_if(leader, &sc->drain);
-            wait_for(&sc->drain, 0, kRoleMma | kBarDrain, failed);
+            mma_commit_if(leader, at(offsetof(Scalars, drain)));
+            wait_for(at(offsetof(Scalars, drain)), 0, kRoleMma | kBarDrain, failed);
         }
         if (lane == 0) record(p.err, failed);
     } else if (warp >= L::kConvWarp) {
@@ -537,14 +566,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         // K codes: thread t's key is row t % 64 of page t / 64.  A line of 128 bytes holds
         // 128 / d keys.
         const int k_line = D == 128 ? t & 63 : (t & 63) >> 1;
-        const uint8_t* k_src = smem + L::kOffRaw + (t >> 6) * L::kPageBytes + k_line * 128;
         const int k_piece = D == 128 ? 0 : 4 * (t & 1);
+        const uint32_t k_src = opaque(smem_u32(smem + L::kOffRaw + (t >> 6) * L::kPageBytes + k_line * 128 +
+                                               ((k_piece ^ (k_line & 7)) << 4)));
         // V codes: a transposing load takes 32 keys x 16 dimensions, lane l giving the address
         // of key l's 16 bytes; lane l then holds dimensions l / 4 and l / 4 + 8, keys
         // 4 (l % 4) .. + 3 of each half, which as fp16 pairs are the 16x256b tensor-memory layout
         const int v_line = D == 128 ? lane : lane >> 1;               // line of the load's key
         const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
-        const uint32_t v_src = smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128);
+        const uint32_t v_src = opaque(smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128));
         // page ids of the split, and the scales of V of a tile's two pages as fp16 pairs relative
         // to the largest of the split (the unit of O^T), fetched ahead like the softmax warps'
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
@@ -566,7 +596,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         if (do_v && n_page > 0) {
             const int2 id0 = page_ids(0);
             id_next = page_ids(1);
-            ok = wait_for(&sc->q_full, 0, kRoleConvert | kBarQ, failed);   // the unit is there
+            ok = wait_for(at(offsetof(Scalars, q_full)), 0, kRoleConvert | kBarQ, failed);   // the unit is there
             inv_unit = 1.f / sc->unit;
             unit_now = v_units(0, id0);
         }
@@ -578,14 +608,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
             const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
             if (paged)
-                ok = wait_for(&sc->raw_full[st], lap, code | kBarRawFull, failed);
+                ok = wait_for(at(offsetof(Scalars, raw_full), st), lap, code | kBarRawFull, failed);
             if (do_k) {
                 // S of tile i - KB has read this K buffer
                 if (ok && i >= KB)
-                    ok = wait_for(&sc->s_full[(i - KB) & 1], (uint32_t)(((i - KB) >> 1) & 1), code | kBarS, failed);
+                    ok = wait_for(at(offsetof(Scalars, s_full), (i - KB) & 1), (uint32_t)(((i - KB) >> 1) & 1), code | kBarS, failed);
                 if (ok && !paged && i == n_page && i > 0) {
                     // first tail tile after pages: Q becomes bf16 once S of tile i - 1 has read it
-                    ok = wait_for(&sc->s_full[(i - 1) & 1], (uint32_t)(((i - 1) >> 1) & 1), code | kBarS, failed);
+                    ok = wait_for(at(offsetof(Scalars, s_full), (i - 1) & 1), (uint32_t)(((i - 1) >> 1) & 1), code | kBarS, failed);
                     if (ok) {
 #pragma unroll 1
                         for (int x = t; x < kN * (D / 8); x += 128)
@@ -598,13 +628,13 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 tc_fence_after();
                 const uint32_t dst = lanes + L::kTmemK + (uint32_t)(64 * (i % KB));
                 if (__builtin_expect(paged, 1)) {
-                    const uint8_t* line = k_src + st * L::kRawBytes;
+                    const uint32_t line = k_src + (uint32_t)(st * L::kRawBytes);
 #pragma unroll 1
                     for (int h = 0; h < D / 64; ++h) {
                         uint4 v[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            v[j] = *reinterpret_cast<const uint4*>(line + (((k_piece + 4 * h + j) ^ (k_line & 7)) << 4));
+                            v[j] = lds_u4(line ^ (uint32_t)((4 * h + j) << 4));
                         uint32_t w[32];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -631,7 +661,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sc->k_full[i % KB]);
+                arrive(at(offsetof(Scalars, k_full), i % KB));
             }
             if (do_v) {
                 const uint32_t unit0 = unit_now.x, unit1 = unit_now.y;   // of the tile's two pages
@@ -641,7 +671,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 // the product of tile i - VB has read this V buffer
                 if (ok && i >= VB)
-                    ok = wait_for(&sc->pv_done[(i - VB) & 1], (uint32_t)(((i - VB) >> 1) & 1), code | kBarPv, failed);
+                    ok = wait_for(at(offsetof(Scalars, pv_done), (i - VB) & 1), (uint32_t)(((i - VB) >> 1) & 1), code | kBarPv, failed);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -700,11 +730,11 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&sc->v_full[i % VB]);
+                arrive(at(offsetof(Scalars, v_full), i % VB));
             }
             if (paged) {                                              // this group has read the raw stage
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sc->raw_free[st]);
+                if (lane == 0) arrive(at(offsetof(Scalars, raw_free), st));
                 if (++st == kStages) { st = 0; lap ^= 1u; }
             }
         }
@@ -724,6 +754,18 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const float* group_part = sc->part + 4 * gr * L::kPart;
         float* neg_ref = sc->neg_ref + (ALT ? 64 * gr : c0);
         float* corr = sc->corr + (ALT ? 64 * gr : c0);
+        const uint32_t refs = opaque(smem_u32(neg_ref));
+        // where the thread's key stores P: piece j (8 rows) of the group is 16 bytes, swizzled.
+        // A group starts at piece c0 / 8, where COLS / 8 is a power of two that leaves j's bits.
+        constexpr bool kPow2 = ALT || (COLS & (COLS - 1)) == 0;
+        const uint32_t p_row = opaque(smem_u32(
+            smem + L::kOffP + (ALT ? gr * L::kPBuf : 0) + t * 128 +
+            (kPow2 ? (c0 >> 6) * (kQ8Tile * 128) + ((((c0 >> 3) & 7) ^ (t & 7)) << 4) : 0)));
+        auto p_at = [&](int j) -> uint32_t {
+            if (kPow2) return (p_row ^ (uint32_t)((j & 7) << 4)) + (uint32_t)((j >> 3) * (kQ8Tile * 128));
+            const int jj = c0 / 8 + j;
+            return p_row + (uint32_t)((jj >> 3) * (kQ8Tile * 128) + (((jj & 7) ^ (t & 7)) << 4));
+        };
         const uint32_t o_base = lanes + L::kTmemO + (ALT ? (uint32_t)gr * L::kNCols : (uint32_t)c0);
         const int half = t >> 6;
 
@@ -790,7 +832,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (tid + e * T < kN * (D / 8)) *q_address(tid + e * T) = qv[e];
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sc->q_full);
+        arrive(at(offsetof(Scalars, q_full)));
         const float a_page = p.scale_log2 * (1.f / q_mul);
 
         float2 l2[COLS / 2];                            // this thread's part of the rows' sums
@@ -828,7 +870,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 a = p.scale_log2;
             }
-            fail |= !wait_for(&sc->s_full[u], (uint32_t)((i >> 1) & 1), code | kBarS, failed);
+            fail |= !wait_for(at(offsetof(Scalars, s_full), u), (uint32_t)((i >> 1) & 1), code | kBarS, failed);
             tc_fence_after();
             float2 x[COLS / 2];
             const uint32_t s_addr = lanes + L::kTmemS + (uint32_t)u * L::kNCols + (uint32_t)c0;
@@ -842,7 +884,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const float2 aa = make_float2(a, a);
 #pragma unroll
                 for (int c = 0; c < COLS; c += 4) {
-                    const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
+                    const float4 nr = lds_f4(refs + 4 * c);
                     x[c / 2] = fma2(make_float2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), aa, make_float2(nr.x, nr.y));
                     x[c / 2 + 1] = fma2(make_float2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), aa, make_float2(nr.z, nr.w));
                 }
@@ -905,7 +947,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 }
                 group_sync(gr);
                 if (prev >= 0) {
-                    fail |= !wait_for(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
+                    fail |= !wait_for(at(offsetof(Scalars, pv_done), prev & 1), (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
                     __syncwarp();
                     tc_fence_after();
 #pragma unroll 1
@@ -935,7 +977,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             // S^T is in registers: the buffer is free
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sc->s_free[u]);
+            if (lane == 0) arrive(at(offsetof(Scalars, s_free), u));
             uint32_t pk[COLS / 2];
             if (__builtin_expect(paged, 1)) {
 #pragma unroll
@@ -956,18 +998,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             }
             // P's buffer is free once the previous product has read it
             if (prev >= 0)
-                fail |= !wait_for(&sc->pv_done[prev & 1], (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
+                fail |= !wait_for(at(offsetof(Scalars, pv_done), prev & 1), (uint32_t)((prev >> 1) & 1), code | kBarPv, failed);
             if (!fail) {
-                uint8_t* pt = smem + L::kOffP + (ALT ? gr * L::kPBuf : 0) + t * 128;
 #pragma unroll
-                for (int j = 0; j < COLS / 8; ++j) {
-                    const int jj = c0 / 8 + j;          // 16-byte piece: 8 rows
-                    *reinterpret_cast<uint4*>(pt + (jj >> 3) * (kQ8Tile * 128) + (((jj & 7) ^ (t & 7)) << 4)) =
-                        make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-                }
+                for (int j = 0; j < COLS / 8; ++j)
+                    sts_u4(p_at(j), make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]));
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&sc->p_full[ALT ? gr : 0]);
+                arrive(at(offsetof(Scalars, p_full), ALT ? gr : 0));
             }
             __syncwarp();
             scale_now = scale_next;
@@ -985,7 +1023,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         }
         // O^T of the last products (in ALT of both groups)
         for (int i = max(n - kStep, 0); i < n; ++i)
-            fail |= !wait_for(&sc->pv_done[i & 1], (uint32_t)((i >> 1) & 1), kRoleSoftmax | kBarPv | 0xffffu, failed);
+            fail |= !wait_for(at(offsetof(Scalars, pv_done), i & 1), (uint32_t)((i >> 1) & 1), kRoleSoftmax | kBarPv | 0xffffu, failed);
         record(p.err, failed);
         if (barrier_any<L::kSoftmaxThreads>(5, fail)) { // sums and references of all groups are there
             sc->abort = 1;
