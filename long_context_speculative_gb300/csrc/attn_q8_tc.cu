@@ -76,9 +76,9 @@ struct Plan {
     static constexpr int kThreads = 32 * (kProducerWarp + 4);
     // A block starts with kLaunchRegs registers a thread; its warpgroups share them out anew.
     static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-    static constexpr int kSoftmaxRegs = ALT ? (COLS <= 32 ? 112 : COLS <= 48 ? 136 : 152) : 88;
-    static constexpr int kConvRegs = ALT ? (COLS <= 32 ? 96 : COLS <= 48 ? 80 : 64) : 56;
-    static constexpr int kLastRegs = ALT ? (COLS <= 32 ? 56 : COLS <= 48 ? 48 : 40) : 40;
+    static constexpr int kSoftmaxRegs = ALT ? (COLS <= 32 ? 112 : 136) : 88;
+    static constexpr int kConvRegs = ALT ? (COLS <= 32 ? 96 : 80) : 56;
+    static constexpr int kLastRegs = ALT ? (COLS <= 32 ? 56 : 48) : 40;
     static_assert(kGroups * kSoftmaxRegs + 2 * kConvRegs + kLastRegs <= kLaunchRegs * (kThreads / 128),
                   "registers of a block");
     // Tensor-memory columns: K and V tiles (64 each), O^T (of each group), two S^T buffers.
@@ -1156,7 +1156,11 @@ cudaError_t launch_shape(const CUtensorMap& pool, const AttnQ8Params& p, int n_r
     return cudaLaunchKernelEx(&cfg, kern, pool, p, n_rb, rows);
 }
 
-// Rows of a CTA in steps of 16 up to 64, then of 32.
+// N in steps of 16 as far as two groups that take the tiles in turn hold all rows, above it
+// four groups with a quarter of the rows each, N in steps of 32.  Measured at 120K (us): 44 rows
+// of 8 heads, in turn 50.7, N = 64 in turn 62.9, four groups 65.7; 56 rows of 4 heads, in turn
+// 43.8, four groups 40.6; 88 rows of 8 heads, N = 96 78.9, N = 128 90.6.  4 rows over 4K:
+// N = 16 10.2, N = 64 in turn 18.8, four groups 12.0.
 template <int D>
 cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStream_t st) {
     const int n_rb = q8_row_blocks(p.R);
@@ -1164,7 +1168,7 @@ cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStre
     if (rows <= 16) return launch_shape<D, 16, true>(pool, p, n_rb, rows, st);
     if (rows <= 32) return launch_shape<D, 32, true>(pool, p, n_rb, rows, st);
     if (rows <= 48) return launch_shape<D, 48, true>(pool, p, n_rb, rows, st);
-    if (rows <= 64) return launch_shape<D, 64, true>(pool, p, n_rb, rows, st);
+    if (rows <= 64) return launch_shape<D, 16, false>(pool, p, n_rb, rows, st);
     if (rows <= 96) return launch_shape<D, 24, false>(pool, p, n_rb, rows, st);
     return launch_shape<D, 32, false>(pool, p, n_rb, rows, st);
 }

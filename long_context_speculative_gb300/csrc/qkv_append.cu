@@ -243,7 +243,7 @@ cudaError_t launch_typed(QkvAppendParams p, cudaStream_t st) {
     const int steps = (p.Hq + kRows - 1) / kRows + 2 * ((p.Hkv + kRows - 1) / kRows);
     const int64_t tokens = (int64_t)p.B * p.n;
     // few tokens: spread each one's heads over several warps
-    int64_t slices = (152 * 32 + tokens - 1) / tokens;
+    int64_t slices = ((int64_t)sm_count() * 32 + tokens - 1) / tokens;
     if (slices > steps) slices = steps;
     p.slices = (int)(slices < 1 ? 1 : slices);
     const int64_t blocks = (tokens * p.slices + kAppendWarps - 1) / kAppendWarps;
