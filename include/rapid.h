@@ -693,8 +693,8 @@ enum {
  * dropped.  The lengths stay as they are until rapid_kv_seal_advance, called
  * after the last layer with the same keep_rows and sizes: sealed_len += 64 n_b,
  * tail_len -= 64 n_b.  Both calls work from device memory alone, so they can be
- * captured with the step.  Pages given to several sequences must not be sealed
- * into.
+ * captured with the step.  No page may be the target of two blocks of a call, and
+ * pages given to several sequences must not be sealed into.
  *
  *  K_layers, V_layers, page_layers, scale_layers  HOST arrays of `layers`
  *             device pointers (tails and pages 16-byte aligned)
@@ -734,7 +734,9 @@ size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_
  *             multiple of 64 or past max_pages, a tail_len outside [0,
  *             tail_capacity - n_q] and a page id outside the pool are clamped,
  *             and bit 1 of the device error word is set
- *  spec_mask, softmax_scale, LSE, workspace  as for rapid_verify_attn
+ *  spec_mask, softmax_scale, LSE, workspace  as for rapid_verify_attn; calls that
+ *             may overlap (two streams, two captured graphs) need workspaces of
+ *             their own
  *
  * Rows of the tail caches that a query does not see have no effect on it,
  * whatever they hold.  With bf16 the products run on tensor cores with fp32
@@ -742,8 +744,9 @@ size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_
  * probabilities are rounded to it (fp16 over pages, bf16 over tail rows).
  *
  * Errors: those of rapid_verify_attn, and RAPID_EINVAL for n_pages < 1, n_pages
- * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], scales
- * not 8-byte aligned, index arrays not 4-byte aligned.
+ * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], B * (2
+ * max_pages + tail_capacity / 32 + 2) not below 2^31, scales not 8-byte aligned,
+ * index arrays not 4-byte aligned.
  */
 rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void* V_tail,
                                   const void* pages, const float* scales, const int32_t* page_table,

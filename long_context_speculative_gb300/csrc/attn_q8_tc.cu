@@ -7,38 +7,49 @@
 //   O^T[dim, row] += V^T P^T         A = V^T (tensor memory), B = P (shared memory, MN-major)
 // A verify step has few rows (4 to 128 for a KV head), so rows in M would leave most of every
 // tensor instruction idle (44 of 128 rows for an 11-node chain); in N they cost what they
-// are, in steps of 16.  It also gives every softmax thread one key: the key's page scales are
-// two numbers of the thread, and the running maximum needs no reduction at all until some
-// score passes the reference by more than 2^8 (the reference of a row then moves, O is
-// rescaled, and the tile is taken again).
+// are, in steps of 16.  It also gives every softmax thread one key: the key's page scale is
+// one number of the thread, and the running maximum needs no reduction at all until some
+// score passes its reference by more than 2^8 (the group of warps votes; the reference of the
+// row then moves, O is rescaled, and the tile is taken again).
 //
 // The 8-bit codes become fp16 exactly, so K and V lose nothing.  Q is held as fp16 times one
 // power of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to
 // 2^-30 of that keep all 8 bits of a bf16).  P is fp16 of 2^(s - ref), 2^7 at the reference
 // and below 2^15, so it keeps 11 bits down to 2^-21 of the row's largest and fades out below
 // 2^-31.  V takes its page's scale relative to the largest scale of the CTA's pages (exact for
-// powers of two down to 2^-15), which multiplies O at the end.  Tail rows and speculative rows are bf16 as they are: those tiles,
-// the last of a sequence, run the same way in bf16.
+// powers of two down to 2^-15), which multiplies O at the end.  Tail rows and speculative rows
+// are bf16 as they are: those tiles, the last of a sequence, run the same way in bf16.
 //
 // Both operands that come from the cache are converted in registers on their way from the raw
 // stages to tensor memory, K by rows and V through transposing 8-bit ldmatrix loads, so a
 // code byte crosses shared memory twice (copy in, read out).  With V as a shared-memory
 // operand in fp16 it would be written and read there once more at twice the width, and
-// shared-memory bandwidth (128 B a clock), not HBM, bounded that version.
+// shared-memory bandwidth (128 B a clock), not HBM, bounded that version (72 us where this
+// one takes 66 with the same roles).
 //
 // CTA = (sequence and split, block of at most 128 group rows; KV head).  Tiles are 128 keys:
 // two pages, or 128 tail rows.  Warps:
 //   softmax     groups of 4; warp w owns the keys, later the output dimensions, of
-//               tensor-memory lane quadrant w % 4.  Up to 64 rows two groups take the tiles in
+//               tensor-memory lane quadrant w % 4.  Up to 48 rows two groups take the tiles in
 //               turn, each with its own references and O^T, joined at the end; above, four
-//               groups take every tile and a quarter of its rows.  Either way the chain of a
-//               tile (load S, compare, exponentials, store P) overlaps another's
+//               groups take every tile and a quarter of its rows (launch_rows).  The chain of a
+//               tile (load S, compare, vote, exponentials, store P) takes a group 2200 to 2700
+//               cycles, nearly whatever its columns: warps' latencies, not a unit's rate
 //   converters  4 for K and 4 for V
 //   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
 //               into a ring of raw stages by TMA
 //   issuer      1: the MMAs, in the order in which their inputs become ready
 // Every wait is bounded in wall-clock time; after a failed wait the kernel records an error
 // code, stops issuing, drains and returns.
+//
+// Measured with the merge (us, floor by bytes at 6778 GB/s): 11 queries of 32 heads over 8 KV
+// heads, d = 128: 120K 50.7 (37.2), 32K 25.1 (10.0); one query over 4K 10.1 (1.3); 64 heads
+// over 8, 128K 79 (39.7); d = 64, 120K 42 (18.6); a tree of 32 nodes, 28 heads over 4, four
+// histories of 32K to 96K 198 (40; 62 by tensor rate).  Of a call about 10 us are the start (the
+// lengths, page ids and first pages one after the other, cold code, the first references) and the
+// end (join, merge).  In between, 44 rows take 1430 cycles a tile, near what HBM delivers; more
+// rows, and d = 64, whose tiles are half the bytes, are bound by the softmax warps' chain: with
+// the polls of waiting warps cut by a third, or with naps between them, the times stay.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>

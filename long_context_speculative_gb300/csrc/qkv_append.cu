@@ -17,6 +17,11 @@
 // each other, so a rotated pair never leaves its lane; a warp takes one token and some of
 // its heads, with the sines and cosines of its lanes' pairs kept in registers over all of
 // them.
+//
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128, bf16, with norms, 35.8 us for 201 MB (5.6
+// TB/s, 0.83 of a plain copy); 3 ragged chunks of 1999 tokens, fp32, d = 64, 21.1 us (0.77);
+// 11 tokens 2.5 us.  Each warp has two steps' loads in flight before it works on the first, in
+// place of one (45.6 us), and 28 warps an SM, in place of 20 (40.4 us).
 #include "common.cuh"
 #include "qkv_append.cuh"
 
@@ -242,7 +247,8 @@ cudaError_t launch_typed(QkvAppendParams p, cudaStream_t st) {
     constexpr int kRows = 32 / (D / 16);
     const int steps = (p.Hq + kRows - 1) / kRows + 2 * ((p.Hkv + kRows - 1) / kRows);
     const int64_t tokens = (int64_t)p.B * p.n;
-    // few tokens: spread each one's heads over several warps
+    // few tokens: spread each one's heads over several warps, up to 32 an SM (up to 64: the
+    // sines of a token are worked out more often, 37.3 us where 32 and 16 take 35.8)
     int64_t slices = ((int64_t)sm_count() * 32 + tokens - 1) / tokens;
     if (slices > steps) slices = steps;
     p.slices = (int)(slices < 1 ? 1 : slices);
