@@ -587,7 +587,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
         const uint32_t v_src = opaque(smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128));
         // page ids of the split, and the scales of V of a tile's two pages as fp16 pairs relative
-        // to the largest of the split (the unit of O^T), fetched ahead like the softmax warps'
+        // to the largest of the split (the unit of O^T), 32 tiles at a time like the softmax warps'
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
         float inv_unit = 1.f;
@@ -601,15 +601,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             return make_uint2(f16x2(x, x), f16x2(y, y));
         };
         int2 id_next = make_int2(0, 0);
-        uint2 unit_now = make_uint2(0, 0);
+        uint2 unit_now = make_uint2(0, 0), unit_next = make_uint2(0, 0);
         bool ok = true;
         unsigned failed = 0;
         if (do_v && n_page > 0) {
-            const int2 id0 = page_ids(0);
-            id_next = page_ids(1);
+            const int2 id0 = page_ids(lane);
+            id_next = page_ids(32 + lane);
             ok = wait_for(at(offsetof(Scalars, q_full)), 0, kRoleConvert | kBarQ, failed);   // the unit is there
             inv_unit = 1.f / sc->unit;
-            unit_now = v_units(0, id0);
+            unit_now = v_units(lane, id0);
         }
         int st = 0;
         uint32_t lap = 0;
@@ -675,10 +675,12 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 arrive(at(offsetof(Scalars, k_full), i % KB));
             }
             if (do_v) {
-                const uint32_t unit0 = unit_now.x, unit1 = unit_now.y;   // of the tile's two pages
-                if (paged) {
-                    unit_now = v_units(i + 1, id_next);
-                    id_next = page_ids(i + 2);
+                const uint32_t unit0 = __shfl_sync(0xffffffffu, unit_now.x, i & 31);   // of the
+                const uint32_t unit1 = __shfl_sync(0xffffffffu, unit_now.y, i & 31);   // tile's two pages
+                if ((i & 31) == 8) unit_next = v_units(i - 8 + 32 + lane, id_next);
+                if ((i & 31) == 31) {
+                    unit_now = unit_next;
+                    id_next = page_ids(i + 33 + lane);
                 }
                 // the product of tile i - VB has read this V buffer
                 if (ok && i >= VB)
@@ -780,8 +782,12 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const uint32_t o_base = lanes + L::kTmemO + (ALT ? (uint32_t)gr * L::kNCols : (uint32_t)c0);
         const int half = t >> 6;
 
-        // scale of K of this thread's key in page tile i, fetched a tile ahead (its page id, two
-        // tiles ahead: neither load is waited for; the producer flags an id outside the pool)
+        // Scales of K of this thread's keys, fetched a batch of the group's tiles ahead (the page
+        // ids two; the producer flags an id outside the pool).  With four groups a batch is 32
+        // tiles, lane l holding the scale of tile l, and a tile's comes by a shuffle: fewer
+        // instructions to a tile (70B shape 79 -> 75.5 us, tree 198 -> 188, together with the same for V).  Groups that take tiles
+        // in turn fetch one tile at a time (d = 64 at 120K: 42 us, with batches of 32 44).
+        constexpr int kBatch = ALT ? 1 : 32;
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
         auto page_of = [&](int j) -> int { return j < my_pages ? __ldg(ids + j) : 0; };
@@ -793,14 +799,17 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         // fp16 forms are relative to.  All loads that wait for nothing go out first.
         constexpr int T = L::kSoftmaxThreads;
         constexpr int kQPieces = (kN * (D / 8) + T - 1) / T;
-        const int page_unit = page_of(tid), page_first = page_of(2 * first_tile + half);
-        int page_next = page_of(2 * (first_tile + kStep) + half);
+        auto page_idx = [&](int turn) {
+            return 2 * (first_tile + kStep * (turn + (kBatch > 1 ? lane : 0))) + half;
+        };
+        const int page_unit = page_of(tid), page_first = page_of(page_idx(0));
+        int page_next = page_of(page_idx(kBatch));
         uint4 qv[kQPieces];
 #pragma unroll
         for (int e = 0; e < kQPieces; ++e)
             qv[e] = tid + e * T < Rb * (D / 8) ? Qg[tid + e * T] : make_uint4(0, 0, 0, 0);
         float unit = tid < my_pages ? v_scale(p, page_unit, g) : 0.f;
-        float scale_now = scale_of(page_first);
+        float scale_now = scale_of(page_first), scale_next = 0.f;
 #pragma unroll 1
         for (int j = tid + T; j < my_pages; j += T) unit = fmaxf(unit, v_scale(p, __ldg(ids + j), g));
         uint32_t q_bits = 0;                            // largest finite magnitude (bits order as values)
@@ -857,14 +866,17 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const int prev = i - kStep;                 // the product that used this group's P and O^T last
             const bool paged = i < n_page;
             const unsigned code = kRoleSoftmax | (unsigned)(i & 0xffff);
-            const float scale_next = scale_of(page_next);
-            const int page_after = page_of(2 * (i + 2 * kStep) + half);
+            const int turn = ALT ? i >> 1 : i;          // of the group's tiles
+            if (turn % kBatch == 0) {
+                scale_next = scale_of(page_next);
+                page_next = page_of(page_idx(turn + 2 * kBatch));
+            }
             // which of the rows see this thread's key
             uint64_t seen;
             float a;                                    // s = a * S^T
             if (__builtin_expect(paged, 1)) {
                 seen = 2 * i + half < my_pages ? ~0ull : 0ull;
-                a = scale_now * a_page;
+                a = (kBatch > 1 ? __shfl_sync(0xffffffffu, scale_now, turn % kBatch) : scale_now) * a_page;
             } else {
                 const int64_t key = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile + t;
                 const int64_t node = key - keys.tail;
@@ -1019,8 +1031,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 arrive(at(offsetof(Scalars, p_full), ALT ? gr : 0));
             }
             __syncwarp();
-            scale_now = scale_next;
-            page_next = page_after;
+            if (turn % kBatch == kBatch - 1) scale_now = scale_next;
         }
         if (tid == 0) griddep_launch_dependents();
         // the rows' sums over this warp's keys
