@@ -43,13 +43,14 @@
 // code, stops issuing, drains and returns.
 //
 // Measured with the merge (us, floor by bytes at 6778 GB/s): 11 queries of 32 heads over 8 KV
-// heads, d = 128: 120K 50.7 (37.2), 32K 25.1 (10.0); one query over 4K 10.1 (1.3); 64 heads
-// over 8, 128K 79 (39.7); d = 64, 120K 42 (18.6); a tree of 32 nodes, 28 heads over 4, four
-// histories of 32K to 96K 198 (40; 62 by tensor rate).  Of a call about 10 us are the start (the
+// heads, d = 128: 120K 49.7 (37.2), 32K 25.0 (10.0); one query over 4K 10.1 (1.3); 64 heads
+// over 8, 128K 75.5 (39.7); d = 64, 120K 41.6 (18.6); a tree of 32 nodes, 28 heads over 4, four
+// histories of 32K to 96K 188 (40; 62 by tensor rate).  Of a call about 10 us are the start (the
 // lengths, page ids and first pages one after the other, cold code, the first references) and the
 // end (join, merge).  In between, 44 rows take 1430 cycles a tile, near what HBM delivers; more
 // rows, and d = 64, whose tiles are half the bytes, are bound by the softmax warps' chain: with
-// the polls of waiting warps cut by a third, or with naps between them, the times stay.
+// the polls of waiting warps cut by a third, or with naps between them, the times stay, and so
+// they do with the vote on a barrier phase of its own that overlaps the exponentials (8 % more).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
