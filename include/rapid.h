@@ -744,8 +744,8 @@ size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_
  * probabilities are rounded to it (fp16 over pages, bf16 over tail rows).
  *
  * Errors: those of rapid_verify_attn, and RAPID_EINVAL for n_pages < 1, n_pages
- * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], B * (2
- * max_pages + tail_capacity / 32 + 2) not below 2^31, scales not 8-byte aligned,
+ * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], B *
+ * (max_pages + tail_capacity / 64 + 2) not below 2^31, scales not 8-byte aligned,
  * index arrays not 4-byte aligned.
  */
 rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void* V_tail,

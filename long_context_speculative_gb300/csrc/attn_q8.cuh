@@ -16,10 +16,10 @@
 
 namespace rapid {
 
-// Keys of a tile, the unit of the split plan: two pages or 128 tail rows on tensor cores, half a
-// page or 32 tail rows on CUDA cores.
+// Keys of a tile, the unit of the split plan: two pages or 128 tail rows on tensor cores, one
+// page or 64 tail rows on CUDA cores.
 constexpr int kQ8Tile = 128;
-constexpr int kQ8SimtTile = 32;
+constexpr int kQ8SimtTile = 64;
 
 struct AttnQ8Params {
     const void* Q;               // [B, Hq, n_q, d]
@@ -65,8 +65,7 @@ __device__ __forceinline__ Q8Keys q8_keys(const AttnQ8Params& p, int b) {
     if (tail < 0) tail = 0;
     if (tail > p.cap - p.n_q) tail = p.cap - p.n_q;
     k.tail = tail;
-    k.page_tiles = TILE >= kPageTokens ? (k.pages + TILE / kPageTokens - 1) / (TILE / kPageTokens)
-                                       : k.pages * (kPageTokens / TILE);
+    k.page_tiles = (k.pages + TILE / kPageTokens - 1) / (TILE / kPageTokens);
     k.tiles = k.page_tiles + (int)((tail + p.n_q + TILE - 1) / TILE);
     return k;
 }

@@ -5,10 +5,13 @@
 // output scale_V sum p code; both are applied to the values as they are unpacked.  One pass
 // with the running maximum and sum of the softmax, in the log2 domain and fp32.
 //
-// The history kernel is bound by the CUDA cores' fp32 products and, on short histories, by the
-// latency of a tile's loads, unpacking and two barriers.  Tiles are half a page, a key for each
-// lane, so that a short history still splits over many CTAs: 5 queries of 4 heads over one KV
-// head, d = 64, 1K of history takes 19.5 us, with tiles of 128 keys 33.6.
+// The history kernel is bound by the CUDA cores and shared memory (two packed products, or one
+// 16-byte read of K, V or P, for 4 to 8 multiplications), on short histories by the latency of
+// a tile: unpacking, two barriers, the two products one after the other.  Measured with the merge:
+// 5 queries of 4 heads over one KV head, d = 64, 1K of history 8.6 us; 10 queries of 16 heads,
+// d = 64, six histories of 1.6K 39 us; 60 queries of 64 heads over 8, d = 128, 512 of history 66 us.
+// With a key to a lane, rows over the warps and P handed round by shuffles these took 19.4, 206
+// and 183.
 #include <cuda_fp16.h>
 
 #include "attn_q8.cuh"
@@ -18,9 +21,9 @@ namespace rapid {
 
 namespace {
 
-constexpr int kSimtThreads = 128;                   // 4 warps
-constexpr int kRowsPerWarp = kQ8SimtRows / 4;
-constexpr int kKeys = kQ8SimtTile;                  // keys of a tile, one per lane
+constexpr int kSimtThreads = 256;
+constexpr int kKeys = kQ8SimtTile;                  // keys of a tile: a page, or 64 tail rows
+static_assert(kKeys == kPageTokens, "a tile is a page");
 
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     uint32_t h;
@@ -28,42 +31,34 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// 16 elements of a page row, scaled.
-__device__ __forceinline__ void load_page16(const uint8_t* src, float scale, float (&x)[16]) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 a = e4m3x2_to_float2(w[i] & 0xffffu), c = e4m3x2_to_float2(w[i] >> 16);
-        x[4 * i] = a.x * scale;
-        x[4 * i + 1] = a.y * scale;
-        x[4 * i + 2] = c.x * scale;
-        x[4 * i + 3] = c.y * scale;
-    }
+// Four codes, scaled.
+__device__ __forceinline__ float4 page4(uint32_t w, float scale) {
+    const float2 a = e4m3x2_to_float2(w & 0xffffu), c = e4m3x2_to_float2(w >> 16);
+    return make_float4(a.x * scale, a.y * scale, c.x * scale, c.y * scale);
 }
 
-__device__ __forceinline__ void load_row16(const float* src, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(src)[i];
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-    }
-}
-// CTA = (slot and block of up to 64 group rows, KV head).  Each lane owns one key of a
-// 32-key step for the scores and d / 32 output columns for the products with V.
-template <int D>
-__global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8Params p) {
-    constexpr int DP = D + 4;                 // padded K pitch: conflict-free float4 rows
-    constexpr int NC = D / 32;                // output columns per lane
+// CTA = (slot and block of up to 64 group rows, KV head).  A tile is unpacked into shared
+// memory while the next page's codes are on their way into registers.  16 lanes own TR rows
+// (tr + 16 i) in both products: 4 keys each of the scores, d / 16 columns each of the output, so
+// that P and the running maxima never leave the warp.
+template <int D, int TR>
+__global__ void __launch_bounds__(kSimtThreads, TR == 4 ? 1 : 2) attn_q8_simt_kernel(const AttnQ8Params p) {
+    constexpr int ROWS = 16 * TR;
+    constexpr int KP = D + 4;                 // pitches of K and P: conflict-free
+    constexpr int PP = kKeys + 4;
+    constexpr int W = kKeys * D / 4 / kSimtThreads;   // words of codes a thread holds, each side
+    constexpr int NV = D / 64;                // float4 columns per lane: 4 kg + 64 h
     extern __shared__ float4 smem_f4[];
-    float* sQ = reinterpret_cast<float*>(smem_f4);   // [64][D], times scale * log2(e)
-    float* sK = sQ + kQ8SimtRows * D;                // [32][DP]
-    float* sV = sK + kKeys * DP;                     // [32][D]
+    float* sQ = reinterpret_cast<float*>(smem_f4);   // [ROWS][D], times scale * log2(e)
+    float* sK = sQ + ROWS * D;                       // [64][KP]
+    float* sV = sK + kKeys * KP;                     // [64][D]
+    float* sP = sV + kKeys * D;                      // [ROWS][PP]
     __shared__ Q8Split s_split;
     __shared__ Q8Keys s_keys;
 
     griddep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int kg = tid & 15, tr = tid >> 4;
     const int n_rb = (p.R + kQ8SimtRows - 1) / kQ8SimtRows;
     const int slot_idx = blockIdx.x / n_rb, rb = blockIdx.x - slot_idx * n_rb;
     const int g = blockIdx.y;
@@ -80,7 +75,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     if (sp.b < 0) return;
     const int b = sp.b;
     const int64_t bg = (int64_t)b * p.Hkv + g;
-    if (threadIdx.x == 0 && sp.s == 0 && rb == 0) {
+    if (tid == 0 && sp.s == 0 && rb == 0) {
         p.part_first[bg] = sp.first;
         p.part_count[bg] = sp.count;
     }
@@ -90,118 +85,163 @@ __global__ void __launch_bounds__(kSimtThreads) attn_q8_simt_kernel(const AttnQ8
     const int r0 = rb * kQ8SimtRows;
     const int nrows = min(kQ8SimtRows, p.R - r0);
 
-    const float* Qg = static_cast<const float*>(p.Q) + ((int64_t)b * p.Hq + (int64_t)g * p.G) * p.n_q * D;
-    for (int idx = threadIdx.x; idx < kQ8SimtRows * D; idx += kSimtThreads) {
-        const int r = idx / D, k = idx - r * D;
-        sQ[idx] = r < nrows ? Qg[(int64_t)(r0 + r) * D + k] * p.scale_log2 : 0.f;
+    const float4* Qg = reinterpret_cast<const float4*>(
+        static_cast<const float*>(p.Q) + (((int64_t)b * p.Hq + (int64_t)g * p.G) * p.n_q + r0) * D);
+    for (int x = tid; x < ROWS * D / 4; x += kSimtThreads) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x < nrows * (D / 4)) q = Qg[x];
+        reinterpret_cast<float4*>(sQ)[x] =
+            make_float4(q.x * p.scale_log2, q.y * p.scale_log2, q.z * p.scale_log2, q.w * p.scale_log2);
     }
-    float acc[kRowsPerWarp][NC];
-    float m[kRowsPerWarp], l[kRowsPerWarp];
+    float2 acc[TR][2 * NV];
+    float m[TR], l[TR];                       // l: this lane's keys only
 #pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
+    for (int i = 0; i < TR; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
+        for (int c = 0; c < 2 * NV; ++c) acc[i][c] = make_float2(0.f, 0.f);
     }
     const float* Kh = static_cast<const float*>(p.K) + bg * p.cap * D;
     const float* Vh = static_cast<const float*>(p.V) + bg * p.cap * D;
     const int64_t tail_keys = keys.tail + p.n_q;
 
+    uint32_t kc[W], vc[W];                    // a page's codes, and its scales
+    float k_scale = 0.f, v_scale = 0.f;
+    auto fetch = [&](int tile) {
+        const int64_t head = (int64_t)q8_page(p, b, tile) * p.Hkv + g;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.pages + head * 2 * kPageTokens * D);
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            kc[u] = __ldg(src + u * kSimtThreads + tid);
+            vc[u] = __ldg(src + kPageTokens * D / 4 + u * kSimtThreads + tid);
+        }
+        k_scale = __ldg(p.scales + head * 2);
+        v_scale = __ldg(p.scales + head * 2 + 1);
+    };
+    if (t_begin < t_end && t_begin < keys.page_tiles) fetch(t_begin);
+
+#pragma unroll 1
     for (int tile = t_begin; tile < t_end; ++tile) {
-        // key of lane 0: a page key, or a tail row once the page tiles are through
         const bool paged = tile < keys.page_tiles;
-        const int64_t k0 = (int64_t)(paged ? tile : tile - keys.page_tiles) * kKeys;
-        const int64_t k_end = paged ? (int64_t)keys.pages * kPageTokens : tail_keys;
-        const int nk = (int)(k_end - k0 < kKeys ? k_end - k0 : kKeys);
-        int64_t head = 0;                      // (page, head): one page holds the whole tile
-        if (paged) head = (int64_t)q8_page(p, b, (int)(k0 / kPageTokens)) * p.Hkv + g;
+        const int64_t k0 = (int64_t)(tile - keys.page_tiles) * kKeys;   // tail tile's first row
         __syncthreads();
-        for (int idx = threadIdx.x; idx < kKeys * (D / 16); idx += kSimtThreads) {
-            const int key = idx / (D / 16), e = (idx - key * (D / 16)) * 16;
-            float x[16], y[16];
-            if (key >= nk) {
+        if (paged) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u) { x[u] = 0.f; y[u] = 0.f; }
-            } else if (paged) {
-                const int64_t row = k0 % kPageTokens + key;
-                load_page16(p.pages + (head * 2 * kPageTokens + row) * D + e, p.scales[head * 2], x);
-                load_page16(p.pages + ((head * 2 + 1) * kPageTokens + row) * D + e,
-                            p.scales[head * 2 + 1], y);
-            } else {
-                load_row16(Kh + (k0 + key) * D + e, x);
-                load_row16(Vh + (k0 + key) * D + e, y);
+            for (int u = 0; u < W; ++u) {
+                const int x = u * kSimtThreads + tid, key = x / (D / 4), c = x - key * (D / 4);
+                *reinterpret_cast<float4*>(sK + key * KP + 4 * c) = page4(kc[u], k_scale);
+                *reinterpret_cast<float4*>(sV + key * D + 4 * c) = page4(vc[u], v_scale);
             }
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                sK[key * DP + e + u] = x[u];
-                sV[key * D + e + u] = y[u];
+            if (tile + 1 < t_end && tile + 1 < keys.page_tiles) fetch(tile + 1);
+        } else {
+#pragma unroll 2
+            for (int x = tid; x < kKeys * D / 4; x += kSimtThreads) {
+                const int key = x / (D / 4), c = x - key * (D / 4);
+                float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+                if (k0 + key < tail_keys) {
+                    kv = *reinterpret_cast<const float4*>(Kh + (k0 + key) * D + 4 * c);
+                    vv = *reinterpret_cast<const float4*>(Vh + (k0 + key) * D + 4 * c);
+                }
+                *reinterpret_cast<float4*>(sK + key * KP + 4 * c) = kv;
+                *reinterpret_cast<float4*>(sV + key * D + 4 * c) = vv;
             }
         }
         __syncthreads();
-        const int64_t node = paged ? -1 : k0 + lane - keys.tail;   // speculative node of this lane's key
-        float sc[kRowsPerWarp];
+        if (2 * warp >= nrows) continue;      // no row in this warp
+        float2 s2[TR][4];
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) sc[i] = 0.f;
-#pragma unroll 4
+        for (int i = 0; i < TR; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s2[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 2
         for (int k = 0; k < D; k += 4) {
-            const float4 kv = *reinterpret_cast<const float4*>(&sK[lane * DP + k]);
+            float4 kv[4];
 #pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i) {
-                const int r = warp + 4 * i;
-                if (r < nrows) {
-                    const float4 qv = *reinterpret_cast<const float4*>(&sQ[r * D + k]);
-                    sc[i] = fmaf(qv.x, kv.x, sc[i]);
-                    sc[i] = fmaf(qv.y, kv.y, sc[i]);
-                    sc[i] = fmaf(qv.z, kv.z, sc[i]);
-                    sc[i] = fmaf(qv.w, kv.w, sc[i]);
+            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sK + (kg + 16 * j) * KP + k);
+#pragma unroll
+            for (int i = 0; i < TR; ++i) {
+                const float4 q = *reinterpret_cast<const float4*>(sQ + (tr + 16 * i) * D + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s2[i][j] = fma2(make_float2(q.x, q.y), make_float2(kv[j].x, kv[j].y), s2[i][j]);
+                    s2[i][j] = fma2(make_float2(q.z, q.w), make_float2(kv[j].z, kv[j].w), s2[i][j]);
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < kRowsPerWarp; ++i) {
-            const int r = warp + 4 * i;
-            if (r >= nrows) continue;
-            bool seen = lane < nk;
-            if (node >= 0 && seen) {
-                const int iq = (r0 + r) % p.n_q;
-                seen = p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0 : node <= iq;
+        for (int i = 0; i < TR; ++i) {
+            const int r = tr + 16 * i;
+            float s[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] = s2[i][j].x + s2[i][j].y;
+            if (!paged) {
+                const int iq = (r0 + min(r, nrows - 1)) % p.n_q;
+                const uint8_t* seen = p.mask ? p.mask + ((int64_t)b * p.n_q + iq) * p.n_q : nullptr;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t key = k0 + kg + 16 * j, node = key - keys.tail;
+                    if (key >= tail_keys || (node >= 0 && !(seen ? seen[node] != 0 : node <= iq))) s[j] = -INFINITY;
+                }
             }
-            const float si = seen ? sc[i] : -INFINITY;
-            const float mnew = fmaxf(m[i], warp_max(si));
+            float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float mnew = fmaxf(m[i], top);
             // a row that has seen no key yet keeps p = 0 instead of exp(-inf + inf)
             const float ref = mnew == -INFINITY ? 0.f : mnew;
             const float corr = exp2f(m[i] - ref);
-            const float pj = exp2f(si - ref);
-            l[i] = l[i] * corr + warp_sum(pj);
             m[i] = mnew;
+            l[i] *= corr;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) acc[i][c] *= corr;
-            sc[i] = pj;
+            for (int j = 0; j < 4; ++j) {
+                const float e = exp2f(s[j] - ref);
+                l[i] += e;
+                sP[r * PP + kg + 16 * j] = e;
+            }
+#pragma unroll
+            for (int c = 0; c < 2 * NV; ++c) acc[i][c] = mul2(acc[i][c], make_float2(corr, corr));
         }
-        for (int j = 0; j < nk; ++j) {
-            float vv[NC];
+        __syncwarp();
+        const int j_end = paged ? kKeys : (int)min(tail_keys - k0, (int64_t)kKeys);
+#pragma unroll 1
+        for (int j0 = 0; j0 < j_end; j0 += 4) {
+            float4 pr[TR];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) vv[c] = sV[j * D + lane + 32 * c];
+            for (int i = 0; i < TR; ++i) pr[i] = *reinterpret_cast<const float4*>(sP + (tr + 16 * i) * PP + j0);
 #pragma unroll
-            for (int i = 0; i < kRowsPerWarp; ++i) {
-                if (warp + 4 * i >= nrows) break;
-                const float pj = __shfl_sync(0xffffffffu, sc[i], j);
-                if (pj == 0.f) continue;       // a hidden row's V may hold anything
+            for (int e = 0; e < 4; ++e) {
+                float4 v[NV];
 #pragma unroll
-                for (int c = 0; c < NC; ++c) acc[i][c] = fmaf(pj, vv[c], acc[i][c]);
+                for (int h = 0; h < NV; ++h)
+                    v[h] = *reinterpret_cast<const float4*>(sV + (j0 + e) * D + 4 * kg + 64 * h);
+#pragma unroll
+                for (int i = 0; i < TR; ++i) {
+                    const float w = e == 0 ? pr[i].x : e == 1 ? pr[i].y : e == 2 ? pr[i].z : pr[i].w;
+                    if (!paged && w == 0.f) continue;   // a hidden row's V may hold anything
+                    const float2 w2 = make_float2(w, w);
+#pragma unroll
+                    for (int h = 0; h < NV; ++h) {
+                        acc[i][2 * h] = fma2(w2, make_float2(v[h].x, v[h].y), acc[i][2 * h]);
+                        acc[i][2 * h + 1] = fma2(w2, make_float2(v[h].z, v[h].w), acc[i][2 * h + 1]);
+                    }
+                }
             }
         }
     }
     const int64_t slot = ((int64_t)g * p.S + slot_idx) * p.R;
 #pragma unroll
-    for (int i = 0; i < kRowsPerWarp; ++i) {
-        const int r = warp + 4 * i;
-        if (r >= nrows) continue;
-        float* dst = p.part_acc + (slot + r0 + r) * D;
+    for (int i = 0; i < TR; ++i) {
+        const int r = tr + 16 * i;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) dst[lane + 32 * c] = acc[i][c];
-        if (lane == 0)
+        for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+        if (r >= nrows) continue;
+        float* dst = p.part_acc + (slot + r0 + r) * D + 4 * kg;
+#pragma unroll
+        for (int h = 0; h < NV; ++h)
+            *reinterpret_cast<float4*>(dst + 64 * h) =
+                make_float4(acc[i][2 * h].x, acc[i][2 * h].y, acc[i][2 * h + 1].x, acc[i][2 * h + 1].y);
+        if (kg == 0)
             *reinterpret_cast<float2*>(p.part_ml + (slot + r0 + r) * 2) = make_float2(m[i], l[i]);
     }
 }
@@ -301,15 +341,22 @@ __global__ void __launch_bounds__(kMergeThreads) attn_q8_merge_kernel(const Attn
     if (lane == 0) p.LSE[row] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <int D>
-cudaError_t simt_typed(const AttnQ8Params& p, cudaStream_t st) {
-    const int smem = (kQ8SimtRows * D + kKeys * (D + 4) + kKeys * D) * (int)sizeof(float);
-    auto kern = attn_q8_simt_kernel<D>;
+template <int D, int TR>
+cudaError_t simt_rows(const AttnQ8Params& p, cudaStream_t st) {
+    constexpr int smem = (16 * TR * D + kKeys * (D + 4) + kKeys * D + 16 * TR * (kKeys + 4)) * (int)sizeof(float);
+    auto kern = attn_q8_simt_kernel<D, TR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int n_rb = (p.R + kQ8SimtRows - 1) / kQ8SimtRows;
     kern<<<dim3(p.S * n_rb, p.Hkv, 1), kSimtThreads, smem, st>>>(p);
     return cudaGetLastError();
+}
+// As few rows a lane as hold the group.
+template <int D>
+cudaError_t simt_typed(const AttnQ8Params& p, cudaStream_t st) {
+    if (p.R <= 16) return simt_rows<D, 1>(p, st);
+    if (p.R <= 32) return simt_rows<D, 2>(p, st);
+    return simt_rows<D, 4>(p, st);
 }
 
 template <typename T, int D>

@@ -30,7 +30,7 @@ bool attn_q8_args_ok(int B, int Hq, int Hkv, int d, int n_q, int64_t cap, int ma
     if (cap < n_q || cap > ((int64_t)1 << 31)) return false;
     if (max_pages < 1 || max_pages > RAPID_Q8_MAX_PAGES) return false;
     // key tiles of all sequences are counted in 32 bits
-    if ((int64_t)B * (2 * (int64_t)max_pages + cap / kQ8SimtTile + 2) >= (int64_t)1 << 31) return false;
+    if ((int64_t)B * (max_pages + cap / kQ8SimtTile + 2) >= (int64_t)1 << 31) return false;
     return (int64_t)(Hq / Hkv) * n_q <= 4096;
 }
 
@@ -55,8 +55,8 @@ Q8Plan plan_attn_q8(int B, int Hq, int Hkv, int d, int n_q, int dtype) {
             if (cost < least) { least = cost; S = slots; }
         }
     } else {
-        // CUDA cores: four CTAs on every SM
-        S = 4 * sms / (Hkv * ((R + kQ8SimtRows - 1) / kQ8SimtRows));
+        // CUDA cores: two CTAs on every SM
+        S = 2 * sms / (Hkv * ((R + kQ8SimtRows - 1) / kQ8SimtRows));
         if (S > 512) S = 512;
     }
     if (S < B) S = B;
