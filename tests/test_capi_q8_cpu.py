@@ -89,6 +89,13 @@ def test_verify_attn_q8(lib):
     _refused(lib.rapid_verify_attn_q8, good, [(22, need - 1)], status=-3)
 
 
+def test_verify_attn_q8_counts_key_tiles_in_32_bits(lib):
+    size = lib.rapid_verify_attn_q8_workspace_size
+    assert size(120, 8, 8, 128, 1, 64, 1 << 24, 1) > 0
+    assert size(128, 8, 8, 128, 1, 64, 1 << 24, 1) == 0          # 128 * 2^24 page tiles and more
+    assert size(64, 8, 8, 128, 1, 1 << 31, 100, 1) == 0 and size(63, 8, 8, 128, 1, 1 << 31, 100, 1) > 0
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     c = _q8.cache(1, 2, 128, torch.bfloat16, [2], [5], 3, seed=1)
     Q = torch.zeros((1, 4, 3, 128), dtype=torch.bfloat16)
