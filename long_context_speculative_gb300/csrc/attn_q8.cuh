@@ -80,8 +80,8 @@ __device__ __forceinline__ int q8_page(const AttnQ8Params& p, int b, int j) {
 
 struct Q8Split {
     int b;               // sequence, or -1 where the slot has no work
-    int s, count;        // split s of count
-    int first;           // slot of the sequence's split 0
+    int t_begin, t_end;  // its tiles
+    int first, count;    // slots of the sequence's splits
 };
 
 // The (sequence, split) of slot c, worked out by one whole warp from the device-side
@@ -123,7 +123,8 @@ static __device__ __noinline__ Q8Split q8_split_of_many(const AttnQ8Params& p, i
 #pragma unroll 1
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const int n = b < p.B ? (tiles_of(b) + lo - 1) / lo : 0;
+        const int tiles = b < p.B ? tiles_of(b) : 0;
+        const int n = (tiles + lo - 1) / lo;
         int end = n;                                  // inclusive scan over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -135,21 +136,24 @@ static __device__ __noinline__ Q8Split q8_split_of_many(const AttnQ8Params& p, i
             const int w = __ffs(hit) - 1;
             const int count = __shfl_sync(0xffffffffu, n, w);
             const int f = first + __shfl_sync(0xffffffffu, end, w) - count;
-            return Q8Split{b0 + w, c - f, count, f};
+            const int t0 = (c - f) * lo;              // below the sequence's tiles: count is tiles / lo, up
+            return Q8Split{b0 + w, t0, min(t0 + lo, __shfl_sync(0xffffffffu, tiles, w)), f, count};
         }
         first += __shfl_sync(0xffffffffu, end, 31);
     }
-    return Q8Split{-1, 0, 0, 0};
+    return Q8Split{-1, 0, 0, 0, 0};
 }
 
 // The same with the sequence's lengths; one sequence needs no search.
 template <int TILE>
 __device__ __forceinline__ Q8Split q8_split_of(const AttnQ8Params& p, int c, Q8Keys* keys) {
-    Q8Split sp{0, c, 0, 0};
+    Q8Split sp{0, 0, 0, 0, 0};
     if (p.B > 1) sp = q8_split_of_many<TILE>(p, c);
     *keys = q8_keys<TILE>(p, sp.b < 0 ? 0 : sp.b);
     if (p.B == 1) {
         const int budget = (keys->tiles + p.S - 1) / p.S;
+        sp.t_begin = c * budget;
+        sp.t_end = min(sp.t_begin + budget, keys->tiles);
         sp.count = (keys->tiles + budget - 1) / budget;
         if (c >= sp.count) sp.b = -1;
     }

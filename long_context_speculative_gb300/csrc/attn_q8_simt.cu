@@ -75,13 +75,12 @@ __global__ void __launch_bounds__(kSimtThreads, TR == 4 ? 1 : 2) attn_q8_simt_ke
     if (sp.b < 0) return;
     const int b = sp.b;
     const int64_t bg = (int64_t)b * p.Hkv + g;
-    if (tid == 0 && sp.s == 0 && rb == 0) {
+    if (tid == 0 && sp.t_begin == 0 && rb == 0) {
         p.part_first[bg] = sp.first;
         p.part_count[bg] = sp.count;
     }
     const Q8Keys keys = s_keys;
-    const int t_begin = (int)((int64_t)sp.s * keys.tiles / sp.count);
-    const int t_end = (int)((int64_t)(sp.s + 1) * keys.tiles / sp.count);
+    const int t_begin = sp.t_begin, t_end = sp.t_end;
     const int r0 = rb * kQ8SimtRows;
     const int nrows = min(kQ8SimtRows, p.R - r0);
 

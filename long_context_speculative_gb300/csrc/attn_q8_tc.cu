@@ -424,7 +424,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         if (lane == 0) {
             sc->split = sp0;
             sc->keys = k;
-            if (sp0.b >= 0 && sp0.s == 0 && rb == 0) {
+            if (sp0.b >= 0 && sp0.t_begin == 0 && rb == 0) {
                 p.part_first[sp0.b * p.Hkv + g] = sp0.first;
                 p.part_count[sp0.b * p.Hkv + g] = sp0.count;
             }
@@ -439,9 +439,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
     const int b = has_work ? sp.b : 0;
     const int64_t bg = (int64_t)b * p.Hkv + g;
     const Q8Keys keys = sc->keys;
-    const int t_begin = has_work ? (int)((int64_t)sp.s * keys.tiles / sp.count) : 0;
-    const int t_end = has_work ? (int)((int64_t)(sp.s + 1) * keys.tiles / sp.count) : 0;
-    const int n = t_end - t_begin;
+    const int t_begin = sp.t_begin, t_end = sp.t_end;
+    const int n = has_work ? t_end - t_begin : 0;
     const int n_page = min(max(keys.page_tiles - t_begin, 0), n);   // the first n_page tiles are pages
     const int64_t tail_keys = keys.tail + p.n_q;
     const uint4* Qg = reinterpret_cast<const uint4*>(
