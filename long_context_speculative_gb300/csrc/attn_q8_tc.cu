@@ -883,12 +883,13 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 seen = key < tail_keys ? ~0ull : 0ull;
                 if (node >= 0 && key < tail_keys) {
                     seen = 0;
-#pragma unroll 1
-                    for (int c = 0; c < COLS; ++c) {
-                        const int iq = (r0 + c0 + c) % p.n_q;
-                        const bool vis = p.mask ? p.mask[((int64_t)b * p.n_q + iq) * p.n_q + node] != 0
-                                                : node <= iq;
+                    const uint8_t* column = p.mask ? p.mask + (int64_t)b * p.n_q * p.n_q + node : nullptr;
+                    int iq = (r0 + c0) % p.n_q;         // of the group row
+#pragma unroll 8
+                    for (int c = 0; c < COLS; ++c) {    // loads of several rows in flight
+                        const bool vis = column ? __ldg(column + iq * p.n_q) != 0 : node <= iq;
                         seen |= (vis ? 1ull : 0ull) << c;
+                        if (++iq == p.n_q) iq = 0;
                     }
                 }
                 a = p.scale_log2;
