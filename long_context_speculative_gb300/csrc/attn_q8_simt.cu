@@ -8,7 +8,7 @@
 // The history kernel is bound by the CUDA cores and shared memory (two packed products, or one
 // 16-byte read of K, V or P, for 4 to 8 multiplications), on short histories by the latency of
 // a tile: unpacking, two barriers, the two products one after the other.  Measured with the merge:
-// 5 queries of 4 heads over one KV head, d = 64, 1K of history 8.6 us; 10 queries of 16 heads,
+// 5 queries of 4 heads over one KV head, d = 64, 1K of history 7.8 us; 10 queries of 16 heads,
 // d = 64, six histories of 1.6K 39 us; 60 queries of 64 heads over 8, d = 128, 512 of history 66 us.
 // With a key to a lane, rows over the warps and P handed round by shuffles these took 19.4, 206
 // and 183.

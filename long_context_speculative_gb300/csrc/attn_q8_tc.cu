@@ -43,11 +43,11 @@
 // code, stops issuing, drains and returns.
 //
 // Measured with the merge (us, floor by bytes at 6778 GB/s): 11 queries of 32 heads over 8 KV
-// heads, d = 128: 120K 49.7 (37.2), 32K 25.0 (10.0); one query over 4K 10.1 (1.3); 64 heads
-// over 8, 128K 75.5 (39.7); d = 64, 120K 41.6 (18.6); a tree of 32 nodes, 28 heads over 4, four
-// histories of 32K to 96K 188 (40; 62 by tensor rate).  Of a call about 10 us are the start (the
+// heads, d = 128: 120K 46.0 (37.2), 32K 21.6 (10.0); one query over 4K 8.4 (1.3); 64 heads
+// over 8, 128K 75 (39.7); d = 64, 120K 38.8 (18.6); a tree of 32 nodes, 28 heads over 4, four
+// histories of 32K to 96K 184 (40; 62 by tensor rate).  Of a call about 9 us are the start (the
 // lengths, page ids and first pages one after the other, cold code, the first references) and the
-// end (join, merge).  In between, 44 rows take 1430 cycles a tile, near what HBM delivers; more
+// end (join, merge).  In between, 44 rows take 1400 cycles a tile, what HBM delivers; more
 // rows, and d = 64, whose tiles are half the bytes, are bound by the softmax warps' chain: with
 // the polls of waiting warps cut by a third, or with naps between them, the times stay, and so
 // they do with the vote on a barrier phase of its own that overlaps the exponentials (8 % more).
@@ -785,8 +785,9 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         // Scales of K of this thread's keys, fetched a batch of the group's tiles ahead (the page
         // ids two; the producer flags an id outside the pool).  With four groups a batch is 32
         // tiles, lane l holding the scale of tile l, and a tile's comes by a shuffle: fewer
-        // instructions to a tile (70B shape 79 -> 75.5 us, tree 198 -> 188, together with the same for V).  Groups that take tiles
-        // in turn fetch one tile at a time (d = 64 at 120K: 42 us, with batches of 32 44).
+        // instructions to a tile (70B shape 79 -> 75.5 us, tree 198 -> 188, together with the same
+        // for V).  Groups that take tiles in turn fetch one tile at a time (d = 64 at 120K: 41.6 us,
+        // with batches of 32 44.3).
         constexpr int kBatch = ALT ? 1 : 32;
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
@@ -1181,9 +1182,9 @@ cudaError_t launch_shape(const CUtensorMap& pool, const AttnQ8Params& p, int n_r
 
 // N in steps of 16 as far as two groups that take the tiles in turn hold all rows, above it
 // four groups with a quarter of the rows each, N in steps of 32.  Measured at 120K (us): 44 rows
-// of 8 heads, in turn 50.7, N = 64 in turn 62.9, four groups 65.7; 56 rows of 4 heads, in turn
-// 43.8, four groups 40.6; 88 rows of 8 heads, N = 96 78.9, N = 128 90.6.  4 rows over 4K:
-// N = 16 10.2, N = 64 in turn 18.8, four groups 12.0.
+// of 8 heads, in turn 45.9, four groups 59.5; 56 rows of 4 heads, in turn 43.8, four groups 40.6
+// (38.1 since); 88 rows of 8 heads, N = 96 75.4, N = 128 86.4.  4 rows over 4K: N = 16 8.4, N = 48
+// in turn 11.3, four groups 10.2.
 template <int D>
 cudaError_t launch_rows(const CUtensorMap& pool, const AttnQ8Params& p, cudaStream_t st) {
     const int n_rb = q8_row_blocks(p.R);

@@ -47,7 +47,8 @@ Q8Plan plan_attn_q8(int B, int Hq, int Hkv, int d, int n_q, int dtype) {
         // A second wave may hold few CTAs (20 sequences of 8 heads: 160 on 152 SMs).  More waves
         // of shorter splits then cost less: k splits of a sequence take w / k of its time, and
         // the start and end of a CTA, 1/32 of it (8 tiles of 256), w times.  20 sequences of 8
-        // heads, 1 query, d = 128: 349 -> 254 us at 32K, 60 -> 56 us at 4K with two waves more.
+        // heads, 1 query, d = 128: 337 -> 248 us at 32K, 58 -> 53 us at 4K; 32 or 38 sequences
+        // (nearly two full waves) stay with two.
         double least = waves * (1 + 1. / 32);
         for (int64_t w = waves + 1; waves > 1 && w <= waves + 2; ++w) {
             const int64_t slots = w * sms / per_slot;
