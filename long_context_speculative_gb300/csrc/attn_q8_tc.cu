@@ -16,9 +16,13 @@
 // power of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to
 // 2^-30 of that keep all 8 bits of a bf16).  P is fp16 of 2^(s - ref), 2^7 at the reference
 // and below 2^15, so it keeps 11 bits down to 2^-21 of the row's largest and fades out below
-// 2^-31.  V takes its page's scale relative to the largest scale of the CTA's pages (exact for
-// powers of two down to 2^-15), which multiplies O at the end.  Tail rows and speculative rows
-// are bf16 as they are: those tiles, the last of a sequence, run the same way in bf16.
+// 2^-31.  V takes its page's scale relative to the largest scale of the CTA's pages, which
+// multiplies O at the end: exact for powers of two down to 2^-15, where e4m3's smallest code is
+// fp16's.  Where the V scales of a CTA's pages lie further apart (an all-zero block, whose scale is
+// 1, beside values below 2^-7 is enough), V and P are bf16 over its pages too, with V at its true
+// size: bf16 has fp32's exponents, so a page counts by its probability and its values whatever lies
+// beside it, and P keeps 8 bits.  Tail rows and speculative rows are bf16 as they are: those tiles,
+// the last of a sequence, run the same way in bf16.
 //
 // Both operands that come from the cache are converted in registers on their way from the raw
 // stages to tensor memory, K by rows and V through transposing 8-bit ldmatrix loads, so a
@@ -74,6 +78,7 @@ constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no
                                        // score passes it
 constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
                                        // (fp16 ends at 65504)
+constexpr float kLeastRel = 1.f / 32768;   // least V scale, relative to the largest, that fp16 holds
 
 // COLS: rows of one softmax group (a multiple of 8).  ALT: two groups take tiles in turn (all
 // rows each); else four take every tile, a quarter of the rows each.
@@ -139,9 +144,10 @@ struct Scalars {
     alignas(16) float neg_ref[128];   // -(reference) of every row (64 g + row in ALT): P = 2^(s + neg_ref)
     alignas(16) float corr[128];
     float part[512];         // per softmax warp: a number for each of its rows
-    float wmax[16], wunit[16];
+    float wmax[16], wunit[16], wlow[16];
     int fail[4];             // a softmax group's failed wait
-    float unit;              // largest scale of V among the split's pages: O = unit * O^T
+    float unit;              // largest scale of V among the split's pages: O = unit * O^T; or -1 where
+                             // they lie too far apart for fp16 (V and P of pages in bf16, O = O^T)
     int flagged;             // elements of the tail rows' V that are not finite
     int64_t flagged_at[kFlagged];      // row * d + dimension
 };
@@ -353,6 +359,33 @@ __device__ __forceinline__ void ldmatrix_t_b8_x2(uint32_t addr, uint32_t (&r)[4]
                  : "memory");
 }
 
+// V of a tile of a wide split (its V scales too far apart for fp16) into tensor memory: bf16 at its
+// true size, by the same walk as the fp16 one, a load at a time.  A call, because the same code inside
+// the converters' loop takes 2 % of the time of splits that never reach it (120K chain 46.4 against
+// 47.4 us).  It needs 32 registers at most, fewer than any role of the kernel holds.
+template <int D>
+static __device__ __noinline__ void wide_v_tile(uint32_t src, uint32_t piece0, uint32_t swizzle, uint32_t dst,
+                                                float unit0, float unit1, bool two) {
+#pragma unroll 1
+    for (int hm = 0; hm < D / 16; ++hm) {
+        const int h = hm >> 2, m = hm & 3;              // 16 dimensions, 32 keys
+        const uint32_t piece = ((piece0 + (uint32_t)h) ^ swizzle) << 4;
+        uint32_t r[4] = {0, 0, 0, 0}, w[8];
+        if (m < 2 || two)
+            ldmatrix_t_b8_x2(src + (uint32_t)((m >> 1) * 2 * kPageTokens * D + (m & 1) * 32 * D) + piece, r);
+        const float s = m < 2 ? unit0 : unit1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint2 y = e4m3x4_to_f16x4(r[e]);
+            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&y.x));
+            const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&y.y));
+            w[2 * e] = bf16x2(a.x * s, a.y * s);
+            w[2 * e + 1] = bf16x2(c.x * s, c.y * s);
+        }
+        tmem_st_16x256b_x2(dst + ((uint32_t)(16 * h) << 16) + (uint32_t)(16 * m), w);
+    }
+}
+
 // Sums of v[0..7] over the warp; lane l returns the one of column l / 4 (halving the columns
 // a lane carries at each of the first three exchanges: 9 shuffles instead of 40).
 __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
@@ -542,6 +575,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 return true;
             };
             bool ok = wait(at(offsetof(Scalars, q_full)), 0, kBarQ);
+            // tiles whose P and V are fp16
+            const int f16_tiles = ok && __reduce_or_sync(0xffffffffu, sc->unit < 0.f ? 1u : 0u) ? 0 : page_tiles;
             ok = ok && scores(0);
             if (tiles > 1) ok = ok && scores(1);
 #pragma unroll 1
@@ -556,7 +591,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const uint32_t dO = tm + L::kTmemO + (uint32_t)pb * L::kNCols;
                 const uint32_t aV = tm + L::kTmemV + (uint32_t)(64 * (i % VB));
                 const uint64_t bP = pd + (uint64_t)(pb * (L::kPBuf >> 4));
-                const uint32_t id = i < page_tiles ? kO16 : kOb;
+                const uint32_t id = i < f16_tiles ? kO16 : kOb;
                 const uint32_t add = i < (ALT ? 2 : 1) ? 0u : 1u;   // the group's first product starts O^T
                 mma_chain_if<kQ8Tile / 16, 128, 0>(leader, dO, aV, bP, id, add);
                 mma_commit_if(leader, at(offsetof(Scalars, pv_done), i & 1));
@@ -587,18 +622,20 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
         const uint32_t v_src = opaque(smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128));
         // page ids of the split, and the scales of V of a tile's two pages as fp16 pairs relative
-        // to the largest of the split (the unit of O^T), 32 tiles at a time like the softmax warps'
+        // to the largest of the split (the unit of O^T), or in fp32 as they are where the split is
+        // wide, 32 tiles at a time like the softmax warps'
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
-        float inv_unit = 1.f;
+        float inv_unit = 1.f;                           // -1 in a wide split
         auto page_ids = [&](int i) -> int2 {
             return make_int2(2 * i < my_pages ? __ldg(ids + 2 * i) : 0,
                              2 * i + 1 < my_pages ? __ldg(ids + 2 * i + 1) : 0);
         };
         auto v_units = [&](int i, int2 id) -> uint2 {                 // 0 where there is no page
-            const float x = 2 * i < my_pages ? v_scale(p, id.x, g) * inv_unit : 0.f;
-            const float y = 2 * i + 1 < my_pages ? v_scale(p, id.y, g) * inv_unit : 0.f;
-            return make_uint2(f16x2(x, x), f16x2(y, y));
+            const float x = 2 * i < my_pages ? v_scale(p, id.x, g) * fabsf(inv_unit) : 0.f;
+            const float y = 2 * i + 1 < my_pages ? v_scale(p, id.y, g) * fabsf(inv_unit) : 0.f;
+            return inv_unit < 0.f ? make_uint2(__float_as_uint(x), __float_as_uint(y))
+                                  : make_uint2(f16x2(x, x), f16x2(y, y));
         };
         int2 id_next = make_int2(0, 0);
         uint2 unit_now = make_uint2(0, 0), unit_next = make_uint2(0, 0);
@@ -613,6 +650,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         }
         int st = 0;
         uint32_t lap = 0;
+        const int n_f16 = inv_unit > 0.f ? n_page : 0;  // tiles whose V is fp16
 #pragma unroll 1
         for (int i = 0; i < n && ok; ++i) {
             const bool paged = i < n_page;
@@ -689,7 +727,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t dst = lanes + L::kTmemV + (uint32_t)(64 * (i % VB));
-                if (__builtin_expect(paged, 1)) {
+                if (__builtin_expect(i < n_f16, 1)) {
                     const bool two = 2 * i + 1 < my_pages;
                     const uint32_t src = v_src + (uint32_t)(st * L::kRawBytes);
 #pragma unroll 1
@@ -711,7 +749,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         }
                         tmem_st_16x256b_x8(dst + ((uint32_t)(16 * h) << 16), w);
                     }
-                } else {
+                } else if (!paged) {
                     // One dimension to a thread.  Elements that are not finite would turn hidden
                     // keys' zero probabilities into NaN: they are zero here and join the rows
                     // that see them at the end.
@@ -740,6 +778,10 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         __syncwarp();
                         tmem_st8(dst + (uint32_t)(8 * j), w);
                     }
+                } else {
+                    wide_v_tile<D>(v_src + (uint32_t)(st * L::kRawBytes),
+                                   (uint32_t)(v_piece + (D == 128 ? 2 * q4 : q4)), (uint32_t)(v_line & 7),
+                                   dst, __uint_as_float(unit0), __uint_as_float(unit1), 2 * i + 1 < my_pages);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -809,10 +851,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
 #pragma unroll
         for (int e = 0; e < kQPieces; ++e)
             qv[e] = tid + e * T < Rb * (D / 8) ? Qg[tid + e * T] : make_uint4(0, 0, 0, 0);
-        float unit = tid < my_pages ? v_scale(p, page_unit, g) : 0.f;
+        float unit = tid < my_pages ? v_scale(p, page_unit, g) : 0.f;   // largest and smallest
+        float low = tid < my_pages ? unit : INFINITY;
         float scale_now = scale_of(page_first), scale_next = 0.f;
 #pragma unroll 1
-        for (int j = tid + T; j < my_pages; j += T) unit = fmaxf(unit, v_scale(p, __ldg(ids + j), g));
+        for (int j = tid + T; j < my_pages; j += T) {
+            const float s = v_scale(p, __ldg(ids + j), g);
+            unit = fmaxf(unit, s);
+            low = fminf(low, s);
+        }
         uint32_t q_bits = 0;                            // largest finite magnitude (bits order as values)
 #pragma unroll
         for (int e = 0; e < kQPieces; ++e) {
@@ -825,10 +872,12 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         }
         float q_top = __uint_as_float(q_bits << 16);
         unit = warp_max(unit);
+        low = -warp_max(-low);
         q_top = warp_max(q_top);
         if (lane == 0) {
             sc->wmax[warp] = q_top;
             sc->wunit[warp] = unit;
+            sc->wlow[warp] = low;
         }
         asm volatile("barrier.cta.sync 5, %0;" ::"n"(T) : "memory");
         unit = q_top = 0.f;
@@ -836,8 +885,9 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         for (int i = 0; i < 4 * L::kGroups; ++i) {
             q_top = fmaxf(q_top, sc->wmax[i]);
             unit = fmaxf(unit, sc->wunit[i]);
+            low = fminf(low, sc->wlow[i]);
         }
-        if (!(unit > 0.f)) unit = 1.f;
+        unit = low < unit * kLeastRel ? -1.f : unit > 0.f ? unit : 1.f;
         if (tid == 0) sc->unit = unit;
         // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
         const int q_exp = max(min(14 - ((int)(__float_as_uint(q_top) >> 23) - 127), 100), -126);
@@ -1004,7 +1054,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             __syncwarp();
             if (lane == 0) arrive(at(offsetof(Scalars, s_free), u));
             uint32_t pk[COLS / 2];
-            if (__builtin_expect(paged, 1)) {
+            if (__builtin_expect(paged && unit > 0.f, 1)) {
 #pragma unroll
                 for (int c = 0; c < COLS / 2; ++c) {
                     const float2 e = make_float2(ex2(x[c].x), ex2(x[c].y));
@@ -1012,7 +1062,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     pk[c] = f16x2(e.x, e.y);
                 }
             } else {
-                const float2 vm = make_float2(1.f / unit, 1.f / unit);   // V as it is: P takes the unit
+                const float v1 = 1.f / fabsf(unit);     // V as it is: P takes the unit
+                const float2 vm = make_float2(v1, v1);
 #pragma unroll
                 for (int c = 0; c < COLS / 2; ++c) {
                     const float2 e = make_float2(ex2(x[c].x), ex2(x[c].y));
@@ -1070,8 +1121,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     const float m = fmaxf(s0 != 0.f ? m0 : -kNoKey, s1 != 0.f ? m1 : -kNoKey);
                     const float w0 = s0 != 0.f ? ex2(m0 - m) : 0.f, w1 = s1 != 0.f ? ex2(m1 - m) : 0.f;
                     const float s = s0 * w0 + s1 * w1;
-                    sc->corr[r] = w0 * unit;
-                    sc->corr[64 + r] = w1 * unit;
+                    sc->corr[r] = w0 * fabsf(unit);
+                    sc->corr[64 + r] = w1 * fabsf(unit);
                     if (r < Rb)
                         *reinterpret_cast<float2*>(p.part_ml + (slot + r) * 2) =
                             make_float2(m == -kNoKey && s == 0.f ? -INFINITY : m, s);
@@ -1107,7 +1158,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
-                        if (mine && c0 + 8 * ch + c < Rb) dst[c * D] = __uint_as_float(o[c]) * unit;
+                        if (mine && c0 + 8 * ch + c < Rb) dst[c * D] = __uint_as_float(o[c]) * fabsf(unit);
                 }
             }
             const int flagged = sc->flagged;
