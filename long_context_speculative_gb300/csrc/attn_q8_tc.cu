@@ -16,13 +16,15 @@
 // power of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to
 // 2^-30 of that keep all 8 bits of a bf16).  P is fp16 of 2^(s - ref), 2^7 at the reference
 // and below 2^15, so it keeps 11 bits down to 2^-21 of the row's largest and fades out below
-// 2^-31.  V takes its page's scale relative to the largest scale of the CTA's pages, which
-// multiplies O at the end: exact for powers of two down to 2^-15, where e4m3's smallest code is
-// fp16's.  Where the V scales of a CTA's pages lie further apart (an all-zero block, whose scale is
-// 1, beside values below 2^-7 is enough), V and P are bf16 over its pages too, with V at its true
-// size: bf16 has fp32's exponents, so a page counts by its probability and its values whatever lies
-// beside it, and P keeps 8 bits.  Tail rows and speculative rows are bf16 as they are: those tiles,
-// the last of a sequence, run the same way in bf16.
+// 2^-31.  V takes its page's scale relative to a unit, the power of two at or below the largest scale
+// of the CTA's pages, which multiplies O at the end: exact for powers of two down to 2^-15, where
+// e4m3's smallest code is fp16's.  Other scales and their products are rounded to fp16, 2^-11 each,
+// as long as the products are normal numbers, down to 2^-5.  Where the V scales of a CTA's pages lie
+// further apart (an all-zero block, whose scale is 1, beside values below 2^-7 is enough), V and P
+// are bf16 over its pages too, with V at its true size: bf16 has fp32's exponents, so a page counts
+// by its probability and its values whatever lies beside it, and P (and V with a scale that is no
+// power of two) keeps 8 bits.  Tail rows and speculative rows are bf16 as they are: those tiles, the
+// last of a sequence, run the same way in bf16.
 //
 // Both operands that come from the cache are converted in registers on their way from the raw
 // stages to tensor memory, K by rows and V through transposing 8-bit ldmatrix loads, so a
@@ -78,7 +80,8 @@ constexpr float kNoKey = 3e38f;        // -(reference) of a row that has seen no
                                        // score passes it
 constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P passes 2^15
                                        // (fp16 ends at 65504)
-constexpr float kLeastRel = 1.f / 32768;   // least V scale, relative to the largest, that fp16 holds
+constexpr float kLeastRel = 1.f / 32768;   // least V scale, relative to the unit, that fp16 holds ...
+constexpr float kOddScale = 1.f / 1024;    // ... of powers of two; others count that much smaller
 
 // COLS: rows of one softmax group (a multiple of 8).  ALT: two groups take tiles in turn (all
 // rows each); else four take every tile, a quarter of the rows each.
@@ -146,8 +149,8 @@ struct Scalars {
     float part[512];         // per softmax warp: a number for each of its rows
     float wmax[16], wunit[16], wlow[16];
     int fail[4];             // a softmax group's failed wait
-    float unit;              // largest scale of V among the split's pages: O = unit * O^T; or -1 where
-                             // they lie too far apart for fp16 (V and P of pages in bf16, O = O^T)
+    float unit;              // power of two below the largest V scale of the split: O = unit * O^T; or -1
+                             // where they lie too far apart for fp16 (V and P of pages in bf16, O = O^T)
     int flagged;             // elements of the tail rows' V that are not finite
     int64_t flagged_at[kFlagged];      // row * d + dimension
 };
@@ -302,6 +305,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// A V scale as the choice between fp16 and bf16 counts it.
+__device__ __forceinline__ float counted(float scale) {
+    return (__float_as_uint(scale) & 0x7fffffu) ? scale * kOddScale : scale;
+}
 // Scale of V of a page (an id outside the pool, which the producer flags, reads as page 0).
 __device__ __forceinline__ float v_scale(const AttnQ8Params& p, int page, int g) {
     const int id = (unsigned)page < (unsigned)p.n_pages ? page : 0;
@@ -622,8 +629,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
         const uint32_t v_src = opaque(smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128));
         // page ids of the split, and the scales of V of a tile's two pages as fp16 pairs relative
-        // to the largest of the split (the unit of O^T), or in fp32 as they are where the split is
-        // wide, 32 tiles at a time like the softmax warps'
+        // to the unit of O^T, or in fp32 as they are where the split is wide, 32 tiles at a time like
+        // the softmax warps'
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
         float inv_unit = 1.f;                           // -1 in a wide split
@@ -852,13 +859,13 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         for (int e = 0; e < kQPieces; ++e)
             qv[e] = tid + e * T < Rb * (D / 8) ? Qg[tid + e * T] : make_uint4(0, 0, 0, 0);
         float unit = tid < my_pages ? v_scale(p, page_unit, g) : 0.f;   // largest and smallest
-        float low = tid < my_pages ? unit : INFINITY;
+        float low = tid < my_pages ? counted(unit) : INFINITY;
         float scale_now = scale_of(page_first), scale_next = 0.f;
 #pragma unroll 1
         for (int j = tid + T; j < my_pages; j += T) {
             const float s = v_scale(p, __ldg(ids + j), g);
             unit = fmaxf(unit, s);
-            low = fminf(low, s);
+            low = fminf(low, counted(s));
         }
         uint32_t q_bits = 0;                            // largest finite magnitude (bits order as values)
 #pragma unroll
@@ -887,6 +894,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             unit = fmaxf(unit, sc->wunit[i]);
             low = fminf(low, sc->wlow[i]);
         }
+        unit = __uint_as_float(__float_as_uint(unit) & 0x7f800000u);
         unit = low < unit * kLeastRel ? -1.f : unit > 0.f ? unit : 1.f;
         if (tid == 0) sc->unit = unit;
         // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)

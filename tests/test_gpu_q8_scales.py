@@ -135,3 +135,32 @@ def test_small_pages_that_hold_the_probability(dtype, log2_ratio):
         Q = _queries(8, n, d, dtype, seed=d).abs()
         _run(c, Q, _p(dtype))
         _run(c, Q, _p(dtype), rep=76 if dtype == BF16 else 2)
+
+
+# ---------------------------------------------------------------------------
+# Scales that are no powers of two
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("log2_ratio", [0, 3, 5, 6, 9, 14, 15, 20, 30])
+def test_scales_that_are_no_powers_of_two(dtype, log2_ratio):
+    # Values code * scale are rounded: twice to fp16 (2^-11 each) where no such scale of a block
+    # lies further than 2^5 below its largest, else once to bf16 (2^-8) together with the
+    # probabilities.  Equal codes in a dimension, down to e4m3's smallest: no rounding averages out.
+    n, d = 3, 128
+    near = log2_ratio <= 5
+    p_round = 0.0 if dtype == F32 else 2.0 ** -11 if near else 2.0 ** -8
+    v_round = 2.0 ** -24 if dtype == F32 else 2.0 ** -10 + 2.0 ** -22 if near else 2.0 ** -8
+    for factor in (1.4, 4 / 3, 1.9990234, 1 + 2.0 ** -12):
+        c, order = _case(dtype, d, 12, 0, n, seed=log2_ratio)
+        c["scales"][:, :, 1] = factor * 2.0 ** -log2_ratio
+        v = (2.0 ** -9 * torch.arange(1, d + 1) * torch.tensor([1.0, -1.0]).repeat(d // 2)).expand(64, d)
+        v = v.to(c["pages"].dtype)
+        c["pages"][:, :, 1] = v
+        c["pages"][order[5], :, 1] = torch.zeros((64, d)).to(c["pages"].dtype)
+        c["scales"][order[5], :, 1] = 1.0                  # the largest, with nothing in it
+        if log2_ratio == 0:
+            c["scales"][order[5], :, 1] = factor
+        c["V"] *= 0                                        # the pages' roundings alone
+        _run(c, _queries(8, n, d, dtype, seed=3), p_round, v_round)
+        _run(c, _queries(8, n, d, dtype, seed=4), p_round, v_round, rep=76 if dtype == BF16 else 2)
