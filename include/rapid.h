@@ -744,8 +744,8 @@ size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_
  * are powers of two (rapid_kv_seal's are), and the probabilities are rounded to
  * it: fp16 over pages, bf16 over tail rows, and bf16 over pages too where the V
  * scales of the pages that one block of the kernel takes (a part of one sequence
- * and head) lie more than 2^15 apart, or one that is no power of two more than
- * 2^5 below the largest.  V with such a scale is rounded by at most 2^-10 of
+ * and head) lie more than 2^15 apart, one that is no power of two more than 2^5
+ * below the largest, or the largest outside [2^-32, 2^32].  V with such a scale is rounded by at most 2^-10 of
  * itself with fp16 and 2^-8 with bf16; K's scale is applied in fp32.
  *
  * Errors: those of rapid_verify_attn, and RAPID_EINVAL for n_pages < 1, n_pages

@@ -20,11 +20,12 @@
 // of the CTA's pages, which multiplies O at the end: exact for powers of two down to 2^-15, where
 // e4m3's smallest code is fp16's.  Other scales and their products are rounded to fp16, 2^-11 each,
 // as long as the products are normal numbers, down to 2^-5.  Where the V scales of a CTA's pages lie
-// further apart (an all-zero block, whose scale is 1, beside values below 2^-7 is enough), V and P
-// are bf16 over its pages too, with V at its true size: bf16 has fp32's exponents, so a page counts
-// by its probability and its values whatever lies beside it, and P (and V with a scale that is no
-// power of two) keeps 8 bits.  Tail rows and speculative rows are bf16 as they are: those tiles, the
-// last of a sequence, run the same way in bf16.
+// further apart (an all-zero block, whose scale is 1, beside values below 2^-7 is enough), or the
+// unit is so far from 1 that the tail rows' P, which are divided by it, could leave fp32's range, V
+// and P are bf16 over its pages too, with V at its true size: bf16 has fp32's exponents, so a page
+// counts by its probability and its values whatever lies beside it, and P (and V with a scale that is
+// no power of two) keeps 8 bits.  Tail rows and speculative rows are bf16 as they are: those tiles,
+// the last of a sequence, run the same way in bf16.
 //
 // Both operands that come from the cache are converted in registers on their way from the raw
 // stages to tensor memory, K by rows and V through transposing 8-bit ldmatrix loads, so a
@@ -82,6 +83,7 @@ constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P p
                                        // (fp16 ends at 65504)
 constexpr float kLeastRel = 1.f / 32768;   // least V scale, relative to the unit, that fp16 holds ...
 constexpr float kOddScale = 1.f / 1024;    // ... of powers of two; others count that much smaller
+constexpr float kMostUnit = 4294967296.f;  // 2^32: a unit past it or below its reciprocal is not used
 
 // COLS: rows of one softmax group (a multiple of 8).  ALT: two groups take tiles in turn (all
 // rows each); else four take every tile, a quarter of the rows each.
@@ -150,7 +152,7 @@ struct Scalars {
     float wmax[16], wunit[16], wlow[16];
     int fail[4];             // a softmax group's failed wait
     float unit;              // power of two below the largest V scale of the split: O = unit * O^T; or -1
-                             // where they lie too far apart for fp16 (V and P of pages in bf16, O = O^T)
+                             // in a wide split (V and P of its pages in bf16, O = O^T)
     int flagged;             // elements of the tail rows' V that are not finite
     int64_t flagged_at[kFlagged];      // row * d + dimension
 };
@@ -366,7 +368,7 @@ __device__ __forceinline__ void ldmatrix_t_b8_x2(uint32_t addr, uint32_t (&r)[4]
                  : "memory");
 }
 
-// V of a tile of a wide split (its V scales too far apart for fp16) into tensor memory: bf16 at its
+// V of a tile of a wide split (its V scales too far apart, or from 1) into tensor memory: bf16 at its
 // true size, by the same walk as the fp16 one, a load at a time.  A call, because the same code inside
 // the converters' loop takes 2 % of the time of splits that never reach it (120K chain 46.4 against
 // 47.4 us).  It needs 32 registers at most, fewer than any role of the kernel holds.
@@ -895,7 +897,8 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             low = fminf(low, sc->wlow[i]);
         }
         unit = __uint_as_float(__float_as_uint(unit) & 0x7f800000u);
-        unit = low < unit * kLeastRel ? -1.f : unit > 0.f ? unit : 1.f;
+        if (my_pages <= 0) unit = 1.f;
+        else if (low < unit * kLeastRel || !(unit * kMostUnit >= 1.f && unit <= kMostUnit)) unit = -1.f;
         if (tid == 0) sc->unit = unit;
         // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
         const int q_exp = max(min(14 - ((int)(__float_as_uint(q_top) >> 23) - 127), 100), -126);

@@ -164,3 +164,21 @@ def test_scales_that_are_no_powers_of_two(dtype, log2_ratio):
         c["V"] *= 0                                        # the pages' roundings alone
         _run(c, _queries(8, n, d, dtype, seed=3), p_round, v_round)
         _run(c, _queries(8, n, d, dtype, seed=4), p_round, v_round, rep=76 if dtype == BF16 else 2)
+
+
+# ---------------------------------------------------------------------------
+# Scales far from one, beside tail rows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("log2_scale", [-126, -110, -64, -33, -32, 32, 33, 64, 110, 119])
+def test_tail_rows_beside_far_scales(dtype, log2_scale):
+    # the tail's values are of order one; pages of a large scale hold zeros
+    n, d = 4, 128
+    c, order = _case(dtype, d, 5, 40, n, seed=7)
+    c["scales"][:, :, 1] = 2.0 ** log2_scale
+    if log2_scale > 0:
+        c["pages"][:, :, 1] = torch.zeros(c["pages"][:, :, 1].shape).to(c["pages"].dtype)
+    Q = _queries(8, n, d, dtype, seed=8) * 4      # probabilities of very different sizes
+    _run(c, Q, _p(dtype))
+    _run(c, Q, _p(dtype), rep=76 if dtype == BF16 else 2)
