@@ -727,8 +727,10 @@ _held = threading.local()
 
 def _scratch(dev, nbytes):
     """Scratch for one call on the current stream.  It is kept for the next call that the same
-    host thread makes on the same stream, which the stream orders behind this one; a call that
-    is being captured gets memory of its own, because its graph may run on any stream."""
+    host thread makes on the same stream, which the stream orders behind this one, until the
+    thread ends; a call that is being captured gets memory of its own, because its graph may run
+    on any stream.  A stream is known by its handle, as in torch's allocator: one that was made
+    outside torch may be destroyed only after its work is done."""
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
     key = (dev, torch._C._cuda_getCurrentRawStream(dev))
@@ -742,7 +744,11 @@ def _scratch(dev, nbytes):
 def verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
                    spec_mask=None, softmax_scale=0.0, out=None, lse=None, workspace=None,
                    stream=None):
-    """O [B,Hq,n_q,d] (dtype of Q) and LSE [B,Hq,n_q] float32 over an 8-bit history."""
+    """O [B,Hq,n_q,d] (dtype of Q) and LSE [B,Hq,n_q] float32 over an 8-bit history.
+
+    Without a workspace the call uses scratch that the host thread keeps for each stream (a few
+    megabytes); do not destroy a stream made outside torch while its calls are pending.  Calls
+    that may overlap in other ways (two graphs of one memory pool) need workspaces of their own."""
     if stream is not None:
         with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
             return verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len,
