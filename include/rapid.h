@@ -739,14 +739,16 @@ size_t rapid_verify_attn_q8_workspace_size(int B, int Hq, int Hkv, int d, int n_
  *             their own
  *
  * Rows of the tail caches that a query does not see have no effect on it,
- * whatever they hold.  With bf16 the products run on tensor cores with fp32
- * sums; the values are exact in the products' operand type where their scales
- * are powers of two (rapid_kv_seal's are), and the probabilities are rounded to
- * it: fp16 over pages, bf16 over tail rows, and bf16 over pages too where the V
- * scales of the pages that one block of the kernel takes (a part of one sequence
- * and head) lie more than 2^15 apart, one that is no power of two more than 2^5
- * below the largest, or the largest outside [2^-32, 2^32].  V with such a scale is rounded by at most 2^-10 of
- * itself with fp16 and 2^-8 with bf16; K's scale is applied in fp32.
+ * whatever they hold, and neither has any other query.  With bf16 the products
+ * run on tensor cores with fp32 sums; the values are exact in the products'
+ * operand type where their scales are powers of two (rapid_kv_seal's are), and
+ * the probabilities are rounded to it: fp16 over pages (11 bits down to 2^-21
+ * of the row's largest, nothing below 2^-31), bf16 over tail rows, and bf16
+ * over pages too where the V scales of the pages that one block of the kernel
+ * takes (a part of one sequence and head) lie more than 2^15 apart, one that
+ * is no power of two more than 2^5 below the largest, or the largest outside
+ * [2^-32, 2^32].  V with such a scale is rounded by at most 2^-10 of itself
+ * with fp16 and 2^-8 with bf16; K's scale is applied in fp32.
  *
  * Errors: those of rapid_verify_attn, and RAPID_EINVAL for n_pages < 1, n_pages
  * * Hkv * 128 above 2^31 - 1, max_pages outside [1, RAPID_Q8_MAX_PAGES], B *

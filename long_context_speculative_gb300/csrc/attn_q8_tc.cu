@@ -12,20 +12,25 @@
 // score passes its reference by more than 2^8 (the group of warps votes; the reference of the
 // row then moves, O is rescaled, and the tile is taken again).
 //
-// The 8-bit codes become fp16 exactly, so K and V lose nothing.  Q is held as fp16 times one
-// power of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to
-// 2^-30 of that keep all 8 bits of a bf16).  P is fp16 of 2^(s - ref), 2^7 at the reference
-// and below 2^15, so it keeps 11 bits down to 2^-21 of the row's largest and fades out below
-// 2^-31.  V takes its page's scale relative to a unit, the power of two at or below the largest scale
-// of the CTA's pages, which multiplies O at the end: exact for powers of two down to 2^-15, where
+// The 8-bit codes become fp16 exactly, so K and V lose nothing.  Q is held as fp16 times one power
+// of two for the CTA (its largest magnitude becomes 2^14..2^15, so elements down to 2^-30 of that
+// keep all 8 bits of a bf16).  Where some 16 bytes of Q hold nothing above 2^-20 of its largest (a
+// padded batch's rows may hold anything), or its largest is below 2^-86, Q stays bf16 and K becomes
+// bf16 over the pages too, both exact: no row depends on what another holds.
+//
+// P is fp16 of 2^(s - ref), 2^7 at the reference and below 2^15, so it keeps 11 bits down to 2^-21
+// of the row's largest and fades out below 2^-31.
+//
+// V takes its page's scale relative to a unit, the power of two at or below the largest scale of
+// the CTA's pages, which multiplies O at the end: exact for powers of two down to 2^-15, where
 // e4m3's smallest code is fp16's.  Other scales and their products are rounded to fp16, 2^-11 each,
-// as long as the products are normal numbers, down to 2^-5.  Where the V scales of a CTA's pages lie
-// further apart (an all-zero block, whose scale is 1, beside values below 2^-7 is enough), or the
-// unit is so far from 1 that the tail rows' P, which are divided by it, could leave fp32's range, V
-// and P are bf16 over its pages too, with V at its true size: bf16 has fp32's exponents, so a page
-// counts by its probability and its values whatever lies beside it, and P (and V with a scale that is
-// no power of two) keeps 8 bits.  Tail rows and speculative rows are bf16 as they are: those tiles,
-// the last of a sequence, run the same way in bf16.
+// as long as the products are normal numbers, down to 2^-5.  Where the V scales of a CTA's pages
+// lie further apart (an all-zero block, whose scale is 1, beside values below 2^-7 is enough), or
+// the unit is so far from 1 that the tail rows' P, which are divided by it, could leave fp32's
+// range, V and P are bf16 over its pages too, with V at its true size: bf16 has fp32's exponents,
+// so a page counts by its probability and its values whatever lies beside it, and P (and V with a
+// scale that is no power of two) keeps 8 bits.  Tail rows and speculative rows are bf16 as they
+// are: those tiles, the last of a sequence, run the same way in bf16.
 //
 // Both operands that come from the cache are converted in registers on their way from the raw
 // stages to tensor memory, K by rows and V through transposing 8-bit ldmatrix loads, so a
@@ -43,6 +48,8 @@
 //               tile (load S, compare, vote, exponentials, store P) takes a group 2200 to 2700
 //               cycles, nearly whatever its columns: warps' latencies, not a unit's rate
 //   converters  4 for K and 4 for V
+//   chooser     1: from the softmax warps' maxima of Q and of V's scales, the powers of two that the
+//               fp16 forms are relative to, or that the split is wide (bf16)
 //   producer    1: copies pages (K and V of a page and head are 128 d contiguous bytes)
 //               into a ring of raw stages by TMA
 //   issuer      1: the MMAs, in the order in which their inputs become ready
@@ -83,6 +90,8 @@ constexpr float kMaxLog2P = 15.f;      // ... and the reference moves before P p
                                        // (fp16 ends at 65504)
 constexpr float kLeastRel = 1.f / 32768;   // least V scale, relative to the unit, that fp16 holds ...
 constexpr float kOddScale = 1.f / 1024;    // ... of powers of two; others count that much smaller
+constexpr int kMostQ = 20;                 // log2 of the range of Q's pieces that fp16 takes ...
+constexpr int kLeastQ = -86;               // ... and of its largest
 constexpr float kMostUnit = 4294967296.f;  // 2^32: a unit past it or below its reciprocal is not used
 
 // COLS: rows of one softmax group (a multiple of 8).  ALT: two groups take tiles in turn (all
@@ -94,6 +103,7 @@ struct Plan {
     static constexpr int kConvWarp = 4 * kGroups;
     static constexpr int kSoftmaxThreads = 128 * kGroups;
     static constexpr int kProducerWarp = kConvWarp + 8;              // 4 for K, 4 for V
+    static constexpr int kChooserWarp = kProducerWarp + 1;
     static constexpr int kMmaWarp = kProducerWarp + 3;
     static constexpr int kThreads = 32 * (kProducerWarp + 4);
     // A block starts with kLaunchRegs registers a thread; its warpgroups share them out anew.
@@ -149,10 +159,13 @@ struct Scalars {
     alignas(16) float neg_ref[128];   // -(reference) of every row (64 g + row in ALT): P = 2^(s + neg_ref)
     alignas(16) float corr[128];
     float part[512];         // per softmax warp: a number for each of its rows
-    float wmax[16], wunit[16], wlow[16];
+    float wunit[16], wlow[16];
+    uint16_t wmax[16], wleast[16];
     int fail[4];             // a softmax group's failed wait
+    int q_wide;              // Q as it is, K of the pages in bf16
+    float q_mul;             // else the power of two of Q's fp16 form
     float unit;              // power of two below the largest V scale of the split: O = unit * O^T; or -1
-                             // in a wide split (V and P of its pages in bf16, O = O^T)
+                             // where they are wide (V and P of the pages in bf16, O = O^T)
     int flagged;             // elements of the tail rows' V that are not finite
     int64_t flagged_at[kFlagged];      // row * d + dimension
 };
@@ -368,33 +381,6 @@ __device__ __forceinline__ void ldmatrix_t_b8_x2(uint32_t addr, uint32_t (&r)[4]
                  : "memory");
 }
 
-// V of a tile of a wide split (its V scales too far apart, or from 1) into tensor memory: bf16 at its
-// true size, by the same walk as the fp16 one, a load at a time.  A call, because the same code inside
-// the converters' loop takes 2 % of the time of splits that never reach it (120K chain 46.4 against
-// 47.4 us).  It needs 32 registers at most, fewer than any role of the kernel holds.
-template <int D>
-static __device__ __noinline__ void wide_v_tile(uint32_t src, uint32_t piece0, uint32_t swizzle, uint32_t dst,
-                                                float unit0, float unit1, bool two) {
-#pragma unroll 1
-    for (int hm = 0; hm < D / 16; ++hm) {
-        const int h = hm >> 2, m = hm & 3;              // 16 dimensions, 32 keys
-        const uint32_t piece = ((piece0 + (uint32_t)h) ^ swizzle) << 4;
-        uint32_t r[4] = {0, 0, 0, 0}, w[8];
-        if (m < 2 || two)
-            ldmatrix_t_b8_x2(src + (uint32_t)((m >> 1) * 2 * kPageTokens * D + (m & 1) * 32 * D) + piece, r);
-        const float s = m < 2 ? unit0 : unit1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint2 y = e4m3x4_to_f16x4(r[e]);
-            const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&y.x));
-            const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&y.y));
-            w[2 * e] = bf16x2(a.x * s, a.y * s);
-            w[2 * e + 1] = bf16x2(c.x * s, c.y * s);
-        }
-        tmem_st_16x256b_x2(dst + ((uint32_t)(16 * h) << 16) + (uint32_t)(16 * m), w);
-    }
-}
-
 // Sums of v[0..7] over the warp; lane l returns the one of column l / 4 (halving the columns
 // a lane carries at each of the first three exchanges: 9 shuffles instead of 40).
 __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
@@ -409,6 +395,84 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
     float s = (h1 ? c[1] : c[0]) + __shfl_xor_sync(0xffffffffu, h1 ? c[0] : c[1], 4);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     return s + __shfl_xor_sync(0xffffffffu, s, 1);
+}
+
+// The pages of a wide split, K or V, as bf16 into tensor memory: K where the pieces of Q are too far
+// apart, V at its true size where the V scales are too far apart or too far from 1.  The converters'
+// loop over again, apart from theirs because the same code inside it costs the splits that never
+// reach it 1 to 5 us.  Two conversions more for every code than fp16 takes: a 120K chain whose V is
+// wide 89 us, whose Q is 70 (47 otherwise), 64 heads over 8 at 128K 103 and 97 (76), the tree 225 and
+// 210 (187), in a graph.  Returns the code of a wait that gave up, or 0.
+template <int D, int COLS, bool ALT>
+static __device__ __noinline__ unsigned wide_tiles(const AttnQ8Params& p, const int32_t* ids, int pages, int g,
+                                                   int tiles, bool do_k, uint32_t sb, uint32_t src,
+                                                   uint32_t piece0, uint32_t lanes) {
+    using L = Plan<D, COLS, ALT>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t swizzle = (uint32_t)(D == 128 ? lane : lane >> 1) & 7u;   // of V's lines
+    unsigned failed = 0;
+    int st = 0;
+    uint32_t lap = 0;
+    auto bar = [&](size_t offset, int i) -> uint32_t { return sb + (uint32_t)offset + 8u * (uint32_t)i; };
+    auto scale_of = [&](int page) -> float {            // K's scale is the softmax warps' business
+        return do_k ? 1.f : page < pages ? v_scale(p, __ldg(ids + page), g) : 0.f;
+    };
+    float next0 = scale_of(0), next1 = scale_of(1);
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+        const float s0 = next0, s1 = next1;
+        next0 = scale_of(2 * i + 2);
+        next1 = scale_of(2 * i + 3);
+        const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
+        const int bufs = do_k ? L::kKBufs : L::kVBufs, j = i - bufs;
+        bool ok = wait_for(bar(offsetof(Scalars, raw_full), st), lap, code | kBarRawFull, failed);
+        if (ok && j >= 0)                               // the product that read this buffer last
+            ok = wait_for(bar(do_k ? offsetof(Scalars, s_full) : offsetof(Scalars, pv_done), j & 1),
+                          (uint32_t)((j >> 1) & 1), code | (do_k ? kBarS : kBarPv), failed);
+        if (!__all_sync(0xffffffffu, ok)) return failed ? failed : code;
+        tc_fence_after();
+        const uint32_t from = src + (uint32_t)(st * L::kRawBytes);
+        const uint32_t dst = lanes + (do_k ? L::kTmemK : L::kTmemV) + (uint32_t)(64 * (i % bufs));
+        const bool two = 2 * i + 1 < pages;
+#pragma unroll 1
+        for (int h = 0; h < D / 64; ++h) {
+            // K: 16 codes of the thread's key, 8 columns.  V: 32 keys x 16 dimensions, 16 columns of
+            // 16 lanes; a page that is not there reads as zeros.
+            uint32_t r[4][4] = {};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if (do_k) {
+                    const uint4 v = lds_u4(from ^ (uint32_t)((4 * h + m) << 4));
+                    r[m][0] = v.x; r[m][1] = v.y; r[m][2] = v.z; r[m][3] = v.w;
+                } else if (m < 2 || two) {
+                    ldmatrix_t_b8_x2(from + (uint32_t)((m >> 1) * L::kPageBytes + (m & 1) * 32 * D) +
+                                         (((piece0 + (uint32_t)h) ^ swizzle) << 4), r[m]);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float s = m < 2 ? s0 : s1;
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint2 y = e4m3x4_to_f16x4(r[m][e]);
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&y.x));
+                    const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&y.y));
+                    w[2 * e] = bf16x2(a.x * s, a.y * s);
+                    w[2 * e + 1] = bf16x2(c.x * s, c.y * s);
+                }
+                if (do_k) tmem_st8(dst + (uint32_t)(8 * (4 * h + m)), w);
+                else tmem_st_16x256b_x2(dst + ((uint32_t)(16 * h) << 16) + (uint32_t)(16 * m), w);
+            }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(bar(do_k ? offsetof(Scalars, k_full) : offsetof(Scalars, v_full), i % bufs));
+        __syncwarp();
+        if (lane == 0) arrive(bar(offsetof(Scalars, raw_free), st));
+        if (++st == L::kStages) { st = 0; lap ^= 1u; }
+    }
+    return 0;
 }
 
 template <int D, int COLS, bool ALT>
@@ -568,6 +632,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
             const uint64_t pd = sdesc(base + L::kOffP, kQ8Tile * 128, 1024);
             const uint32_t leader = elect_one();
+            int s16_tiles = 0;                          // tiles whose Q and K are fp16
             auto wait = [&](uint32_t bar, uint32_t par, unsigned code) {
                 return __all_sync(0xffffffffu, wait_for(bar, par, kRoleMma | code, failed)) != 0;
             };
@@ -578,14 +643,15 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 tc_fence_after();
                 const uint32_t dS = tm + L::kTmemS + (uint32_t)(j & 1) * L::kNCols;
                 const uint32_t aK = tm + L::kTmemK + (uint32_t)(64 * (j % KB));
-                const uint32_t id = j < page_tiles ? kS16 : kSb;
+                const uint32_t id = j < s16_tiles ? kS16 : kSb;
                 mma_chain_if<D / 16, 2, L::kQBlock / 16 - 8>(leader, dS, aK, qd, id, 0u);
                 mma_commit_if(leader, at(offsetof(Scalars, s_full), j & 1));
                 return true;
             };
             bool ok = wait(at(offsetof(Scalars, q_full)), 0, kBarQ);
-            // tiles whose P and V are fp16
-            const int f16_tiles = ok && __reduce_or_sync(0xffffffffu, sc->unit < 0.f ? 1u : 0u) ? 0 : page_tiles;
+            if (ok && !__reduce_or_sync(0xffffffffu, (uint32_t)sc->q_wide)) s16_tiles = page_tiles;
+            // ... and whose P and V are
+            const int o16_tiles = ok && __reduce_or_sync(0xffffffffu, sc->unit < 0.f ? 1u : 0u) ? 0 : page_tiles;
             ok = ok && scores(0);
             if (tiles > 1) ok = ok && scores(1);
 #pragma unroll 1
@@ -600,7 +666,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 const uint32_t dO = tm + L::kTmemO + (uint32_t)pb * L::kNCols;
                 const uint32_t aV = tm + L::kTmemV + (uint32_t)(64 * (i % VB));
                 const uint64_t bP = pd + (uint64_t)(pb * (L::kPBuf >> 4));
-                const uint32_t id = i < f16_tiles ? kO16 : kOb;
+                const uint32_t id = i < o16_tiles ? kO16 : kOb;
                 const uint32_t add = i < (ALT ? 2 : 1) ? 0u : 1u;   // the group's first product starts O^T
                 mma_chain_if<kQ8Tile / 16, 128, 0>(leader, dO, aV, bP, id, add);
                 mma_commit_if(leader, at(offsetof(Scalars, pv_done), i & 1));
@@ -608,6 +674,30 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
             if (!ok) sc->abort = 1;
             mma_commit_if(leader, at(offsetof(Scalars, drain)));
             wait_for(at(offsetof(Scalars, drain)), 0, kRoleMma | kBarDrain, failed);
+        }
+        else if (warp == L::kChooserWarp) {
+            // ------------------------------ chooser ---------------------------
+            // From the softmax warps' maxima and minima: the unit of O^T, the power of two of Q, and
+            // whether fp16 holds them.  In a warp of its own, because the same lines at the start
+            // of the softmax warps change their loop for the worse (120K chain 49 us).
+            asm volatile("barrier.cta.sync 6, %0;" ::"n"(L::kSoftmaxThreads + 32) : "memory");
+            const bool on = lane < 4 * L::kGroups;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, on ? sc->wmax[lane] : 0u);
+            const uint32_t least = __reduce_min_sync(0xffffffffu, on ? sc->wleast[lane] : 0xffffu) + 1;
+            const float low = -warp_max(on ? -sc->wlow[lane] : -INFINITY);
+            float unit = warp_max(on ? sc->wunit[lane] : 0.f);
+            unit = __uint_as_float(__float_as_uint(unit) & 0x7f800000u);
+            if (n_page == 0) unit = 1.f;
+            else if (low < unit * kLeastRel || !(unit * kMostUnit >= 1.f && unit <= kMostUnit)) unit = -1.f;
+            // Q's largest magnitude, 1.f * 2^k, becomes 1.f * 2^14
+            const int k = (int)(top >> 7) - 127, k_least = (int)(least >> 7) - 127;
+            const bool apart = n_page > 0 && top && (k - k_least > kMostQ || k < kLeastQ);
+            if (lane == 0) {
+                sc->unit = unit;
+                sc->q_wide = apart;
+                sc->q_mul = __uint_as_float((uint32_t)(127 + (apart || !top ? 0 : 14 - k)) << 23);
+            }
+            asm volatile("barrier.cta.arrive 7, %0;" ::"n"(L::kSoftmaxThreads + 32) : "memory");
         }
         if (lane == 0) record(p.err, failed);
     } else if (warp >= L::kConvWarp) {
@@ -631,37 +721,48 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         const int v_piece = D == 128 ? 0 : 4 * (lane & 1);
         const uint32_t v_src = opaque(smem_u32(smem + L::kOffRaw + kPageTokens * D + v_line * 128));
         // page ids of the split, and the scales of V of a tile's two pages as fp16 pairs relative
-        // to the unit of O^T, or in fp32 as they are where the split is wide, 32 tiles at a time like
-        // the softmax warps'
+        // to the unit of O^T, 32 tiles at a time like the softmax warps'
         const int32_t* ids = p.page_table + (int64_t)b * p.max_pages + 2 * t_begin;
         const int my_pages = min(keys.pages - 2 * t_begin, 2 * n_page);   // ids[0, my_pages) exist
-        float inv_unit = 1.f;                           // -1 in a wide split
+        float inv_unit = 1.f;
         auto page_ids = [&](int i) -> int2 {
             return make_int2(2 * i < my_pages ? __ldg(ids + 2 * i) : 0,
                              2 * i + 1 < my_pages ? __ldg(ids + 2 * i + 1) : 0);
         };
         auto v_units = [&](int i, int2 id) -> uint2 {                 // 0 where there is no page
-            const float x = 2 * i < my_pages ? v_scale(p, id.x, g) * fabsf(inv_unit) : 0.f;
-            const float y = 2 * i + 1 < my_pages ? v_scale(p, id.y, g) * fabsf(inv_unit) : 0.f;
-            return inv_unit < 0.f ? make_uint2(__float_as_uint(x), __float_as_uint(y))
-                                  : make_uint2(f16x2(x, x), f16x2(y, y));
+            const float x = 2 * i < my_pages ? v_scale(p, id.x, g) * inv_unit : 0.f;
+            const float y = 2 * i + 1 < my_pages ? v_scale(p, id.y, g) * inv_unit : 0.f;
+            return make_uint2(f16x2(x, x), f16x2(y, y));
         };
         int2 id_next = make_int2(0, 0);
         uint2 unit_now = make_uint2(0, 0), unit_next = make_uint2(0, 0);
-        bool ok = true;
+        bool ok = true, wide = false;
         unsigned failed = 0;
+        if (do_k && n_page > 0) {
+            ok = wait_for(at(offsetof(Scalars, q_full)), 0, kRoleConvert | kBarQ, failed);
+            wide = ok && sc->q_wide;
+        }
         if (do_v && n_page > 0) {
             const int2 id0 = page_ids(lane);
             id_next = page_ids(32 + lane);
             ok = wait_for(at(offsetof(Scalars, q_full)), 0, kRoleConvert | kBarQ, failed);   // the unit is there
             inv_unit = 1.f / sc->unit;
+            wide = ok && inv_unit < 0.f;
             unit_now = v_units(lane, id0);
         }
-        int st = 0;
+        int st = 0, first = 0;
         uint32_t lap = 0;
-        const int n_f16 = inv_unit > 0.f ? n_page : 0;  // tiles whose V is fp16
+        ok = __all_sync(0xffffffffu, ok) != 0;
+        if (__builtin_expect(ok && wide, 0)) {
+            failed = wide_tiles<D, COLS, ALT>(p, ids, my_pages, g, n_page, do_k, sb, do_k ? k_src : v_src,
+                                              (uint32_t)(v_piece + (D == 128 ? 2 * q4 : q4)), lanes);
+            ok = __all_sync(0xffffffffu, failed == 0) != 0;
+            first = n_page;
+            st = n_page % kStages;
+            lap = (uint32_t)(n_page / kStages) & 1u;
+        }
 #pragma unroll 1
-        for (int i = 0; i < n && ok; ++i) {
+        for (int i = first; i < n && ok; ++i) {
             const bool paged = i < n_page;
             const unsigned code = kRoleConvert | (unsigned)(i & 0xffff);
             const int64_t k0 = (int64_t)(t_begin + i - keys.page_tiles) * kQ8Tile;   // tail tile's first row
@@ -736,7 +837,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t dst = lanes + L::kTmemV + (uint32_t)(64 * (i % VB));
-                if (__builtin_expect(i < n_f16, 1)) {
+                if (__builtin_expect(paged, 1)) {
                     const bool two = 2 * i + 1 < my_pages;
                     const uint32_t src = v_src + (uint32_t)(st * L::kRawBytes);
 #pragma unroll 1
@@ -758,7 +859,7 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         }
                         tmem_st_16x256b_x8(dst + ((uint32_t)(16 * h) << 16), w);
                     }
-                } else if (!paged) {
+                } else {
                     // One dimension to a thread.  Elements that are not finite would turn hidden
                     // keys' zero probabilities into NaN: they are zero here and join the rows
                     // that see them at the end.
@@ -787,10 +888,6 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                         __syncwarp();
                         tmem_st8(dst + (uint32_t)(8 * j), w);
                     }
-                } else {
-                    wide_v_tile<D>(v_src + (uint32_t)(st * L::kRawBytes),
-                                   (uint32_t)(v_piece + (D == 128 ? 2 * q4 : q4)), (uint32_t)(v_line & 7),
-                                   dst, __uint_as_float(unit0), __uint_as_float(unit1), 2 * i + 1 < my_pages);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -861,51 +958,49 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
         for (int e = 0; e < kQPieces; ++e)
             qv[e] = tid + e * T < Rb * (D / 8) ? Qg[tid + e * T] : make_uint4(0, 0, 0, 0);
         float unit = tid < my_pages ? v_scale(p, page_unit, g) : 0.f;   // largest and smallest
-        float low = tid < my_pages ? counted(unit) : INFINITY;
         float scale_now = scale_of(page_first), scale_next = 0.f;
+        // largest finite magnitude of Q's pieces (bits order as values), and the least of a piece
+        // that is not all 0, less 1
+        uint32_t q_bits = 0, q_least = 0xffffu;
+#pragma unroll
+        for (int e = 0; e < kQPieces; ++e) {
+            const uint32_t w[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = w[j] & 0x7fffu, y = w[j] >> 16 & 0x7fffu;
+                m = max(m, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
+            }
+            q_bits = max(q_bits, m);
+            q_least = min(q_least, m - 1);
+        }
+        q_bits = __reduce_max_sync(0xffffffffu, q_bits);
+        q_least = __reduce_min_sync(0xffffffffu, q_least);
+        if (lane == 0) {
+            sc->wmax[warp] = (uint16_t)q_bits;
+            sc->wleast[warp] = (uint16_t)q_least;
+        }
+        float low = tid < my_pages ? counted(unit) : INFINITY;
 #pragma unroll 1
         for (int j = tid + T; j < my_pages; j += T) {
             const float s = v_scale(p, __ldg(ids + j), g);
             unit = fmaxf(unit, s);
             low = fminf(low, counted(s));
         }
-        uint32_t q_bits = 0;                            // largest finite magnitude (bits order as values)
-#pragma unroll
-        for (int e = 0; e < kQPieces; ++e) {
-            const uint32_t w[4] = {qv[e].x, qv[e].y, qv[e].z, qv[e].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t x = w[j] & 0x7fffu, y = w[j] >> 16 & 0x7fffu;
-                q_bits = max(q_bits, max(x < 0x7f80u ? x : 0u, y < 0x7f80u ? y : 0u));
-            }
-        }
-        float q_top = __uint_as_float(q_bits << 16);
         unit = warp_max(unit);
         low = -warp_max(-low);
-        q_top = warp_max(q_top);
         if (lane == 0) {
-            sc->wmax[warp] = q_top;
             sc->wunit[warp] = unit;
             sc->wlow[warp] = low;
         }
-        asm volatile("barrier.cta.sync 5, %0;" ::"n"(T) : "memory");
-        unit = q_top = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < 4 * L::kGroups; ++i) {
-            q_top = fmaxf(q_top, sc->wmax[i]);
-            unit = fmaxf(unit, sc->wunit[i]);
-            low = fminf(low, sc->wlow[i]);
-        }
-        unit = __uint_as_float(__float_as_uint(unit) & 0x7f800000u);
-        if (my_pages <= 0) unit = 1.f;
-        else if (low < unit * kLeastRel || !(unit * kMostUnit >= 1.f && unit <= kMostUnit)) unit = -1.f;
-        if (tid == 0) sc->unit = unit;
-        // q_top = 1.f * 2^k becomes 1.f * 2^14 (2^100 is as far as a vanishing Q is raised)
-        const int q_exp = max(min(14 - ((int)(__float_as_uint(q_top) >> 23) - 127), 100), -126);
-        const float q_mul = __uint_as_float((uint32_t)(127 + q_exp) << 23);
+        asm volatile("barrier.cta.arrive 6, %0;" ::"n"(T + 32) : "memory");   // to the chooser ...
+        asm volatile("barrier.cta.sync 7, %0;" ::"n"(T + 32) : "memory");     // ... and its answer
+        unit = sc->unit;
+        const float q_mul = sc->q_mul;
+        const bool q_wide = sc->q_wide;
 #pragma unroll
         for (int e = 0; e < kQPieces; ++e) {
-            if (n_page > 0) {
+            if (n_page > 0 && !q_wide) {
                 uint32_t* w = reinterpret_cast<uint32_t*>(&qv[e]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
