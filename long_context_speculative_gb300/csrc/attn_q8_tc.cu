@@ -57,9 +57,9 @@
 // code, stops issuing, drains and returns.
 //
 // Measured with the merge (us, floor by bytes at 6778 GB/s): 11 queries of 32 heads over 8 KV
-// heads, d = 128: 120K 46.0 (37.2), 32K 21.6 (10.0); one query over 4K 8.4 (1.3); 64 heads
-// over 8, 128K 75 (39.7); d = 64, 120K 38.8 (18.6); a tree of 32 nodes, 28 heads over 4, four
-// histories of 32K to 96K 184 (40; 62 by tensor rate).  Of a call about 9 us are the start (the
+// heads, d = 128: 120K 46.5 (37.2), 32K 21.7 (10.0); one query over 4K 8.7 (1.3); 64 heads
+// over 8, 128K 76 (39.7); d = 64, 120K 39 (18.6); a tree of 32 nodes, 28 heads over 4, four
+// histories of 32K to 96K 187 (40; 62 by tensor rate).  Of a call about 9 us are the start (the
 // lengths, page ids and first pages one after the other, cold code, the first references) and the
 // end (join, merge).  In between, 44 rows take 1400 cycles a tile, what HBM delivers; more
 // rows, and d = 64, whose tiles are half the bytes, are bound by the softmax warps' chain: with
@@ -400,9 +400,9 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8], int lane) {
 // The pages of a wide split, K or V, as bf16 into tensor memory: K where the pieces of Q are too far
 // apart, V at its true size where the V scales are too far apart or too far from 1.  The converters'
 // loop over again, apart from theirs because the same code inside it costs the splits that never
-// reach it 1 to 5 us.  Two conversions more for every code than fp16 takes: a 120K chain whose V is
-// wide 89 us, whose Q is 70 (47 otherwise), 64 heads over 8 at 128K 103 and 97 (76), the tree 225 and
-// 210 (187), in a graph.  Returns the code of a wait that gave up, or 0.
+// reach it 1 to 5 us.  Every code takes two conversions more than to fp16: a 120K chain whose V is
+// wide 83 us, whose Q is 65 (46.5 otherwise), 64 heads over 8 at 128K 98 and 93 (76), the tree 223
+// and 205 (187).  Returns the code of a wait that gave up, or 0.
 template <int D, int COLS, bool ALT>
 static __device__ __noinline__ unsigned wide_tiles(const AttnQ8Params& p, const int32_t* ids, int pages, int g,
                                                    int tiles, bool do_k, uint32_t sb, uint32_t src,

@@ -56,7 +56,8 @@ Q8Plan plan_attn_q8(int B, int Hq, int Hkv, int d, int n_q, int dtype) {
             if (cost < least) { least = cost; S = slots; }
         }
     } else {
-        // CUDA cores: two CTAs on every SM
+        // CUDA cores: slots for two CTAs on every SM, which is what runs at once up to 32 rows; above,
+        // one CTA fits (182 or 214 registers a thread) and the slots are two waves
         S = 2 * sms / (Hkv * ((R + kQ8SimtRows - 1) / kQ8SimtRows));
         if (S > 512) S = 512;
     }

@@ -9,14 +9,18 @@
 // e4m3's NaN and takes no part in the maximum; an all-zero block has scale 1; the exponent
 // is at least -64, so values below 2^-74 become zero.
 //
-// What bounds it is the copy: 2 (or 4) bytes read and 1 written for each element, the rows
-// that stay read and written once.  A CTA holds a whole block (K and V of one head) in
-// registers between the maximum and the store, so the block is read once.
+// What bounds it, while few rows stay, is the copy: 2 (or 4) bytes read and 1 written for each
+// element, the rows that stay read and written once.  A CTA holds a whole block (K and V of one
+// head) in registers between the maximum and the store, so the block is read once.  The blocks that
+// the rows which stay will overwrite, and the moving of those rows, are one CTA's work for each head,
+// 64 rows after 64: with about half of the tail kept it does all of it, and few heads leave most of
+// the machine idle.
 //
-// Measured: 33 blocks of 8 heads on 32 layers, bf16, d = 128, 66.5 us for 420 MB (0.93 of a plain
-// copy); at most one block of each of 4 sequences on 32 layers 5.0 us (floor 2.3: the lengths, the
-// page ids and the rows are read one after the other).  Held as fp32 instead of packed, a block
-// leaves room for two CTAs an SM instead of four: 95 us.
+// Measured: 33 blocks of 8 heads on 32 layers, d = 128, bf16 66.3 us for 420 MB (0.93 of a plain
+// copy), fp32 110 (0.94); at most one block of each of 4 sequences on 32 layers, bf16 4.9 us (floor
+// 2.3: the lengths, the page ids and the rows are read one after the other), fp32 7.8 (3.9).  4096
+// tail rows of which 2000 stay: 32 layers 171 us (139), one layer 60 (4.3; 19 with none kept).  Held
+// as fp32 instead of packed, a bf16 block leaves room for two CTAs an SM instead of four: 95 us.
 #include "common.cuh"
 #include "kv_seal.cuh"
 
