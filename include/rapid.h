@@ -50,6 +50,12 @@
  *   rapid_verify_attn_q8   block, head and side, and verify attention reads
  *                      them, the rows not sealed yet and the step's rows.
  *
+ *   rapid_latent_append  a cache of latent rows, one a token for all heads, in
+ *   rapid_latent_attn  bf16 or 8 bits: norm, rotation and append, the absorbed
+ *   rapid_latent_read  form of verify attention over the rows, reading rows
+ *   rapid_latent_commit  back, keeping an accepted path's rows, and the
+ *   rapid_latent_prefill_attn  expanded form for prompt chunks.
+ *
  *   rapid_retrieval_scores  cosine scores of chunk embeddings against the
  *   rapid_retrieval_select  query, and the budgeted, thresholded choice of
  *                      chunks for the draft's retrieved context ("RAPID ...",
@@ -59,8 +65,8 @@
  *  - All tensor arguments are DEVICE pointers owned by the caller.  The library
  *    allocates nothing on these paths; scratch space is the caller's
  *    `workspace` (size from the matching *_workspace_size call, 256-byte
- *    aligned).  Only rapid_kv_commit, rapid_qkv_append and rapid_kv_seal
- *    write to the KV cache.
+ *    aligned).  Only rapid_kv_commit, rapid_qkv_append, rapid_kv_seal,
+ *    rapid_latent_append and rapid_latent_commit write to a cache.
  *  - Calls are asynchronous and stream-ordered on `stream` (a cudaStream_t
  *    passed as void*; NULL = the legacy default stream).  No call
  *    synchronises the device; results are valid once the stream reaches them.
@@ -355,9 +361,10 @@ int rapid_version(void);
  * (bit 0: a bounded wait for an asynchronous copy or a peer gave up, so the
  * outputs of that call are invalid; bit 1: a kernel found an invalid
  * device-side input -- a history length, parent, draft token or node count
- * out of range in rapid_verify_attn[_q8] / rapid_accept*, a page id outside
+ * out of range in rapid_verify_attn[_q8] / rapid_latent_attn / rapid_accept*, a page id outside
  * the pool, or an input that rapid_kv_commit, rapid_kv_advance,
- * rapid_qkv_append, rapid_kv_seal, rapid_kv_seal_advance or
+ * rapid_qkv_append, rapid_kv_seal, rapid_kv_seal_advance, rapid_latent_append,
+ * rapid_latent_read, rapid_latent_commit, rapid_latent_prefill_attn or
  * rapid_retrieval_select refused, leaving that sequence alone).  Synchronises the device to read the word;
  * clears it when `clear` is non-zero.  Returns -1 if the word could not be
  * read.
@@ -762,6 +769,179 @@ rapid_status rapid_verify_attn_q8(const void* Q, const void* K_tail, const void*
                                   const int32_t* sealed_len, const int32_t* tail_len,
                                   const uint8_t* spec_mask, float softmax_scale, void* O, float* LSE,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* A latent cache: one row a token for all heads                             */
+/* ------------------------------------------------------------------------ */
+
+enum {
+    RAPID_LATENT_DIM = 512,        /* values of the latent vector              */
+    RAPID_LATENT_ROPE_DIM = 64,    /* values of the rotated key behind it      */
+    RAPID_LATENT_ROW = 576,        /* both: keys of the absorbed form          */
+    RAPID_LATENT_HEAD_DIM = 128,   /* plain key values, and values, of a head
+                                      of the expanded form                     */
+    RAPID_LATENT_GROUP = 128,      /* 8-bit rows: codes that share a scale     */
+    RAPID_LATENT_Q8_ROW_BYTES = 656,
+    RAPID_LATENT_MAX_HEADS = 1024,
+    RAPID_LATENT_MAX_ROWS = 1 << 30
+};
+
+/* Element type of a latent cache beside RAPID_DTYPE_BF16: 8-bit rows. */
+enum { RAPID_CACHE_LATENT_Q8 = 2 };
+
+/*
+ * The cache.  A target whose keys and values all come from one latent vector
+ * a token holds, per layer, a cache [B, kv_capacity] of rows:
+ *   RAPID_DTYPE_BF16       576 bf16: the normed latent vector, the rotated key
+ *   RAPID_CACHE_LATENT_Q8  656 bytes: 512 e4m3 codes; 64 bf16, the rotated key;
+ *                          4 floats, value = code * scale, one for 128 codes
+ * A step's n_q rows stand behind the history, as in the caches of
+ * rapid_verify_attn: rapid_latent_append writes them, rapid_latent_attn reads
+ * them under the chain or tree mask, rapid_latent_commit keeps the accepted
+ * ones and rapid_kv_advance grows the history.
+ *
+ * rapid_latent_append takes the rows that a layer's projections give for n
+ * tokens of every sequence (a verify step's nodes, or a prompt chunk of any
+ * length) in one pass:
+ *   c := c / sqrt(mean(c^2) + eps) * kv_weight   (where a weight is given)
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t), t = pos * inv_freq[pair],
+ *                        for the key, and for the 64 values q of every head
+ *   cache[b, prefix_len[b] + i] := the row,   q_out[b, i, h] := the query part
+ * with pos = prefix_len[b] + (row_offset[b][i], or i).  Arithmetic is fp32
+ * with one rounding at the store; the angle is reduced modulo one turn
+ * exactly.  8-bit rows: scale = 2^ceil(log2(max|c| / 448)) of the group (an
+ * exponent below -64 becomes -64; a group of zeros has scale 1), code =
+ * e4m3(c / scale) to nearest even.  A group with a value that is not finite
+ * gets a NaN scale and stands for NaN as a whole.
+ *
+ *  kv         rows of 576 bf16; token i of sequence b starts at element
+ *             b * kv_strides[0] + i * kv_strides[1]
+ *  kv_strides HOST array of two element strides, or NULL: packed [B, n, 576]
+ *  q, q_out   64 bf16 of every head (both or neither NULL); (b, i, h) starts at
+ *             element b * s[0] + i * s[1] + h * s[2] of q and b * s[3] +
+ *             i * s[4] + h * s[5] of q_out.  q_out = q with the same strides
+ *             rotates in place; any other overlap is not allowed
+ *  q_strides  HOST array s of six element strides, or NULL: both packed
+ *             [B, n, H, 64].  Every stride a multiple of 8 (16 bytes)
+ *  kv_weight  device bf16 [512] or NULL: no norm
+ *  inv_freq   device float [32]: radians per position of each pair (elements
+ *             i, i + 32, or 2 i, 2 i + 1 with RAPID_ROPE_INTERLEAVED); an
+ *             infinite or NaN entry does not rotate
+ *  prefix_len device int32 [B]; row_offset device int32 [B, n] or NULL;
+ *  n_rows     device int32 [B] or NULL (n): sequence b has rows [0, n_rows[b]);
+ *             the rows behind them are neither read nor written
+ *
+ * Errors: RAPID_EINVAL for NULL pointers, bad sizes (B * n above 2^31, H
+ * outside [1, RAPID_LATENT_MAX_HEADS] with q, kv_capacity outside [1,
+ * RAPID_LATENT_MAX_ROWS]), a bad eps, flag, cache type, stride or alignment (16
+ * bytes; 4 for index arrays and inv_freq); RAPID_ECUDA on launch failure.  A
+ * sequence whose n_rows is outside [0, n] or whose rows do not fit the cache is
+ * left alone, in q_out too, and bit 1 of the device error word is set.
+ */
+rapid_status rapid_latent_append(const void* kv, const int64_t* kv_strides, const void* q,
+                                 const int64_t* q_strides, int B, int n, int H,
+                                 const void* kv_weight, float eps, const float* inv_freq,
+                                 uint32_t flags, const int32_t* prefix_len,
+                                 const int32_t* row_offset, const int32_t* n_rows, void* q_out,
+                                 void* cache, int cache_dtype, int64_t kv_capacity, void* stream);
+
+/*
+ * Rows of the cache in bf16, for the products that expand them into keys and
+ * values of every head: rows[b, i] := the values of cache[b, first[b] + i],
+ * rounded to bf16 (exact where a row's scales are powers of two).
+ *
+ *  first      device int32 [B] or NULL (0)
+ *  n_rows     device int32 [B] or NULL (n); rows behind them stay as they are
+ *  rows       device bf16 [B, n, 576], 16-byte aligned
+ *
+ * Errors: RAPID_EINVAL for NULL pointers, B < 1, n < 1, B * n above 2^31, a bad
+ * cache type, capacity or alignment; RAPID_ECUDA on launch failure.  A sequence
+ * with n_rows outside [0, n] or rows outside the cache is left alone and bit 1
+ * of the device error word is set.
+ */
+rapid_status rapid_latent_read(const void* cache, int cache_dtype, int B, int64_t kv_capacity, int n,
+                               const int32_t* first, const int32_t* n_rows, void* rows, void* stream);
+
+/*
+ * rapid_kv_commit for latent caches: the accepted path's rows of every layer
+ * move next to the root (row prefix_len[b] + 1 + k takes row prefix_len[b] +
+ * path[b][k]), bit for bit.
+ *
+ *  caches     HOST array of `layers` device pointers, 16-byte aligned
+ *
+ * The other arguments, the errors and the treatment of invalid device inputs
+ * are rapid_kv_commit's (kv_capacity at most RAPID_LATENT_MAX_ROWS).
+ */
+rapid_status rapid_latent_commit(void* const* caches, int layers, int cache_dtype, int B,
+                                 int64_t kv_capacity, int n_q, const int32_t* prefix_len,
+                                 const int32_t* path, const int32_t* n_accepted, void* stream);
+
+/* Bytes of scratch that rapid_latent_attn needs; 0 for sizes it rejects. */
+size_t rapid_latent_attn_workspace_size(int B, int H, int n_q, int64_t kv_capacity, int cache_dtype);
+
+/*
+ * Absorbed attention over a latent cache: verify attention (rapid_verify_attn)
+ * whose keys are the cache rows themselves, one for all heads, and whose
+ * values are their latent vectors:
+ *   s_j = softmax_scale * <Q[b,h,i], [c_j, r_j]>,  O[b,h,i] = sum_j softmax(s)_j c_j.
+ * The caller has multiplied the queries by the key expansion, and multiplies O
+ * by the value expansion.  n_q = 1 is decoding.
+ *
+ *  Q          [B, H, n_q, 576] bf16: the absorbed query, the rotated part
+ *  cache      [B, kv_capacity] rows of cache_dtype
+ *  prefix_len, spec_mask, LSE, workspace  as for rapid_verify_attn
+ *  softmax_scale  <= 0 selects 1/sqrt(192), the width of an expanded head
+ *  O          [B, H, n_q, 512] bf16
+ *
+ * What a query does not see has no effect on it, whatever it holds: rows
+ * behind the mask, rows behind the step, other queries.  A row with a value
+ * that is not finite makes the outputs of the queries that see it NaN.
+ *
+ * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], H outside [1,
+ * RAPID_LATENT_MAX_HEADS], n_q outside [1, RAPID_MAX_NQ], kv_capacity below n_q
+ * or above RAPID_LATENT_MAX_ROWS, a bad cache type or alignment (16 bytes), a
+ * softmax_scale that is not finite; RAPID_ENOMEM for a short workspace;
+ * RAPID_ECUDA on launch failure.  A prefix_len outside [0, kv_capacity - n_q]
+ * is clamped and bit 1 of the device error word is set.
+ */
+rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype, int B, int H, int n_q,
+                               int64_t kv_capacity, const int32_t* prefix_len,
+                               const uint8_t* spec_mask, float softmax_scale, void* O, float* LSE,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Expanded attention of a prompt chunk: n tokens of every sequence behind
+ * prefix_len[b] earlier ones, token i seeing keys [0, prefix_len[b] + i]:
+ *   s_j = softmax_scale * <Q[b,i,h], [K[b,j,h], K_rope[b,j]]>,
+ *   O[b,i,h] = sum_j softmax(s)_j V[b,j,h].
+ *
+ *  Q          bf16 [B, n, H, 192]: 128 plain values, 64 rotated
+ *  K, V       bf16 [B, kv_rows, H, 128]: the expansion of the cache rows
+ *             [0, prefix_len[b] + n_rows[b])
+ *  K_rope     bf16 [B, kv_rows, 64], shared by all heads (the last 64 values of
+ *             bf16 cache rows or of rapid_latent_read's, where they stand)
+ *  strides    HOST array of eleven element strides: batch, token, head of Q, of
+ *             K and of V, batch and token of K_rope; or NULL: all packed.  Every
+ *             stride a multiple of 8 (16 bytes)
+ *  n_rows     device int32 [B] or NULL (n): sequence b has tokens [0, n_rows[b]);
+ *             O and LSE behind them stay as they are
+ *  O          bf16 [B, n, H, 128]; LSE float [B, H, n]
+ *  softmax_scale  <= 0 selects 1/sqrt(192)
+ *
+ * A key that a token does not see has no effect on it, whatever it holds; nor
+ * has another token's query.
+ *
+ * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], n < 1, B * n
+ * above 2^31, H outside [1, RAPID_LATENT_MAX_HEADS], kv_rows outside [1,
+ * RAPID_LATENT_MAX_ROWS], a bad stride or alignment (16 bytes), a softmax_scale
+ * that is not finite; RAPID_ECUDA on launch failure.  A sequence with n_rows
+ * outside [0, n], a negative prefix_len or prefix_len + n_rows above kv_rows is
+ * left alone and bit 1 of the device error word is set.
+ */
+rapid_status rapid_latent_prefill_attn(const void* Q, const void* K, const void* V, const void* K_rope,
+                                       const int64_t* strides, int B, int n, int H, int64_t kv_rows,
+                                       const int32_t* prefix_len, const int32_t* n_rows,
+                                       float softmax_scale, void* O, float* LSE, void* stream);
 
 #ifdef __cplusplus
 }

@@ -36,6 +36,13 @@ RAPID_NOALLOC_MAX_NODES = 4096
 RAPID_ROPE_INTERLEAVED = 1
 RAPID_Q8_PAGE_TOKENS = 64
 RAPID_Q8_MAX_PAGES = 1 << 24
+RAPID_CACHE_LATENT_Q8 = 2
+RAPID_LATENT_DIM = 512
+RAPID_LATENT_ROPE_DIM = 64
+RAPID_LATENT_ROW = 576
+RAPID_LATENT_HEAD_DIM = 128
+RAPID_LATENT_GROUP = 128
+RAPID_LATENT_Q8_ROW_BYTES = 656
 
 _lib = None
 
@@ -117,6 +124,20 @@ def lib() -> ctypes.CDLL:
     L.rapid_verify_attn_q8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i64,
                                        i32, i32, vp, vp, vp, f32, vp, vp, vp, sz, vp]
     L.rapid_verify_attn_q8.restype = i32
+    L.rapid_latent_append.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, f32, vp, u32, vp, vp, vp,
+                                      vp, vp, i32, i64, vp]
+    L.rapid_latent_append.restype = i32
+    L.rapid_latent_read.argtypes = [vp, i32, i32, i64, i32, vp, vp, vp, vp]
+    L.rapid_latent_read.restype = i32
+    L.rapid_latent_commit.argtypes = [vp, i32, i32, i32, i64, i32, vp, vp, vp, vp]
+    L.rapid_latent_commit.restype = i32
+    L.rapid_latent_attn_workspace_size.argtypes = [i32, i32, i32, i64, i32]
+    L.rapid_latent_attn_workspace_size.restype = sz
+    L.rapid_latent_attn.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, vp, f32, vp, vp, vp, sz, vp]
+    L.rapid_latent_attn.restype = i32
+    L.rapid_latent_prefill_attn.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i64, vp, vp, f32, vp,
+                                            vp, vp]
+    L.rapid_latent_prefill_attn.restype = i32
     _lib = L
     return L
 
@@ -594,6 +615,155 @@ def rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_le
     _check(st, "rapid_verify_attn_q8")
 
 
+def _latent_cache(cache, dev, name="cache"):
+    """Address, element type code and sizes of a latent cache: bf16 [B, capacity, 576], or uint8
+    [B, capacity, 656] for 8-bit rows."""
+    q8 = cache.dtype == torch.uint8
+    if cache.dim() != 3:
+        raise RapidError(f"{name} must be [B, capacity, 576] bf16 or [B, capacity, 656] uint8")
+    B, cap, _ = cache.shape
+    ptr = _arg(cache, dev, torch.uint8 if q8 else torch.bfloat16,
+               (B, cap, RAPID_LATENT_Q8_ROW_BYTES if q8 else RAPID_LATENT_ROW), name)
+    return ptr, RAPID_CACHE_LATENT_Q8 if q8 else RAPID_DTYPE_BF16, B, cap
+
+
+def _strided(t, dev, shape, name):
+    """Address and strides of a bf16 tensor whose last dimension is contiguous (a view of a wider
+    one will do); the stride of a dimension of size 1 means nothing and is given as 0."""
+    if t.shape != shape or t.dtype != torch.bfloat16 or t.get_device() != dev:
+        _refuse(t, dev, torch.bfloat16, shape, name)
+    *outer, last = t.stride()
+    if last != 1:
+        raise RapidError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), [s if k > 1 else 0 for s, k in zip(outer, shape)]
+
+
+def rapid_latent_append(kv, q, q_out, kv_weight, eps, inv_freq, flags, prefix_len, row_offset,
+                        n_rows, cache, stream=None):
+    """Norm and rotate the rows kv [B, n, 576], write them to cache rows prefix_len + i (in 8 bits
+    where the cache is uint8); rotate q [B, n, H, 64] into q_out (both None: no queries)."""
+    dev = _device_of(cache, "cache")
+    ptr, code, B, cap = _latent_cache(cache, dev)
+    if kv.dim() != 3:
+        raise RapidError("kv must be [B, n, 576]")
+    n, i32 = kv.shape[1], torch.int32
+    kv_ptr, ks = _strided(kv, dev, (B, n, RAPID_LATENT_ROW), "kv")
+    q_ptr = o_ptr = q_strides = None
+    H = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None or q.dim() != 4:
+            raise RapidError("q and q_out are [B, n, H, 64], both or neither")
+        H = q.shape[2]
+        q_ptr, qs = _strided(q, dev, (B, n, H, RAPID_LATENT_ROPE_DIM), "q")
+        o_ptr, os_ = _strided(q_out, dev, (B, n, H, RAPID_LATENT_ROPE_DIM), "q_out")
+        q_strides = (ctypes.c_int64 * 6)(*qs, *os_)
+    st = lib().rapid_latent_append(
+        kv_ptr, (ctypes.c_int64 * 2)(*ks), q_ptr, q_strides, B, n, H,
+        _arg(kv_weight, dev, torch.bfloat16, (RAPID_LATENT_DIM,), "kv_weight"), eps,
+        _arg(inv_freq, dev, torch.float32, (RAPID_LATENT_ROPE_DIM // 2,), "inv_freq"), flags,
+        _arg(prefix_len, dev, i32, (B,), "prefix_len"),
+        _arg(row_offset, dev, i32, (B, n), "row_offset"), _arg(n_rows, dev, i32, (B,), "n_rows"),
+        o_ptr, ptr, code, cap, _raw_stream(stream, dev))
+    _check(st, "rapid_latent_append")
+
+
+def rapid_latent_read(cache, first, n_rows, rows, stream=None):
+    """Rows first[b] + i of a latent cache into rows [B, n, 576] bf16."""
+    dev = _device_of(cache, "cache")
+    ptr, code, B, cap = _latent_cache(cache, dev)
+    if rows.dim() != 3:
+        raise RapidError("rows must be [B, n, 576]")
+    n = rows.shape[1]
+    st = lib().rapid_latent_read(
+        ptr, code, B, cap, n, _arg(first, dev, torch.int32, (B,), "first"),
+        _arg(n_rows, dev, torch.int32, (B,), "n_rows"),
+        _arg(rows, dev, torch.bfloat16, (B, n, RAPID_LATENT_ROW), "rows"), _raw_stream(stream, dev))
+    _check(st, "rapid_latent_read")
+
+
+class LatentLayerTable:
+    """The device addresses of every layer's latent cache (all of one type and size), checked and
+    packed once for repeated rapid_latent_commit calls."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not caches:
+            raise RapidError("rapid_latent_commit needs at least one layer")
+        if len(caches) > RAPID_COMMIT_MAX_LAYERS:
+            raise RapidError(f"at most {RAPID_COMMIT_MAX_LAYERS} layers per call")
+        dev = _device_of(caches[0], "cache")
+        found = [_latent_cache(t, dev) for t in caches]
+        if len({f[1:] for f in found}) != 1:
+            raise RapidError("the caches of all layers must have one type and size")
+        _, self.dtype, self.B, self.cap = found[0]
+        self.layers = len(caches)
+        self._ptrs = (ctypes.c_void_p * self.layers)(*[f[0] for f in found])
+        self._keep = caches                               # the tensors outlive the table
+
+    def commit(self, prefix_len, path, n_accepted, stream=None):
+        """Keep the accepted path's rows of every layer (device tensors, as rapid_accept's)."""
+        dev = _device_of(self._keep[0], "cache")
+        if path.dim() != 2:
+            raise RapidError("path must be [B, n_q]")
+        n_q, i32 = path.shape[1], torch.int32
+        st = lib().rapid_latent_commit(
+            self._ptrs, self.layers, self.dtype, self.B, self.cap, n_q,
+            _arg(prefix_len, dev, i32, (self.B,), "prefix_len"),
+            _arg(path, dev, i32, (self.B, n_q), "path"),
+            _arg(n_accepted, dev, i32, (self.B,), "n_accepted"), _raw_stream(stream, dev))
+        _check(st, "rapid_latent_commit")
+
+
+def rapid_latent_commit(table, prefix_len, path, n_accepted, stream=None):
+    """LatentLayerTable.commit under the C call's name."""
+    table.commit(prefix_len, path, n_accepted, stream)
+
+
+def rapid_latent_attn_workspace_size(B, H, n_q, kv_capacity, cache_dtype) -> int:
+    return int(lib().rapid_latent_attn_workspace_size(B, H, n_q, kv_capacity, cache_dtype))
+
+
+def rapid_latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, O, LSE, workspace, stream=None):
+    """Absorbed verify attention over a latent cache; shapes are read from the tensors."""
+    dev = _device_of(Q, "Q")
+    if Q.dim() != 4:
+        raise RapidError("Q must be [B, H, n_q, 576]")
+    B, H, n_q, _ = Q.shape
+    ptr, code, cache_B, cap = _latent_cache(cache, dev)
+    if cache_B != B:
+        raise RapidError(f"Q has {B} sequences, the cache {cache_B}")
+    bf16 = torch.bfloat16
+    mask_dt = torch.bool if spec_mask is not None and spec_mask.dtype == torch.bool else torch.uint8
+    st = lib().rapid_latent_attn(
+        _arg(Q, dev, bf16, (B, H, n_q, RAPID_LATENT_ROW), "Q"), ptr, code, B, H, n_q, cap,
+        _arg(prefix_len, dev, torch.int32, (B,), "prefix_len"),
+        _arg(spec_mask, dev, mask_dt, (B, n_q, n_q), "spec_mask"), softmax_scale,
+        _arg(O, dev, bf16, (B, H, n_q, RAPID_LATENT_DIM), "O"),
+        _arg(LSE, dev, torch.float32, (B, H, n_q), "LSE"),
+        _arg(workspace, dev, torch.uint8, (workspace.numel(),), "workspace"), workspace.numel(),
+        _raw_stream(stream, dev))
+    _check(st, "rapid_latent_attn")
+
+
+def rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, O, LSE, stream=None):
+    """Expanded causal attention of a prompt chunk; Q, K, V and K_rope may be strided views."""
+    dev = _device_of(Q, "Q")
+    if Q.dim() != 4 or K.dim() != 4:
+        raise RapidError("Q is [B, n, H, 192], K and V [B, kv_rows, H, 128]")
+    B, n, H, _ = Q.shape
+    L, d = K.shape[1], RAPID_LATENT_HEAD_DIM
+    parts = [_strided(Q, dev, (B, n, H, d + RAPID_LATENT_ROPE_DIM), "Q"),
+             _strided(K, dev, (B, L, H, d), "K"), _strided(V, dev, (B, L, H, d), "V"),
+             _strided(K_rope, dev, (B, L, RAPID_LATENT_ROPE_DIM), "K_rope")]
+    i32 = torch.int32
+    st = lib().rapid_latent_prefill_attn(
+        *[x[0] for x in parts], (ctypes.c_int64 * 11)(*[s for x in parts for s in x[1]]), B, n, H, L,
+        _arg(prefix_len, dev, i32, (B,), "prefix_len"), _arg(n_rows, dev, i32, (B,), "n_rows"),
+        softmax_scale, _arg(O, dev, torch.bfloat16, (B, n, H, d), "O"),
+        _arg(LSE, dev, torch.float32, (B, H, n), "LSE"), _raw_stream(stream, dev))
+    _check(st, "rapid_latent_prefill_attn")
+
+
 def rapid_device_error(clear: bool = True) -> int:
     return int(lib().rapid_device_error(1 if clear else 0))
 
@@ -765,4 +935,82 @@ def verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tai
             _dtype_code(Q)))
     rapid_verify_attn_q8(Q, K_tail, V_tail, pages, scales, page_table, sealed_len, tail_len,
                          spec_mask, softmax_scale, out, lse, workspace)
+    return out, lse
+
+
+def latent_append(kv, cache, prefix_len, inv_freq, q=None, q_out=None, kv_weight=None, eps=1e-6,
+                  interleaved=False, row_offset=None, n_rows=None, stream=None):
+    """Append n rows of a latent cache's layer: kv [B, n, 576] normed (where a weight is given),
+    rotated and written to cache rows prefix_len + i, in 8 bits where the cache is uint8.
+    With q [B, n, H, 64], the rotated part of the queries, returns q_out [B, n, H, 64] (any
+    strided view, q itself too; made here if None)."""
+    with _on(stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        rapid_latent_append(kv, q, q_out, kv_weight, eps, inv_freq,
+                            RAPID_ROPE_INTERLEAVED if interleaved else 0, prefix_len, row_offset,
+                            n_rows, cache)
+    return q_out
+
+
+def latent_read(cache, first, n, n_rows=None, out=None, stream=None):
+    """Rows [first[b], first[b] + n) of a latent cache (first None: 0) as bf16 [B, n, 576]; rows
+    from n_rows[b] on are left as they are (unset in a new tensor)."""
+    with _on(stream):
+        if out is None:
+            out = torch.empty((cache.shape[0], n, RAPID_LATENT_ROW), dtype=torch.bfloat16,
+                              device=cache.device)
+        elif out.dim() != 3 or out.shape[1] != n:
+            raise RapidError(f"out must be [B, {n}, 576]")
+        rapid_latent_read(cache, first, n_rows, out)
+    return out
+
+
+@functools.lru_cache(maxsize=64)
+def _latent_attn_bytes(dev, B, H, n_q, cap, code):
+    """The workspace's size depends on the device (its number of SMs) and these sizes alone."""
+    nbytes = rapid_latent_attn_workspace_size(B, H, n_q, cap, code)
+    if nbytes == 0:
+        raise RapidError("unsupported latent_attn shape")
+    return nbytes
+
+
+def latent_attn(Q, cache, prefix_len, spec_mask=None, softmax_scale=0.0, out=None, lse=None,
+                workspace=None, stream=None):
+    """Absorbed verify attention: O [B, H, n_q, 512] bf16 and LSE [B, H, n_q] float32 of
+    Q [B, H, n_q, 576] over a latent cache; n_q = 1 decodes.
+
+    Without a workspace the call uses scratch that the host thread keeps for each stream, as
+    verify_attn_q8 does; calls that may overlap in other ways (two graphs of one memory pool)
+    need workspaces of their own."""
+    if stream is not None:
+        with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
+            return latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, out, lse, workspace)
+    B, H, n_q, _ = Q.shape
+    if out is None:
+        out = torch.empty((B, H, n_q, RAPID_LATENT_DIM), dtype=Q.dtype, device=Q.device)
+    if lse is None:
+        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=Q.device)
+    if workspace is None:
+        dev = _device_of(Q, "Q")
+        workspace = _scratch(dev, _latent_attn_bytes(
+            dev, B, H, n_q, cache.shape[1],
+            RAPID_CACHE_LATENT_Q8 if cache.dtype == torch.uint8 else RAPID_DTYPE_BF16))
+    rapid_latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, out, lse, workspace)
+    return out, lse
+
+
+def latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows=None, softmax_scale=0.0, out=None,
+                        lse=None, stream=None):
+    """Expanded causal attention of a prompt chunk behind prefix_len[b] tokens: O [B, n, H, 128]
+    bf16 and LSE [B, H, n] float32 of Q [B, n, H, 192] over K, V [B, kv_rows, H, 128] and K_rope
+    [B, kv_rows, 64] (strided views will do).  Tokens from n_rows[b] on are left as they are
+    (unset in new tensors)."""
+    with _on(stream):
+        B, n, H, _ = Q.shape
+        if out is None:
+            out = torch.empty((B, n, H, RAPID_LATENT_HEAD_DIM), dtype=Q.dtype, device=Q.device)
+        if lse is None:
+            lse = torch.empty((B, H, n), dtype=torch.float32, device=Q.device)
+        rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, out, lse)
     return out, lse
