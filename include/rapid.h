@@ -783,7 +783,8 @@ enum {
     RAPID_LATENT_GROUP = 128,      /* 8-bit rows: codes that share a scale     */
     RAPID_LATENT_Q8_ROW_BYTES = 656,
     RAPID_LATENT_MAX_HEADS = 1024,
-    RAPID_LATENT_MAX_ROWS = 1 << 30
+    RAPID_LATENT_MAX_ROWS = 1 << 29,       /* kv_capacity, kv_rows             */
+    RAPID_LATENT_MAX_QUERIES = 1 << 30     /* B * H * n_q                      */
 };
 
 /* Element type of a latent cache beside RAPID_DTYPE_BF16: 8-bit rows. */
@@ -898,8 +899,8 @@ size_t rapid_latent_attn_workspace_size(int B, int H, int n_q, int64_t kv_capaci
  * that is not finite makes the outputs of the queries that see it NaN.
  *
  * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], H outside [1,
- * RAPID_LATENT_MAX_HEADS], n_q outside [1, RAPID_MAX_NQ], kv_capacity below n_q
- * or above RAPID_LATENT_MAX_ROWS, a bad cache type or alignment (16 bytes), a
+ * RAPID_LATENT_MAX_HEADS], n_q outside [1, RAPID_MAX_NQ], B * H * n_q above
+ * RAPID_LATENT_MAX_QUERIES, kv_capacity below n_q or above RAPID_LATENT_MAX_ROWS, a bad cache type or alignment (16 bytes), a
  * softmax_scale that is not finite; RAPID_ENOMEM for a short workspace;
  * RAPID_ECUDA on launch failure.  A prefix_len outside [0, kv_capacity - n_q]
  * is clamped and bit 1 of the device error word is set.

@@ -21,9 +21,31 @@ bool strides_ok(const int64_t* s, int n) {
 }
 rapid_status status_of(cudaError_t e) { return e == cudaSuccess ? RAPID_OK : RAPID_ECUDA; }
 
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+struct AttnPlan {
+    int S, RB;
+    size_t acc, ml, index;       // bytes of the workspace's parts
+    size_t bytes() const { return acc + ml + 2 * index; }
+};
+
+AttnPlan plan_attn(int B, int H, int n_q, int64_t cap) {
+    AttnPlan pl;
+    const int R = H * n_q, nr = latent_attn_block_rows(R);
+    pl.S = latent_attn_slots(B, R, cap);
+    pl.RB = (R + nr - 1) / nr;
+    const size_t rows = pl.S > B ? (size_t)pl.S * R : 0;      // one split each: no partials
+    pl.acc = align_up(rows * kLatent * sizeof(float));
+    pl.ml = align_up(rows * 2 * sizeof(float));
+    pl.index = align_up((size_t)B * sizeof(int));
+    return pl;
+}
+
 bool attn_args_ok(int B, int H, int n_q, int64_t cap, int cache_dtype) {
     if (B < 1 || B > 65535 || H < 1 || H > RAPID_LATENT_MAX_HEADS || !cache_ok(cache_dtype)) return false;
-    return n_q >= 1 && n_q <= RAPID_MAX_NQ && capacity_ok(cap) && cap >= n_q;
+    if (n_q < 1 || n_q > RAPID_MAX_NQ || !capacity_ok(cap) || cap < n_q) return false;
+    return (int64_t)B * H * n_q <= RAPID_LATENT_MAX_QUERIES;
 }
 
 }  // namespace
@@ -117,7 +139,7 @@ rapid_status rapid_latent_commit(void* const* caches, int layers, int cache_dtyp
 
 size_t rapid_latent_attn_workspace_size(int B, int H, int n_q, int64_t kv_capacity, int cache_dtype) {
     if (!attn_args_ok(B, H, n_q, kv_capacity, cache_dtype)) return 0;
-    return 256;
+    return plan_attn(B, H, n_q, kv_capacity).bytes();
 }
 
 rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype, int B, int H, int n_q,
@@ -130,14 +152,19 @@ rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype
     for (const void* x : rows16)
         if (!aligned(x, 16)) return RAPID_EINVAL;
     if (!aligned(prefix_len, 4) || !aligned(LSE, 4) || !std::isfinite(softmax_scale)) return RAPID_EINVAL;
-    if (workspace_bytes < rapid_latent_attn_workspace_size(B, H, n_q, kv_capacity, cache_dtype))
-        return RAPID_ENOMEM;
+    const AttnPlan pl = plan_attn(B, H, n_q, kv_capacity);
+    if (workspace_bytes < pl.bytes()) return RAPID_ENOMEM;
     LatentAttnParams p{};
     p.Q = Q; p.cache = static_cast<const uint8_t*>(cache);
     p.prefix_len = prefix_len; p.mask = spec_mask; p.O = O; p.LSE = LSE;
     p.err = device_error_word();
     p.cap = kv_capacity;
-    p.B = B; p.H = H; p.n_q = n_q;
+    p.B = B; p.H = H; p.n_q = n_q; p.S = pl.S; p.RB = pl.RB;
+    char* ws = static_cast<char*>(workspace);
+    p.part_acc = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + pl.acc);
+    p.part_first = reinterpret_cast<int*>(ws + pl.acc + pl.ml);
+    p.part_count = reinterpret_cast<int*>(ws + pl.acc + pl.ml + pl.index);
     p.q8 = cache_dtype == RAPID_CACHE_LATENT_Q8;
     p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)(kLatentHead + kLatentRope))) * kLog2e;
     return status_of(launch_latent_attn(p, static_cast<cudaStream_t>(stream)));

@@ -67,9 +67,17 @@ struct LatentAttnParams {
     const uint8_t* mask;         // [B, n_q, n_q] or nullptr (chain)
     void* O;                     // [B, H, n_q, 512] bf16
     float* LSE;                  // [B, H, n_q]
+    // Partials of sequences with several splits, by slot: un-normalised outputs [S, H n_q, 512]
+    // and their (running maximum, sum) in the log2 domain; a sequence's splits are the slots
+    // part_first[b] .. + part_count[b] - 1.
+    float* part_acc;
+    float* part_ml;
+    int* part_first;
+    int* part_count;
     unsigned int* err;
     int64_t cap;
     int B, H, n_q, q8;
+    int S, RB;                   // slots (S == B: one split each), row blocks
     float scale_log2;            // softmax scale * log2(e)
 };
 
@@ -89,6 +97,8 @@ struct LatentPrefillParams {
 cudaError_t launch_latent_append(LatentAppendParams p, cudaStream_t st);
 cudaError_t launch_latent_read(const LatentReadParams& p, cudaStream_t st);
 cudaError_t launch_latent_commit(const LatentCommitParams& p, int layers, int B, cudaStream_t st);
+int latent_attn_block_rows(int R);                    // rows of a block for R = H n_q rows
+int latent_attn_slots(int B, int R, int64_t cap);
 cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t st);
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t st);
 

@@ -1,112 +1,801 @@
-// Absorbed attention over a latent cache: verify attention whose keys are the cache rows (576
-// values, one row for all heads) and whose values are their first 512.
+// Absorbed attention over a latent cache on tensor cores: verify attention whose keys are the
+// cache rows (576 values, one row for all heads) and whose values are their first 512.
 //
 //   s_j = <q, [c_j, r_j]>,   O = sum_j softmax(scale s)_j c_j
 //
 // over the history rows and, as the chain or tree mask says, the n_q rows behind them.
-// One block per query; its warps take keys in turn, a lane holds 18 values of the query and 16
-// of the output.
-#include <cuda_fp8.h>
+//
+// All H * n_q queries of a sequence share the rows, so one tile of rows in shared memory is read
+// as both operands: by QK as K (64 keys x 576, K-major), by PV as V (64 keys x 512, MN-major).
+// The accumulator is what decides the shape: 512 fp32 values for each query fill tensor memory
+// at 128 queries, with no room for S.  So a CTA takes at most 64 queries, and forms
+//   S[row, key]   = Q K^T           M = 64, N = 64, K = 576
+//   O^T[dim, row] += V^T P^T        4 x (M = 128, N = rows, K = 64)
+// the second product transposed: rows in N cost what they are (16, 32 or 64 of them), rows in M
+// would leave half of the tensor unit's lanes idle.
+//
+// CTA = (sequence and split of its keys, block of rows).  Shared memory holds Q, two tiles of
+// 64 keys and one P tile; a tile's room is refilled in five pieces (the key's 64 rotated values,
+// then 128 values at a time) as soon as the products that read a piece are done, so copies run
+// beside the products of the same tile.  Warps:
+//   0-3    softmax: warp w has rows 16 w .. 16 w + 15 of S, and dimensions 32 w .. 32 w + 31 of
+//          each 128 of O^T.  The running maximum moves only when a score passes it by more than
+//          2^8 (the warps vote on a barrier); O^T is rescaled then
+//   4      copies tiles by TMA (bf16 rows); Q
+//   5      issues the products in the order in which their inputs become ready
+//   6-13   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
+//          quarter of a key, the next tile's in registers while it stores this one.  An e4m3 code
+//          is 2^-120 of a bf16 with the same bits further up, exactly, so a code costs a shift, a
+//          mask and two exact multiplications, no conversion
+// P is rounded to bf16 (2^-9 of each probability, and it averages out); sums are fp32.
+//
+// Rows that a query does not see have no effect on it, whatever they hold: in tiles that a mask
+// touches, rows behind the step are zeroed in shared memory before they are read as values, and
+// so are rows with a value that is not finite, whose probabilities become NaN where they are seen.
+//
+// Every wait is bounded in wall-clock time; after a failed wait the kernel records an error code,
+// stops issuing, drains and returns.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 #include "latent.cuh"
+#include "tcgen05.cuh"
 
 namespace rapid {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kKeys = 64;                        // keys of a tile
+constexpr int kChunk = kKeys * 128;              // 64 values of a tile's keys: 8 KB
+constexpr int kChunks = kLatentRow / 64;         // 9; the last is the rotated part
+constexpr int kTile = kChunks * kChunk;
+constexpr int kPieces = 5;                       // of a tile: rotated part, then 2 chunks at a time
+constexpr int kProducerWarp = 4, kMmaWarp = 5, kConvWarp = 6, kConvWarps = 8;
+constexpr int kBarBytes = 1536;
 
-RAPID_DEVICE void unpack8(uint4 r, float* x) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+template <int NR, bool Q8>
+struct Plan {
+    static constexpr int kThreads = 32 * (Q8 ? kConvWarp + kConvWarps : kConvWarp);
+    static constexpr int kQChunk = NR * 128;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffTile = kChunks * kQChunk;
+    static constexpr int kOffP = kOffTile + 2 * kTile;
+    static constexpr int kOffBar = kOffP + NR * 128;
+    static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;   // + alignment
+    // tensor-memory columns: O^T (4 blocks of NR), two S buffers
+    static constexpr uint32_t kTmemO = 0, kTmemS = 4 * NR;
+    static constexpr uint32_t kTmemCols = 4 * NR + 2 * kKeys <= 256 ? 256 : 512;
+    static constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) |
+                                         ((uint32_t)(NR >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kKeys >> 3) << 17) |
+                             ((uint32_t)(64 >> 4) << 24);
+
+// Codes recorded by a timed-out wait: role << 24 | barrier << 16 | tile.
+enum : unsigned int {
+    kRoleProducer = 0x21u << 24, kRoleMma = 0x22u << 24, kRoleSoftmax = 0x23u << 24,
+    kRoleConvert = 0x24u << 24,
+    kBarFull = 1u << 16, kBarEmpty = 2u << 16, kBarS = 3u << 16, kBarPV = 4u << 16, kBarLast = 5u << 16
+};
+
+struct Slot {
+    int b, s, S_b, tiles;    // sequence (-1: no work), split, its splits, its tiles
+};
+
+struct Bars {
+    uint64_t full[2][kPieces], empty[2][kPieces];
+    uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
+    uint32_t tmem_base;
+    int abort;
+    Slot slot;
+    uint32_t flagged[2];     // keys of a masked tile with a value that is not finite
+    float factor[2][64];     // rescale factors of the rows, by tile parity
+};
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block too small");
+
+RAPID_DEVICE float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+RAPID_DEVICE uint32_t bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+RAPID_DEVICE uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+RAPID_DEVICE void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+// 16 lanes x 64 columns -> 32 registers: 4 c .. 4 c + 3 of lane l are columns 8 c + 2 (l % 4), + 1
+// of row l / 4, then of row l / 4 + 8.
+RAPID_DEVICE void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Barrier 1 of the four softmax warps: whether any thread says so.
+RAPID_DEVICE bool softmax_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+RAPID_DEVICE int64_t clamped_len(const LatentAttnParams& p, int b) {
+    const int64_t P = p.prefix_len[b], most = p.cap - p.n_q;
+    return P < 0 ? 0 : P > most ? most : P;
+}
+RAPID_DEVICE int seq_tiles(const LatentAttnParams& p, int b) {
+    return (int)((clamped_len(p, b) + p.n_q + kKeys - 1) / kKeys);
+}
+
+// Which sequence and split a slot holds, worked out by one warp from the lengths: the least
+// number of tiles a split for which all splits fit into the p.S >= B slots.
+RAPID_DEVICE Slot find_slot(const LatentAttnParams& p, int c, int lane) {
+    int64_t total = 0;
+    int longest = 1;
+    for (int b = lane; b < p.B; b += 32) {
+        const int t = seq_tiles(p, b);
+        total += t;
+        longest = max(longest, t);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    int lo = (int)((total + p.S - 1) / p.S), hi = max(lo, longest);
+    if (p.S == p.B) lo = hi;                      // one split each
+    if (p.B == 1) hi = lo;
+    while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        int used = 0;
+        for (int b = lane; b < p.B; b += 32) used += (seq_tiles(p, b) + mid - 1) / mid;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) used += __shfl_xor_sync(0xffffffffu, used, o);
+        if (used <= p.S) hi = mid; else lo = mid + 1;
+    }
+    int first = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int tiles = b < p.B ? seq_tiles(p, b) : 0;
+        const int S_b = (tiles + lo - 1) / lo;
+        int upto = S_b;                           // inclusive scan
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, c < first + upto);
+        if (here) {
+            const int l = __ffs(here) - 1;
+            Slot r;
+            r.b = b0 + l;
+            r.S_b = __shfl_sync(0xffffffffu, S_b, l);
+            r.s = c - first - (__shfl_sync(0xffffffffu, upto, l) - r.S_b);
+            r.tiles = __shfl_sync(0xffffffffu, tiles, l);
+            return r;
+        }
+        first += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return Slot{-1, 0, 0, 0};
+}
+
+template <int NR, bool Q8>
+__global__ void __launch_bounds__(Plan<NR, Q8>::kThreads, 1)
+latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
+                   const LatentAttnParams p) {
+    using L = Plan<NR, Q8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Row blocks of one split are neighbours: they read the same tiles at the same time, once
+    // from memory and then from L2.
+    const int slot_idx = blockIdx.x / p.RB, rb = blockIdx.x - slot_idx * p.RB;
+    const int R = p.H * p.n_q;
+    const int r0 = rb * NR, Rb = min(NR, R - r0);
+    if (tid == 0) {
+        for (int u = 0; u < 2; ++u) {
+            for (int g = 0; g < kPieces; ++g) {
+                mbar_init(&bars->full[u][g], Q8 ? kConvWarps : 1);
+                mbar_init(&bars->empty[u][g], 1);
+            }
+            mbar_init(&bars->s_full[u], 1);
+            mbar_init(&bars->s_free[u], 4);
+            bars->flagged[u] = 0;
+        }
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->p_full, 4);
+        mbar_init(&bars->pv_done, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&bars->tmem_base)),
+                     "r"(L::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    griddep_wait();
+    if (warp == 0) {
+        const Slot sl = find_slot(p, slot_idx, lane);
+        if (lane == 0) {
+            bars->slot = sl;
+            if (sl.b >= 0 && sl.s == 0 && rb == 0) {
+                p.part_first[sl.b] = slot_idx;
+                p.part_count[sl.b] = sl.S_b;
+                const int64_t P = p.prefix_len[sl.b];
+                if (p.err && (P < 0 || P > p.cap - p.n_q)) atomicOr(p.err, kErrBadInput);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Slot sl = bars->slot;
+    const int b = sl.b < 0 ? 0 : sl.b;
+    const int t_begin = sl.b < 0 ? 0 : (int)((int64_t)sl.s * sl.tiles / sl.S_b);
+    const int t_end = sl.b < 0 ? 0 : (int)((int64_t)(sl.s + 1) * sl.tiles / sl.S_b);
+    const int n = t_end - t_begin;                // >= 1 with work: S_b <= tiles
+    const uint32_t tmem = bars->tmem_base;
+    const int64_t P = clamped_len(p, b);
+
+    if (n <= 0) {
+        // a slot that no split needs
+    } else if (warp < 4) {
+        // ------------------------------ softmax -------------------------------
+        const bool rows_here = 16 * warp < NR;
+        const int ra = 16 * warp + (lane >> 2), q4 = lane & 3;
+        const bool live[2] = {rows_here && ra < Rb, rows_here && ra + 8 < Rb};
+        uint64_t spec[2] = {0, 0};                // the step's rows that each row sees
+        if ((int64_t)t_end * kKeys > P) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = (r0 + ra + 8 * k) % p.n_q;
+                if (!p.mask) {
+                    spec[k] = (2ull << i) - 1;
+                } else {
+                    const uint8_t* m = p.mask + ((int64_t)b * p.n_q + i) * p.n_q;
+                    for (int j = 16 * q4; j < min(16 * q4 + 16, p.n_q); ++j)
+                        if (live[k] && m[j]) spec[k] |= 1ull << j;
+                    spec[k] |= __shfl_xor_sync(0xffffffffu, spec[k], 1);
+                    spec[k] |= __shfl_xor_sync(0xffffffffu, spec[k], 2);
+                }
+            }
+        }
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
+        const float c = p.scale_log2;
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+        bool dead = false;
+        for (int j = 0; j < n; ++j) {
+            const int buf = j & 1;
+            if (!dead)
+                dead = !__all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((j >> 1) & 1), p.err,
+                                                          kRoleSoftmax | kBarS | (unsigned)(j & 0xffff)));
+            uint32_t sr[32];
+            bool moved = false;
+            const int64_t base = (int64_t)(t_begin + j) * kKeys;
+            const bool masked = base + kKeys > P;
+            if (!dead) {
+                tc_fence_after();
+                if (rows_here) {
+                    tmem_ld_16x256b_x8(lane_addr + L::kTmemS + (uint32_t)(buf * kKeys), sr);
+                    tmem_wait_ld();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->s_free[buf]);
+            }
+            if (masked) {
+                // the tile as values: two threads a key, 4 chunks each
+                uint8_t* tile = smem + L::kOffTile + buf * kTile;
+                const int key = tid >> 1;
+                const bool inside = base + key < P + p.n_q;
+                bool odd = false;
+                if (!dead)                            // done long ago: what was copied is visible here
+                    for (int g = 0; g < kPieces; ++g)
+                        mbar_wait(&bars->full[buf][g], (uint32_t)((j >> 1) & 1), p.err, kRoleSoftmax | kBarFull);
+                if (inside && !dead) {
+#pragma unroll 4
+                    for (int x = 0; x < 32; ++x) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            tile + (4 * (tid & 1) + (x >> 3)) * kChunk + key * 128 + ((x & 7) << 4));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            odd |= (w[u] & 0x7f80u) == 0x7f80u || (w[u] & 0x7f800000u) == 0x7f800000u;
+                    }
+                }
+                if (odd) atomicOr(&bars->flagged[key >> 5], 1u << (key & 31));
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const uint64_t flagged = bars->flagged[0] | ((uint64_t)bars->flagged[1] << 32);
+                if (!dead && (!inside || ((flagged >> key) & 1))) {
+                    for (int x = 0; x < 32; ++x)
+                        *reinterpret_cast<uint4*>(tile + (4 * (tid & 1) + (x >> 3)) * kChunk + key * 128 +
+                                                  ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (tid < 2) bars->flagged[tid] = 0;      // (read again only after the vote below)
+                if (!dead && rows_here) {
+                    const int64_t delta = P - base;       // < 64
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint64_t see = delta > 0 ? ((1ull << delta) - 1) | (spec[k] << delta)
+                                                 : delta > -64 ? spec[k] >> -delta : 0;
+                        if (!live[k]) see = 0;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int col = 8 * x + 2 * q4 + e;
+                                uint32_t& s = sr[4 * x + 2 * k + e];
+                                if (!((see >> col) & 1)) s = 0xff800000u;          // -inf
+                                else if ((flagged >> col) & 1) s = 0x7fffffffu;    // NaN
+                            }
+                    }
+                }
+            }
+            float fac[2] = {1.f, 1.f};
+            if (!dead && rows_here) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        mx = fmaxf(mx, fmaxf(__uint_as_float(sr[4 * x + 2 * k]), __uint_as_float(sr[4 * x + 2 * k + 1])));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    mx *= c;
+                    if (live[k] && mx > m_run[k] + 8.f) {     // the first finite score too
+                        fac[k] = ex2(m_run[k] - mx);          // 0 where m_run is -inf
+                        m_run[k] = mx;
+                        l_run[k] *= fac[k];
+                        moved = j > 0;
+                    }
+                    if (q4 == 0) bars->factor[buf][ra + 8 * k] = fac[k];
+                }
+            }
+            // (also keeps the warps within a tile of each other)
+            if (softmax_any(moved || dead)) {
+                if (softmax_any(dead)) { dead = true; break; }
+                // O^T is rescaled: after the product that last added to it
+                if (j > 0) {
+                    dead = !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
+                                                              kRoleSoftmax | kBarPV | (unsigned)(j & 0xffff)));
+                    if (!dead) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < NR / 4; ++x) {    // 16 columns at a time
+                            uint32_t o[16];
+                            tmem_ld16(lane_addr + L::kTmemO + (uint32_t)(16 * x), o);
+                            tmem_wait_ld();
+                            const float* f = bars->factor[buf] + (16 * x) % NR;
+#pragma unroll
+                            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f[u]);
+                            tmem_st16(lane_addr + L::kTmemO + (uint32_t)(16 * x), o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+            }
+            uint32_t pk[16];
+            if (!dead && rows_here) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float neg = m_run[k] == -INFINITY ? 0.f : -m_run[k];
+                    const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float2 y = fma2(make_float2(__uint_as_float(sr[4 * x + 2 * k]),
+                                                          __uint_as_float(sr[4 * x + 2 * k + 1])), c2, n2);
+                        const float2 e = make_float2(ex2(y.x), ex2(y.y));
+                        sum = add2(sum, e);
+                        pk[2 * x + k] = bf16x2(e.x, e.y);
+                    }
+                    l_run[k] += sum.x + sum.y;
+                }
+            }
+            if (!dead && j > 0)                   // the P tile has been read
+                dead = !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
+                                                          kRoleSoftmax | kBarPV | (unsigned)(j & 0xffff)));
+            if (!dead) {
+                if (rows_here) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint8_t* row = smem + L::kOffP + (ra + 8 * k) * 128 + 4 * q4;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            *reinterpret_cast<uint32_t*>(row + ((x ^ (ra & 7)) << 4)) = pk[2 * x + k];
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->p_full);
+            }
+        }
+        if (tid == 0) griddep_launch_dependents();
+        if (!dead)
+            dead = !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (uint32_t)((n - 1) & 1), p.err,
+                                                      kRoleSoftmax | kBarLast));
+        if (rows_here) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                l_run[k] += __shfl_xor_sync(0xffffffffu, l_run[k], 1);
+                l_run[k] += __shfl_xor_sync(0xffffffffu, l_run[k], 2);
+            }
+        }
+        dead = softmax_any(dead);
+        if (!dead) {
+            tc_fence_after();
+            const bool whole = sl.S_b == 1;
+            if (rows_here && q4 == 0) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = ra + 8 * k;
+                    if (!live[k]) continue;
+                    if (whole) {
+                        bars->factor[0][r] = l_run[k] == 0.f ? 0.f : 1.f / l_run[k];
+                        p.LSE[(int64_t)b * R + r0 + r] =
+                            l_run[k] == 0.f ? -INFINITY : (m_run[k] + log2f(l_run[k])) * kLn2;
+                    } else {
+                        float* ml = p.part_ml + ((int64_t)slot_idx * R + r0 + r) * 2;
+                        ml[0] = m_run[k];
+                        ml[1] = l_run[k];
+                    }
+                }
+            }
+            if (whole) asm volatile("bar.sync 1, 128;" ::: "memory");
+            // lane = dimension, register = row
+#pragma unroll 1
+            for (int x = 0; x < NR / 4; ++x) {
+                const int blk = 16 * x / NR, col = 16 * x % NR;
+                if (col >= Rb) continue;
+                uint32_t o[16];
+                tmem_ld16(lane_addr + L::kTmemO + (uint32_t)(16 * x), o);
+                tmem_wait_ld();
+                const int dim = 128 * blk + tid;
+                if (whole) {
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.O) +
+                                         ((int64_t)b * R + r0 + col) * kLatent + dim;
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        if (col + u < Rb)
+                            dst[(int64_t)u * kLatent] = __float2bfloat16_rn(__uint_as_float(o[u]) *
+                                                                            bars->factor[0][col + u]);
+                } else {
+                    float* dst = p.part_acc + ((int64_t)slot_idx * R + r0 + col) * kLatent + dim;
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        if (col + u < Rb) dst[(int64_t)u * kLatent] = __uint_as_float(o[u]);
+                }
+            }
+        }
+        if (dead) bars->abort = 1;
+    } else if (warp == kProducerWarp) {
+        // ------------------------------ copies --------------------------------
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->q_full, kChunks * L::kQChunk);
+            for (int ch = 0; ch < kChunks; ++ch)
+                tma_load_2d(smem + L::kOffQ + ch * L::kQChunk, &tmQ, 64 * ch, b * R + r0, &bars->q_full);
+            int issued = 0;                       // pieces
+            if constexpr (!Q8) {
+                bool ok = true;
+                for (int j = 0; j < n && ok; ++j) {
+                    const int st = j & 1;
+                    uint8_t* tile = smem + L::kOffTile + st * kTile;
+                    const int y = (t_begin + j) * kKeys;
+                    for (int g = 0; g < kPieces; ++g) {
+                        if ((j >= 2 && !mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
+                                                        kRoleProducer | kBarEmpty | (unsigned)(j & 0xffff))) ||
+                            *((volatile int*)&bars->abort)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bars->full[st][g], g == 0 ? kChunk : 2 * kChunk);
+                        if (g == 0) {
+                            tma_load_3d(tile + 8 * kChunk, &tmC, 512, y, b, &bars->full[st][0]);
+                        } else {
+                            const int ch = 2 * (g - 1);
+                            tma_load_3d(tile + ch * kChunk, &tmC, 64 * ch, y, b, &bars->full[st][g]);
+                            tma_load_3d(tile + (ch + 1) * kChunk, &tmC, 64 * ch + 64, y, b, &bars->full[st][g]);
+                        }
+                        ++issued;
+                    }
+                }
+                if (!ok) {
+                    bars->abort = 1;
+                    // let the copies in flight land before the CTA exits
+                    for (int x = max(0, issued - 2 * kPieces); x < issued; ++x)
+                        mbar_wait(&bars->full[(x / kPieces) & 1][x % kPieces], (uint32_t)((x / kPieces >> 1) & 1),
+                                  p.err, kRoleProducer | kBarFull);
+                }
+            }
+            mbar_wait_sleep(&bars->q_full, 0, p.err, kRoleProducer | kBarLast);
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------ products ------------------------------
+        if (lane == 0) {
+            const uint32_t base = smem_u32(smem);
+            const uint64_t qd0 = sdesc(base + L::kOffQ, 16, 1024);
+            const uint64_t kd0 = sdesc(base + L::kOffTile, 16, 1024);
+            const uint64_t vd0 = sdesc(base + L::kOffTile, kChunk, 1024);
+            const uint64_t pd0 = sdesc(base + L::kOffP, 16, 1024);
+            bool ok = mbar_wait(&bars->q_full, 0, p.err, kRoleMma | kBarLast);
+            int nqk = 0, g = 0, npv = 0;
+            uint64_t t_last = global_timer_ns();
+            while (ok && npv < n) {
+                bool progressed = false;
+                if (npv < nqk && mbar_try_wait(&bars->p_full, (uint32_t)(npv & 1))) {
+                    tc_fence_after();
+                    const uint64_t vd = vd0 + (uint64_t)((npv & 1) * (kTile >> 4));
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            mma_bf16(tmem + L::kTmemO + (uint32_t)(m * NR),
+                                     vd + (uint64_t)((2 * m * kChunk + k * 2048) >> 4), pd0 + (uint64_t)(2 * k),
+                                     L::kIdescPV, npv > 0 || k > 0);
+                        mma_commit(&bars->empty[npv & 1][1 + m]);
+                    }
+                    mma_commit(&bars->pv_done);
+                    ++npv;
+                    progressed = true;
+                }
+                if (nqk < n &&
+                    (g > 0 || nqk < 2 || mbar_try_wait(&bars->s_free[nqk & 1], (uint32_t)(((nqk >> 1) + 1) & 1))) &&
+                    mbar_try_wait(&bars->full[nqk & 1][g], (uint32_t)((nqk >> 1) & 1))) {
+                    tc_fence_after();
+                    const uint32_t dS = tmem + L::kTmemS + (uint32_t)((nqk & 1) * kKeys);
+                    const uint64_t kd = kd0 + (uint64_t)((nqk & 1) * (kTile >> 4));
+                    const int c0 = g == 0 ? 8 : 2 * (g - 1), c1 = g == 0 ? 9 : c0 + 2;
+                    for (int ch = c0; ch < c1; ++ch)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(dS, qd0 + (uint64_t)((ch * L::kQChunk + 32 * k) >> 4),
+                                     kd + (uint64_t)((ch * kChunk + 32 * k) >> 4), kIdescS, g > 0 || k > 0);
+                    if (++g == kPieces) {
+                        mma_commit(&bars->empty[nqk & 1][0]);
+                        mma_commit(&bars->s_full[nqk & 1]);
+                        g = 0;
+                        ++nqk;
+                    }
+                    progressed = true;
+                }
+                if (progressed) {
+                    t_last = global_timer_ns();
+                } else if (global_timer_ns() - t_last > kWaitLimitNs || *((volatile int*)&bars->abort)) {
+                    if (p.err) {
+                        atomicOr(p.err, kErrWaitTimeout);
+                        atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarS | (unsigned)(npv & 0xffff));
+                    }
+                    ok = false;
+                }
+            }
+            if (!ok) bars->abort = 1;
+            mma_commit(&bars->drain);             // nothing in flight when tensor memory is freed
+            mbar_wait(&bars->drain, 0, p.err, kRoleMma | kBarLast);
+        }
+    } else if constexpr (Q8) {
+        // ------------------------------ conversion ----------------------------
+        const int ct = tid - 32 * kConvWarp, key = ct >> 2, q = ct & 3;
+        const uint8_t* rows = p.cache + (int64_t)b * p.cap * kLatentQ8Row;
+        uint4 v[8], r[2], sc;
+        auto load = [&](int t, int u) {           // pieces 4 u + q; u = 8: the rotated part; 9: the scales
+            const int64_t row = (int64_t)t * kKeys + key;
+            const uint4* src = reinterpret_cast<const uint4*>(rows + row * kLatentQ8Row);
+            const bool in = row < p.cap;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            if (u < 8) v[u] = in ? __ldg(src + 4 * u + q) : zero;
+            else if (u == 8) {
+                r[0] = in ? __ldg(src + 32 + q) : zero;
+                r[1] = in ? __ldg(src + 36 + q) : zero;
+            } else sc = in ? __ldg(src + 40) : zero;
+        };
+#pragma unroll
+        for (int u = 0; u < 10; ++u) load(t_begin, u);
+        for (int j = 0; j < n; ++j) {
+            const int st = j & 1, next = t_begin + j + 1;
+            const bool more = j + 1 < n;
+            uint8_t* row = smem + L::kOffTile + st * kTile + key * 128;
+            const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+            bool ok = true;
+#pragma unroll
+            for (int g = 0; g < kPieces; ++g) {
+                if (j >= 2)
+                    ok = __all_sync(0xffffffffu, mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
+                                                                 kRoleConvert | kBarEmpty | (unsigned)(j & 0xffff)));
+                if (!ok) break;
+                if (g == 0) {
+                    uint8_t* d = row + 8 * kChunk;
+                    *reinterpret_cast<uint4*>(d + ((q ^ (key & 7)) << 4)) = r[0];
+                    *reinterpret_cast<uint4*>(d + (((q + 4) ^ (key & 7)) << 4)) = r[1];
+                    if (more) { load(next, 8); load(next, 9); }
+                } else {
+                    // 2^e twice: a power of two (or NaN) has its bits in the upper half of the float
+                    const uint32_t s2 = __byte_perm(scales[g - 1], 0, 0x3232);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int u = 2 * (g - 1) + h;
+                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t x = __byte_perm(w[k >> 1], 0, k & 1 ? 0x3424 : 0x1404);
+                            const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+                            o[k] = mul_bf16x2(mul_bf16x2(y, 0x7b807b80u), s2);   // 2^120
+                        }
+                        if (more) load(next, u);
+                        uint8_t* d = row + u * kChunk;
+                        *reinterpret_cast<uint4*>(d + (((2 * q) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(d + (((2 * q + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->full[st][g]);
+            }
+            if (!ok) {
+                bars->abort = 1;
+                break;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols)
+                     : "memory");
     }
 }
 
-__global__ void __launch_bounds__(kThreads) latent_attn_kernel(const LatentAttnParams p) {
-    __shared__ float s_acc[kWarps][kLatent];
-    __shared__ float s_m[kWarps], s_l[kWarps];
+// Joins the splits of a row by log-sum-exp: one block for 128 dimensions of a row, its warps
+// take splits in turn.
+__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParams p) {
+    __shared__ float4 s_acc[4][32];
+    __shared__ float s_l[4];
     griddep_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x;                  // (b, h, i)
-    const int i = (int)(row % p.n_q);
-    const int b = (int)(row / p.n_q / p.H);
-    int64_t P = p.prefix_len[b];
-    if (P < 0 || P > p.cap - p.n_q) {
-        if (threadIdx.x == 0 && p.err) atomicOr(p.err, kErrBadInput);
-        P = P < 0 ? 0 : p.cap - p.n_q;
+    const int R = p.H * p.n_q;
+    const int64_t row = blockIdx.x;
+    const int b = (int)(row / R), r = (int)(row - (int64_t)b * R);
+    const int count = p.part_count[b];
+    if (count <= 1) return;                       // written by its only split
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)p.part_first[b] * R + r;
+    const float* ml = p.part_ml + first * 2;
+    float M = -INFINITY;
+    for (int s = lane; s < count; s += 32) M = fmaxf(M, ml[(int64_t)s * R * 2]);
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.f : M;
+    const float* acc = p.part_acc + first * kLatent + 128 * blockIdx.y + 4 * lane;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = warp; s < count; s += 4) {
+        const float f = ex2(ml[(int64_t)s * R * 2] - ref);
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(acc + (int64_t)s * R * kLatent));
+        l = fmaf(f, ml[(int64_t)s * R * 2 + 1], l);
+        a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y);
+        a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
     }
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.Q) + row * kLatentRow;
-    float qv[18], acc[16], m = -INFINITY, l = 0.f;
-    unpack8(reinterpret_cast<const uint4*>(q)[2 * lane], qv);
-    unpack8(reinterpret_cast<const uint4*>(q)[2 * lane + 1], qv + 8);
-    qv[16] = __bfloat162float(q[kLatent + 2 * lane]);
-    qv[17] = __bfloat162float(q[kLatent + 2 * lane + 1]);
-#pragma unroll
-    for (int u = 0; u < 16; ++u) acc[u] = 0.f;
-    const int rb = p.q8 ? kLatentQ8Row : 2 * kLatentRow;
-    for (int64_t j = warp; j < P + p.n_q; j += kWarps) {
-        if (j >= P) {
-            const int jj = (int)(j - P);
-            if (p.mask ? p.mask[((int64_t)b * p.n_q + i) * p.n_q + jj] == 0 : jj > i) continue;
-        }
-        const uint8_t* kr = p.cache + ((int64_t)b * p.cap + j) * rb;
-        float k[18];
-        if (p.q8) {
-            const float scale = reinterpret_cast<const float*>(kr + kLatentQ8Scale)[lane >> 3];
-            const uint4 c = reinterpret_cast<const uint4*>(kr)[lane];
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const __half_raw h = __nv_cvt_fp8_to_halfraw((w[u / 4] >> (8 * (u % 4))) & 0xff, __NV_E4M3);
-                k[u] = __half2float(*reinterpret_cast<const __half*>(&h)) * scale;
-            }
-        } else {
-            unpack8(reinterpret_cast<const uint4*>(kr)[2 * lane], k);
-            unpack8(reinterpret_cast<const uint4*>(kr)[2 * lane + 1], k + 8);
-        }
-        const __nv_bfloat16* rope = reinterpret_cast<const __nv_bfloat16*>(kr + (p.q8 ? kLatentQ8Rope : 2 * kLatent));
-        k[16] = __bfloat162float(rope[2 * lane]);
-        k[17] = __bfloat162float(rope[2 * lane + 1]);
-        float s = 0.f;
-#pragma unroll
-        for (int u = 0; u < 18; ++u) s = fmaf(qv[u], k[u], s);
-        s = warp_sum(s) * p.scale_log2;
-        const float mn = fmaxf(m, s), corr = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float w = s == -INFINITY ? 0.f : exp2f(s - mn);
-        m = s != s ? s : mn;
-        l = l * corr + w;
-#pragma unroll
-        for (int u = 0; u < 16; ++u) acc[u] = fmaf(w, k[u], acc[u] * corr);
-    }
-#pragma unroll
-    for (int u = 0; u < 16; ++u) s_acc[warp][16 * lane + u] = acc[u];
-    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+    s_acc[warp][lane] = a;
+    if (lane == 0) s_l[warp] = l;
     __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    float f[kWarps];
-    for (int w = 0; w < kWarps; ++w) {
-        f[w] = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - M);
-        L += s_l[w] * f[w];
+    if (warp > 0) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    float o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const float* x = reinterpret_cast<const float*>(s_acc) + 4 * lane + u;
+        o[u] = ((x[0] + x[128]) + (x[256] + x[384])) * inv;
     }
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.O) + row * kLatent;
-    for (int c = threadIdx.x; c < kLatent; c += kThreads) {
-        float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x += f[w] * s_acc[w][c];
-        o[c] = __float2bfloat16_rn(M == -INFINITY ? 0.f : x / L);
-    }
-    if (threadIdx.x == 0) p.LSE[row] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + row * kLatent + 128 * blockIdx.y) + lane;
+    *dst = make_uint2(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]));
+    if (lane == 0 && blockIdx.y == 0) p.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
+              const cuuint64_t* strides, uint32_t box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint32_t box[3] = {64, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NR, bool Q8>
+cudaError_t launch_rows(const CUtensorMap& tmQ, const CUtensorMap& tmC, const LatentAttnParams& p,
+                        cudaStream_t st) {
+    auto kern = latent_attn_kernel<NR, Q8>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<NR, Q8>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.S * p.RB, 1, 1);
+    cfg.blockDim = dim3(Plan<NR, Q8>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Plan<NR, Q8>::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmC, p);
+    if (e != cudaSuccess || p.S == p.B) return e;
+    cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.H * p.n_q), kLatent / 128, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel, p);
 }
 
 }  // namespace
 
+int latent_attn_block_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+
+// Slots for the splits: CTAs run one to an SM, in w waves; a wave costs its tiles and the start
+// and end of a CTA (about 4 tiles' time).  Fewer slots than sequences: one for each.
+int latent_attn_slots(int B, int R, int64_t cap) {
+    const int nr = latent_attn_block_rows(R);
+    const int64_t rb = (R + nr - 1) / nr, sms = sm_count(), tiles = (cap + kKeys - 1) / kKeys * B;
+    int64_t S = B;
+    double least = 1e30;
+    for (int w = 1; w <= 4; ++w) {
+        const int64_t slots = w * sms / rb;
+        if (slots <= B) continue;
+        const double cost = w * ((double)((tiles + slots - 1) / slots) + 4.);
+        if (cost < least) { least = cost; S = slots; }
+    }
+    return (int)S;
+}
+
 cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t st) {
-    latent_attn_kernel<<<(unsigned)((int64_t)p.B * p.H * p.n_q), kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    CUtensorMap tmQ, tmC;
+    const int64_t R = (int64_t)p.H * p.n_q;
+    const int nr = latent_attn_block_rows((int)R);
+    const cuuint64_t q_dims[2] = {kLatentRow, (cuuint64_t)(p.B * R)};
+    const cuuint64_t q_strides[1] = {2 * kLatentRow};
+    if (!make_map(&tmQ, p.Q, 2, q_dims, q_strides, (uint32_t)nr)) return cudaErrorInvalidValue;
+    if (p.q8) {
+        if (nr == 16) return launch_rows<16, true>(tmQ, tmQ, p, st);
+        return nr == 32 ? launch_rows<32, true>(tmQ, tmQ, p, st) : launch_rows<64, true>(tmQ, tmQ, p, st);
+    }
+    const cuuint64_t c_dims[3] = {kLatentRow, (cuuint64_t)p.cap, (cuuint64_t)p.B};
+    const cuuint64_t c_strides[2] = {2 * kLatentRow, (cuuint64_t)p.cap * 2 * kLatentRow};
+    if (!make_map(&tmC, p.cache, 3, c_dims, c_strides, kKeys)) return cudaErrorInvalidValue;
+    if (nr == 16) return launch_rows<16, false>(tmQ, tmC, p, st);
+    return nr == 32 ? launch_rows<32, false>(tmQ, tmC, p, st) : launch_rows<64, false>(tmQ, tmC, p, st);
 }
 
 }  // namespace rapid
