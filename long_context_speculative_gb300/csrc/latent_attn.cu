@@ -22,8 +22,8 @@
 //          each 128 of O^T.  The running maximum moves only when a score passes it by more than
 //          2^8 (the warps vote on a barrier); O^T is rescaled then
 //   4      copies tiles by TMA (bf16 rows); Q
-//   5      issues the products in the order in which their inputs become ready
-//   6-13   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
+//   5, 6   issue QK and PV
+//   7-14   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
 //          quarter of a key, the next tile's in registers while it stores this one.  An e4m3 code
 //          is 2^-120 of a bf16 with the same bits further up, exactly, so a code costs a shift, a
 //          mask and two exact multiplications, no conversion
@@ -51,7 +51,7 @@ constexpr int kChunk = kKeys * 128;              // 64 values of a tile's keys: 
 constexpr int kChunks = kLatentRow / 64;         // 9; the last is the rotated part
 constexpr int kTile = kChunks * kChunk;
 constexpr int kPieces = 5;                       // of a tile: rotated part, then 2 chunks at a time
-constexpr int kProducerWarp = 4, kMmaWarp = 5, kConvWarp = 6, kConvWarps = 8;
+constexpr int kProducerWarp = 4, kQkWarp = 5, kPvWarp = 6, kConvWarp = 7, kConvWarps = 8;
 constexpr int kBarBytes = 1536;
 
 template <int NR, bool Q8>
@@ -86,7 +86,7 @@ struct Slot {
 
 struct Bars {
     uint64_t full[2][kPieces], empty[2][kPieces];
-    uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
+    uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain[2];
     uint32_t tmem_base;
     int abort;
     Slot slot;
@@ -213,7 +213,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars* bars = reinterpret_cast<Bars*>(smem + L::kOffBar);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // Row blocks of one split are neighbours: they read the same tiles at the same time, once
     // from memory and then from L2.
     const int slot_idx = blockIdx.x / p.RB, rb = blockIdx.x - slot_idx * p.RB;
@@ -226,17 +226,17 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 mbar_init(&bars->empty[u][g], 1);
             }
             mbar_init(&bars->s_full[u], 1);
+            mbar_init(&bars->drain[u], 1);
             mbar_init(&bars->s_free[u], 4);
             bars->flagged[u] = 0;
         }
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->p_full, 4);
         mbar_init(&bars->pv_done, 1);
-        mbar_init(&bars->drain, 1);
         bars->abort = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
                      "r"(L::kTmemCols)
@@ -297,7 +297,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         for (int j = 0; j < n; ++j) {
             const int buf = j & 1;
             if (!dead)
-                dead = !__all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((j >> 1) & 1), p.err,
+                dead = !__all_sync(0xffffffffu, mbar_wait_sleep(&bars->s_full[buf], (uint32_t)((j >> 1) & 1), p.err,
                                                           kRoleSoftmax | kBarS | (unsigned)(j & 0xffff)));
             uint32_t sr[32];
             bool moved = false;
@@ -388,7 +388,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (softmax_any(dead)) { dead = true; break; }
                 // O^T is rescaled: after the product that last added to it
                 if (j > 0) {
-                    dead = !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
+                    dead = !__all_sync(0xffffffffu, mbar_wait_sleep(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
                                                               kRoleSoftmax | kBarPV | (unsigned)(j & 0xffff)));
                     if (!dead) {
                         tc_fence_after();
@@ -425,7 +425,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 }
             }
             if (!dead && j > 0)                   // the P tile has been read
-                dead = !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
+                dead = !__all_sync(0xffffffffu, mbar_wait_sleep(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
                                                           kRoleSoftmax | kBarPV | (unsigned)(j & 0xffff)));
             if (!dead) {
                 if (rows_here) {
@@ -445,7 +445,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         if (tid == 0) griddep_launch_dependents();
         if (!dead)
-            dead = !__all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (uint32_t)((n - 1) & 1), p.err,
+            dead = !__all_sync(0xffffffffu, mbar_wait_sleep(&bars->pv_done, (uint32_t)((n - 1) & 1), p.err,
                                                       kRoleSoftmax | kBarLast));
         if (rows_here) {
 #pragma unroll
@@ -542,69 +542,68 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
             mbar_wait_sleep(&bars->q_full, 0, p.err, kRoleProducer | kBarLast);
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kQkWarp || warp == kPvWarp) {
         // ------------------------------ products ------------------------------
-        if (lane == 0) {
-            const uint32_t base = smem_u32(smem);
-            const uint64_t qd0 = sdesc(base + L::kOffQ, 16, 1024);
+        // A warp for each product: what they wait for is on barriers alone.  The whole warp runs
+        // the loop (addresses and descriptors stay in uniform registers) and one lane issues.
+        const uint32_t base = smem_u32(smem);
+        const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+        const uint32_t leader = elect_one();
+        const int tiles = __reduce_max_sync(0xffffffffu, n);
+        auto wait = [&](uint64_t* bar, int phase, unsigned code) {
+            return __all_sync(0xffffffffu, mbar_wait_sleep(bar, (uint32_t)(phase & 1), p.err, kRoleMma | code)) != 0;
+        };
+        bool ok = true;
+        if (warp == kQkWarp) {
+            const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
             const uint64_t kd0 = sdesc(base + L::kOffTile, 16, 1024);
-            const uint64_t vd0 = sdesc(base + L::kOffTile, kChunk, 1024);
-            const uint64_t pd0 = sdesc(base + L::kOffP, 16, 1024);
-            bool ok = mbar_wait(&bars->q_full, 0, p.err, kRoleMma | kBarLast);
-            int nqk = 0, g = 0, npv = 0;
-            uint64_t t_last = global_timer_ns();
-            while (ok && npv < n) {
-                bool progressed = false;
-                if (npv < nqk && mbar_try_wait(&bars->p_full, (uint32_t)(npv & 1))) {
+            ok = wait(&bars->q_full, 0, kBarLast);
+#pragma unroll 1
+            for (int j = 0; ok && j < tiles; ++j) {
+                const int st = j & 1;
+                const uint32_t dS = tm + L::kTmemS + (uint32_t)(st * kKeys);
+                const uint64_t kd = kd0 + (uint64_t)(st * (kTile >> 4));
+                if (j >= 2) ok = wait(&bars->s_free[st], (j >> 1) + 1, kBarS | (unsigned)(j & 0xffff));
+#pragma unroll
+                for (int g = 0; g < kPieces; ++g) {
+                    ok = ok && wait(&bars->full[st][g], j >> 1, kBarFull | (unsigned)(j & 0xffff));
+                    if (!ok) break;
                     tc_fence_after();
-                    const uint64_t vd = vd0 + (uint64_t)((npv & 1) * (kTile >> 4));
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            mma_bf16(tmem + L::kTmemO + (uint32_t)(m * NR),
-                                     vd + (uint64_t)((2 * m * kChunk + k * 2048) >> 4), pd0 + (uint64_t)(2 * k),
-                                     L::kIdescPV, npv > 0 || k > 0);
-                        mma_commit(&bars->empty[npv & 1][1 + m]);
-                    }
-                    mma_commit(&bars->pv_done);
-                    ++npv;
-                    progressed = true;
+                    const int c0 = g == 0 ? 8 : 2 * (g - 1);      // first chunk of the piece
+                    mma4_if<2, 2>(leader, dS, qd + (uint64_t)(c0 * L::kQChunk >> 4), kd + (uint64_t)(c0 * kChunk >> 4),
+                                  kIdescS, g > 0 ? 1u : 0u);
+                    if (g > 0)
+                        mma4_if<2, 2>(leader, dS, qd + (uint64_t)((c0 + 1) * L::kQChunk >> 4),
+                                      kd + (uint64_t)((c0 + 1) * kChunk >> 4), kIdescS, 1u);
                 }
-                if (nqk < n &&
-                    (g > 0 || nqk < 2 || mbar_try_wait(&bars->s_free[nqk & 1], (uint32_t)(((nqk >> 1) + 1) & 1))) &&
-                    mbar_try_wait(&bars->full[nqk & 1][g], (uint32_t)((nqk >> 1) & 1))) {
-                    tc_fence_after();
-                    const uint32_t dS = tmem + L::kTmemS + (uint32_t)((nqk & 1) * kKeys);
-                    const uint64_t kd = kd0 + (uint64_t)((nqk & 1) * (kTile >> 4));
-                    const int c0 = g == 0 ? 8 : 2 * (g - 1), c1 = g == 0 ? 9 : c0 + 2;
-                    for (int ch = c0; ch < c1; ++ch)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(dS, qd0 + (uint64_t)((ch * L::kQChunk + 32 * k) >> 4),
-                                     kd + (uint64_t)((ch * kChunk + 32 * k) >> 4), kIdescS, g > 0 || k > 0);
-                    if (++g == kPieces) {
-                        mma_commit(&bars->empty[nqk & 1][0]);
-                        mma_commit(&bars->s_full[nqk & 1]);
-                        g = 0;
-                        ++nqk;
-                    }
-                    progressed = true;
-                }
-                if (progressed) {
-                    t_last = global_timer_ns();
-                } else if (global_timer_ns() - t_last > kWaitLimitNs || *((volatile int*)&bars->abort)) {
-                    if (p.err) {
-                        atomicOr(p.err, kErrWaitTimeout);
-                        atomicCAS(p.err + 1, 0u, 0x80000000u | kRoleMma | kBarS | (unsigned)(npv & 0xffff));
-                    }
-                    ok = false;
-                }
+                if (!ok) break;
+                mma_commit_if(leader, &bars->empty[st][0]);
+                mma_commit_if(leader, &bars->s_full[st]);
             }
-            if (!ok) bars->abort = 1;
-            mma_commit(&bars->drain);             // nothing in flight when tensor memory is freed
-            mbar_wait(&bars->drain, 0, p.err, kRoleMma | kBarLast);
+        } else {
+            const uint64_t vd0 = sdesc(base + L::kOffTile, kChunk, 1024);
+            const uint64_t pd = sdesc(base + L::kOffP, 16, 1024);
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j) {
+                const int st = j & 1;
+                const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
+                ok = wait(&bars->p_full, j, kBarPV | (unsigned)(j & 0xffff));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t add = j > 0 ? 1u : 0u;
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    mma4_if<2048 / 16, 2>(leader, tm + L::kTmemO + (uint32_t)(m * NR),
+                                          vd + (uint64_t)(2 * m * kChunk >> 4), pd, L::kIdescPV, add);
+                    mma_commit_if(leader, &bars->empty[st][1 + m]);
+                }
+                mma_commit_if(leader, &bars->pv_done);
+            }
         }
+        if (!ok) bars->abort = 1;
+        // nothing in flight when tensor memory is freed
+        mma_commit_if(leader, &bars->drain[warp - kQkWarp]);
+        mbar_wait(&bars->drain[warp - kQkWarp], 0, p.err, kRoleMma | kBarLast);
     } else if constexpr (Q8) {
         // ------------------------------ conversion ----------------------------
         const int ct = tid - 32 * kConvWarp, key = ct >> 2, q = ct & 3;
@@ -672,7 +671,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmemCols)
                      : "memory");

@@ -46,6 +46,76 @@ RAPID_DEVICE void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint
         : "memory");
 }
 
+// One lane of the warp, the same one at every call.
+RAPID_DEVICE uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// Four products in a row, issued by the lane with `leader` set while the whole warp runs the code:
+// addresses and descriptors then stay in uniform registers, and the tensor unit gets an instruction
+// every 30 to 40 clocks where a single lane's own loop gives one every 80 to 140.  The descriptors
+// grow by A_STEP and B_STEP (16-byte units) a product; the first one starts the sum where
+// `accumulate` is 0.
+template <int A_STEP, int B_STEP>
+RAPID_DEVICE void mma4_if(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t"
+        ".reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "add.u64 a1, %1, %6;\n\t"
+        "add.u64 a2, %1, %7;\n\t"
+        "add.u64 a3, %1, %8;\n\t"
+        "add.u64 b1, %2, %9;\n\t"
+        "add.u64 b2, %2, %10;\n\t"
+        "add.u64 b3, %2, %11;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(A_STEP), "n"(2 * A_STEP),
+        "n"(3 * A_STEP), "n"(B_STEP), "n"(2 * B_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+// ... with A in tensor memory, 8 columns a product.
+template <int B_STEP>
+RAPID_DEVICE void mma4_ta_if(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t"
+        ".reg .b64 b1, b2, b3;\n\t"
+        ".reg .b32 a1, a2, a3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\t"
+        "add.u32 a2, %1, 16;\n\t"
+        "add.u32 a3, %1, 24;\n\t"
+        "add.u64 b1, %2, %6;\n\t"
+        "add.u64 b2, %2, %7;\n\t"
+        "add.u64 b3, %2, %8;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader), "n"(B_STEP), "n"(2 * B_STEP),
+        "n"(3 * B_STEP)
+        : "memory");
+}
+RAPID_DEVICE void mma_commit_if(uint32_t leader, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(leader)
+        : "memory");
+}
+
 RAPID_DEVICE void mma_commit(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
