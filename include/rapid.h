@@ -923,7 +923,8 @@ rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype
  *             bf16 cache rows or of rapid_latent_read's, where they stand)
  *  strides    HOST array of eleven element strides: batch, token, head of Q, of
  *             K and of V, batch and token of K_rope; or NULL: all packed.  Every
- *             stride a multiple of 8 (16 bytes)
+ *             stride a multiple of 8 (16 bytes), and positive where its dimension
+ *             is larger than 1
  *  n_rows     device int32 [B] or NULL (n): sequence b has tokens [0, n_rows[b]);
  *             O and LSE behind them stay as they are
  *  O          bf16 [B, n, H, 128]; LSE float [B, H, n]

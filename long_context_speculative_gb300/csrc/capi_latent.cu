@@ -189,6 +189,10 @@ rapid_status rapid_latent_prefill_attn(const void* Q, const void* K, const void*
                                 kv_rows * kLatentRope, kLatentRope};
     const int64_t* s = strides ? strides : packed;
     if (!strides_ok(s, 11)) return RAPID_EINVAL;
+    // rows are copied by their strides: a dimension that repeats a row has none
+    const int64_t size[11] = {B, n, H, B, kv_rows, H, B, kv_rows, H, B, kv_rows};
+    for (int i = 0; i < 11; ++i)
+        if (size[i] > 1 && s[i] == 0) return RAPID_EINVAL;
     LatentPrefillParams p{};
     p.Q = Q; p.K = K; p.V = V; p.K_rope = K_rope;
     p.prefix_len = prefix_len; p.n_rows = n_rows; p.O = O; p.LSE = LSE;
