@@ -182,10 +182,12 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 }
             }
             if (masked) {
-                // all 256 softmax threads: half a key's values each
+                // all 256 softmax threads: half a key's values each.  Only a tile that has S of
+                // these keys knows which lap of the ring they are in, and waits for both.
                 const int ch = 5 * j + 3 + (tid & 1), key = tid >> 1;
-                if (!dead) dead = !wait(&bars->full[(5 * j + 3) % kRing], (5 * j + 3) / kRing, kBarFull) ||
-                                  !wait(&bars->full[(5 * j + 4) % kRing], (5 * j + 4) / kRing, kBarFull);
+                if (mine && !dead) dead = !wait(&bars->full[(5 * j + 3) % kRing], (5 * j + 3) / kRing, kBarFull) ||
+                                          !wait(&bars->full[(5 * j + 4) % kRing], (5 * j + 4) / kRing, kBarFull);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
                 uint8_t* v = smem + kOffRing + (ch % kRing) * kChunk + key * 128;
                 const bool inside = (int64_t)j * kTile + key < P + count;
                 bool odd = false;
