@@ -910,6 +910,9 @@ rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype
                                const uint8_t* spec_mask, float softmax_scale, void* O, float* LSE,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of scratch that rapid_latent_prefill_attn needs; 0 for sizes it rejects. */
+size_t rapid_latent_prefill_attn_workspace_size(int B, int n, int H, int64_t kv_rows);
+
 /*
  * Expanded attention of a prompt chunk: n tokens of every sequence behind
  * prefix_len[b] earlier ones, token i seeing keys [0, prefix_len[b] + i]:
@@ -929,21 +932,24 @@ rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype
  *             O and LSE behind them stay as they are
  *  O          bf16 [B, n, H, 128]; LSE float [B, H, n]
  *  softmax_scale  <= 0 selects 1/sqrt(192)
+ *  workspace  as for rapid_latent_attn
  *
  * A key that a token does not see has no effect on it, whatever it holds; nor
  * has another token's query.
  *
- * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], n < 1, B * n
- * above 2^31, H outside [1, RAPID_LATENT_MAX_HEADS], kv_rows outside [1,
- * RAPID_LATENT_MAX_ROWS], a bad stride or alignment (16 bytes), a softmax_scale
- * that is not finite; RAPID_ECUDA on launch failure.  A sequence with n_rows
+ * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], n < 1, H outside
+ * [1, RAPID_LATENT_MAX_HEADS], B * n * H above RAPID_LATENT_MAX_QUERIES, kv_rows
+ * outside [1, RAPID_LATENT_MAX_ROWS], a bad stride or alignment (16 bytes), a
+ * softmax_scale that is not finite; RAPID_ENOMEM for a short workspace;
+ * RAPID_ECUDA on launch failure.  A sequence with n_rows
  * outside [0, n], a negative prefix_len or prefix_len + n_rows above kv_rows is
  * left alone and bit 1 of the device error word is set.
  */
 rapid_status rapid_latent_prefill_attn(const void* Q, const void* K, const void* V, const void* K_rope,
                                        const int64_t* strides, int B, int n, int H, int64_t kv_rows,
                                        const int32_t* prefix_len, const int32_t* n_rows,
-                                       float softmax_scale, void* O, float* LSE, void* stream);
+                                       float softmax_scale, void* O, float* LSE, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -42,6 +42,27 @@ AttnPlan plan_attn(int B, int H, int n_q, int64_t cap) {
     return pl;
 }
 
+struct PrefillPlan {
+    int slots;
+    size_t acc, ml, index;
+    size_t bytes() const { return acc + ml + 2 * index; }
+};
+
+bool prefill_args_ok(int B, int n, int H, int64_t kv_rows) {
+    if (B < 1 || B > 65535 || n < 1 || H < 1 || H > RAPID_LATENT_MAX_HEADS) return false;
+    return (int64_t)B * n * H <= RAPID_LATENT_MAX_QUERIES && capacity_ok(kv_rows);
+}
+
+PrefillPlan plan_prefill(int B, int n, int H, int64_t kv_rows) {
+    PrefillPlan pl;
+    const size_t rows = latent_prefill_block_rows();
+    pl.slots = latent_prefill_slots(B, n, H, kv_rows);
+    pl.acc = align_up(pl.slots * rows * kLatentHead * sizeof(float));
+    pl.ml = align_up(pl.slots * rows * 2 * sizeof(float));
+    pl.index = pl.slots ? align_up(B * ((n + rows - 1) / rows) * sizeof(int)) : kAlign;
+    return pl;
+}
+
 bool attn_args_ok(int B, int H, int n_q, int64_t cap, int cache_dtype) {
     if (B < 1 || B > 65535 || H < 1 || H > RAPID_LATENT_MAX_HEADS || !cache_ok(cache_dtype)) return false;
     if (n_q < 1 || n_q > RAPID_MAX_NQ || !capacity_ok(cap) || cap < n_q) return false;
@@ -170,14 +191,18 @@ rapid_status rapid_latent_attn(const void* Q, const void* cache, int cache_dtype
     return status_of(launch_latent_attn(p, static_cast<cudaStream_t>(stream)));
 }
 
+size_t rapid_latent_prefill_attn_workspace_size(int B, int n, int H, int64_t kv_rows) {
+    return prefill_args_ok(B, n, H, kv_rows) ? plan_prefill(B, n, H, kv_rows).bytes() : 0;
+}
+
 rapid_status rapid_latent_prefill_attn(const void* Q, const void* K, const void* V, const void* K_rope,
                                        const int64_t* strides, int B, int n, int H, int64_t kv_rows,
                                        const int32_t* prefix_len, const int32_t* n_rows,
-                                       float softmax_scale, void* O, float* LSE, void* stream) {
-    if (!Q || !K || !V || !K_rope || !prefix_len || !O || !LSE) return RAPID_EINVAL;
-    if (B < 1 || B > 65535 || n < 1 || H < 1 || H > RAPID_LATENT_MAX_HEADS) return RAPID_EINVAL;
-    if ((int64_t)B * n > ((int64_t)1 << 31) || !capacity_ok(kv_rows)) return RAPID_EINVAL;
-    const void* rows16[] = {Q, K, V, K_rope, O};
+                                       float softmax_scale, void* O, float* LSE, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    if (!Q || !K || !V || !K_rope || !prefix_len || !O || !LSE || !workspace) return RAPID_EINVAL;
+    if (!prefill_args_ok(B, n, H, kv_rows)) return RAPID_EINVAL;
+    const void* rows16[] = {Q, K, V, K_rope, O, workspace};
     for (const void* x : rows16)
         if (!aligned(x, 16)) return RAPID_EINVAL;
     if (!aligned(prefix_len, 4) || !aligned(n_rows, 4) || !aligned(LSE, 4)) return RAPID_EINVAL;
@@ -193,7 +218,15 @@ rapid_status rapid_latent_prefill_attn(const void* Q, const void* K, const void*
     const int64_t size[11] = {B, n, H, B, kv_rows, H, B, kv_rows, H, B, kv_rows};
     for (int i = 0; i < 11; ++i)
         if (size[i] > 1 && s[i] == 0) return RAPID_EINVAL;
+    const PrefillPlan pl = plan_prefill(B, n, H, kv_rows);
+    if (workspace_bytes < pl.bytes()) return RAPID_ENOMEM;
     LatentPrefillParams p{};
+    char* ws = static_cast<char*>(workspace);
+    p.part_acc = reinterpret_cast<float*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + pl.acc);
+    p.part_first = reinterpret_cast<int*>(ws + pl.acc + pl.ml);
+    p.part_count = reinterpret_cast<int*>(ws + pl.acc + pl.ml + pl.index);
+    p.slots = pl.slots;
     p.Q = Q; p.K = K; p.V = V; p.K_rope = K_rope;
     p.prefix_len = prefix_len; p.n_rows = n_rows; p.O = O; p.LSE = LSE;
     p.err = device_error_word();

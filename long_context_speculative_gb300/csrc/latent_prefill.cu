@@ -14,6 +14,8 @@
 //             moves only when a score passes it by more than 2^8, and O is rescaled then
 //   8         copies by TMA
 //   9, 10     issue the products of the two tiles
+// Few CTAs behind long prefixes (fewer blocks of tokens than two waves) share their keys out: a split
+// takes a run of key tiles and leaves (O, maximum, sum) in the workspace, joined by log-sum-exp.
 // P is rounded to bf16 (2^-9 of each probability, and it averages out); sums are fp32.
 //
 // Keys that a token does not see have no effect on it, whatever they hold: in tiles of keys that
@@ -57,11 +59,18 @@ enum : unsigned int {
     kBarLast = 6u << 16
 };
 
+struct Piece {
+    int b, h, qb;            // block of tokens of a head (b = -1: no work)
+    int s, S;                // split, splits of the block
+    int slot;                // first split's slot
+};
+
 struct Bars {
     uint64_t full[kRing], empty[kRing];
     uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain[2];
     uint32_t tmem_base;
     int abort;
+    Piece piece;
     uint32_t flagged[4];     // keys of a tile with a value that is not finite
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block too small");
@@ -96,6 +105,70 @@ RAPID_DEVICE void tma_load_4d(void* dst, const CUtensorMap* tm, int x, int y, in
         : "memory");
 }
 
+// Key tiles of block qb of sequence b (0: no tokens there, or a refused sequence).
+RAPID_DEVICE int block_tiles(const LatentPrefillParams& p, int b, int qb) {
+    const int count = p.n_rows ? p.n_rows[b] : p.n;
+    const int64_t P = p.prefix_len[b];
+    if (count < 0 || count > p.n || P < 0 || P + count > p.kv_rows) return 0;
+    const int last = min(2 * kTile * (qb + 1), count) - 1;
+    return last < 2 * kTile * qb ? 0 : (int)((P + last) / kTile + 1);
+}
+
+// Which block and split a slot holds, worked out by one warp: the least number of key tiles a split
+// for which all splits fit into p.slots.  Splits lie in the order (sequence, block, head, split).
+RAPID_DEVICE Piece find_piece(const LatentPrefillParams& p, int blocks, int c, int lane) {
+    const int pairs = p.B * blocks;
+    int longest = 1;
+    int64_t total = 0;
+    for (int x = lane; x < pairs; x += 32) {
+        const int t = block_tiles(p, x / blocks, x % blocks);
+        total += (int64_t)t * p.H;
+        longest = max(longest, t);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    }
+    int lo = max(1, (int)((total + p.slots - 1) / p.slots)), hi = max(lo, longest);
+    while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        int used = 0;
+        for (int x = lane; x < pairs; x += 32) used += (block_tiles(p, x / blocks, x % blocks) + mid - 1) / mid;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) used += __shfl_xor_sync(0xffffffffu, used, o);
+        if (used * p.H <= p.slots) hi = mid; else lo = mid + 1;
+    }
+    int first = 0;
+    for (int x0 = 0; x0 < pairs; x0 += 32) {
+        const int x = x0 + lane;
+        const int S = x < pairs ? (block_tiles(p, x / blocks, x % blocks) + lo - 1) / lo : 0;
+        int upto = S * p.H;                       // inclusive scan
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, c < first + upto);
+        if (here) {
+            const int l = __ffs(here) - 1;
+            Piece r;
+            r.S = __shfl_sync(0xffffffffu, S, l);
+            const int start = first + __shfl_sync(0xffffffffu, upto, l) - r.S * p.H;
+            r.b = (x0 + l) / blocks;
+            r.qb = (x0 + l) % blocks;
+            r.h = (c - start) / r.S;
+            r.s = (c - start) % r.S;
+            r.slot = start;
+            return r;
+        }
+        first += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return Piece{-1, 0, 0, 0, 1, 0};
+}
+
+// SPLIT: the grid is p.slots pieces of key runs; else a CTA for every block of tokens.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmR,
@@ -104,16 +177,37 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars* bars = reinterpret_cast<Bars*>(smem + kOffBar);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    // The blocks of a head are neighbours (their keys stay in L2), the longest first.
     const int blocks = (p.n + 2 * kTile - 1) / (2 * kTile);
-    const int bh = blockIdx.x / blocks, qb = blocks - 1 - (blockIdx.x - bh * blocks);
-    const int b = bh / p.H, h = bh - b * p.H;
-    const int i0 = qb * 2 * kTile;               // first token of the CTA
     griddep_wait();
+    Piece pc;
+    if constexpr (SPLIT) {
+        if (warp == 0) {
+            pc = find_piece(p, blocks, blockIdx.x, lane);
+            if (lane == 0) bars->piece = pc;
+            if (blockIdx.x == 0 && p.err)         // refused sequences
+                for (int b = lane; b < p.B; b += 32) {
+                    const int count = p.n_rows ? p.n_rows[b] : p.n;
+                    const int64_t P = p.prefix_len[b];
+                    if (count < 0 || count > p.n || P < 0 || P + count > p.kv_rows) atomicOr(p.err, kErrBadInput);
+                }
+        }
+        __syncthreads();
+        pc = bars->piece;
+        if (pc.b < 0) return;
+        if (tid == 0 && pc.h == 0 && pc.s == 0) {
+            p.part_first[pc.b * blocks + pc.qb] = pc.slot;
+            p.part_count[pc.b * blocks + pc.qb] = pc.S;
+        }
+    } else {
+        // The blocks of a head are neighbours (their keys stay in L2), the longest first.
+        const int bh = blockIdx.x / blocks;
+        pc = Piece{bh / p.H, bh % p.H, blocks - 1 - (int)(blockIdx.x - bh * blocks), 0, 1, 0};
+    }
+    const int b = pc.b, h = pc.h, i0 = pc.qb * 2 * kTile;   // first token of the CTA
     const int count = p.n_rows ? p.n_rows[b] : p.n;
     const int64_t P = p.prefix_len[b];
-    if (count < 0 || count > p.n || P < 0 || P + count > p.kv_rows) {   // refused: left alone
-        if (qb == 0 && h == 0 && tid == 0 && p.err) atomicOr(p.err, kErrBadInput);
+    if (!SPLIT && (count < 0 || count > p.n || P < 0 || P + count > p.kv_rows)) {   // refused: left alone
+        if (pc.qb == 0 && h == 0 && tid == 0 && p.err) atomicOr(p.err, kErrBadInput);
         return;
     }
     if (i0 >= count) return;
@@ -144,13 +238,16 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    // tiles of keys that tile t of the CTA sees any of; the first that some token does not see whole
+    // tiles of keys that tile t of the CTA sees any of
     auto key_tiles = [&](int t) -> int {
         const int last = min(i0 + kTile * (t + 1), count) - 1;
         return last < i0 + kTile * t ? 0 : (int)((P + last) / kTile + 1);
     };
-    const int n0 = key_tiles(0), n1 = key_tiles(1), n = max(n0, n1);
-    const int first_masked = (int)((P + i0 + 1) / kTile);
+    const int seen0 = key_tiles(0), seen1 = key_tiles(1), seen = max(seen0, seen1);
+    // the split's run of them, from j0 on, and the first that some token does not see whole
+    const int j0 = (int)((int64_t)pc.s * seen / pc.S), j1 = (int)((int64_t)(pc.s + 1) * seen / pc.S);
+    const int n = j1 - j0, n0 = max(0, min(seen0 - j0, n)), n1 = max(0, min(seen1 - j0, n));
+    const int first_masked = (int)((P + i0 + 1) / kTile) - j0;
 
     if (warp < 8) {
         // ------------------------------ softmax -------------------------------
@@ -189,7 +286,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                                           !wait(&bars->full[(5 * j + 4) % kRing], (5 * j + 4) / kRing, kBarFull);
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 uint8_t* v = smem + kOffRing + (ch % kRing) * kChunk + key * 128;
-                const bool inside = (int64_t)j * kTile + key < P + count;
+                const bool inside = (int64_t)(j0 + j) * kTile + key < P + count;
                 bool odd = false;
                 if (inside && !dead) {
 #pragma unroll
@@ -216,7 +313,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 if (tid < 4) bars->flagged[tid] = 0;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (mine && !dead) {
-                    const int64_t lim = P + i - (int64_t)j * kTile;       // columns <= lim are seen
+                    const int64_t lim = P + i - (int64_t)(j0 + j) * kTile;       // columns <= lim are seen
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -282,26 +379,39 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             if (lane == 0) mbar_arrive(&bars->p_full[t]);
         }
         if (!dead && nt > 0) dead = !wait(&bars->pv_done[t], nt - 1, kBarLast);
+        const bool part = SPLIT && pc.S > 1;
+        const int64_t part_row = (int64_t)blockIdx.x * 2 * kTile + kTile * t + row;
+        if (part && !dead) {
+            p.part_ml[part_row * 2] = m_run;      // (no keys: -inf and 0, and no O)
+            p.part_ml[part_row * 2 + 1] = l_run;
+        }
         if (!dead && nt > 0) {
             tc_fence_after();
-            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+            const float inv = part ? 1.f : l_run == 0.f ? 0.f : 1.f / l_run;
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.O) +
                                                   (((int64_t)b * p.n + i) * p.H + h) * kLatentHead);
+            float4* acc = reinterpret_cast<float4*>(p.part_acc + part_row * kLatentHead);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 uint32_t o[16];
                 tmem_ld16(o_addr + (uint32_t)(16 * x), o);
                 tmem_wait_ld();
+                if (i >= count) continue;
+                if (part) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        acc[4 * x + u] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 1]),
+                                                     __uint_as_float(o[4 * u + 2]), __uint_as_float(o[4 * u + 3]));
+                    continue;
+                }
                 uint32_t w[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
                     w[u] = bf16x2(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
-                if (i < count) {
-                    dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
-                    dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+                dst[2 * x] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[2 * x + 1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            if (i < count)
+            if (i < count && !part)
                 p.LSE[((int64_t)b * p.H + h) * p.n + i] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * kLn2;
         }
         if (dead) bars->abort = 1;
@@ -330,9 +440,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                         }
                         mbar_arrive_expect_tx(&bars->full[sl], kChunk);
                         uint8_t* dst = smem + kOffRing + sl * kChunk;
-                        if (x < 2) tma_load_4d(dst, &tmK, 64 * x, j * kTile, h, b, &bars->full[sl]);
-                        else if (x == 2) tma_load_3d(dst, &tmR, 0, j * kTile, b, &bars->full[sl]);
-                        else tma_load_4d(dst, &tmV, 64 * (x - 3), j * kTile, h, b, &bars->full[sl]);
+                        if (x < 2) tma_load_4d(dst, &tmK, 64 * x, (j0 + j) * kTile, h, b, &bars->full[sl]);
+                        else if (x == 2) tma_load_3d(dst, &tmR, 0, (j0 + j) * kTile, b, &bars->full[sl]);
+                        else tma_load_4d(dst, &tmV, 64 * (x - 3), (j0 + j) * kTile, h, b, &bars->full[sl]);
                         ++issued;
                     }
                     if (j == 0) load_q(1);
@@ -415,6 +525,42 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     }
 }
 
+// Joins the splits of a token and head by log-sum-exp: one warp each.
+__global__ void __launch_bounds__(128) latent_prefill_merge_kernel(const LatentPrefillParams p) {
+    griddep_wait();
+    const int lane = threadIdx.x & 31, blocks = (p.n + 2 * kTile - 1) / (2 * kTile);
+    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);   // (b, i, h)
+    const int h = (int)(unit % p.H), b = (int)(unit / p.H / p.n), i = (int)(unit / p.H % p.n);
+    if (b >= p.B) return;
+    const int qb = i / (2 * kTile), count = p.n_rows ? p.n_rows[b] : p.n;
+    if (i >= count || block_tiles(p, b, qb) == 0) return;
+    const int S = p.part_count[b * blocks + qb];
+    if (S <= 1) return;                           // written by its only split
+    const int64_t row = ((int64_t)p.part_first[b * blocks + qb] + (int64_t)h * S) * 2 * kTile + i % (2 * kTile);
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row;
+    float M = -INFINITY;
+    for (int s = lane; s < S; s += 32) M = fmaxf(M, ml[(int64_t)s * 2 * kTile].x);
+    M = warp_max(M);
+    const float ref = M == -INFINITY ? 0.f : M;
+    const float4* acc = reinterpret_cast<const float4*>(p.part_acc + row * kLatentHead) + lane;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < S; ++s) {
+        const float2 x = ml[(int64_t)s * 2 * kTile];
+        if (x.y == 0.f) continue;                 // saw no key: left no O
+        const float f = ex2(x.x - ref);
+        const float4 v = __ldcs(acc + (int64_t)s * 2 * kTile * (kLatentHead / 4));
+        l = fmaf(f, x.y, l);
+        a.x = fmaf(f, v.x, a.x); a.y = fmaf(f, v.y, a.y);
+        a.z = fmaf(f, v.z, a.z); a.w = fmaf(f, v.w, a.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + (((int64_t)b * p.n + i) * p.H + h) * kLatentHead)[lane] =
+        make_uint2(bf16x2(a.x * inv, a.y * inv), bf16x2(a.z * inv, a.w * inv));
+    if (lane == 0) p.LSE[((int64_t)b * p.H + h) * p.n + i] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
 // Rows of `width` values with element strides for the outer dimensions (rows first); the
 // stride of a dimension of size 1 means nothing, and the encoder wants one.
 bool make_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims, const int64_t* strides) {
@@ -442,9 +588,11 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t st)
     if (!make_map(&tmQ, p.Q, 4, qd, qs) || !make_map(&tmK, p.K, 4, kd, ks) || !make_map(&tmV, p.V, 4, kd, vs) ||
         !make_map(&tmR, p.K_rope, 3, rd, rs))
         return cudaErrorInvalidValue;
-    const int64_t grid = (int64_t)p.B * p.H * ((p.n + 2 * kTile - 1) / (2 * kTile));
-    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const int64_t grid = p.slots ? p.slots : (int64_t)p.B * p.H * ((p.n + 2 * kTile - 1) / (2 * kTile));
+    const int64_t rows = ((int64_t)p.B * p.n * p.H + 3) / 4;
+    if (grid > 0x7fffffff || rows > 0x7fffffff) return cudaErrorInvalidValue;
+    auto kern = p.slots ? latent_prefill_kernel<true> : latent_prefill_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
@@ -456,7 +604,22 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_prefill_kernel, tmQ, tmK, tmV, tmR, p);
+    e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, tmR, p);
+    if (e != cudaSuccess || !p.slots) return e;
+    cfg.gridDim = dim3((unsigned)rows, 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, p);
 }
+
+// Slots for splits, or 0: every block of tokens its own CTA.  With fewer blocks than two waves of
+// CTAs hold, the longest of them alone would decide the time; two waves of pieces of equal
+// length do not.  A prompt's own keys alone (kv_rows about n) are short, and stay whole.
+int latent_prefill_slots(int B, int n, int H, int64_t kv_rows) {
+    const int64_t units = (int64_t)B * H * ((n + 2 * kTile - 1) / (2 * kTile)), slots = 2 * (int64_t)sm_count();
+    return units <= slots && kv_rows > 4 * kTile ? (int)slots : 0;
+}
+
+size_t latent_prefill_block_rows() { return 2 * kTile; }
 
 }  // namespace rapid

@@ -135,8 +135,10 @@ def lib() -> ctypes.CDLL:
     L.rapid_latent_attn_workspace_size.restype = sz
     L.rapid_latent_attn.argtypes = [vp, vp, i32, i32, i32, i32, i64, vp, vp, f32, vp, vp, vp, sz, vp]
     L.rapid_latent_attn.restype = i32
+    L.rapid_latent_prefill_attn_workspace_size.argtypes = [i32, i32, i32, i64]
+    L.rapid_latent_prefill_attn_workspace_size.restype = sz
     L.rapid_latent_prefill_attn.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i64, vp, vp, f32, vp,
-                                            vp, vp]
+                                            vp, vp, sz, vp]
     L.rapid_latent_prefill_attn.restype = i32
     _lib = L
     return L
@@ -745,7 +747,12 @@ def rapid_latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, O, LSE, wo
     _check(st, "rapid_latent_attn")
 
 
-def rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, O, LSE, stream=None):
+def rapid_latent_prefill_attn_workspace_size(B, n, H, kv_rows) -> int:
+    return int(lib().rapid_latent_prefill_attn_workspace_size(B, n, H, kv_rows))
+
+
+def rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, O, LSE, workspace,
+                              stream=None):
     """Expanded causal attention of a prompt chunk; Q, K, V and K_rope may be strided views."""
     dev = _device_of(Q, "Q")
     if Q.dim() != 4 or K.dim() != 4:
@@ -760,7 +767,9 @@ def rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale
         *[x[0] for x in parts], (ctypes.c_int64 * 11)(*[s for x in parts for s in x[1]]), B, n, H, L,
         _arg(prefix_len, dev, i32, (B,), "prefix_len"), _arg(n_rows, dev, i32, (B,), "n_rows"),
         softmax_scale, _arg(O, dev, torch.bfloat16, (B, n, H, d), "O"),
-        _arg(LSE, dev, torch.float32, (B, H, n), "LSE"), _raw_stream(stream, dev))
+        _arg(LSE, dev, torch.float32, (B, H, n), "LSE"),
+        _arg(workspace, dev, torch.uint8, (workspace.numel(),), "workspace"), workspace.numel(),
+        _raw_stream(stream, dev))
     _check(st, "rapid_latent_prefill_attn")
 
 
@@ -1000,17 +1009,31 @@ def latent_attn(Q, cache, prefix_len, spec_mask=None, softmax_scale=0.0, out=Non
     return out, lse
 
 
+@functools.lru_cache(maxsize=64)
+def _latent_prefill_bytes(dev, B, n, H, kv_rows):
+    nbytes = rapid_latent_prefill_attn_workspace_size(B, n, H, kv_rows)
+    if nbytes == 0:
+        raise RapidError("unsupported latent_prefill_attn shape")
+    return nbytes
+
+
 def latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows=None, softmax_scale=0.0, out=None,
-                        lse=None, stream=None):
+                        lse=None, workspace=None, stream=None):
     """Expanded causal attention of a prompt chunk behind prefix_len[b] tokens: O [B, n, H, 128]
     bf16 and LSE [B, H, n] float32 of Q [B, n, H, 192] over K, V [B, kv_rows, H, 128] and K_rope
     [B, kv_rows, 64] (strided views will do).  Tokens from n_rows[b] on are left as they are
-    (unset in new tensors)."""
-    with _on(stream):
-        B, n, H, _ = Q.shape
-        if out is None:
-            out = torch.empty((B, n, H, RAPID_LATENT_HEAD_DIM), dtype=Q.dtype, device=Q.device)
-        if lse is None:
-            lse = torch.empty((B, H, n), dtype=torch.float32, device=Q.device)
-        rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, out, lse)
+    (unset in new tensors).  Scratch as for latent_attn."""
+    if stream is not None:
+        with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
+            return latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, out, lse,
+                                       workspace)
+    B, n, H, _ = Q.shape
+    if out is None:
+        out = torch.empty((B, n, H, RAPID_LATENT_HEAD_DIM), dtype=Q.dtype, device=Q.device)
+    if lse is None:
+        lse = torch.empty((B, H, n), dtype=torch.float32, device=Q.device)
+    if workspace is None:
+        dev = _device_of(Q, "Q")
+        workspace = _scratch(dev, _latent_prefill_bytes(dev, B, n, H, K.shape[1]))
+    rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, out, lse, workspace)
     return out, lse
