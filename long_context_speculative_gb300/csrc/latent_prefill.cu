@@ -14,7 +14,7 @@
 //             moves only when a score passes it by more than 2^8, and O is rescaled then
 //   8         copies by TMA
 //   9, 10     issue the products of the two tiles
-// Few CTAs behind long prefixes (fewer blocks of tokens than two waves) share their keys out: a split
+// Few blocks of tokens, or blocks behind long prefixes (latent_prefill_slots), share their keys out: a split
 // takes a run of key tiles and leaves (O, maximum, sum) in the workspace, joined by log-sum-exp.
 // P is rounded to bf16 (2^-9 of each probability, and it averages out); sums are fp32.
 //
@@ -67,7 +67,8 @@ struct Piece {
 
 struct Bars {
     uint64_t full[kRing], empty[kRing];
-    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain[2];
+    uint64_t q_full[2], s_full[2], pv_done[2], drain[2];
+    uint64_t p_full[2][2];   // P of a tile's first and second 64 keys
     uint32_t tmem_base;
     int abort;
     Piece piece;
@@ -219,7 +220,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->q_full[t], 1);
             mbar_init(&bars->s_full[t], 1);
-            mbar_init(&bars->p_full[t], 4);
+            for (int u = 0; u < 2; ++u) mbar_init(&bars->p_full[t][u], 4);
             mbar_init(&bars->pv_done[t], 1);
             mbar_init(&bars->drain[t], 1);
         }
@@ -342,6 +343,18 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 l_run *= fac;
                 moved = j > 0;
             }
+            if (__any_sync(0xffffffffu, moved)) {
+                // O is rescaled (S of this tile was issued behind the product that last added to O)
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    uint32_t o[16];
+                    tmem_ld16(o_addr + (uint32_t)(16 * x), o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * fac);
+                    tmem_st16(o_addr + (uint32_t)(16 * x), o);
+                }
+            }
             const float neg = m_run == -INFINITY ? 0.f : -m_run;
             const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
             float2 sum = make_float2(0.f, 0.f);
@@ -356,27 +369,14 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     pk[u] = bf16x2(e.x, e.y);
                 }
                 tmem_st16(s_addr + (uint32_t)(16 * x), pk);
-            }
-            l_run += sum.x + sum.y;
-            if (__any_sync(0xffffffffu, moved)) {
-                // O is rescaled: after the product that last added to it
-                dead = !wait(&bars->pv_done[t], j - 1, kBarPV | (unsigned)(j & 0xffff));
-                if (dead) continue;
-                tc_fence_after();
-#pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    uint32_t o[16];
-                    tmem_ld16(o_addr + (uint32_t)(16 * x), o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * fac);
-                    tmem_st16(o_addr + (uint32_t)(16 * x), o);
+                if (x & 1) {                      // 64 keys' product can start
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->p_full[t][x >> 1]);
                 }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->p_full[t]);
+            l_run += sum.x + sum.y;
         }
         if (!dead && nt > 0) dead = !wait(&bars->pv_done[t], nt - 1, kBarLast);
         const bool part = SPLIT && pc.S > 1;
@@ -489,19 +489,21 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             bool ok = nt == 0 || (wait(&bars->q_full[t], 0, kBarLast) && scores(0));
 #pragma unroll 1
             for (int j = 0; ok && j < nt; ++j) {
-                ok = wait(&bars->p_full[t], j, kBarP | (unsigned)(j & 0xffff));
-                const uint32_t add = j > 0 ? 1u : 0u;
+                ok = chunk(5 * j + 3) && chunk(5 * j + 4);
+                const int sl0 = (5 * j + 3) % kRing, sl1 = (5 * j + 4) % kRing;
+                const uint64_t v0 = vd + (uint64_t)(sl0 * (kChunk >> 4)), v1 = vd + (uint64_t)(sl1 * (kChunk >> 4));
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int sl = (5 * j + 3 + x) % kRing;
-                    ok = ok && chunk(5 * j + 3 + x);
+                for (int u = 0; u < 2; ++u) {         // 64 keys at a time
+                    ok = ok && wait(&bars->p_full[t][u], j, kBarP | (unsigned)(j & 0xffff));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t vb = vd + (uint64_t)(sl * (kChunk >> 4));
-                    mma4_ta_if<128>(leader, dO + (uint32_t)(64 * x), dS, vb, kIdescPV, add);
-                    mma4_ta_if<128>(leader, dO + (uint32_t)(64 * x), dS + 32, vb + 512, kIdescPV, 1u);
-                    mma_commit_if(leader, &bars->empty[sl]);
+                    const uint32_t add = u > 0 || j > 0 ? 1u : 0u;
+                    mma4_ta_if<128>(leader, dO, dS + (uint32_t)(32 * u), v0 + (uint64_t)(512 * u), kIdescPV, add);
+                    mma4_ta_if<128>(leader, dO + 64, dS + (uint32_t)(32 * u), v1 + (uint64_t)(512 * u), kIdescPV, add);
                 }
+                if (!ok) break;
+                mma_commit_if(leader, &bars->empty[sl0]);
+                mma_commit_if(leader, &bars->empty[sl1]);
                 if (!ok) break;
                 mma_commit_if(leader, &bars->pv_done[t]);
                 if (j + 1 < nt) ok = scores(j + 1);
@@ -612,12 +614,17 @@ cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, p);
 }
 
-// Slots for splits, or 0: every block of tokens its own CTA.  With fewer blocks than two waves of
-// CTAs hold, the longest of them alone would decide the time; two waves of pieces of equal
-// length do not.  A prompt's own keys alone (kv_rows about n) are short, and stay whole.
+// Slots for splits, or 0: every block of tokens its own CTA.  With no more blocks than SMs the longest
+// of them alone would decide the time: one wave of pieces of equal length (16 tokens of 16 heads
+// behind 16000, 41 us; two waves of shorter pieces 53).  Up to twice as many, two waves, if the
+// blocks are about equally long because most keys are earlier ones (three ragged chunks of up to 999
+// behind up to 12001, 192 blocks: 159 us, 259 unsplit; but 256 blocks of 1000 behind 1000 take
+// 101, and 88 unsplit).  Few keys stay whole.
 int latent_prefill_slots(int B, int n, int H, int64_t kv_rows) {
-    const int64_t units = (int64_t)B * H * ((n + 2 * kTile - 1) / (2 * kTile)), slots = 2 * (int64_t)sm_count();
-    return units <= slots && kv_rows > 4 * kTile ? (int)slots : 0;
+    const int64_t units = (int64_t)B * H * ((n + 2 * kTile - 1) / (2 * kTile)), sms = sm_count();
+    if (kv_rows <= 4 * kTile) return 0;
+    if (units <= sms) return (int)sms;
+    return units <= 2 * sms && kv_rows >= 4 * (int64_t)n ? (int)(2 * sms) : 0;
 }
 
 size_t latent_prefill_block_rows() { return 2 * kTile; }
