@@ -25,8 +25,8 @@
 //   5, 6   issue QK and PV
 //   7-14   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
 //          quarter of a key, the next tile's in registers while it stores this one.  An e4m3 code
-//          is 2^-120 of a bf16 with the same bits further up, exactly, so a code costs a shift, a
-//          mask and two exact multiplications, no conversion
+//          is 2^-120 of a bf16 with the same bits further up, exactly, so two codes cost a
+//          shift, two masks and an exact multiplication, no conversion
 // P is rounded to bf16 (2^-9 of each probability, and it averages out); sums are fp32.
 //
 // Rows that a query does not see have no effect on it, whatever they hold: in tiles that a mask
@@ -56,7 +56,7 @@ constexpr int kBarBytes = 1536;
 
 template <int NR, bool Q8>
 struct Plan {
-    static constexpr int kThreads = 32 * (Q8 ? kConvWarp + kConvWarps : kConvWarp);
+    static constexpr int kThreads = 32 * (Q8 ? kConvWarp + kConvWarps : kPvWarp + 1);
     static constexpr int kQChunk = NR * 128;
     static constexpr int kOffQ = 0;
     static constexpr int kOffTile = kChunks * kQChunk;
@@ -109,6 +109,9 @@ RAPID_DEVICE uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+RAPID_DEVICE void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 RAPID_DEVICE void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -501,167 +504,199 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             }
         }
         if (dead) bars->abort = 1;
-    } else if (warp == kProducerWarp) {
-        // ------------------------------ copies --------------------------------
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->q_full, kChunks * L::kQChunk);
-            for (int ch = 0; ch < kChunks; ++ch)
-                tma_load_2d(smem + L::kOffQ + ch * L::kQChunk, &tmQ, 64 * ch, b * R + r0, &bars->q_full);
-            int issued = 0;                       // pieces
-            if constexpr (!Q8) {
-                bool ok = true;
-                for (int j = 0; j < n && ok; ++j) {
-                    const int st = j & 1;
-                    uint8_t* tile = smem + L::kOffTile + st * kTile;
-                    const int y = (t_begin + j) * kKeys;
-                    for (int g = 0; g < kPieces; ++g) {
-                        if ((j >= 2 && !mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
-                                                        kRoleProducer | kBarEmpty | (unsigned)(j & 0xffff))) ||
-                            *((volatile int*)&bars->abort)) {
-                            ok = false;
-                            break;
+    } else if (warp < kConvWarp) {
+        if (warp == kProducerWarp) {
+            // ------------------------------ copies --------------------------------
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->q_full, kChunks * L::kQChunk);
+                for (int ch = 0; ch < kChunks; ++ch)
+                    tma_load_2d(smem + L::kOffQ + ch * L::kQChunk, &tmQ, 64 * ch, b * R + r0, &bars->q_full);
+                int issued = 0;                       // pieces
+                if constexpr (!Q8) {
+                    bool ok = true;
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int st = j & 1;
+                        uint8_t* tile = smem + L::kOffTile + st * kTile;
+                        const int y = (t_begin + j) * kKeys;
+                        for (int g = 0; g < kPieces; ++g) {
+                            if ((j >= 2 && !mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
+                                                            kRoleProducer | kBarEmpty | (unsigned)(j & 0xffff))) ||
+                                *((volatile int*)&bars->abort)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&bars->full[st][g], g == 0 ? kChunk : 2 * kChunk);
+                            if (g == 0) {
+                                tma_load_3d(tile + 8 * kChunk, &tmC, 512, y, b, &bars->full[st][0]);
+                            } else {
+                                const int ch = 2 * (g - 1);
+                                tma_load_3d(tile + ch * kChunk, &tmC, 64 * ch, y, b, &bars->full[st][g]);
+                                tma_load_3d(tile + (ch + 1) * kChunk, &tmC, 64 * ch + 64, y, b, &bars->full[st][g]);
+                            }
+                            ++issued;
                         }
-                        mbar_arrive_expect_tx(&bars->full[st][g], g == 0 ? kChunk : 2 * kChunk);
-                        if (g == 0) {
-                            tma_load_3d(tile + 8 * kChunk, &tmC, 512, y, b, &bars->full[st][0]);
-                        } else {
-                            const int ch = 2 * (g - 1);
-                            tma_load_3d(tile + ch * kChunk, &tmC, 64 * ch, y, b, &bars->full[st][g]);
-                            tma_load_3d(tile + (ch + 1) * kChunk, &tmC, 64 * ch + 64, y, b, &bars->full[st][g]);
-                        }
-                        ++issued;
+                    }
+                    if (!ok) {
+                        bars->abort = 1;
+                        // let the copies in flight land before the CTA exits
+                        for (int x = max(0, issued - 2 * kPieces); x < issued; ++x)
+                            mbar_wait(&bars->full[(x / kPieces) & 1][x % kPieces], (uint32_t)((x / kPieces >> 1) & 1),
+                                      p.err, kRoleProducer | kBarFull);
                     }
                 }
-                if (!ok) {
-                    bars->abort = 1;
-                    // let the copies in flight land before the CTA exits
-                    for (int x = max(0, issued - 2 * kPieces); x < issued; ++x)
-                        mbar_wait(&bars->full[(x / kPieces) & 1][x % kPieces], (uint32_t)((x / kPieces >> 1) & 1),
-                                  p.err, kRoleProducer | kBarFull);
-                }
+                mbar_wait_sleep(&bars->q_full, 0, p.err, kRoleProducer | kBarLast);
             }
-            mbar_wait_sleep(&bars->q_full, 0, p.err, kRoleProducer | kBarLast);
-        }
-    } else if (warp == kQkWarp || warp == kPvWarp) {
-        // ------------------------------ products ------------------------------
-        // A warp for each product: what they wait for is on barriers alone.  The whole warp runs
-        // the loop (addresses and descriptors stay in uniform registers) and one lane issues.
-        const uint32_t base = smem_u32(smem);
-        const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
-        const uint32_t leader = elect_one();
-        const int tiles = __reduce_max_sync(0xffffffffu, n);
-        auto wait = [&](uint64_t* bar, int phase, unsigned code) {
-            return __all_sync(0xffffffffu, mbar_wait_sleep(bar, (uint32_t)(phase & 1), p.err, kRoleMma | code)) != 0;
-        };
-        bool ok = true;
-        if (warp == kQkWarp) {
-            const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
-            const uint64_t kd0 = sdesc(base + L::kOffTile, 16, 1024);
-            ok = wait(&bars->q_full, 0, kBarLast);
+        } else if (warp == kQkWarp || warp == kPvWarp) {
+            // ------------------------------ products ------------------------------
+            // A warp for each product: what they wait for is on barriers alone.  The whole warp runs
+            // the loop (addresses and descriptors stay in uniform registers) and one lane issues.
+            const uint32_t base = smem_u32(smem);
+            const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+            const uint32_t leader = elect_one();
+            const int tiles = __reduce_max_sync(0xffffffffu, n);
+            auto wait = [&](uint64_t* bar, int phase, unsigned code) {
+                return __all_sync(0xffffffffu, mbar_wait_sleep(bar, (uint32_t)(phase & 1), p.err, kRoleMma | code)) != 0;
+            };
+            bool ok = true;
+            if (warp == kQkWarp) {
+                const uint64_t qd = sdesc(base + L::kOffQ, 16, 1024);
+                const uint64_t kd0 = sdesc(base + L::kOffTile, 16, 1024);
+                ok = wait(&bars->q_full, 0, kBarLast);
 #pragma unroll 1
-            for (int j = 0; ok && j < tiles; ++j) {
-                const int st = j & 1;
-                const uint32_t dS = tm + L::kTmemS + (uint32_t)(st * kKeys);
-                const uint64_t kd = kd0 + (uint64_t)(st * (kTile >> 4));
-                if (j >= 2) ok = wait(&bars->s_free[st], (j >> 1) + 1, kBarS | (unsigned)(j & 0xffff));
+                for (int j = 0; ok && j < tiles; ++j) {
+                    const int st = j & 1;
+                    const uint32_t dS = tm + L::kTmemS + (uint32_t)(st * kKeys);
+                    const uint64_t kd = kd0 + (uint64_t)(st * (kTile >> 4));
+                    if (j >= 2) ok = wait(&bars->s_free[st], (j >> 1) + 1, kBarS | (unsigned)(j & 0xffff));
 #pragma unroll
-                for (int g = 0; g < kPieces; ++g) {
-                    ok = ok && wait(&bars->full[st][g], j >> 1, kBarFull | (unsigned)(j & 0xffff));
+                    for (int g = 0; g < kPieces; ++g) {
+                        ok = ok && wait(&bars->full[st][g], j >> 1, kBarFull | (unsigned)(j & 0xffff));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const int c0 = g == 0 ? 8 : 2 * (g - 1);      // first chunk of the piece
+                        mma4_if<2, 2>(leader, dS, qd + (uint64_t)(c0 * L::kQChunk >> 4), kd + (uint64_t)(c0 * kChunk >> 4),
+                                      kIdescS, g > 0 ? 1u : 0u);
+                        if (g > 0)
+                            mma4_if<2, 2>(leader, dS, qd + (uint64_t)((c0 + 1) * L::kQChunk >> 4),
+                                          kd + (uint64_t)((c0 + 1) * kChunk >> 4), kIdescS, 1u);
+                    }
+                    if (!ok) break;
+                    mma_commit_if(leader, &bars->empty[st][0]);
+                    mma_commit_if(leader, &bars->s_full[st]);
+                }
+            } else {
+                const uint64_t vd0 = sdesc(base + L::kOffTile, kChunk, 1024);
+                const uint64_t pd = sdesc(base + L::kOffP, 16, 1024);
+#pragma unroll 1
+                for (int j = 0; j < tiles; ++j) {
+                    const int st = j & 1;
+                    const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
+                    ok = wait(&bars->p_full, j, kBarPV | (unsigned)(j & 0xffff));
                     if (!ok) break;
                     tc_fence_after();
-                    const int c0 = g == 0 ? 8 : 2 * (g - 1);      // first chunk of the piece
-                    mma4_if<2, 2>(leader, dS, qd + (uint64_t)(c0 * L::kQChunk >> 4), kd + (uint64_t)(c0 * kChunk >> 4),
-                                  kIdescS, g > 0 ? 1u : 0u);
-                    if (g > 0)
-                        mma4_if<2, 2>(leader, dS, qd + (uint64_t)((c0 + 1) * L::kQChunk >> 4),
-                                      kd + (uint64_t)((c0 + 1) * kChunk >> 4), kIdescS, 1u);
-                }
-                if (!ok) break;
-                mma_commit_if(leader, &bars->empty[st][0]);
-                mma_commit_if(leader, &bars->s_full[st]);
-            }
-        } else {
-            const uint64_t vd0 = sdesc(base + L::kOffTile, kChunk, 1024);
-            const uint64_t pd = sdesc(base + L::kOffP, 16, 1024);
-#pragma unroll 1
-            for (int j = 0; j < tiles; ++j) {
-                const int st = j & 1;
-                const uint64_t vd = vd0 + (uint64_t)(st * (kTile >> 4));
-                ok = wait(&bars->p_full, j, kBarPV | (unsigned)(j & 0xffff));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t add = j > 0 ? 1u : 0u;
+                    const uint32_t add = j > 0 ? 1u : 0u;
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    mma4_if<2048 / 16, 2>(leader, tm + L::kTmemO + (uint32_t)(m * NR),
-                                          vd + (uint64_t)(2 * m * kChunk >> 4), pd, L::kIdescPV, add);
-                    mma_commit_if(leader, &bars->empty[st][1 + m]);
+                    for (int m = 0; m < 4; ++m) {
+                        mma4_if<2048 / 16, 2>(leader, tm + L::kTmemO + (uint32_t)(m * NR),
+                                              vd + (uint64_t)(2 * m * kChunk >> 4), pd, L::kIdescPV, add);
+                        mma_commit_if(leader, &bars->empty[st][1 + m]);
+                    }
+                    mma_commit_if(leader, &bars->pv_done);
                 }
-                mma_commit_if(leader, &bars->pv_done);
             }
+            if (!ok) bars->abort = 1;
+            // nothing in flight when tensor memory is freed
+            mma_commit_if(leader, &bars->drain[warp - kQkWarp]);
+            mbar_wait(&bars->drain[warp - kQkWarp], 0, p.err, kRoleMma | kBarLast);
         }
-        if (!ok) bars->abort = 1;
-        // nothing in flight when tensor memory is freed
-        mma_commit_if(leader, &bars->drain[warp - kQkWarp]);
-        mbar_wait(&bars->drain[warp - kQkWarp], 0, p.err, kRoleMma | kBarLast);
     } else if constexpr (Q8) {
         // ------------------------------ conversion ----------------------------
+        // Thread: a quarter of a key.  Of a piece (128 values) it has two times 16: 16 bytes in, 32 out.
         const int ct = tid - 32 * kConvWarp, key = ct >> 2, q = ct & 3;
-        const uint8_t* rows = p.cache + (int64_t)b * p.cap * kLatentQ8Row;
-        uint4 v[8], r[2], sc;
-        auto load = [&](int t, int u) {           // pieces 4 u + q; u = 8: the rotated part; 9: the scales
-            const int64_t row = (int64_t)t * kKeys + key;
-            const uint4* src = reinterpret_cast<const uint4*>(rows + row * kLatentQ8Row);
-            const bool in = row < p.cap;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.cache + ((int64_t)b * p.cap + (int64_t)t_begin * kKeys + key) * kLatentQ8Row);
+        int64_t left = p.cap - (int64_t)t_begin * kKeys - key;    // rows of the cache from this one on
+        uint4 v[8], r[2];
+        float sc[4];
+        auto load = [&](int g) {                  // piece g - 1 of the values, or the rotated part and the scales
             const uint4 zero = make_uint4(0, 0, 0, 0);
-            if (u < 8) v[u] = in ? __ldg(src + 4 * u + q) : zero;
-            else if (u == 8) {
+            const bool in = left > 0;
+            if (g > 0) {
+                v[2 * g - 2] = in ? __ldg(src + 8 * (g - 1) + q) : zero;
+                v[2 * g - 1] = in ? __ldg(src + 8 * (g - 1) + 4 + q) : zero;
+            } else {
                 r[0] = in ? __ldg(src + 32 + q) : zero;
                 r[1] = in ? __ldg(src + 36 + q) : zero;
-            } else sc = in ? __ldg(src + 40) : zero;
+                const uint4 x = in ? __ldg(src + 40) : zero;
+                sc[0] = __uint_as_float(x.x); sc[1] = __uint_as_float(x.y);
+                sc[2] = __uint_as_float(x.z); sc[3] = __uint_as_float(x.w);
+            }
         };
 #pragma unroll
-        for (int u = 0; u < 10; ++u) load(t_begin, u);
+        for (int g = 0; g < kPieces; ++g) load(g);
+        // 16-byte units 2 q and 2 q + 1 of a chunk; units q and q + 4 of the rotated part
+        const uint32_t dst = smem_u32(smem) + L::kOffTile + (uint32_t)(key * 128);
+        const uint32_t unit0 = dst + (uint32_t)(((2 * q) ^ (key & 7)) << 4);
+        const uint32_t unit_r = dst + (uint32_t)(8 * kChunk + ((q ^ (key & 7)) << 4));
+        // 16 codes to bf16: code * 2^-120 by moving its bits, then * 2^120 scale (scales above 2^7, which
+        // would overflow there, in two steps)
+        auto convert = [&](uint4 c, float scale, uint32_t to) {
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            const float up = scale * 1.329227995784916e36f;        // 2^120
+            const bool big = isinf(up);
+            const uint32_t s2 = __byte_perm(__float_as_uint(big ? scale : up), 0, 0x3232);
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t x = __byte_perm(w[k >> 1], 0, k & 1 ? 0x3424 : 0x1404);
+                o[k] = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+            }
+            if (big) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], 0x7b807b80u);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], s2);
+            sts128(to, o[0], o[1], o[2], o[3]);
+            sts128(to ^ 16u, o[4], o[5], o[6], o[7]);
+        };
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            const int st = j & 1, next = t_begin + j + 1;
+            const int st = j & 1;
+            const uint32_t off = (uint32_t)(st * kTile);
             const bool more = j + 1 < n;
-            uint8_t* row = smem + L::kOffTile + st * kTile + key * 128;
-            const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
             bool ok = true;
+            src += kKeys * kLatentQ8Row / 16;     // (loads from here on are the next tile's)
+            left -= kKeys;
+            // Two halves: the rotated part and 256 values, then the others.  The last piece of a half
+            // is free only after its others (the products that read them are issued in order).
 #pragma unroll
-            for (int g = 0; g < kPieces; ++g) {
+            for (int half = 0; half < 2; ++half) {
                 if (j >= 2)
-                    ok = __all_sync(0xffffffffu, mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
-                                                                 kRoleConvert | kBarEmpty | (unsigned)(j & 0xffff)));
+                    ok = __all_sync(0xffffffffu, mbar_wait_sleep(&bars->empty[st][2 + 2 * half], (uint32_t)(((j >> 1) + 1) & 1),
+                                                                 p.err, kRoleConvert | kBarEmpty | (unsigned)(j & 0xffff)));
                 if (!ok) break;
-                if (g == 0) {
-                    uint8_t* d = row + 8 * kChunk;
-                    *reinterpret_cast<uint4*>(d + ((q ^ (key & 7)) << 4)) = r[0];
-                    *reinterpret_cast<uint4*>(d + (((q + 4) ^ (key & 7)) << 4)) = r[1];
-                    if (more) { load(next, 8); load(next, 9); }
-                } else {
-                    // 2^e twice: a power of two (or NaN) has its bits in the upper half of the float
-                    const uint32_t s2 = __byte_perm(scales[g - 1], 0, 0x3232);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int u = 2 * (g - 1) + h;
-                        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t x = __byte_perm(w[k >> 1], 0, k & 1 ? 0x3424 : 0x1404);
-                            const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-                            o[k] = mul_bf16x2(mul_bf16x2(y, 0x7b807b80u), s2);   // 2^120
-                        }
-                        if (more) load(next, u);
-                        uint8_t* d = row + u * kChunk;
-                        *reinterpret_cast<uint4*>(d + (((2 * q) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4*>(d + (((2 * q + 1) ^ (key & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
+                if (half == 0) {
+                    sts128(unit_r + off, r[0].x, r[0].y, r[0].z, r[0].w);
+                    sts128((unit_r + off) ^ 64u, r[1].x, r[1].y, r[1].z, r[1].w);
                 }
+                const float s0 = sc[2 * half], s1 = sc[2 * half + 1];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int g = 1 + 2 * half + u;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        convert(v[2 * g - 2 + k], u ? s1 : s0, unit0 + off + (uint32_t)((2 * g - 2 + k) * kChunk));
+                    if (more) load(g);
+                }
+                if (half == 1 && more) load(0);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->full[st][g]);
+                if (lane == 0) {
+                    if (half == 0) mbar_arrive(&bars->full[st][0]);
+                    mbar_arrive(&bars->full[st][1 + 2 * half]);
+                    mbar_arrive(&bars->full[st][2 + 2 * half]);
+                }
             }
             if (!ok) {
                 bars->abort = 1;
