@@ -21,10 +21,10 @@
 //   0-3    softmax: warp w has rows 16 w .. 16 w + 15 of S, and dimensions 32 w .. 32 w + 31 of
 //          each 128 of O^T.  The running maximum moves only when a score passes it by more than
 //          2^8 (the warps vote on a barrier); O^T is rescaled then
-//   4      copies tiles by TMA (bf16 rows); Q
+//   4      copies by TMA: Q; tiles of bf16 rows, the rotated part of 8-bit rows
 //   5, 6   issue QK and PV
 //   7-14   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
-//          quarter of a key, the next tile's in registers while it stores this one.  An e4m3 code
+//          quarter of a key, the next tile's on their way while it stores this one.  An e4m3 code
 //          is 2^-120 of a bf16 with the same bits further up, exactly, so two codes cost a
 //          shift, two masks and an exact multiplication, no conversion
 // P is rounded to bf16 (2^-9 of each probability, and it averages out); sums are fp32.
@@ -109,6 +109,19 @@ RAPID_DEVICE uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
+}
+// Bytes of x by the nibbles of SEL; with 8 added, eight times a byte's sign.
+template <uint32_t SEL>
+RAPID_DEVICE uint32_t signed_bytes(uint32_t x) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
+    return r;
+}
+// A value that the compiler does not know.
+RAPID_DEVICE uint32_t opaque(uint32_t x) {
+    uint32_t y;
+    asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 RAPID_DEVICE void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -225,7 +238,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     if (tid == 0) {
         for (int u = 0; u < 2; ++u) {
             for (int g = 0; g < kPieces; ++g) {
-                mbar_init(&bars->full[u][g], Q8 ? kConvWarps : 1);
+                mbar_init(&bars->full[u][g], Q8 && g > 0 ? kConvWarps : 1);
                 mbar_init(&bars->empty[u][g], 1);
             }
             mbar_init(&bars->s_full[u], 1);
@@ -511,38 +524,37 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 mbar_arrive_expect_tx(&bars->q_full, kChunks * L::kQChunk);
                 for (int ch = 0; ch < kChunks; ++ch)
                     tma_load_2d(smem + L::kOffQ + ch * L::kQChunk, &tmQ, 64 * ch, b * R + r0, &bars->q_full);
-                int issued = 0;                       // pieces
-                if constexpr (!Q8) {
-                    bool ok = true;
-                    for (int j = 0; j < n && ok; ++j) {
-                        const int st = j & 1;
-                        uint8_t* tile = smem + L::kOffTile + st * kTile;
-                        const int y = (t_begin + j) * kKeys;
-                        for (int g = 0; g < kPieces; ++g) {
-                            if ((j >= 2 && !mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
-                                                            kRoleProducer | kBarEmpty | (unsigned)(j & 0xffff))) ||
-                                *((volatile int*)&bars->abort)) {
-                                ok = false;
-                                break;
-                            }
-                            mbar_arrive_expect_tx(&bars->full[st][g], g == 0 ? kChunk : 2 * kChunk);
-                            if (g == 0) {
-                                tma_load_3d(tile + 8 * kChunk, &tmC, 512, y, b, &bars->full[st][0]);
-                            } else {
-                                const int ch = 2 * (g - 1);
-                                tma_load_3d(tile + ch * kChunk, &tmC, 64 * ch, y, b, &bars->full[st][g]);
-                                tma_load_3d(tile + (ch + 1) * kChunk, &tmC, 64 * ch + 64, y, b, &bars->full[st][g]);
-                            }
-                            ++issued;
+                constexpr int kCopied = Q8 ? 1 : kPieces;      // pieces of a tile: 8-bit rows, the rotated part
+                int issued = 0;
+                bool ok = true;
+                for (int j = 0; j < n && ok; ++j) {
+                    const int st = j & 1;
+                    uint8_t* tile = smem + L::kOffTile + st * kTile;
+                    const int y = (t_begin + j) * kKeys;
+                    for (int g = 0; g < kCopied; ++g) {
+                        if ((j >= 2 && !mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
+                                                        kRoleProducer | kBarEmpty | (unsigned)(j & 0xffff))) ||
+                            *((volatile int*)&bars->abort)) {
+                            ok = false;
+                            break;
                         }
+                        mbar_arrive_expect_tx(&bars->full[st][g], g == 0 ? kChunk : 2 * kChunk);
+                        if (g == 0) {
+                            tma_load_3d(tile + 8 * kChunk, &tmC, Q8 ? 0 : kLatent, y, b, &bars->full[st][0]);
+                        } else {
+                            const int ch = 2 * (g - 1);
+                            tma_load_3d(tile + ch * kChunk, &tmC, 64 * ch, y, b, &bars->full[st][g]);
+                            tma_load_3d(tile + (ch + 1) * kChunk, &tmC, 64 * ch + 64, y, b, &bars->full[st][g]);
+                        }
+                        ++issued;
                     }
-                    if (!ok) {
-                        bars->abort = 1;
-                        // let the copies in flight land before the CTA exits
-                        for (int x = max(0, issued - 2 * kPieces); x < issued; ++x)
-                            mbar_wait(&bars->full[(x / kPieces) & 1][x % kPieces], (uint32_t)((x / kPieces >> 1) & 1),
-                                      p.err, kRoleProducer | kBarFull);
-                    }
+                }
+                if (!ok) {
+                    bars->abort = 1;
+                    // let the copies in flight land before the CTA exits
+                    for (int x = max(0, issued - 2 * kCopied); x < issued; ++x)
+                        mbar_wait(&bars->full[(x / kCopied) & 1][x % kCopied], (uint32_t)((x / kCopied >> 1) & 1),
+                                  p.err, kRoleProducer | kBarFull);
                 }
                 mbar_wait_sleep(&bars->q_full, 0, p.err, kRoleProducer | kBarLast);
             }
@@ -611,89 +623,71 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
     } else if constexpr (Q8) {
         // ------------------------------ conversion ----------------------------
-        // Thread: a quarter of a key.  Of a piece (128 values) it has two times 16: 16 bytes in, 32 out.
+        // Thread: a quarter of a key, 16 codes at a time: 16 bytes in, 32 out.
         const int ct = tid - 32 * kConvWarp, key = ct >> 2, q = ct & 3;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.cache + ((int64_t)b * p.cap + (int64_t)t_begin * kKeys + key) * kLatentQ8Row);
         int64_t left = p.cap - (int64_t)t_begin * kKeys - key;    // rows of the cache from this one on
-        uint4 v[8], r[2];
-        float sc[4];
-        auto load = [&](int g) {                  // piece g - 1 of the values, or the rotated part and the scales
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            const bool in = left > 0;
-            if (g > 0) {
-                v[2 * g - 2] = in ? __ldg(src + 8 * (g - 1) + q) : zero;
-                v[2 * g - 1] = in ? __ldg(src + 8 * (g - 1) + 4 + q) : zero;
-            } else {
-                r[0] = in ? __ldg(src + 32 + q) : zero;
-                r[1] = in ? __ldg(src + 36 + q) : zero;
-                const uint4 x = in ? __ldg(src + 40) : zero;
-                sc[0] = __uint_as_float(x.x); sc[1] = __uint_as_float(x.y);
-                sc[2] = __uint_as_float(x.z); sc[3] = __uint_as_float(x.w);
-            }
-        };
+        uint4 v[8], sc;
+        auto load = [&](int u) { v[u] = left > 0 ? __ldg(src + 4 * u + q) : make_uint4(0, 0, 0, 0); };
+        auto load_scales = [&] { sc = left > 0 ? __ldg(src + kLatentQ8Scale / 16) : make_uint4(0, 0, 0, 0); };
 #pragma unroll
-        for (int g = 0; g < kPieces; ++g) load(g);
-        // 16-byte units 2 q and 2 q + 1 of a chunk; units q and q + 4 of the rotated part
-        const uint32_t dst = smem_u32(smem) + L::kOffTile + (uint32_t)(key * 128);
-        const uint32_t unit0 = dst + (uint32_t)(((2 * q) ^ (key & 7)) << 4);
-        const uint32_t unit_r = dst + (uint32_t)(8 * kChunk + ((q ^ (key & 7)) << 4));
-        // 16 codes to bf16: code * 2^-120 by moving its bits, then * 2^120 scale (scales above 2^7, which
-        // would overflow there, in two steps)
-        auto convert = [&](uint4 c, float scale, uint32_t to) {
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-            const float up = scale * 1.329227995784916e36f;        // 2^120
-            const bool big = isinf(up);
-            const uint32_t s2 = __byte_perm(__float_as_uint(big ? scale : up), 0, 0x3232);
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t x = __byte_perm(w[k >> 1], 0, k & 1 ? 0x3424 : 0x1404);
-                o[k] = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-            }
-            if (big) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], 0x7b807b80u);
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = mul_bf16x2(o[k], s2);
-            sts128(to, o[0], o[1], o[2], o[3]);
-            sts128(to ^ 16u, o[4], o[5], o[6], o[7]);
-        };
+        for (int u = 0; u < 8; ++u) load(u);
+        load_scales();
+        // 16-byte units 2 q and 2 q + 1 of a chunk
+        const uint32_t unit0 = smem_u32(smem) + L::kOffTile + (uint32_t)(key * 128 + (((2 * q) ^ (key & 7)) << 4));
+        const uint32_t sixteen = opaque(16u);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
-            const uint32_t off = (uint32_t)(st * kTile);
             const bool more = j + 1 < n;
-            bool ok = true;
             src += kKeys * kLatentQ8Row / 16;     // (loads from here on are the next tile's)
             left -= kKeys;
-            // Two halves: the rotated part and 256 values, then the others.  The last piece of a half
-            // is free only after its others (the products that read them are issued in order).
+            // * 2^120 scale; scales above 2^7, which would overflow there, in two steps
+            float up[4] = {__uint_as_float(sc.x), __uint_as_float(sc.y), __uint_as_float(sc.z), __uint_as_float(sc.w)};
+            const bool big = up[0] > 128.f || up[1] > 128.f || up[2] > 128.f || up[3] > 128.f;
+            if (!big)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) up[u] *= 1.329227995784916e36f;
+            if (more) load_scales();
+            bool ok = true;
+            // Two halves of 256 values, each converted while the room is still in use.  The last piece of a
+            // half is free only after its others (the products that read them are issued in order).
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                uint32_t o[4][8];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int u = 4 * half + x;
+                    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+                    if (more) load(u);
+                    const uint32_t s2 = __byte_perm(__float_as_uint(up[u >> 1]), 0, 0x3232);
+                    // Two codes: each with its sign in the byte above it, 4 bits up (a multiplication: the
+                    // integer pipe is the busiest), sign and magnitude kept; that is code * 2^-120.
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        o[x][k] = ((k & 1 ? signed_bytes<0xb3a2>(w[k >> 1]) : signed_bytes<0x9180>(w[k >> 1])) * sixteen) &
+                                  0x87f087f0u;
+                    if (big) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[x][k] = mul_bf16x2(o[x][k], 0x7b807b80u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[x][k] = mul_bf16x2(o[x][k], s2);
+                }
                 if (j >= 2)
                     ok = __all_sync(0xffffffffu, mbar_wait_sleep(&bars->empty[st][2 + 2 * half], (uint32_t)(((j >> 1) + 1) & 1),
                                                                  p.err, kRoleConvert | kBarEmpty | (unsigned)(j & 0xffff)));
                 if (!ok) break;
-                if (half == 0) {
-                    sts128(unit_r + off, r[0].x, r[0].y, r[0].z, r[0].w);
-                    sts128((unit_r + off) ^ 64u, r[1].x, r[1].y, r[1].z, r[1].w);
-                }
-                const float s0 = sc[2 * half], s1 = sc[2 * half + 1];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int g = 1 + 2 * half + u;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        convert(v[2 * g - 2 + k], u ? s1 : s0, unit0 + off + (uint32_t)((2 * g - 2 + k) * kChunk));
-                    if (more) load(g);
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t to = unit0 + (uint32_t)(st * kTile + (4 * half + x) * kChunk);
+                    sts128(to, o[x][0], o[x][1], o[x][2], o[x][3]);
+                    sts128(to ^ 16u, o[x][4], o[x][5], o[x][6], o[x][7]);
                 }
-                if (half == 1 && more) load(0);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (half == 0) mbar_arrive(&bars->full[st][0]);
                     mbar_arrive(&bars->full[st][1 + 2 * half]);
                     mbar_arrive(&bars->full[st][2 + 2 * half]);
                 }
@@ -821,13 +815,15 @@ cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t st) {
     const cuuint64_t q_dims[2] = {kLatentRow, (cuuint64_t)(p.B * R)};
     const cuuint64_t q_strides[1] = {2 * kLatentRow};
     if (!make_map(&tmQ, p.Q, 2, q_dims, q_strides, (uint32_t)nr)) return cudaErrorInvalidValue;
+    // bf16 rows, or the rotated part of 8-bit rows
+    const cuuint64_t row = p.q8 ? kLatentQ8Row : 2 * kLatentRow;
+    const cuuint64_t c_dims[3] = {(cuuint64_t)(p.q8 ? kLatentRope : kLatentRow), (cuuint64_t)p.cap, (cuuint64_t)p.B};
+    const cuuint64_t c_strides[2] = {row, (cuuint64_t)p.cap * row};
+    if (!make_map(&tmC, p.cache + (p.q8 ? kLatentQ8Rope : 0), 3, c_dims, c_strides, kKeys)) return cudaErrorInvalidValue;
     if (p.q8) {
-        if (nr == 16) return launch_rows<16, true>(tmQ, tmQ, p, st);
-        return nr == 32 ? launch_rows<32, true>(tmQ, tmQ, p, st) : launch_rows<64, true>(tmQ, tmQ, p, st);
+        if (nr == 16) return launch_rows<16, true>(tmQ, tmC, p, st);
+        return nr == 32 ? launch_rows<32, true>(tmQ, tmC, p, st) : launch_rows<64, true>(tmQ, tmC, p, st);
     }
-    const cuuint64_t c_dims[3] = {kLatentRow, (cuuint64_t)p.cap, (cuuint64_t)p.B};
-    const cuuint64_t c_strides[2] = {2 * kLatentRow, (cuuint64_t)p.cap * 2 * kLatentRow};
-    if (!make_map(&tmC, p.cache, 3, c_dims, c_strides, kKeys)) return cudaErrorInvalidValue;
     if (nr == 16) return launch_rows<16, false>(tmQ, tmC, p, st);
     return nr == 32 ? launch_rows<32, false>(tmQ, tmC, p, st) : launch_rows<64, false>(tmQ, tmC, p, st);
 }
