@@ -20,7 +20,7 @@
 // beside the products of the same tile.  Warps:
 //   0-3    softmax: warp w has rows 16 w .. 16 w + 15 of S, and dimensions 32 w .. 32 w + 31 of
 //          each 128 of O^T.  The running maximum moves only when a score passes it by more than
-//          2^8 (the warps vote on a barrier); O^T is rescaled then
+//          2^16 (the warps vote on a barrier); O^T is rescaled then
 //   4      copies by TMA: Q; tiles of bf16 rows, the rotated part of 8-bit rows
 //   5, 6   issue QK and PV
 //   7-14   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
@@ -53,6 +53,9 @@ constexpr int kTile = kChunks * kChunk;
 constexpr int kPieces = 5;                       // of a tile: rotated part, then 2 chunks at a time
 constexpr int kProducerWarp = 4, kQkWarp = 5, kPvWarp = 6, kConvWarp = 7, kConvWarps = 8;
 constexpr int kBarBytes = 1536;
+// A row's reference (what its exponents are relative to) follows its maximum only when a score passes
+// it by more than 2^kRise: P and the sums have fp32's exponents, and relative precision.
+constexpr float kRise = 16.f;
 
 template <int NR, bool Q8>
 struct Plan {
@@ -91,7 +94,7 @@ struct Bars {
     int abort;
     Slot slot;
     uint32_t flagged[2];     // keys of a masked tile with a value that is not finite
-    float factor[2][64];     // rescale factors of the rows, by tile parity
+    float factor[64];        // rescale factors of the rows, later 1 / sum
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block too small");
 
@@ -316,7 +319,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 dead = !__all_sync(0xffffffffu, mbar_wait_sleep(&bars->s_full[buf], (uint32_t)((j >> 1) & 1), p.err,
                                                           kRoleSoftmax | kBarS | (unsigned)(j & 0xffff)));
             uint32_t sr[32];
-            bool moved = false;
+            float top[2];
             const int64_t base = (int64_t)(t_begin + j) * kKeys;
             const bool masked = base + kKeys > P;
             if (!dead) {
@@ -379,7 +382,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     }
                 }
             }
-            float fac[2] = {1.f, 1.f};
+            // Most tiles leave every reference alone: no lane's scores pass it by more than kRise.
+            bool rises = false;
             if (!dead && rows_here) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -387,20 +391,26 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
                         mx = fmaxf(mx, fmaxf(__uint_as_float(sr[4 * x + 2 * k]), __uint_as_float(sr[4 * x + 2 * k + 1])));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    mx *= c;
-                    if (live[k] && mx > m_run[k] + 8.f) {     // the first finite score too
-                        fac[k] = ex2(m_run[k] - mx);          // 0 where m_run is -inf
-                        m_run[k] = mx;
-                        l_run[k] *= fac[k];
-                        moved = j > 0;
-                    }
-                    if (q4 == 0) bars->factor[buf][ra + 8 * k] = fac[k];
+                    top[k] = mx * c;
+                    rises |= live[k] && top[k] > m_run[k] + kRise;     // the first finite score too
                 }
             }
             // (also keeps the warps within a tile of each other)
-            if (softmax_any(moved || dead)) {
+            if (softmax_any(rises || dead)) {
+                if (!dead && rows_here) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float mx = top[k], fac = 1.f;
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        if (live[k] && mx > m_run[k] + kRise) {
+                            fac = ex2(m_run[k] - mx);         // 0 where m_run is -inf
+                            m_run[k] = mx;
+                            l_run[k] *= fac;
+                        }
+                        if (q4 == 0) bars->factor[ra + 8 * k] = fac;
+                    }
+                }
                 if (softmax_any(dead)) { dead = true; break; }
                 // O^T is rescaled: after the product that last added to it
                 if (j > 0) {
@@ -413,7 +423,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             uint32_t o[16];
                             tmem_ld16(lane_addr + L::kTmemO + (uint32_t)(16 * x), o);
                             tmem_wait_ld();
-                            const float* f = bars->factor[buf] + (16 * x) % NR;
+                            const float* f = bars->factor + (16 * x) % NR;
 #pragma unroll
                             for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * f[u]);
                             tmem_st16(lane_addr + L::kTmemO + (uint32_t)(16 * x), o);
@@ -421,7 +431,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         tmem_wait_st();
                     }
                 }
+                // the factors are written again no sooner than this
+                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
+            // (looked at before the exponentials, waited for behind them)
+            const bool free = j == 0 || mbar_try_wait(&bars->pv_done, (uint32_t)((j - 1) & 1));
             uint32_t pk[16];
             if (!dead && rows_here) {
 #pragma unroll
@@ -440,7 +454,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     l_run[k] += sum.x + sum.y;
                 }
             }
-            if (!dead && j > 0)                   // the P tile has been read
+            if (!dead && !__all_sync(0xffffffffu, free))     // the P tile has been read
                 dead = !__all_sync(0xffffffffu, mbar_wait_sleep(&bars->pv_done, (uint32_t)((j - 1) & 1), p.err,
                                                           kRoleSoftmax | kBarPV | (unsigned)(j & 0xffff)));
             if (!dead) {
@@ -480,7 +494,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     const int r = ra + 8 * k;
                     if (!live[k]) continue;
                     if (whole) {
-                        bars->factor[0][r] = l_run[k] == 0.f ? 0.f : 1.f / l_run[k];
+                        bars->factor[r] = l_run[k] == 0.f ? 0.f : 1.f / l_run[k];
                         p.LSE[(int64_t)b * R + r0 + r] =
                             l_run[k] == 0.f ? -INFINITY : (m_run[k] + log2f(l_run[k])) * kLn2;
                     } else {
@@ -507,7 +521,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     for (int u = 0; u < 16; ++u)
                         if (col + u < Rb)
                             dst[(int64_t)u * kLatent] = __float2bfloat16_rn(__uint_as_float(o[u]) *
-                                                                            bars->factor[0][col + u]);
+                                                                            bars->factor[col + u]);
                 } else {
                     float* dst = p.part_acc + ((int64_t)slot_idx * R + r0 + col) * kLatent + dim;
 #pragma unroll

@@ -11,7 +11,7 @@
 // Keys and values pass through a ring of eight 16 KB chunks (128 keys x 64 values: k 0, k 1, r, v 0,
 // v 1 of each tile of keys), so the next keys come while this tile's values wait.  Warps:
 //   0-3, 4-7  softmax of the two tiles: a thread has a token's 128 scores.  The running maximum
-//             moves only when a score passes it by more than 2^8, and O is rescaled then
+//             moves only when a score passes it by more than 2^16, and O is rescaled then
 //   8         copies by TMA
 //   9, 10     issue the products of the two tiles
 // Few blocks of tokens, or blocks behind long prefixes (latent_prefill_slots), share their keys out: a split
@@ -337,7 +337,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
             float fac = 1.f;
             bool moved = false;
-            if (top > m_run + 8.f) {              // the first finite score too
+            if (top > m_run + 16.f) {              // the first finite score too
                 fac = ex2(m_run - top);           // 0 where m_run is -inf
                 m_run = top;
                 l_run *= fac;
