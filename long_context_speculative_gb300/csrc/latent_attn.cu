@@ -721,11 +721,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
 }
 
-// Joins the splits of a row by log-sum-exp: one block for 128 dimensions of a row, its warps
-// take splits in turn.
-__global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParams p) {
-    __shared__ float4 s_acc[4][32];
-    __shared__ float s_l[4];
+// Joins the splits of a row by log-sum-exp: one block for 128 dimensions of a row.  Its threads work
+// out the splits' weights together, then its warps add up splits in turn, 8 loads in flight each.
+// Many splits (few rows) get 16 warps: 152 splits of 16 rows take 4 us, 14 with 4 warps.
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) latent_merge_kernel(const LatentAttnParams p) {
+    extern __shared__ float weight[];             // [p.S]
+    __shared__ float4 s_acc[WARPS][32];
+    __shared__ float s_red[WARPS];
     griddep_wait();
     const int R = p.H * p.n_q;
     const int64_t row = blockIdx.x;
@@ -734,36 +737,49 @@ __global__ void __launch_bounds__(128) latent_merge_kernel(const LatentAttnParam
     if (count <= 1) return;                       // written by its only split
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t first = (int64_t)p.part_first[b] * R + r;
-    const float* ml = p.part_ml + first * 2;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + first;
+    auto block = [&](float x, bool sum) -> float {
+        x = sum ? warp_sum(x) : warp_max(x);
+        __syncthreads();
+        if (lane == 0) s_red[warp] = x;
+        __syncthreads();
+        x = s_red[0];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) x = sum ? x + s_red[w] : fmaxf(x, s_red[w]);
+        return x;
+    };
     float M = -INFINITY;
-    for (int s = lane; s < count; s += 32) M = fmaxf(M, ml[(int64_t)s * R * 2]);
-    M = warp_max(M);
+    for (int s = threadIdx.x; s < count; s += 32 * WARPS) M = fmaxf(M, ml[(int64_t)s * R].x);
+    M = block(M, false);
     const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    for (int s = threadIdx.x; s < count; s += 32 * WARPS) {
+        const float2 x = ml[(int64_t)s * R];
+        const float f = ex2(x.x - ref);
+        weight[s] = f;
+        l = fmaf(f, x.y, l);
+    }
+    l = block(l, true);
     const float* acc = p.part_acc + first * kLatent + 128 * blockIdx.y + 4 * lane;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int s = warp; s < count; s += 4) {
-        const float f = ex2(ml[(int64_t)s * R * 2] - ref);
+#pragma unroll 8
+    for (int s = warp; s < count; s += WARPS) {
+        const float f = weight[s];
         const float4 x = __ldcs(reinterpret_cast<const float4*>(acc + (int64_t)s * R * kLatent));
-        l = fmaf(f, ml[(int64_t)s * R * 2 + 1], l);
         a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y);
         a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
     }
     s_acc[warp][lane] = a;
-    if (lane == 0) s_l[warp] = l;
     __syncthreads();
     if (warp > 0) return;
-    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    float o[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const float* x = reinterpret_cast<const float*>(s_acc) + 4 * lane + u;
-        o[u] = ((x[0] + x[128]) + (x[256] + x[384])) * inv;
+    for (int w = 1; w < WARPS; ++w) {
+        const float4 x = s_acc[w][lane];
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.O) + row * kLatent + 128 * blockIdx.y) + lane;
-    *dst = make_uint2(bf16x2(o[0], o[1]), bf16x2(o[2], o[3]));
+    *dst = make_uint2(bf16x2(a.x * inv, a.y * inv), bf16x2(a.z * inv, a.w * inv));
     if (lane == 0 && blockIdx.y == 0) p.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
@@ -797,9 +813,13 @@ cudaError_t launch_rows(const CUtensorMap& tmQ, const CUtensorMap& tmC, const La
     e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmC, p);
     if (e != cudaSuccess || p.S == p.B) return e;
     cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.H * p.n_q), kLatent / 128, 1);
+    cfg.dynamicSmemBytes = (size_t)p.S * sizeof(float);
+    if (p.S > 32) {
+        cfg.blockDim = dim3(512, 1, 1);
+        return cudaLaunchKernelEx(&cfg, latent_merge_kernel<16>, p);
+    }
     cfg.blockDim = dim3(128, 1, 1);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, latent_merge_kernel, p);
+    return cudaLaunchKernelEx(&cfg, latent_merge_kernel<4>, p);
 }
 
 }  // namespace
