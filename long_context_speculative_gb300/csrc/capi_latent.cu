@@ -66,7 +66,8 @@ PrefillPlan plan_prefill(int B, int n, int H, int64_t kv_rows) {
 bool attn_args_ok(int B, int H, int n_q, int64_t cap, int cache_dtype) {
     if (B < 1 || B > 65535 || H < 1 || H > RAPID_LATENT_MAX_HEADS || !cache_ok(cache_dtype)) return false;
     if (n_q < 1 || n_q > RAPID_MAX_NQ || !capacity_ok(cap) || cap < n_q) return false;
-    return (int64_t)B * H * n_q <= RAPID_LATENT_MAX_QUERIES;
+    // tiles of 64 rows of all sequences are counted in 32 bits
+    return (int64_t)B * H * n_q <= RAPID_LATENT_MAX_QUERIES && B * ((cap + 127) / 64) < ((int64_t)1 << 31);
 }
 
 }  // namespace

@@ -84,7 +84,9 @@ enum : unsigned int {
 };
 
 struct Slot {
-    int b, s, S_b, tiles;    // sequence (-1: no work), split, its splits, its tiles
+    int b, s, S_b;           // sequence (-1: no work), split, splits of the sequence
+    int t_begin, n;          // tiles of the split
+    int P;                   // history of the sequence, clamped
 };
 
 struct Bars {
@@ -136,6 +138,13 @@ RAPID_DEVICE void tma_load_3d(void* dst, const CUtensorMap* tm, int x, int y, in
         "l"(tm), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+RAPID_DEVICE void tma_load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
 // 16 lanes x 64 columns -> 32 registers: 4 c .. 4 c + 3 of lane l are columns 8 c + 2 (l % 4), + 1
 // of row l / 4, then of row l / 4 + 8.
 RAPID_DEVICE void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
@@ -164,70 +173,79 @@ RAPID_DEVICE bool softmax_any(bool x) {
     return r != 0;
 }
 
-RAPID_DEVICE int64_t clamped_len(const LatentAttnParams& p, int b) {
-    const int64_t P = p.prefix_len[b], most = p.cap - p.n_q;
-    return P < 0 ? 0 : P > most ? most : P;
-}
-RAPID_DEVICE int seq_tiles(const LatentAttnParams& p, int b) {
-    return (int)((clamped_len(p, b) + p.n_q + kKeys - 1) / kKeys);
+RAPID_DEVICE int clamped_len(const LatentAttnParams& p, int len) {
+    return max(0, min(len, (int)p.cap - p.n_q));
 }
 
 // Which sequence and split a slot holds, worked out by one warp from the lengths: the least
-// number of tiles a split for which all splits fit into the p.S >= B slots.
+// number of tiles a split for which all splits fit into the p.S >= B slots.  (Tiles of all sequences are
+// counted in 32 bits: B * cap / 64 stays below 2^31.)
 RAPID_DEVICE Slot find_slot(const LatentAttnParams& p, int c, int lane) {
-    int64_t total = 0;
-    int longest = 1;
+    // the first 32 sequences' tiles are kept in a register
+    const int len0 = lane < p.B ? p.prefix_len[lane] : 0;
+    const int mine = lane < p.B ? (clamped_len(p, len0) + p.n_q + kKeys - 1) / kKeys : 0;
+    auto tiles_of = [&](int b) {
+        return b < 32 ? mine : (clamped_len(p, p.prefix_len[b]) + p.n_q + kKeys - 1) / kKeys;
+    };
+    int total = 0, longest = 1;
     for (int b = lane; b < p.B; b += 32) {
-        const int t = seq_tiles(p, b);
+        const int t = tiles_of(b);
         total += t;
         longest = max(longest, t);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-    }
-    int lo = (int)((total + p.S - 1) / p.S), hi = max(lo, longest);
+    total = __reduce_add_sync(0xffffffffu, total);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    int lo = (total + p.S - 1) / p.S, hi = max(lo, longest);
     if (p.S == p.B) lo = hi;                      // one split each
     if (p.B == 1) hi = lo;
     while (lo < hi) {
         const int mid = lo + (hi - lo) / 2;
         int used = 0;
-        for (int b = lane; b < p.B; b += 32) used += (seq_tiles(p, b) + mid - 1) / mid;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) used += __shfl_xor_sync(0xffffffffu, used, o);
-        if (used <= p.S) hi = mid; else lo = mid + 1;
+        for (int b = lane; b < p.B; b += 32) used += (tiles_of(b) + mid - 1) / mid;
+        if (__reduce_add_sync(0xffffffffu, used) <= p.S) hi = mid; else lo = mid + 1;
     }
     int first = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         const int b = b0 + lane;
-        const int tiles = b < p.B ? seq_tiles(p, b) : 0;
+        const int tiles = b < p.B ? tiles_of(b) : 0;
         const int S_b = (tiles + lo - 1) / lo;
         int upto = S_b;                           // inclusive scan
+        if (p.B > 1) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
         }
-        const uint32_t here = __ballot_sync(0xffffffffu, c < first + upto);
+        const uint32_t here = __ballot_sync(0xffffffffu, b < p.B && c < first + upto);
         if (here) {
             const int l = __ffs(here) - 1;
-            Slot r;
-            r.b = b0 + l;
-            r.S_b = __shfl_sync(0xffffffffu, S_b, l);
-            r.s = c - first - (__shfl_sync(0xffffffffu, upto, l) - r.S_b);
-            r.tiles = __shfl_sync(0xffffffffu, tiles, l);
+            Slot r;                               // (lane l's are the ones that count)
+            r.b = b;
+            r.S_b = S_b;
+            r.s = c - first - (upto - S_b);
+            r.t_begin = (int)((int64_t)r.s * tiles / max(S_b, 1));
+            r.n = (int)((int64_t)(r.s + 1) * tiles / max(S_b, 1)) - r.t_begin;
+            const int len = b < 32 ? len0 : p.prefix_len[b < p.B ? b : 0];
+            r.P = clamped_len(p, len);
+            if (lane == l && r.s == 0 && p.err && len != r.P) atomicOr(p.err, kErrBadInput);
+            r.b = __shfl_sync(0xffffffffu, r.b, l);
+            r.S_b = __shfl_sync(0xffffffffu, r.S_b, l);
+            r.s = __shfl_sync(0xffffffffu, r.s, l);
+            r.t_begin = __shfl_sync(0xffffffffu, r.t_begin, l);
+            r.n = __shfl_sync(0xffffffffu, r.n, l);
+            r.P = __shfl_sync(0xffffffffu, r.P, l);
             return r;
         }
         first += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return Slot{-1, 0, 0, 0};
+    return Slot{-1, 0, 1, 0, 0, 0};
 }
 
 template <int NR, bool Q8>
 __global__ void __launch_bounds__(Plan<NR, Q8>::kThreads, 1)
 latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
-                   const LatentAttnParams p) {
+                   const __grid_constant__ CUtensorMap tmR, const LatentAttnParams p) {
     using L = Plan<NR, Q8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -270,8 +288,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (sl.b >= 0 && sl.s == 0 && rb == 0) {
                 p.part_first[sl.b] = slot_idx;
                 p.part_count[sl.b] = sl.S_b;
-                const int64_t P = p.prefix_len[sl.b];
-                if (p.err && (P < 0 || P > p.cap - p.n_q)) atomicOr(p.err, kErrBadInput);
             }
         }
     }
@@ -279,12 +295,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const Slot sl = bars->slot;
-    const int b = sl.b < 0 ? 0 : sl.b;
-    const int t_begin = sl.b < 0 ? 0 : (int)((int64_t)sl.s * sl.tiles / sl.S_b);
-    const int t_end = sl.b < 0 ? 0 : (int)((int64_t)(sl.s + 1) * sl.tiles / sl.S_b);
-    const int n = t_end - t_begin;                // >= 1 with work: S_b <= tiles
+    const int b = sl.b, t_begin = sl.t_begin, n = sl.n;
+    const int64_t P = sl.P;
     const uint32_t tmem = bars->tmem_base;
-    const int64_t P = clamped_len(p, b);
 
     if (n <= 0) {
         // a slot that no split needs
@@ -294,7 +307,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int ra = 16 * warp + (lane >> 2), q4 = lane & 3;
         const bool live[2] = {rows_here && ra < Rb, rows_here && ra + 8 < Rb};
         uint64_t spec[2] = {0, 0};                // the step's rows that each row sees
-        if ((int64_t)t_end * kKeys > P) {
+        if ((int64_t)(t_begin + n) * kKeys > P) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int i = (r0 + ra + 8 * k) % p.n_q;
@@ -507,12 +520,15 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             if (whole) asm volatile("bar.sync 1, 128;" ::: "memory");
             // lane = dimension, register = row
 #pragma unroll 1
-            for (int x = 0; x < NR / 4; ++x) {
-                const int blk = 16 * x / NR, col = 16 * x % NR;
-                if (col >= Rb) continue;
-                uint32_t o[16];
-                tmem_ld16(lane_addr + L::kTmemO + (uint32_t)(16 * x), o);
+            for (int x0 = 0; x0 < NR / 4; x0 += 2) {
+                uint32_t both[2][16];
+                tmem_ld16(lane_addr + L::kTmemO + (uint32_t)(16 * x0), both[0]);
+                tmem_ld16(lane_addr + L::kTmemO + (uint32_t)(16 * x0 + 16), both[1]);
                 tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const uint32_t (&o)[16] = both[y];
+                const int x = x0 + y, blk = 16 * x / NR, col = 16 * x % NR;
                 const int dim = 128 * blk + tid;
                 if (whole) {
                     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.O) +
@@ -528,6 +544,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     for (int u = 0; u < 16; ++u)
                         if (col + u < Rb) dst[(int64_t)u * kLatent] = __uint_as_float(o[u]);
                 }
+              }
             }
         }
         if (dead) bars->abort = 1;
@@ -536,8 +553,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // ------------------------------ copies --------------------------------
             if (lane == 0) {
                 mbar_arrive_expect_tx(&bars->q_full, kChunks * L::kQChunk);
-                for (int ch = 0; ch < kChunks; ++ch)
-                    tma_load_2d(smem + L::kOffQ + ch * L::kQChunk, &tmQ, 64 * ch, b * R + r0, &bars->q_full);
+                tma_load_3d(smem + L::kOffQ, &tmQ, 0, b * R + r0, 0, &bars->q_full);
                 constexpr int kCopied = Q8 ? 1 : kPieces;      // pieces of a tile: 8-bit rows, the rotated part
                 int issued = 0;
                 bool ok = true;
@@ -553,13 +569,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                             break;
                         }
                         mbar_arrive_expect_tx(&bars->full[st][g], g == 0 ? kChunk : 2 * kChunk);
-                        if (g == 0) {
-                            tma_load_3d(tile + 8 * kChunk, &tmC, Q8 ? 0 : kLatent, y, b, &bars->full[st][0]);
-                        } else {
-                            const int ch = 2 * (g - 1);
-                            tma_load_3d(tile + ch * kChunk, &tmC, 64 * ch, y, b, &bars->full[st][g]);
-                            tma_load_3d(tile + (ch + 1) * kChunk, &tmC, 64 * ch + 64, y, b, &bars->full[st][g]);
-                        }
+                        if (Q8)
+                            tma_load_3d(tile + 8 * kChunk, &tmC, 0, y, b, &bars->full[st][0]);
+                        else
+                            tma_load_4d(tile + (g == 0 ? 8 : 2 * (g - 1)) * kChunk, g == 0 ? &tmR : &tmC, 0, y,
+                                        g == 0 ? 0 : 2 * (g - 1), b, &bars->full[st][g]);
                         ++issued;
                     }
                 }
@@ -783,20 +797,21 @@ __global__ void __launch_bounds__(32 * WARPS) latent_merge_kernel(const LatentAt
     if (lane == 0 && blockIdx.y == 0) p.LSE[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
+// Rows as chunks of 64 values: box_rows rows of box_chunks chunks, chunk by chunk.
 bool make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
-              const cuuint64_t* strides, uint32_t box_rows) {
+              const cuuint64_t* strides, uint32_t box_rows, uint32_t box_chunks) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    cuuint32_t box[3] = {64, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
+    cuuint32_t box[4] = {64, box_rows, box_chunks, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NR, bool Q8>
-cudaError_t launch_rows(const CUtensorMap& tmQ, const CUtensorMap& tmC, const LatentAttnParams& p,
-                        cudaStream_t st) {
+cudaError_t launch_rows(const CUtensorMap& tmQ, const CUtensorMap& tmC, const CUtensorMap& tmR,
+                        const LatentAttnParams& p, cudaStream_t st) {
     auto kern = latent_attn_kernel<NR, Q8>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<NR, Q8>::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -810,7 +825,7 @@ cudaError_t launch_rows(const CUtensorMap& tmQ, const CUtensorMap& tmC, const La
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmC, p);
+    e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmC, tmR, p);
     if (e != cudaSuccess || p.S == p.B) return e;
     cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.H * p.n_q), kLatent / 128, 1);
     cfg.dynamicSmemBytes = (size_t)p.S * sizeof(float);
@@ -843,23 +858,28 @@ int latent_attn_slots(int B, int R, int64_t cap) {
 }
 
 cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t st) {
-    CUtensorMap tmQ, tmC;
+    CUtensorMap tmQ, tmC, tmR;
     const int64_t R = (int64_t)p.H * p.n_q;
     const int nr = latent_attn_block_rows((int)R);
-    const cuuint64_t q_dims[2] = {kLatentRow, (cuuint64_t)(p.B * R)};
-    const cuuint64_t q_strides[1] = {2 * kLatentRow};
-    if (!make_map(&tmQ, p.Q, 2, q_dims, q_strides, (uint32_t)nr)) return cudaErrorInvalidValue;
-    // bf16 rows, or the rotated part of 8-bit rows
-    const cuuint64_t row = p.q8 ? kLatentQ8Row : 2 * kLatentRow;
-    const cuuint64_t c_dims[3] = {(cuuint64_t)(p.q8 ? kLatentRope : kLatentRow), (cuuint64_t)p.cap, (cuuint64_t)p.B};
-    const cuuint64_t c_strides[2] = {row, (cuuint64_t)p.cap * row};
-    if (!make_map(&tmC, p.cache + (p.q8 ? kLatentQ8Rope : 0), 3, c_dims, c_strides, kKeys)) return cudaErrorInvalidValue;
+    const cuuint64_t q_dims[3] = {64, (cuuint64_t)(p.B * R), kChunks};
+    const cuuint64_t q_strides[2] = {2 * kLatentRow, 128};
+    if (!make_map(&tmQ, p.Q, 3, q_dims, q_strides, (uint32_t)nr, kChunks)) return cudaErrorInvalidValue;
     if (p.q8) {
-        if (nr == 16) return launch_rows<16, true>(tmQ, tmC, p, st);
-        return nr == 32 ? launch_rows<32, true>(tmQ, tmC, p, st) : launch_rows<64, true>(tmQ, tmC, p, st);
+        // the rotated part of the rows
+        const cuuint64_t dims[3] = {64, (cuuint64_t)p.cap, (cuuint64_t)p.B};
+        const cuuint64_t strides[2] = {kLatentQ8Row, (cuuint64_t)p.cap * kLatentQ8Row};
+        if (!make_map(&tmC, p.cache + kLatentQ8Rope, 3, dims, strides, kKeys, 1)) return cudaErrorInvalidValue;
+        if (nr == 16) return launch_rows<16, true>(tmQ, tmC, tmC, p, st);
+        return nr == 32 ? launch_rows<32, true>(tmQ, tmC, tmC, p, st) : launch_rows<64, true>(tmQ, tmC, tmC, p, st);
     }
-    if (nr == 16) return launch_rows<16, false>(tmQ, tmC, p, st);
-    return nr == 32 ? launch_rows<32, false>(tmQ, tmC, p, st) : launch_rows<64, false>(tmQ, tmC, p, st);
+    const cuuint64_t dims[4] = {64, (cuuint64_t)p.cap, kChunks - 1, (cuuint64_t)p.B};
+    const cuuint64_t strides[3] = {2 * kLatentRow, 128, (cuuint64_t)p.cap * 2 * kLatentRow};
+    const cuuint64_t r_dims[4] = {64, (cuuint64_t)p.cap, 1, (cuuint64_t)p.B};
+    if (!make_map(&tmC, p.cache, 4, dims, strides, kKeys, 2) ||
+        !make_map(&tmR, p.cache + 2 * kLatent, 4, r_dims, strides, kKeys, 1))
+        return cudaErrorInvalidValue;
+    if (nr == 16) return launch_rows<16, false>(tmQ, tmC, tmR, p, st);
+    return nr == 32 ? launch_rows<32, false>(tmQ, tmC, tmR, p, st) : launch_rows<64, false>(tmQ, tmC, tmR, p, st);
 }
 
 }  // namespace rapid
