@@ -130,6 +130,7 @@ RAPID_DEVICE void append_row(const LatentAppendParams& p, int b, int i, int64_t 
 
 // Units of one warp: token * (slices + 1) + slice; slice `slices` is the token's cache row, the
 // others share its query heads, 8 heads (4 lanes each) a step.
+template <bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const LatentAppendParams p) {
     griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
         sn[u] = __shfl_sync(0xffffffffu, my_sn, 4 * u + c);
         cs[u] = __shfl_sync(0xffffffffu, my_cs, 4 * u + c);
     }
-    const int p0 = p.interleaved ? 2 * c : c, p1 = p.interleaved ? 2 * c + 1 : c + 4;
+    const int p0 = INTERLEAVED ? 2 * c : c, p1 = INTERLEAVED ? 2 * c + 1 : c + 4;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_batch + i * p.q_token;
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.q_out) + b * p.o_batch + i * p.o_token;
     const int steps = (p.H + 7) / 8;
@@ -181,12 +182,12 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
         unpack8(r1, x + 8);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int ia = p.interleaved ? 2 * u : u, ib = p.interleaved ? 2 * u + 1 : u + 8;
+            const int ia = INTERLEAVED ? 2 * u : u, ib = INTERLEAVED ? 2 * u + 1 : u + 8;
             y[u] = x[ia] * cs[u] - x[ib] * sn[u];
             y[u + 8] = x[ib] * cs[u] + x[ia] * sn[u];
         }
         if (h >= p.H) return;
-        if (p.interleaved) {
+        if (INTERLEAVED) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) { x[2 * u] = y[u]; x[2 * u + 1] = y[u + 8]; }
         } else {
@@ -323,7 +324,8 @@ cudaError_t launch_latent_append(LatentAppendParams p, cudaStream_t st) {
     p.slices = (int)slices;
     const int64_t blocks = (tokens * (p.slices + 1) + kAppendWarps - 1) / kAppendWarps;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch(latent_append_kernel, dim3((unsigned)blocks), kAppendThreads, p, st);
+    return p.interleaved ? launch(latent_append_kernel<true>, dim3((unsigned)blocks), kAppendThreads, p, st)
+                         : launch(latent_append_kernel<false>, dim3((unsigned)blocks), kAppendThreads, p, st);
 }
 
 cudaError_t launch_latent_read(const LatentReadParams& p, cudaStream_t st) {

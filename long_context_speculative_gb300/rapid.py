@@ -630,14 +630,23 @@ def _latent_cache(cache, dev, name="cache"):
 
 
 def _strided(t, dev, shape, name):
-    """Address and strides of a bf16 tensor whose last dimension is contiguous (a view of a wider
-    one will do); the stride of a dimension of size 1 means nothing and is given as 0."""
+    """Address of a bf16 tensor of this shape (its strides are _outer_strides')."""
     if t.shape != shape or t.dtype != torch.bfloat16 or t.get_device() != dev:
         _refuse(t, dev, torch.bfloat16, shape, name)
-    *outer, last = t.stride()
-    if last != 1:
-        raise RapidError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), [s if k > 1 else 0 for s, k in zip(outer, shape)]
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _outer_strides(*tensors):
+    """The element strides of the outer dimensions of tensors, each given as (shape, strides, name),
+    as a C array.  The last dimension must be contiguous (a view of a wider tensor will do); the
+    stride of a dimension of size 1 means nothing and is given as 0."""
+    out = []
+    for shape, strides, name in tensors:
+        if strides[-1] != 1 and shape[-1] > 1:
+            raise RapidError(f"{name}: the last dimension must be contiguous")
+        out += [s if k > 1 else 0 for s, k in zip(strides[:-1], shape)]
+    return (ctypes.c_int64 * len(out))(*out)
 
 
 def rapid_latent_append(kv, q, q_out, kv_weight, eps, inv_freq, flags, prefix_len, row_offset,
@@ -649,18 +658,19 @@ def rapid_latent_append(kv, q, q_out, kv_weight, eps, inv_freq, flags, prefix_le
     if kv.dim() != 3:
         raise RapidError("kv must be [B, n, 576]")
     n, i32 = kv.shape[1], torch.int32
-    kv_ptr, ks = _strided(kv, dev, (B, n, RAPID_LATENT_ROW), "kv")
+    kv_shape = (B, n, RAPID_LATENT_ROW)
+    kv_ptr = _strided(kv, dev, kv_shape, "kv")
     q_ptr = o_ptr = q_strides = None
     H = 0
     if q is not None or q_out is not None:
         if q is None or q_out is None or q.dim() != 4:
             raise RapidError("q and q_out are [B, n, H, 64], both or neither")
         H = q.shape[2]
-        q_ptr, qs = _strided(q, dev, (B, n, H, RAPID_LATENT_ROPE_DIM), "q")
-        o_ptr, os_ = _strided(q_out, dev, (B, n, H, RAPID_LATENT_ROPE_DIM), "q_out")
-        q_strides = (ctypes.c_int64 * 6)(*qs, *os_)
+        q_shape = (B, n, H, RAPID_LATENT_ROPE_DIM)
+        q_ptr, o_ptr = _strided(q, dev, q_shape, "q"), _strided(q_out, dev, q_shape, "q_out")
+        q_strides = _outer_strides((q_shape, q.stride(), "q"), (q_shape, q_out.stride(), "q_out"))
     st = lib().rapid_latent_append(
-        kv_ptr, (ctypes.c_int64 * 2)(*ks), q_ptr, q_strides, B, n, H,
+        kv_ptr, _outer_strides((kv_shape, kv.stride(), "kv")), q_ptr, q_strides, B, n, H,
         _arg(kv_weight, dev, torch.bfloat16, (RAPID_LATENT_DIM,), "kv_weight"), eps,
         _arg(inv_freq, dev, torch.float32, (RAPID_LATENT_ROPE_DIM // 2,), "inv_freq"), flags,
         _arg(prefix_len, dev, i32, (B,), "prefix_len"),
@@ -759,12 +769,13 @@ def rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale
         raise RapidError("Q is [B, n, H, 192], K and V [B, kv_rows, H, 128]")
     B, n, H, _ = Q.shape
     L, d = K.shape[1], RAPID_LATENT_HEAD_DIM
-    parts = [_strided(Q, dev, (B, n, H, d + RAPID_LATENT_ROPE_DIM), "Q"),
-             _strided(K, dev, (B, L, H, d), "K"), _strided(V, dev, (B, L, H, d), "V"),
-             _strided(K_rope, dev, (B, L, RAPID_LATENT_ROPE_DIM), "K_rope")]
-    i32 = torch.int32
+    q_shape, kv_shape = (B, n, H, d + RAPID_LATENT_ROPE_DIM), (B, L, H, d)
+    r_shape, i32 = (B, L, RAPID_LATENT_ROPE_DIM), torch.int32
     st = lib().rapid_latent_prefill_attn(
-        *[x[0] for x in parts], (ctypes.c_int64 * 11)(*[s for x in parts for s in x[1]]), B, n, H, L,
+        _strided(Q, dev, q_shape, "Q"), _strided(K, dev, kv_shape, "K"),
+        _strided(V, dev, kv_shape, "V"), _strided(K_rope, dev, r_shape, "K_rope"),
+        _outer_strides((q_shape, Q.stride(), "Q"), (kv_shape, K.stride(), "K"),
+                       (kv_shape, V.stride(), "V"), (r_shape, K_rope.stride(), "K_rope")), B, n, H, L,
         _arg(prefix_len, dev, i32, (B,), "prefix_len"), _arg(n_rows, dev, i32, (B,), "n_rows"),
         softmax_scale, _arg(O, dev, torch.bfloat16, (B, n, H, d), "O"),
         _arg(LSE, dev, torch.float32, (B, H, n), "LSE"),
@@ -953,25 +964,29 @@ def latent_append(kv, cache, prefix_len, inv_freq, q=None, q_out=None, kv_weight
     rotated and written to cache rows prefix_len + i, in 8 bits where the cache is uint8.
     With q [B, n, H, 64], the rotated part of the queries, returns q_out [B, n, H, 64] (any
     strided view, q itself too; made here if None)."""
-    with _on(stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        rapid_latent_append(kv, q, q_out, kv_weight, eps, inv_freq,
-                            RAPID_ROPE_INTERLEAVED if interleaved else 0, prefix_len, row_offset,
-                            n_rows, cache)
+    if stream is not None:
+        with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
+            return latent_append(kv, cache, prefix_len, inv_freq, q, q_out, kv_weight, eps,
+                                 interleaved, row_offset, n_rows)
+    if q is not None and q_out is None:
+        q_out = q.new_empty(q.shape)
+    rapid_latent_append(kv, q, q_out, kv_weight, eps, inv_freq,
+                        RAPID_ROPE_INTERLEAVED if interleaved else 0, prefix_len, row_offset,
+                        n_rows, cache)
     return q_out
 
 
 def latent_read(cache, first, n, n_rows=None, out=None, stream=None):
     """Rows [first[b], first[b] + n) of a latent cache (first None: 0) as bf16 [B, n, 576]; rows
     from n_rows[b] on are left as they are (unset in a new tensor)."""
-    with _on(stream):
-        if out is None:
-            out = torch.empty((cache.shape[0], n, RAPID_LATENT_ROW), dtype=torch.bfloat16,
-                              device=cache.device)
-        elif out.dim() != 3 or out.shape[1] != n:
-            raise RapidError(f"out must be [B, {n}, 576]")
-        rapid_latent_read(cache, first, n_rows, out)
+    if stream is not None:
+        with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
+            return latent_read(cache, first, n, n_rows, out)
+    if out is None:
+        out = cache.new_empty((cache.shape[0], n, RAPID_LATENT_ROW), dtype=torch.bfloat16)
+    elif out.dim() != 3 or out.shape[1] != n:
+        raise RapidError(f"out must be [B, {n}, 576]")
+    rapid_latent_read(cache, first, n_rows, out)
     return out
 
 
@@ -997,9 +1012,9 @@ def latent_attn(Q, cache, prefix_len, spec_mask=None, softmax_scale=0.0, out=Non
             return latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, out, lse, workspace)
     B, H, n_q, _ = Q.shape
     if out is None:
-        out = torch.empty((B, H, n_q, RAPID_LATENT_DIM), dtype=Q.dtype, device=Q.device)
+        out = Q.new_empty((B, H, n_q, RAPID_LATENT_DIM))
     if lse is None:
-        lse = torch.empty((B, H, n_q), dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty((B, H, n_q), dtype=torch.float32)
     if workspace is None:
         dev = _device_of(Q, "Q")
         workspace = _scratch(dev, _latent_attn_bytes(
@@ -1029,9 +1044,9 @@ def latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows=None, softmax_scale=
                                        workspace)
     B, n, H, _ = Q.shape
     if out is None:
-        out = torch.empty((B, n, H, RAPID_LATENT_HEAD_DIM), dtype=Q.dtype, device=Q.device)
+        out = Q.new_empty((B, n, H, RAPID_LATENT_HEAD_DIM))
     if lse is None:
-        lse = torch.empty((B, H, n), dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty((B, H, n), dtype=torch.float32)
     if workspace is None:
         dev = _device_of(Q, "Q")
         workspace = _scratch(dev, _latent_prefill_bytes(dev, B, n, H, K.shape[1]))
