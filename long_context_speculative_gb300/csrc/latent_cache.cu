@@ -83,10 +83,20 @@ RAPID_DEVICE void append_row(const LatentAppendParams& p, int b, int i, int64_t 
     unpack8(r0, x);
     unpack8(r1, x + 8);
     if (p.weight) {
+        // The squares are taken of c 2^-k, 2^k the size of the largest value or of sqrt(eps), so that
+        // they stay in fp32's range whatever the row's size.
+        float big = sqrtf(p.eps);
+#pragma unroll
+        for (int u = 0; u < 16; ++u) big = fmaxf(big, fabsf(x[u]));
+        const int k = min((int)(__reduce_max_sync(0xffffffffu, __float_as_uint(big)) >> 23), 253) - 127;
+        const float down = __uint_as_float((uint32_t)(127 - max(k, -126)) << 23);
         float ss = 0.f;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) ss = fmaf(x[u], x[u], ss);
-        const float inv = rsqrtf(warp_sum(ss) * (1.f / kLatent) + p.eps);
+        for (int u = 0; u < 16; ++u) {
+            x[u] *= down;
+            ss = fmaf(x[u], x[u], ss);
+        }
+        const float inv = rsqrtf(warp_sum(ss) * (1.f / kLatent) + p.eps * down * down);
         float w[16];
         unpack8(w0, w);
         unpack8(w1, w + 8);
