@@ -43,9 +43,9 @@ AttnPlan plan_attn(int B, int H, int n_q, int64_t cap) {
 }
 
 struct PrefillPlan {
-    int slots;
+    int ctas;
     size_t acc, ml, index;
-    size_t bytes() const { return acc + ml + 2 * index; }
+    size_t bytes() const { return acc + ml + index; }
 };
 
 bool prefill_args_ok(int B, int n, int H, int64_t kv_rows) {
@@ -56,10 +56,10 @@ bool prefill_args_ok(int B, int n, int H, int64_t kv_rows) {
 PrefillPlan plan_prefill(int B, int n, int H, int64_t kv_rows) {
     PrefillPlan pl;
     const size_t rows = latent_prefill_block_rows();
-    pl.slots = latent_prefill_slots(B, n, H, kv_rows);
-    pl.acc = align_up(pl.slots * rows * kLatentHead * sizeof(float));
-    pl.ml = align_up(pl.slots * rows * 2 * sizeof(float));
-    pl.index = pl.slots ? align_up(B * ((n + rows - 1) / rows) * sizeof(int)) : kAlign;
+    pl.ctas = latent_prefill_ctas(B, n, H, kv_rows);
+    pl.acc = align_up(2 * pl.ctas * rows * kLatentHead * sizeof(float));
+    pl.ml = align_up(2 * pl.ctas * rows * 2 * sizeof(float));
+    pl.index = pl.ctas ? align_up((B * ((n + rows - 1) / rows) + 1) * sizeof(int64_t)) : kAlign;
     return pl;
 }
 
@@ -225,9 +225,8 @@ rapid_status rapid_latent_prefill_attn(const void* Q, const void* K, const void*
     char* ws = static_cast<char*>(workspace);
     p.part_acc = reinterpret_cast<float*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + pl.acc);
-    p.part_first = reinterpret_cast<int*>(ws + pl.acc + pl.ml);
-    p.part_count = reinterpret_cast<int*>(ws + pl.acc + pl.ml + pl.index);
-    p.slots = pl.slots;
+    p.part_first = reinterpret_cast<int64_t*>(ws + pl.acc + pl.ml);
+    p.ctas = pl.ctas;
     p.Q = Q; p.K = K; p.V = V; p.K_rope = K_rope;
     p.prefix_len = prefix_len; p.n_rows = n_rows; p.O = O; p.LSE = LSE;
     p.err = device_error_word();

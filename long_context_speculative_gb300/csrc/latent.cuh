@@ -89,14 +89,13 @@ struct LatentPrefillParams {
     float* LSE;                  // [B, H, n]
     unsigned int* err;
     int64_t q_stride[3], k_stride[3], v_stride[3], r_stride[2];   // batch, token, head (elements)
-    // Splits of the keys (slots > 0): un-normalised O [slots, 256, 128] and (running maximum, sum)
-    // in the log2 domain by slot; where a block of tokens has them, [B, blocks]
+    // Parts of blocks of tokens (ctas > 0): un-normalised O [2 ctas, 32, 256, 4] and (running maximum, sum) in
+    // the log2 domain; where the key tiles of each block [B, blocks] start in the line, and its length
     float* part_acc;
     float* part_ml;
-    int* part_first;
-    int* part_count;
+    int64_t* part_first;
     int64_t kv_rows;
-    int B, H, n, slots;
+    int B, H, n, ctas;
     float scale_log2;
 };
 
@@ -106,7 +105,7 @@ cudaError_t launch_latent_commit(const LatentCommitParams& p, int layers, int B,
 int latent_attn_block_rows(int R);                    // rows of a block for R = H n_q rows
 int latent_attn_slots(int B, int R, int64_t cap);
 cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t st);
-int latent_prefill_slots(int B, int n, int H, int64_t kv_rows);
+int latent_prefill_ctas(int B, int n, int H, int64_t kv_rows);
 size_t latent_prefill_block_rows();                   // tokens of a block
 cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t st);
 
