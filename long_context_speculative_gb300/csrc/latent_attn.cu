@@ -110,6 +110,11 @@ RAPID_DEVICE uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+RAPID_DEVICE uint32_t times_zero(uint32_t x, uint32_t acc) {       // bf16 pairs: x * 0 + acc
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+    return r;
+}
 RAPID_DEVICE uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -346,36 +351,42 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 if (lane == 0) mbar_arrive(&bars->s_free[buf]);
             }
             if (masked) {
-                // the tile as values: two threads a key, 4 chunks each
+                // The tile as values: two threads a key, 4 chunks each, 16-byte units in an order without
+                // bank conflicts.  Only rows of the step can be hidden from some queries and seen by others.
                 uint8_t* tile = smem + L::kOffTile + buf * kTile;
-                const int key = tid >> 1;
+                const int key = tid >> 1, turn = key ^ ((tid & 1) << 2);
+                uint8_t* mine = tile + 4 * (tid & 1) * kChunk + key * 128;
                 const bool inside = base + key < P + p.n_q;
-                bool odd = false;
+                uint64_t flagged = 0;
                 if (!dead)                            // done long ago: what was copied is visible here
                     for (int g = 0; g < kPieces; ++g)
                         mbar_wait(&bars->full[buf][g], (uint32_t)((j >> 1) & 1), p.err, kRoleSoftmax | kBarFull);
-                if (inside && !dead) {
-#pragma unroll 4
-                    for (int x = 0; x < 32; ++x) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(
-                            tile + (4 * (tid & 1) + (x >> 3)) * kChunk + key * 128 + ((x & 7) << 4));
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if (p.mask || p.n_q > 1) {
+                    bool odd = false;
+                    if (inside && base + key >= P && !dead) {
+                        uint32_t acc[4] = {0, 0, 0, 0};       // value * 0 is NaN where it is not finite
+#pragma unroll 8
+                        for (int x = 0; x < 32; ++x) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(mine + (x >> 3) * kChunk + (((x ^ turn) & 7) << 4));
+                            acc[0] = times_zero(v.x, acc[0]); acc[1] = times_zero(v.y, acc[1]);
+                            acc[2] = times_zero(v.z, acc[2]); acc[3] = times_zero(v.w, acc[3]);
+                        }
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            odd |= (w[u] & 0x7f80u) == 0x7f80u || (w[u] & 0x7f800000u) == 0x7f800000u;
+                            odd |= (acc[u] & 0x7fffu) > 0x7f80u || (acc[u] & 0x7fff0000u) > 0x7f800000u;
                     }
+                    if (odd) atomicOr(&bars->flagged[key >> 5], 1u << (key & 31));
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    flagged = bars->flagged[0] | ((uint64_t)bars->flagged[1] << 32);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (tid < 2) bars->flagged[tid] = 0;      // (set again only after the vote below)
                 }
-                if (odd) atomicOr(&bars->flagged[key >> 5], 1u << (key & 31));
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                const uint64_t flagged = bars->flagged[0] | ((uint64_t)bars->flagged[1] << 32);
                 if (!dead && (!inside || ((flagged >> key) & 1))) {
+#pragma unroll 8
                     for (int x = 0; x < 32; ++x)
-                        *reinterpret_cast<uint4*>(tile + (4 * (tid & 1) + (x >> 3)) * kChunk + key * 128 +
-                                                  ((x & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4*>(mine + (x >> 3) * kChunk + (((x ^ turn) & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (tid < 2) bars->flagged[tid] = 0;      // (read again only after the vote below)
                 if (!dead && rows_here) {
                     const int64_t delta = P - base;       // < 64
 #pragma unroll
@@ -383,14 +394,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         uint64_t see = delta > 0 ? ((1ull << delta) - 1) | (spec[k] << delta)
                                                  : delta > -64 ? spec[k] >> -delta : 0;
                         if (!live[k]) see = 0;
+                        const uint64_t here = see >> (2 * q4), odd = (flagged & see) >> (2 * q4);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const int col = 8 * x + 2 * q4 + e;
                                 uint32_t& s = sr[4 * x + 2 * k + e];
-                                if (!((see >> col) & 1)) s = 0xff800000u;          // -inf
-                                else if ((flagged >> col) & 1) s = 0x7fffffffu;    // NaN
+                                if (!((here >> (8 * x + e)) & 1)) s = 0xff800000u;          // -inf
+                                if ((odd >> (8 * x + e)) & 1) s = 0x7fffffffu;              // NaN
                             }
                     }
                 }
