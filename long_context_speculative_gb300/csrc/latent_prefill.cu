@@ -205,8 +205,10 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
         run = bars->run;
         if (run.left == 0) return;
     } else {
-        // The blocks of a head are neighbours (their keys stay in L2), the longest first.
-        const int bh = blockIdx.x / blocks, b = bh / p.H, qb = blocks - 1 - (int)(blockIdx.x - bh * blocks);
+        // The last blocks of all heads first, which are the longest: short ones fill the end (8K, 32 heads:
+        // 412 us, 462 with the blocks of a head as neighbours).
+        const int heads = p.B * p.H, row = blockIdx.x / heads, bh = blockIdx.x - row * heads;
+        const int b = bh / p.H, qb = blocks - 1 - row;
         run = Run{b * blocks + qb, bh % p.H, 0, block_tiles(p, b, qb)};
         if (run.left == 0) {
             const int count = p.n_rows ? p.n_rows[b] : p.n;
