@@ -10,6 +10,11 @@
 //
 // All three kernels copy: no value is read twice.  A row is one warp's work: lane l holds values
 // 16 l .. 16 l + 15 of the latent vector (a scale group is 8 lanes) and pair l of the key.
+//
+// Measured: three ragged chunks of up to 4095 tokens with 32 heads, bf16 rows, 15.4 us for 97 MB (6.3 TB/s,
+// 0.93 of a plain copy; 28 us before the pairs' layout was a template parameter, when the lanes'
+// registers were indexed in memory); 11 tokens of 128 heads 2.3 us.  Reading a 120K history in 8 bits
+// back 37.5 us (222 MB, 5.9 TB/s, 0.87); committing 16 sequences' paths of 60 layers 6.0 us (0.92).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -18,7 +18,7 @@
 // With few blocks of tokens (latent_prefill_ctas) the blocks' key tiles form one line, in the order
 // (sequence, block, head, tile), and each of one wave of CTAs takes an equal run of it: parts of blocks
 // leave (O, maximum, sum) in the workspace, joined by log-sum-exp, whole ones are written at once.
-// P is rounded to bf16 (2^-9 of each probability, and it averages out); sums are fp32.
+// P is rounded to bf16 (at most 2^-8 of each probability, and it averages out); sums are fp32.
 //
 // Keys that a token does not see have no effect on it, whatever they hold: in tiles of keys that some
 // token of the CTA does not see whole, a warp zeroes the values of keys behind the chunk in shared memory,
@@ -27,6 +27,13 @@
 //
 // Every wait is bounded in wall-clock time; after a failed wait the kernel records an error code,
 // stops issuing, drains and returns.
+//
+// Measured (us; floor by operations at 1910 TFLOP/s): 8192 tokens of 32 heads 412 to 422 (360), 1.65
+// PFLOP/s; three ragged chunks of up to 999 tokens of 16 heads behind up to 12001 132 (61); 16 tokens of 16
+// heads behind 16000 39 (4.5).  A tile of keys takes 2850 clocks for both tiles of tokens, 2710 of them the
+// tensor unit's (68 for M = N = 128, 36 for M = 128, N = 64 with P in tensor memory).  The ragged chunks
+// lose 6000 clocks between two pieces of a CTA (Q, whose room is in use until the last scores, then
+// its first scores) and 10 us in the join.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

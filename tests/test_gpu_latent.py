@@ -276,7 +276,7 @@ def test_attn_chain(q8, B, H, n, prefix):
 
 
 @pytest.mark.parametrize("q8", [False, True])
-@pytest.mark.parametrize("B", [33, 77, 200])
+@pytest.mark.parametrize("B", [33, 77, 200, 700])
 def test_attn_many_sequences(q8, B):
     # more than a warp's lanes; more splits than, and as many as, sequences; one split each
     prefix = [(37 * b) % 401 for b in range(B)]
