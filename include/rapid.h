@@ -868,7 +868,8 @@ rapid_status rapid_latent_read(const void* cache, int cache_dtype, int B, int64_
  * move next to the root (row prefix_len[b] + 1 + k takes row prefix_len[b] +
  * path[b][k]), bit for bit.
  *
- *  caches     HOST array of `layers` device pointers, 16-byte aligned
+ *  caches     HOST array of `layers` device pointers, 16-byte aligned, to caches
+ *             that do not overlap
  *
  * The other arguments, the errors and the treatment of invalid device inputs
  * are rapid_kv_commit's (kv_capacity at most RAPID_LATENT_MAX_ROWS).
@@ -895,12 +896,14 @@ size_t rapid_latent_attn_workspace_size(int B, int H, int n_q, int64_t kv_capaci
  *  O          [B, H, n_q, 512] bf16
  *
  * What a query does not see has no effect on it, whatever it holds: rows
- * behind the mask, rows behind the step, other queries.  A row with a value
- * that is not finite makes the outputs of the queries that see it NaN.
+ * behind the mask, rows behind the step, other queries.  A value that is not
+ * finite in a row that a query sees reaches that query's outputs as it would in
+ * the formula, mostly as NaN.
  *
  * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], H outside [1,
  * RAPID_LATENT_MAX_HEADS], n_q outside [1, RAPID_MAX_NQ], B * H * n_q above
- * RAPID_LATENT_MAX_QUERIES, kv_capacity below n_q or above RAPID_LATENT_MAX_ROWS, a bad cache type or alignment (16 bytes), a
+ * RAPID_LATENT_MAX_QUERIES, kv_capacity below n_q or above
+ * RAPID_LATENT_MAX_ROWS, a bad cache type or alignment (16 bytes), a
  * softmax_scale that is not finite; RAPID_ENOMEM for a short workspace;
  * RAPID_ECUDA on launch failure.  A prefix_len outside [0, kv_capacity - n_q]
  * is clamped and bit 1 of the device error word is set.

@@ -708,6 +708,10 @@ class LatentLayerTable:
         if len({f[1:] for f in found}) != 1:
             raise RapidError("the caches of all layers must have one type and size")
         _, self.dtype, self.B, self.cap = found[0]
+        size = caches[0].numel() * caches[0].element_size()
+        at = sorted(f[0] for f in found)
+        if any(b - a < size for a, b in zip(at, at[1:])):
+            raise RapidError("the caches of two layers overlap")
         self.layers = len(caches)
         self._ptrs = (ctypes.c_void_p * self.layers)(*[f[0] for f in found])
         self._keep = caches                               # the tensors outlive the table

@@ -231,6 +231,16 @@ def test_commit(q8, layers, n_q):
         assert torch.equal(x.cpu().view(torch.uint8), y.view(torch.uint8))
 
 
+def test_commit_refuses_caches_that_overlap():
+    room = torch.zeros((3, 2, 16, DK), dtype=BF16, device=DEV)
+    rapid.LatentLayerTable([room[2], room[0], room[1]])
+    whole = room.view(-1)
+    shifted = whole[8:8 + room[0].numel()].view(2, 16, DK)
+    for caches in ([room[0], room[0]], [room[1], room[0], room[1]], [room[1], shifted], [shifted, room[1], room[2]]):
+        with pytest.raises(rapid.RapidError):
+            rapid.LatentLayerTable(caches)
+
+
 def test_commit_leaves_invalid_sequences_alone():
     caches = _latent.make_cache((6, 16), False, _gen(9))
     dev = caches.to(DEV)
