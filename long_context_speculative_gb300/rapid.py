@@ -210,7 +210,7 @@ def _device_of(t, name):
     dev = t.get_device()
     if dev < 0:
         raise RapidError(f"{name}: librapid works on CUDA tensors only (no CPU path)")
-    cur = torch.cuda.current_device()
+    cur = torch._C._cuda_getDevice()        # (a tensor on a device: CUDA is initialised)
     if dev != cur:
         raise RapidError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
     return dev
@@ -739,26 +739,50 @@ def rapid_latent_attn_workspace_size(B, H, n_q, kv_capacity, cache_dtype) -> int
     return int(lib().rapid_latent_attn_workspace_size(B, H, n_q, kv_capacity, cache_dtype))
 
 
-def rapid_latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, O, LSE, workspace, stream=None):
-    """Absorbed verify attention over a latent cache; shapes are read from the tensors."""
-    dev = _device_of(Q, "Q")
+def _latent_attn(dev, Q, cache, prefix_len, spec_mask, softmax_scale, O, LSE, workspace, stream):
+    """The call, with O, LSE or the workspace made here where they are None (those need no checks)."""
     if Q.dim() != 4:
         raise RapidError("Q must be [B, H, n_q, 576]")
-    B, H, n_q, _ = Q.shape
+    shape = Q.shape
+    B, H, n_q, _ = shape
     ptr, code, cache_B, cap = _latent_cache(cache, dev)
     if cache_B != B:
         raise RapidError(f"Q has {B} sequences, the cache {cache_B}")
-    bf16 = torch.bfloat16
-    mask_dt = torch.bool if spec_mask is not None and spec_mask.dtype == torch.bool else torch.uint8
+    q_ptr = _arg(Q, dev, torch.bfloat16, (B, H, n_q, RAPID_LATENT_ROW), "Q")
+    if O is None:
+        O = Q.new_empty((B, H, n_q, RAPID_LATENT_DIM))
+        o_ptr = O.data_ptr()
+    else:
+        o_ptr = _arg(O, dev, torch.bfloat16, (B, H, n_q, RAPID_LATENT_DIM), "O")
+    if LSE is None:
+        LSE = Q.new_empty((B, H, n_q), dtype=torch.float32)
+        lse_ptr = LSE.data_ptr()
+    else:
+        lse_ptr = _arg(LSE, dev, torch.float32, (B, H, n_q), "LSE")
+    if workspace is None:
+        nbytes = _latent_attn_bytes(dev, B, H, n_q, cap, code)
+        workspace = _scratch(dev, nbytes)
+        ws_ptr = workspace.data_ptr()
+    else:
+        nbytes = workspace.numel()
+        ws_ptr = _arg(workspace, dev, torch.uint8, (nbytes,), "workspace")
+    mask_ptr = None
+    if spec_mask is not None:
+        mask_ptr = _arg(spec_mask, dev, torch.bool if spec_mask.dtype == torch.bool else torch.uint8,
+                        (B, n_q, n_q), "spec_mask")
     st = lib().rapid_latent_attn(
-        _arg(Q, dev, bf16, (B, H, n_q, RAPID_LATENT_ROW), "Q"), ptr, code, B, H, n_q, cap,
-        _arg(prefix_len, dev, torch.int32, (B,), "prefix_len"),
-        _arg(spec_mask, dev, mask_dt, (B, n_q, n_q), "spec_mask"), softmax_scale,
-        _arg(O, dev, bf16, (B, H, n_q, RAPID_LATENT_DIM), "O"),
-        _arg(LSE, dev, torch.float32, (B, H, n_q), "LSE"),
-        _arg(workspace, dev, torch.uint8, (workspace.numel(),), "workspace"), workspace.numel(),
-        _raw_stream(stream, dev))
+        q_ptr, ptr, code, B, H, n_q, cap, _arg(prefix_len, dev, torch.int32, (B,), "prefix_len"),
+        mask_ptr, softmax_scale, o_ptr, lse_ptr, ws_ptr, nbytes, _raw_stream(stream, dev))
     _check(st, "rapid_latent_attn")
+    return O, LSE
+
+
+def rapid_latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, O, LSE, workspace, stream=None):
+    """Absorbed verify attention over a latent cache; shapes are read from the tensors."""
+    if O is None or LSE is None or workspace is None:
+        raise RapidError("O, LSE and workspace must be tensors")
+    _latent_attn(_device_of(Q, "Q"), Q, cache, prefix_len, spec_mask, softmax_scale, O, LSE, workspace,
+                 stream)
 
 
 def rapid_latent_prefill_attn_workspace_size(B, n, H, kv_rows) -> int:
@@ -1014,18 +1038,8 @@ def latent_attn(Q, cache, prefix_len, spec_mask=None, softmax_scale=0.0, out=Non
     if stream is not None:
         with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
             return latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, out, lse, workspace)
-    B, H, n_q, _ = Q.shape
-    if out is None:
-        out = Q.new_empty((B, H, n_q, RAPID_LATENT_DIM))
-    if lse is None:
-        lse = Q.new_empty((B, H, n_q), dtype=torch.float32)
-    if workspace is None:
-        dev = _device_of(Q, "Q")
-        workspace = _scratch(dev, _latent_attn_bytes(
-            dev, B, H, n_q, cache.shape[1],
-            RAPID_CACHE_LATENT_Q8 if cache.dtype == torch.uint8 else RAPID_DTYPE_BF16))
-    rapid_latent_attn(Q, cache, prefix_len, spec_mask, softmax_scale, out, lse, workspace)
-    return out, lse
+    return _latent_attn(_device_of(Q, "Q"), Q, cache, prefix_len, spec_mask, softmax_scale, out, lse,
+                        workspace, None)
 
 
 @functools.lru_cache(maxsize=64)
