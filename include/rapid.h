@@ -795,7 +795,11 @@ enum { RAPID_CACHE_LATENT_Q8 = 2 };
  * a token holds, per layer, a cache [B, kv_capacity] of rows:
  *   RAPID_DTYPE_BF16       576 bf16: the normed latent vector, the rotated key
  *   RAPID_CACHE_LATENT_Q8  656 bytes: 512 e4m3 codes; 64 bf16, the rotated key;
- *                          4 floats, value = code * scale, one for 128 codes
+ *                          4 floats, value = code * scale, one for 128 codes.
+ *                          Any code and scale may stand there: the value is
+ *                          taken in fp32 and rounded to bf16, which is exact for
+ *                          powers of two (rapid_latent_append's), and NaN where
+ *                          either is
  * A step's n_q rows stand behind the history, as in the caches of
  * rapid_verify_attn: rapid_latent_append writes them, rapid_latent_attn reads
  * them under the chain or tree mask, rapid_latent_commit keeps the accepted
@@ -849,7 +853,7 @@ rapid_status rapid_latent_append(const void* kv, const int64_t* kv_strides, cons
 /*
  * Rows of the cache in bf16, for the products that expand them into keys and
  * values of every head: rows[b, i] := the values of cache[b, first[b] + i],
- * rounded to bf16 (exact where a row's scales are powers of two).
+ * as rapid_latent_attn takes them.
  *
  *  first      device int32 [B] or NULL (0)
  *  n_rows     device int32 [B] or NULL (n); rows behind them stay as they are

@@ -24,9 +24,10 @@
 //   4      copies by TMA: Q; tiles of bf16 rows, the rotated part of 8-bit rows
 //   5, 6   issue QK and PV
 //   7-14   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
-//          quarter of a key, the next tile's on their way while it stores this one.  An e4m3 code
-//          is 2^-120 of a bf16 with the same bits further up, exactly, so two codes cost a byte
-//          selection, a multiplication by 16, a mask and an exact product, and no conversion
+//          quarter of a key, the next tile's on their way while it stores this one.  A value is
+//          code * scale in fp32, rounded to bf16, what rapid_latent_read gives: any scale will
+//          do, and a NaN code is NaN.  (Bits of the codes moved in place and multiplied as bf16
+//          pairs hold for powers of two and numbers only, and are no faster: tree 393 against 385)
 // P is rounded to bf16 (at most 2^-8 of each probability, and it averages out); sums are fp32.
 //
 // Rows that a query does not see have no effect on it, whatever they hold: in tiles that a mask
@@ -37,17 +38,18 @@
 // stops issuing, drains and returns.
 //
 // Measured with the join (us; floor by bytes at 6788 GB/s or operations at 1910 TFLOP/s): 128 heads,
-// 11 queries over 120K bf16 rows 386 (197); 128 heads, 1 query over 120K 8-bit rows 55 (18);
-// 16 heads, a tree of 32 over four 8-bit histories of 32K to 96K 393 (153); 16 heads, 1 query
+// 11 queries over 120K bf16 rows 386 (197); 128 heads, 1 query over 120K 8-bit rows 53 (18);
+// 16 heads, a tree of 32 over four 8-bit histories of 32K to 96K 385 (153); 16 heads, 1 query
 // over 120K bf16 rows 37 (21), over 1K 9.1 (0.2).  With 64 rows the operands' reads from shared memory
 // bound the products (128 B a clock: 36.7 clocks for M = N = 64, 52 for M = 128, N = 64, so 2153 a
 // tile; a tile takes 2340, and sharing the copies of two row blocks in a cluster changes nothing).
-// 8-bit rows take 3400 clocks: the converters share issue slots and the shared-memory port with the softmax
+// 8-bit rows take some 3300 clocks: the converters share issue slots and the shared-memory port with the softmax
 // warps (16 converter warps are slower than 8, 68 us against 64 then).  One query of 16 heads takes
 // 3650 a tile, 5.9 TB/s; of a short call, the start (lengths, first copies), the end and the join are
 // 8 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "latent.cuh"
@@ -126,23 +128,10 @@ RAPID_DEVICE uint32_t times_zero(uint32_t x, uint32_t acc) {       // bf16 pairs
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
     return r;
 }
-RAPID_DEVICE uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// Bytes of x by the nibbles of SEL; with 8 added, eight times a byte's sign.
-template <uint32_t SEL>
-RAPID_DEVICE uint32_t signed_bytes(uint32_t x) {
-    uint32_t r;
-    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
-    return r;
-}
-// A value that the compiler does not know.
-RAPID_DEVICE uint32_t opaque(uint32_t x) {
-    uint32_t y;
-    asm volatile("mov.b32 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
+// Two codes as floats.
+RAPID_DEVICE float2 e4m3x2(uint16_t x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(x, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 RAPID_DEVICE void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -690,19 +679,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         load_scales();
         // 16-byte units 2 q and 2 q + 1 of a chunk
         const uint32_t unit0 = smem_u32(smem) + L::kOffTile + (uint32_t)(key * 128 + (((2 * q) ^ (key & 7)) << 4));
-        const uint32_t sixteen = opaque(16u);
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
             const bool more = j + 1 < n;
             src += kKeys * kLatentQ8Row / 16;     // (loads from here on are the next tile's)
             left -= kKeys;
-            // * 2^120 scale; scales above 2^7, which would overflow there, in two steps
-            float up[4] = {__uint_as_float(sc.x), __uint_as_float(sc.y), __uint_as_float(sc.z), __uint_as_float(sc.w)};
-            const bool big = up[0] > 128.f || up[1] > 128.f || up[2] > 128.f || up[3] > 128.f;
-            if (!big)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) up[u] *= 1.329227995784916e36f;
+            const float scale[4] = {__uint_as_float(sc.x), __uint_as_float(sc.y), __uint_as_float(sc.z),
+                                    __uint_as_float(sc.w)};
             if (more) load_scales();
             bool ok = true;
             // Two halves of 256 values, each converted while the room is still in use.  The last piece of a
@@ -715,19 +699,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     const int u = 4 * half + x;
                     const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
                     if (more) load(u);
-                    const uint32_t s2 = __byte_perm(__float_as_uint(up[u >> 1]), 0, 0x3232);
-                    // Two codes: each with its sign in the byte above it, 4 bits up (a multiplication: the
-                    // integer pipe is the busiest), sign and magnitude kept; that is code * 2^-120.
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        o[x][k] = ((k & 1 ? signed_bytes<0xb3a2>(w[k >> 1]) : signed_bytes<0x9180>(w[k >> 1])) * sixteen) &
-                                  0x87f087f0u;
-                    if (big) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[x][k] = mul_bf16x2(o[x][k], 0x7b807b80u);
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 y = mul2(e4m3x2((uint16_t)(w[k >> 1] >> (16 * (k & 1)))),
+                                              make_float2(scale[u >> 1], scale[u >> 1]));
+                        o[x][k] = bf16x2(y.x, y.y);
                     }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) o[x][k] = mul_bf16x2(o[x][k], s2);
                 }
                 if (j >= 2)
                     ok = __all_sync(0xffffffffu, mbar_wait_sleep(&bars->empty[st][2 + 2 * half], (uint32_t)(((j >> 1) + 1) & 1),
