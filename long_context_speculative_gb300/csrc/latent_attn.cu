@@ -592,13 +592,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                         ++issued;
                     }
                 }
-                if (!ok) {
-                    bars->abort = 1;
-                    // let the copies in flight land before the CTA exits
-                    for (int x = max(0, issued - 2 * kCopied); x < issued; ++x)
-                        mbar_wait(&bars->full[(x / kCopied) & 1][x % kCopied], (uint32_t)((x / kCopied >> 1) & 1),
-                                  p.err, kRoleProducer | kBarFull);
-                }
+                if (!ok) bars->abort = 1;
+                // The copies in flight land before the CTA exits, whichever role may have given up: the last
+                // two tiles', the last phases of their barriers.
+                for (int x = max(0, issued - 2 * kCopied); x < issued; ++x)
+                    mbar_wait_sleep(&bars->full[(x / kCopied) & 1][x % kCopied], (uint32_t)((x / kCopied >> 1) & 1),
+                                    p.err, kRoleProducer | kBarFull);
                 mbar_wait_sleep(&bars->q_full, 0, p.err, kRoleProducer | kBarLast);
             }
         } else if (warp == kQkWarp || warp == kPvWarp) {

@@ -515,12 +515,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     ++k;
                     next_piece(run, pc.n);
                 }
-                if (!ok) {
-                    bars->abort = 1;
-                    // let the copies in flight land before the CTA exits
-                    for (int c = max(0, ch - kRing); c < ch; ++c)
-                        mbar_wait(&bars->full[c % kRing], (uint32_t)((c / kRing) & 1), p.err, kRoleProducer | kBarFull);
-                }
+                if (!ok) bars->abort = 1;
+                // The copies in flight land before the CTA exits, whichever role may have given up: the last
+                // chunks of the ring, the last phases of their barriers.
+                for (int c = max(0, ch - kRing); c < ch; ++c)
+                    mbar_wait_sleep(&bars->full[c % kRing], (uint32_t)((c / kRing) & 1), p.err, kRoleProducer | kBarFull);
                 for (int t = 0; t < 2; ++t)
                     mbar_wait_sleep(&bars->q_full[t], (uint32_t)((q_loads - 1) & 1), p.err, kRoleProducer | kBarLast);
             }
