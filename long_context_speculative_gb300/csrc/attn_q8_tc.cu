@@ -609,13 +609,14 @@ attn_q8_tc_kernel(const __grid_constant__ CUtensorMap pool, const AttnQ8Params p
                 ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
                 if (++st == kStages) { st = 0; lap ^= 1u; }
             }
-            if (!ok && lane == 0) {
-                sc->abort = 1;
+            if (lane == 0) {
+                if (!ok) sc->abort = 1;
+                // The copies still in flight land before the CTA exits, whichever role may have given up
+                // (the last phases of their barriers).
 #pragma unroll 1
-                // let the copies still in flight land before the CTA exits
                 for (int i = max(0, issued - kStages); i < issued; ++i)
-                    mbar_wait(&sc->raw_full[i % kStages], (i / kStages) & 1, p.err,
-                              kRoleProducer | kBarRawFull | (unsigned)(i & 0xffff));
+                    mbar_wait_sleep(&sc->raw_full[i % kStages], (i / kStages) & 1, p.err,
+                                    kRoleProducer | kBarRawFull | (unsigned)(i & 0xffff));
             }
         } else if (warp == L::kMmaWarp) {
             // ------------------------------ issuer ----------------------------

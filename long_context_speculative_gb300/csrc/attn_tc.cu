@@ -380,12 +380,11 @@ attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK,
                     }
                 }
             }
-            if (*((volatile int*)&bars->abort)) {
-                // let the copies still in flight land before the CTA exits
-                for (int i = max(0, issued - kStages); i < issued; ++i)
-                    mbar_wait(&bars->kv_full[i % kStages], (i / kStages) & 1, p.err,
-                              kRoleProducer | kBarKvFull | (unsigned)(i & 0xffff));
-            }
+            // The copies still in flight land before the CTA exits, whichever role may have given up (the
+            // last phases of their barriers).
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait_sleep(&bars->kv_full[i % kStages], (i / kStages) & 1, p.err,
+                                kRoleProducer | kBarKvFull | (unsigned)(i & 0xffff));
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------ MMA issuer ----------------------------

@@ -220,12 +220,11 @@ lm_head_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                     ++issued;
                 }
             }
-            if (!ok) {
-                bars->abort = 1;
-                // the copies still in flight land before the CTA exits
-                for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-                    mbar_wait(&bars->full[i % S], (i / S) & 1, nullptr, 0);
-            }
+            if (!ok) bars->abort = 1;
+            // The copies still in flight land before the CTA exits, whichever role may have given up (the
+            // last phases of their barriers).
+            for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+                mbar_wait_sleep(&bars->full[i % S], (i / S) & 1, err, kLmProducer | (unsigned)(i & 0xffff));
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ----------------------------
