@@ -24,10 +24,9 @@
 //   4      copies by TMA: Q; tiles of bf16 rows, the rotated part of 8-bit rows
 //   5, 6   issue QK and PV
 //   7-14   (8-bit rows) convert codes on their way from global memory to the tile: a thread has a
-//          quarter of a key, the next tile's on their way while it stores this one.  A value is
+//          quarter of a key, and the next tile's are loaded once this one is stored.  A value is
 //          code * scale in fp32, rounded to bf16, what rapid_latent_read gives: any scale will
-//          do, and a NaN code is NaN.  (Bits of the codes moved in place and multiplied as bf16
-//          pairs hold for powers of two and numbers only, and are no faster: tree 393 against 385)
+//          do, and a NaN code is NaN
 // P is rounded to bf16 (at most 2^-8 of each probability, and it averages out); sums are fp32.
 //
 // Rows that a query does not see have no effect on it, whatever they hold: in tiles that a mask
@@ -39,7 +38,7 @@
 //
 // Measured with the join (us; floor by bytes at 6788 GB/s or operations at 1910 TFLOP/s): 128 heads,
 // 11 queries over 120K bf16 rows 386 (197); 128 heads, 1 query over 120K 8-bit rows 53 (18);
-// 16 heads, a tree of 32 over four 8-bit histories of 32K to 96K 385 (153); 16 heads, 1 query
+// 16 heads, a tree of 32 over four 8-bit histories of 32K to 96K 380 (153); 16 heads, 1 query
 // over 120K bf16 rows 37 (21), over 1K 9.1 (0.2).  With 64 rows the operands' reads from shared memory
 // bound the products (128 B a clock: 36.7 clocks for M = N = 64, 52 for M = 128, N = 64, so 2153 a
 // tile; a tile takes 2340, and sharing the copies of two row blocks in a cluster changes nothing).
@@ -572,10 +571,21 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 constexpr int kCopied = Q8 ? 1 : kPieces;      // pieces of a tile: 8-bit rows, the rotated part
                 int issued = 0;
                 bool ok = true;
+                // 8-bit rows are asked into L2 two tiles ahead (the converters load a tile late, below)
+                auto ahead = [&](int j) {
+                    if (!Q8 || j >= n) return;
+                    const int64_t row = (int64_t)(t_begin + j) * kKeys, rows = min((int64_t)kKeys, p.cap - row);
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                     p.cache + ((int64_t)b * p.cap + row) * kLatentQ8Row),
+                                 "r"((uint32_t)(rows * kLatentQ8Row))
+                                 : "memory");
+                };
+                ahead(1);
                 for (int j = 0; j < n && ok; ++j) {
                     const int st = j & 1;
                     uint8_t* tile = smem + L::kOffTile + st * kTile;
                     const int y = (t_begin + j) * kKeys;
+                    ahead(j + 2);
                     for (int g = 0; g < kCopied; ++g) {
                         if ((j >= 2 && !mbar_wait_sleep(&bars->empty[st][g], (uint32_t)(((j >> 1) + 1) & 1), p.err,
                                                         kRoleProducer | kBarEmpty | (unsigned)(j & 0xffff))) ||
@@ -671,22 +681,19 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             p.cache + ((int64_t)b * p.cap + (int64_t)t_begin * kKeys + key) * kLatentQ8Row);
         int64_t left = p.cap - (int64_t)t_begin * kKeys - key;    // rows of the cache from this one on
         uint4 v[8], sc;
-        auto load = [&](int u) { v[u] = left > 0 ? __ldg(src + 4 * u + q) : make_uint4(0, 0, 0, 0); };
-        auto load_scales = [&] { sc = left > 0 ? __ldg(src + kLatentQ8Scale / 16) : make_uint4(0, 0, 0, 0); };
+        auto load_tile = [&] {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) load(u);
-        load_scales();
+            for (int u = 0; u < 8; ++u) v[u] = left > 0 ? src[4 * u + q] : make_uint4(0, 0, 0, 0);
+            sc = left > 0 ? src[kLatentQ8Scale / 16] : make_uint4(0, 0, 0, 0);
+        };
+        load_tile();
         // 16-byte units 2 q and 2 q + 1 of a chunk
         const uint32_t unit0 = smem_u32(smem) + L::kOffTile + (uint32_t)(key * 128 + (((2 * q) ^ (key & 7)) << 4));
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
-            const bool more = j + 1 < n;
-            src += kKeys * kLatentQ8Row / 16;     // (loads from here on are the next tile's)
-            left -= kKeys;
             const float scale[4] = {__uint_as_float(sc.x), __uint_as_float(sc.y), __uint_as_float(sc.z),
                                     __uint_as_float(sc.w)};
-            if (more) load_scales();
             bool ok = true;
             // Two halves of 256 values, each converted while the room is still in use.  The last piece of a
             // half is free only after its others (the products that read them are issued in order).
@@ -697,7 +704,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 for (int x = 0; x < 4; ++x) {
                     const int u = 4 * half + x;
                     const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-                    if (more) load(u);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float2 y = mul2(e4m3x2((uint16_t)(w[k >> 1] >> (16 * (k & 1)))),
@@ -726,6 +732,13 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 bars->abort = 1;
                 break;
             }
+            // A proxy fence waits for the loads before it, so the next tile's are issued behind the tile's last
+            // one.  (Non-coherent loads would not be waited for, but the rows may have been written while
+            // this kernel was already there; those issued early and without the look ahead into L2: 385 us
+            // for the tree against 380.)
+            src += kKeys * kLatentQ8Row / 16;
+            left -= kKeys;
+            if (j + 1 < n) load_tile();
         }
     }
     tc_fence_before();

@@ -8,6 +8,9 @@
 // a floating-point code no precision, and dividing and multiplying by it is exact.  All
 // arithmetic is fp32, rounded once at the store.
 //
+// Loads are coherent ones: a kernel may be there before its predecessor has ended, and read what that wrote
+// once griddep_wait() has returned.
+//
 // All three kernels copy: no value is read twice.  A row is one warp's work: lane l holds values
 // 16 l .. 16 l + 15 of the latent vector (a scale group is 8 lanes) and pair l of the key.
 //
@@ -73,17 +76,17 @@ RAPID_DEVICE float group_scale(float amax) {
 RAPID_DEVICE void append_row(const LatentAppendParams& p, int b, int i, int64_t pos, uint8_t* row,
                              int lane) {
     const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.kv) + b * p.kv_batch + i * p.kv_token;
-    const uint4 r0 = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane);
-    const uint4 r1 = __ldg(reinterpret_cast<const uint4*>(src) + 2 * lane + 1);
+    const uint4 r0 = reinterpret_cast<const uint4*>(src)[2 * lane];
+    const uint4 r1 = reinterpret_cast<const uint4*>(src)[2 * lane + 1];
     const int ka = p.interleaved ? 2 * lane : lane, kb = p.interleaved ? 2 * lane + 1 : lane + 32;
     const float ra = __bfloat162float(src[kLatent + ka]), rb = __bfloat162float(src[kLatent + kb]);
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
     if (p.weight) {
-        w0 = __ldg(static_cast<const uint4*>(p.weight) + 2 * lane);
-        w1 = __ldg(static_cast<const uint4*>(p.weight) + 2 * lane + 1);
+        w0 = static_cast<const uint4*>(p.weight)[2 * lane];
+        w1 = static_cast<const uint4*>(p.weight)[2 * lane + 1];
     }
     float sn, cs;
-    sincos_turn(turns_per_position(__ldg(p.inv_freq + lane)), pos, &sn, &cs);
+    sincos_turn(turns_per_position(p.inv_freq[lane]), pos, &sn, &cs);
     float x[16];
     unpack8(r0, x);
     unpack8(r1, x + 8);
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(const Lat
     // either way.  The 8 heads of a step share the angles: each works out one pair a lane.
     const int c = lane & 3, sub = lane >> 2;
     float my_sn, my_cs, sn[8], cs[8];
-    sincos_turn(turns_per_position(__ldg(p.inv_freq + 8 * c + sub)), pos, &my_sn, &my_cs);
+    sincos_turn(turns_per_position(p.inv_freq[8 * c + sub]), pos, &my_sn, &my_cs);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         sn[u] = __shfl_sync(0xffffffffu, my_sn, 4 * u + c);
@@ -251,10 +254,10 @@ __global__ void __launch_bounds__(128) latent_read_kernel(const LatentReadParams
     for (int r = 0; r < kReadRows; ++r) {
         if (r >= m) continue;
         const uint4* s = reinterpret_cast<const uint4*>(src + (int64_t)r * kRow);
-        x[r] = __ldg(s + lane);
-        if (!Q8) y[r] = __ldg(s + 32 + lane);
-        if (lane < 8) z[r] = __ldg(s + (Q8 ? 32 : 64) + lane);
-        if (Q8) scale[r] = __ldg(reinterpret_cast<const float*>(s + kLatentQ8Scale / 16) + (lane >> 3));
+        x[r] = s[lane];
+        if (!Q8) y[r] = s[32 + lane];
+        if (lane < 8) z[r] = s[(Q8 ? 32 : 64) + lane];
+        if (Q8) scale[r] = reinterpret_cast<const float*>(s + kLatentQ8Scale / 16)[lane >> 3];
     }
 #pragma unroll
     for (int r = 0; r < kReadRows; ++r) {
