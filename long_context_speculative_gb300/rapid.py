@@ -792,6 +792,8 @@ def rapid_latent_prefill_attn_workspace_size(B, n, H, kv_rows) -> int:
 def rapid_latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, O, LSE, workspace,
                               stream=None):
     """Expanded causal attention of a prompt chunk; Q, K, V and K_rope may be strided views."""
+    if O is None or LSE is None or workspace is None:
+        raise RapidError("O, LSE and workspace must be tensors")
     dev = _device_of(Q, "Q")
     if Q.dim() != 4 or K.dim() != 4:
         raise RapidError("Q is [B, n, H, 192], K and V [B, kv_rows, H, 128]")
@@ -1011,6 +1013,8 @@ def latent_read(cache, first, n, n_rows=None, out=None, stream=None):
         with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
             return latent_read(cache, first, n, n_rows, out)
     if out is None:
+        if cache.dim() != 3 or n < 1:
+            raise RapidError("cache is [B, capacity, 576] bf16 or [B, capacity, 656] uint8, and n at least 1")
         out = cache.new_empty((cache.shape[0], n, RAPID_LATENT_ROW), dtype=torch.bfloat16)
     elif out.dim() != 3 or out.shape[1] != n:
         raise RapidError(f"out must be [B, {n}, 576]")
@@ -1060,6 +1064,8 @@ def latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows=None, softmax_scale=
         with torch.cuda.stream(stream):    # what is allocated here belongs to that stream
             return latent_prefill_attn(Q, K, V, K_rope, prefix_len, n_rows, softmax_scale, out, lse,
                                        workspace)
+    if Q.dim() != 4 or K.dim() != 4:
+        raise RapidError("Q is [B, n, H, 192], K and V [B, kv_rows, H, 128]")
     B, n, H, _ = Q.shape
     if out is None:
         out = Q.new_empty((B, n, H, RAPID_LATENT_HEAD_DIM))

@@ -1,0 +1,41 @@
+"""CPU checks of arguments of the latent cache's calls that the C entries and the binding refuse
+before they touch a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from long_context_speculative_gb300 import build as lib_build
+from long_context_speculative_gb300 import rapid
+
+P = ctypes.c_void_p(256)        # a fake, aligned device address (never dereferenced)
+BF16, I32 = torch.bfloat16, torch.int32
+
+
+@pytest.fixture(scope="module")
+def lib():
+    lib_build.build()
+    return rapid.lib()
+
+
+def _z(*s, dtype=BF16):
+    return torch.zeros(s, dtype=dtype)
+
+
+def test_prefill_refuses_other_numbers_of_dimensions(lib):
+    one = _z(1, dtype=I32)
+    good = [_z(1, 3, 2, 192), _z(1, 9, 2, 128), _z(1, 9, 2, 128), _z(1, 9, 64)]
+    for i in range(2):
+        for bad in (good[i][0], good[i][None], _z(), good[i].flatten()):
+            args = list(good)
+            args[i] = bad
+            with pytest.raises(rapid.RapidError):
+                rapid.latent_prefill_attn(*args, one)
+    with pytest.raises(rapid.RapidError):
+        rapid.rapid_latent_prefill_attn(*good, one, None, 0.0, _z(1, 3, 2, 128), _z(1, 2, 3, dtype=torch.float32), None)
+
+
+def test_read_refuses_other_numbers_of_dimensions_and_rows(lib):
+    for cache, n in ((_z(), 3), (_z(64, 576), 3), (_z(1, 1, 64, 576), 3), (_z(1, 64, 576), 0), (_z(1, 64, 576), -1)):
+        with pytest.raises(rapid.RapidError):
+            rapid.latent_read(cache, None, n)
