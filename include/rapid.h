@@ -827,7 +827,9 @@ enum { RAPID_CACHE_LATENT_Q8 = 2 };
  *             i * s[4] + h * s[5] of q_out.  q_out = q with the same strides
  *             rotates in place; any other overlap is not allowed
  *  q_strides  HOST array s of six element strides, or NULL: both packed
- *             [B, n, H, 64].  Every stride a multiple of 8 (16 bytes)
+ *             [B, n, H, 64].  Every stride a multiple of 8 (16 bytes), and
+ *             those of q_out at least 64 where the dimension is larger than 1
+ *             (its rows do not overlap)
  *  kv_weight  device bf16 [512] or NULL: no norm
  *  inv_freq   device float [32]: radians per position of each pair (elements
  *             i, i + 32, or 2 i, 2 i + 1 with RAPID_ROPE_INTERLEAVED); an

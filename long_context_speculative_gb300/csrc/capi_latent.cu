@@ -105,6 +105,10 @@ rapid_status rapid_latent_append(const void* kv, const int64_t* kv_strides, cons
         const int64_t q_packed[6] = {n * token, token, kLatentRope, n * token, token, kLatentRope};
         const int64_t* qs = q_strides ? q_strides : q_packed;
         if (!strides_ok(qs, 6)) return RAPID_EINVAL;
+        // rows of q_out that repeat or run into each other would be written at once
+        const int64_t size[3] = {B, n, H};
+        for (int i = 0; i < 3; ++i)
+            if (size[i] > 1 && qs[3 + i] < kLatentRope) return RAPID_EINVAL;
         p.q_batch = qs[0]; p.q_token = qs[1]; p.q_head = qs[2];
         p.o_batch = qs[3]; p.o_token = qs[4]; p.o_head = qs[5];
         p.H = H;

@@ -39,3 +39,18 @@ def test_read_refuses_other_numbers_of_dimensions_and_rows(lib):
     for cache, n in ((_z(), 3), (_z(64, 576), 3), (_z(1, 1, 64, 576), 3), (_z(1, 64, 576), 0), (_z(1, 64, 576), -1)):
         with pytest.raises(rapid.RapidError):
             rapid.latent_read(cache, None, n)
+
+
+def test_append_refuses_query_rows_that_repeat(lib):
+    # kv kv_strides q q_strides B n H weight eps inv flags prefix row_offset n_rows q_out cache type cap stream
+    def call(strides, B=2, n=11, H=16):
+        s = (ctypes.c_int64 * 6)(*strides)
+        return lib.rapid_latent_append(P, None, P, s, B, n, H, P, ctypes.c_float(1e-6), P, 0, P, P, P, P, P, 1,
+                                       4096, None)
+
+    packed = [11 * 1024, 1024, 64]
+    for i in range(3):
+        for bad in (0, 8, 56):
+            out = list(packed)
+            out[i] = bad
+            assert call(packed + out) == -1, (i, bad)

@@ -80,3 +80,23 @@ def test_calls_that_read_what_the_last_call_wrote(q8):
     for _ in range(3):
         for x, y in zip(_chain(q8, False), want):
             assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_append_rotates_queries_that_repeat_and_refuses_to_write_them_over_each_other():
+    g = torch.Generator().manual_seed(1)
+    B, n, H = 2, 3, 5
+    cache = torch.zeros((B, 16, 576), dtype=BF16, device=DEV)
+    kv = torch.randn((B, n, 576), generator=g).to(BF16).to(DEV)
+    inv = (5e5 ** (-torch.arange(0, 64, 2).double() / 64)).float().to(DEV)
+    length = torch.zeros(B, dtype=torch.int32, device=DEV)
+    one = torch.randn((B, n, 1, 64), generator=g).to(BF16).to(DEV)
+    want = rapid.latent_append(kv, cache, length, inv, q=one.expand(-1, -1, H, -1).contiguous())
+    # one row for all heads, read for each of them
+    assert torch.equal(rapid.latent_append(kv, cache, length, inv, q=one.expand(-1, -1, H, -1)), want)
+    for out in (one.clone().expand(-1, -1, H, -1), one[:, :1].expand(-1, n, -1, -1).expand(-1, -1, H, -1),
+                want.flatten().as_strided((B, n, H, 64), (n * H * 64, H * 64, 32, 1))):
+        with pytest.raises(rapid.RapidError):
+            rapid.latent_append(kv, cache, length, inv, q=want, q_out=out)
+    # sizes of 1 have no stride
+    assert torch.equal(rapid.latent_append(kv, cache, length, inv, q=one, q_out=one.as_strided((B, n, 1, 64), (n * 64, 64, 0, 1))),
+                       want[:, :, :1])
