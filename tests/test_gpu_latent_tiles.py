@@ -102,3 +102,118 @@ def test_prefill_rings_of_any_fill(H, prefix, counts):
         m = n if counts is None else counts[b]
         assert ((O[b, :m, heads].double() - want[b, :m]).abs() <= eO[b, :m]).all()
         assert ((S[b, heads, :m].double() - lse[b, :, :m]).abs() <= eL[b, :, :m]).all()
+
+
+def _rising(H, n, prefix, q8, g):
+    """Queries and rows whose scores pass all before them by far more than 2^16 at tiles that differ from query
+    to query (three in four of them), or fall, or stay."""
+    k = len(prefix)
+    Q = torch.randn((k, H, n, DK), generator=g)
+    cap = max(prefix) + n + 3
+    x = torch.randn((k, cap, DK), generator=g)
+    tile = torch.arange(cap) // TILE
+    x[..., 3] = 20.0 * tile                       # times 16 and 192^-0.5: 23 a tile
+    x[..., 130] = 24.0 * (tile >= 2)
+    x[..., 500] = 24.0 * (tile >= 3) + 24.0 * (tile >= 5)
+    row = torch.arange(H * n).view(H, n)
+    Q[..., 3] = torch.where(row % 4 == 0, 16.0, torch.where(row % 4 == 1, -16.0, 0.0))
+    Q[..., 130] = torch.where(row % 3 == 0, 16.0, 0.0)
+    Q[..., 500] = torch.where(row % 5 < 2, 16.0, 0.0)
+    if not q8:
+        cache = x.bfloat16()
+    else:
+        y = x[..., :512].unflatten(-1, (4, 128))
+        s = _latent.group_scale(y.abs().amax(-1).double()).float()
+        cache = _latent.pack((y / s[..., None]).flatten(-2).to(torch.float8_e4m3fn), x[..., 512:].bfloat16(), s)
+    return Q.to(BF16).to(DEV), cache.to(DEV)
+
+
+def _references_that_move(Q, cache, P, n):
+    """How many of a query's tiles move its reference, by the scores themselves (most of any query)."""
+    x = (Q[0].double().flatten(0, 1) @ _latent.values(cache[0, :P]).T) * _latent.SCALE / math.log(2)
+    top = x[:, :P // TILE * TILE].unflatten(1, (-1, TILE)).amax(-1)
+    ref, moved = top[:, 0].clone(), torch.zeros(top.shape[0], device=DEV)
+    for t in range(1, top.shape[1]):
+        up = top[:, t] > ref + 16
+        moved += up
+        ref = torch.where(up, top[:, t], ref)
+    return moved
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("H,n,B", SHAPES)
+def test_attn_references_move_from_tile_to_tile(q8, H, n, B):
+    g = torch.Generator().manual_seed(H + 1)
+    prefix = [6 * TILE - n, 450, 129, 320]
+    Q, cache = _rising(H, n, prefix, q8, g)
+    assert _slots(B, H, n, cache.shape[1], q8) == B
+    moved = _references_that_move(Q, cache, prefix[0], n)
+    assert moved.max() >= 4 and (moved == 0).any()
+    _compare(Q, cache, prefix, B)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_attn_references_move_in_splits_of_several_tiles(q8):
+    # few splits of many rows, joined: at least five tiles each
+    g = torch.Generator().manual_seed(3)
+    H, n, P = 128, 11, 2400
+    Q, cache = _rising(H, n, [P], q8, g)
+    S = _slots(1, H, n, cache.shape[1], q8)
+    assert 1 < S and (P + n + TILE - 1) // TILE >= 5 * S, S
+    assert _references_that_move(Q, cache, P, n).max() >= 4
+    _compare(Q, cache, [P], 1)
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("H,n,B", [(3, 5, 700), (6, 5, 700), (1, 64, 700), (13, 5, 400)])
+def test_attn_hidden_rows_behind_several_tiles_may_hold_anything(q8, H, n, B):
+    g = torch.Generator().manual_seed(n + H)
+    prefix = [3 * TILE - 2, 4 * TILE, 2 * TILE + 33]
+    Q = torch.randn((3, H, n, DK), generator=g).to(BF16).to(DEV)
+    cache = _latent.make_cache((3, max(prefix) + n + 70), q8, g).to(DEV)
+    assert _slots(B, H, n, cache.shape[1], q8) == B
+    mask = (torch.rand((3, n, n), generator=g) < 0.5).to(torch.uint8).to(DEV)
+    mask[:, :, 2] = 0                                     # rows of the step that nobody sees
+    mask[:, :, 3] = 0
+    mask[:, 1, 3] = 1                                     # one that one query sees
+    clean_O, clean_L = _compare(Q, cache, prefix, B, mask)
+    x = cache.clone()
+    for b, P in enumerate(prefix):
+        if q8:
+            _latent.parts(x)[2][b, P + 2:P + 4] = NAN
+            _latent.parts(x)[1][b, P + 2:P + 4] = INF
+        else:
+            x[b, P + 2:P + 4] = NAN
+            x[b, P + 3, ::2] = INF
+        x[b, P + n:] = 0xff if q8 else NAN                # behind the step
+    O, L = rapid.latent_attn(_copies(Q, B), _copies(x, B), _copies(_ints(prefix), B), _copies(mask, B))
+    assert torch.isnan(O[:, :, 1]).all() and torch.isnan(L[:, :, 1]).all()
+    others = [i for i in range(n) if i != 1]
+    assert torch.equal(O[:, :, others], _copies(clean_O[:, :, others], B))
+    assert torch.equal(L[:, :, others], _copies(clean_L[:, :, others], B))
+
+
+@pytest.mark.parametrize("n,H", [(1, 3), (300, 2), (100, 5)])
+def test_prefill_references_move_in_runs_of_several_tiles(n, H):
+    # blocks behind a long prefix, their keys shared out over all SMs: a run is several tiles of 128
+    g = torch.Generator().manual_seed(n)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = (n + 255) // 256
+    P = 128 * (4 * sms // (H * blocks) + 3)
+    L = P + n
+    Q = torch.randn((1, n, H, 192), generator=g)
+    K = torch.randn((1, L, H, 128), generator=g)
+    V = torch.randn((1, L, H, 128), generator=g).to(BF16).to(DEV)
+    R = torch.randn((1, L, 64), generator=g).to(BF16).to(DEV)
+    tile = torch.arange(L) // 128
+    K[..., 3] = (20.0 * (tile % 5))[None, :, None]        # up by 23 a tile four times, and down
+    K[..., 70] = (0.5 * tile)[None, :, None]
+    Q[..., 3] = torch.where(torch.arange(n)[:, None] % 3 == 0, 16.0, 0.0)
+    Q[..., 70] = torch.where(torch.arange(n)[:, None] % 4 == 1, 16.0, 0.0)
+    Q, K = Q.to(BF16).to(DEV), K.to(BF16).to(DEV)
+    # (parts of two slots an SM of 256 tokens, maxima and sums)
+    assert rapid.rapid_latent_prefill_attn_workspace_size(1, n, H, L) > 2 * sms * 256 * 128 * 4
+    O, S = rapid.latent_prefill_attn(Q, K, V, R, _ints([P]))
+    want, lse, eO, eL = _latent.prefill(Q, K, V, R, [P])
+    assert ((O.double() - want).abs() <= eO).all(), float(((O.double() - want).abs() / eO).max())
+    assert ((S.double() - lse).abs() <= eL).all()
