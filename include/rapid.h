@@ -875,7 +875,7 @@ rapid_status rapid_latent_read(const void* cache, int cache_dtype, int B, int64_
  * path[b][k]), bit for bit.
  *
  *  caches     HOST array of `layers` device pointers, 16-byte aligned, to caches
- *             that do not overlap
+ *             that do not overlap (RAPID_EINVAL where two do)
  *
  * The other arguments, the errors and the treatment of invalid device inputs
  * are rapid_kv_commit's (kv_capacity at most RAPID_LATENT_MAX_ROWS).

@@ -1,4 +1,5 @@
 // C ABI of the latent cache: append, read back, commit, absorbed and expanded attention.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -155,11 +156,17 @@ rapid_status rapid_latent_commit(void* const* caches, int layers, int cache_dtyp
         if (!caches[l] || !aligned(caches[l], 16)) return RAPID_EINVAL;
         p.cache[l] = static_cast<uint8_t*>(caches[l]);
     }
+    p.row_bytes = latent_row_bytes(cache_dtype == RAPID_CACHE_LATENT_Q8);
+    // layers move their rows at the same time: a cache twice, or two that overlap, would be moved twice
+    uintptr_t at[kLatentMaxLayers];
+    for (int l = 0; l < layers; ++l) at[l] = reinterpret_cast<uintptr_t>(caches[l]);
+    std::sort(at, at + layers);
+    for (int l = 1; l < layers; ++l)
+        if ((double)(at[l] - at[l - 1]) < (double)B * kv_capacity * p.row_bytes) return RAPID_EINVAL;
     p.prefix_len = prefix_len; p.path = path; p.n_acc = n_accepted;
     p.err = device_error_word();
     p.cap = kv_capacity;
     p.n_q = n_q;
-    p.row_bytes = latent_row_bytes(cache_dtype == RAPID_CACHE_LATENT_Q8);
     return status_of(launch_latent_commit(p, layers, B, static_cast<cudaStream_t>(stream)));
 }
 

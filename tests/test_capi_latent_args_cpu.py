@@ -54,3 +54,12 @@ def test_append_refuses_query_rows_that_repeat(lib):
             out = list(packed)
             out[i] = bad
             assert call(packed + out) == -1, (i, bad)
+
+
+def test_commit_refuses_caches_that_overlap(lib):
+    # caches layers type B cap n_q prefix path n_accepted stream
+    size = {1: 2 * 64 * 1152, 2: 2 * 64 * 656}
+    for code, nbytes in size.items():
+        for at in ((0, 0), (0, nbytes - 16), (nbytes, 0, 2 * nbytes - 16), (3 * nbytes, 0, 5 * nbytes, 3 * nbytes)):
+            table = (ctypes.c_void_p * len(at))(*[4096 + a for a in at])
+            assert lib.rapid_latent_commit(table, len(at), code, 2, 64, 11, P, P, P, None) == -1, (code, at)

@@ -100,3 +100,17 @@ def test_append_rotates_queries_that_repeat_and_refuses_to_write_them_over_each_
     # sizes of 1 have no stride
     assert torch.equal(rapid.latent_append(kv, cache, length, inv, q=one, q_out=one.as_strided((B, n, 1, 64), (n * 64, 64, 0, 1))),
                        want[:, :, :1])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_commit_on_caches_side_by_side_in_any_order(q8):
+    g = torch.Generator().manual_seed(2)
+    caches = _latent.make_cache((5, 2, 16), q8, g).to(DEV)
+    want = caches.clone()
+    for b, P in enumerate((3, 8)):
+        want[:, b, P + 1:P + 3] = caches[:, b, [P + 2, P + 5]]
+    path = torch.tensor([[2, 5, -1, -1, -1, -1]] * 2, dtype=torch.int32, device=DEV)
+    two = torch.full((2,), 2, dtype=torch.int32, device=DEV)
+    table = rapid.LatentLayerTable([caches[i] for i in (3, 0, 4, 1, 2)])
+    table.commit(torch.tensor([3, 8], dtype=torch.int32, device=DEV), path, two)
+    assert torch.equal(caches.view(torch.uint8), want.view(torch.uint8))
