@@ -233,7 +233,7 @@ template <bool Q8>
 __global__ void __launch_bounds__(128) latent_read_kernel(const LatentReadParams p) {
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int per = (p.n + kReadRows - 1) / kReadRows;      // units of a sequence
+    const int per = (p.n - 1) / kReadRows + 1;            // units of a sequence
     const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int b = (int)(unit / per);
     if (b >= p.B) return;
@@ -347,7 +347,7 @@ cudaError_t launch_latent_append(LatentAppendParams p, cudaStream_t st) {
 }
 
 cudaError_t launch_latent_read(const LatentReadParams& p, cudaStream_t st) {
-    const int64_t units = (int64_t)p.B * ((p.n + kReadRows - 1) / kReadRows);
+    const int64_t units = (int64_t)p.B * ((p.n - 1) / kReadRows + 1);
     const int64_t blocks = (units + 3) / 4;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return p.q8 ? launch(latent_read_kernel<true>, dim3((unsigned)blocks), 128, p, st)
