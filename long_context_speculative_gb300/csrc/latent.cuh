@@ -96,6 +96,7 @@ struct LatentPrefillParams {
     int64_t* part_first;
     int64_t kv_rows;
     int B, H, n, ctas;
+    int group;                   // heads (of all sequences) whose blocks are taken longest first, ctas == 0
     float scale_log2;
 };
 
@@ -107,6 +108,6 @@ int latent_attn_slots(int B, int R, int64_t cap);
 cudaError_t launch_latent_attn(const LatentAttnParams& p, cudaStream_t st);
 int latent_prefill_ctas(int B, int n, int H, int64_t kv_rows);
 size_t latent_prefill_block_rows();                   // tokens of a block
-cudaError_t launch_latent_prefill(const LatentPrefillParams& p, cudaStream_t st);
+cudaError_t launch_latent_prefill(LatentPrefillParams p, cudaStream_t st);
 
 }  // namespace rapid

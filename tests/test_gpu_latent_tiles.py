@@ -217,3 +217,30 @@ def test_prefill_references_move_in_runs_of_several_tiles(n, H):
     want, lse, eO, eL = _latent.prefill(Q, K, V, R, [P])
     assert ((O.double() - want).abs() <= eO).all(), float(((O.double() - want).abs() / eO).max())
     assert ((S.double() - lse).abs() <= eL).all()
+
+
+@pytest.mark.parametrize("B,H,n,P", [(3, 27, 1100, 0), (1, 130, 700, 40), (2, 11, 300, 12000), (1, 9, 9000, 0)])
+def test_prefill_every_block_of_many_heads(B, H, n, P):
+    # more blocks than the SMs share out by key tiles: heads are taken in groups, the last one larger
+    g = torch.Generator().manual_seed(H)
+    gd = torch.Generator(device=DEV).manual_seed(H)
+    L = P + n
+    Q, K, V, R = (torch.randn(s, generator=gd, device=DEV).to(BF16) for s in
+                  ((B, n, H, 192), (B, L, H, 128), (B, L, H, 128), (B, L, 64)))
+    O = torch.full((B, n, H, 128), 7.0, dtype=BF16, device=DEV)
+    S = torch.full((B, H, n), 7.0, device=DEV)
+    rapid.latent_prefill_attn(Q, K, V, R, _ints([P] * B), out=O, lse=S)
+    assert (O != 7).any(-1).all() and (S != 7).all()
+    heads = sorted({0, H // 2, H - 1, int(torch.randint(H, (1,), generator=g))})
+    rows = torch.tensor(sorted({0, 1, 255, 256, n // 2, n - 2, n - 1} & set(range(n))), device=DEV)
+    for b in range(B):
+        for h in heads:
+            k = torch.cat([K[b, :, h], R[b]], -1).double()
+            x = (Q[b, rows, h].double() @ k.T * _latent.SCALE)
+            hidden = torch.arange(L, device=DEV)[None] > P + rows[:, None]
+            x = x.masked_fill(hidden, -math.inf)
+            p, lse = _latent._softmax(x)
+            mag = Q[b, rows, h].double().abs() @ k.abs().T * _latent.SCALE
+            o = p @ V[b, :, h].double()
+            eo, el = _latent._bounds(x, mag, p, V[b, :, h].double(), o, lse, L, 192 // 16 + 1)
+            assert ((O[b, rows, h].double() - o).abs() <= eo).all() and ((S[b, h, rows].double() - lse).abs() <= el).all()
