@@ -901,6 +901,10 @@ size_t rapid_latent_attn_workspace_size(int B, int H, int n_q, int64_t kv_capaci
  *  softmax_scale  <= 0 selects 1/sqrt(192), the width of an expanded head
  *  O          [B, H, n_q, 512] bf16
  *
+ * The products run on tensor cores with fp32 sums.  The probabilities are
+ * rounded to bf16 for the product with the values (by at most 2^-8 of each;
+ * the sum that divides them is of the unrounded ones), and O once more.
+ *
  * What a query does not see has no effect on it, whatever it holds: rows
  * behind the mask, rows behind the step, other queries.  A value that is not
  * finite in a row that a query sees reaches that query's outputs as it would in
@@ -943,8 +947,8 @@ size_t rapid_latent_prefill_attn_workspace_size(int B, int n, int H, int64_t kv_
  *  softmax_scale  <= 0 selects 1/sqrt(192)
  *  workspace  as for rapid_latent_attn
  *
- * A key that a token does not see has no effect on it, whatever it holds; nor
- * has another token's query.
+ * Arithmetic and roundings are rapid_latent_attn's.  A key that a token does not
+ * see has no effect on it, whatever it holds; nor has another token's query.
  *
  * Errors: RAPID_EINVAL for NULL tensors, B outside [1, 65535], n < 1, H outside
  * [1, RAPID_LATENT_MAX_HEADS], B * n * H above RAPID_LATENT_MAX_QUERIES, kv_rows

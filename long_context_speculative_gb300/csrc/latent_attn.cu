@@ -36,10 +36,12 @@
 // Every wait is bounded in wall-clock time; after a failed wait the kernel records an error code,
 // stops issuing, drains and returns.
 //
-// Measured with the join (us; floor by bytes at 6788 GB/s or operations at 1910 TFLOP/s): 128 heads,
-// 11 queries over 120K bf16 rows 386 (197); 128 heads, 1 query over 120K 8-bit rows 53 (18);
-// 16 heads, a tree of 32 over four 8-bit histories of 32K to 96K 380 (153); 16 heads, 1 query
-// over 120K bf16 rows 37 (21), over 1K 9.1 (0.2).  With 64 rows the operands' reads from shared memory
+// Measured with the join, calls back to back over inputs that do not stay in L2, SM clock 2070 MHz (us; floor
+// by bytes at 6788 GB/s or operations at 1910 TFLOP/s): 128 heads, 11 queries over 120K bf16 rows 386 (197);
+// 128 heads, 1 query over 120K 8-bit rows 55 (18), bf16 50 (21); 16 heads, a tree of 32 over four 8-bit
+// histories of 32K to 96K 380 (153); 16 heads, 1 query over 120K bf16 rows 34 (21), over 1K 9.4 (0.2); 64
+// sequences of 4K with 1 query of 16 heads 76 (45), 8 bits 74 (26), of 128 heads 122 (47), 8 bits 137 (38).
+// With 64 rows the operands' reads from shared memory
 // bound the products (128 B a clock: 36.7 clocks for M = N = 64, 52 for M = 128, N = 64, so 2153 a
 // tile; a tile takes 2340, and sharing the copies of two row blocks in a cluster changes nothing).
 // 8-bit rows take some 3300 clocks: the converters share issue slots and the shared-memory port with the softmax

@@ -14,10 +14,11 @@
 // All three kernels copy: no value is read twice.  A row is one warp's work: lane l holds values
 // 16 l .. 16 l + 15 of the latent vector (a scale group is 8 lanes) and pair l of the key.
 //
-// Measured: three ragged chunks of up to 4095 tokens with 32 heads, bf16 rows, 15.4 us for 97 MB (6.3 TB/s,
-// 0.93 of a plain copy; 28 us before the pairs' layout was a template parameter, when the lanes'
-// registers were indexed in memory); 11 tokens of 128 heads 2.3 us.  Reading a 120K history in 8 bits
-// back 37.5 us (222 MB, 5.9 TB/s, 0.87); committing 16 sequences' paths of 60 layers 6.0 us (0.92).
+// Measured, calls back to back over inputs that do not stay in L2 (us; floor by bytes at 6788 GB/s): three ragged
+// chunks of up to 4095 tokens with 32 heads 19.1 (14.2), 8-bit rows 19.2 (13.6), 15.4 where the 97 MB stay in L2
+// (28 before the pairs' layout was a template parameter, when the lanes' registers were indexed in memory);
+// 8192 tokens of 128 heads, 8-bit rows 50.4 (41.7); 11 tokens of 128 heads 2.1.  Reading a 120K history in
+// 8 bits back 37.1 (32.7); committing 16 sequences' paths of 60 layers 9.8 (5.5), 6.0 where they stay in L2.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

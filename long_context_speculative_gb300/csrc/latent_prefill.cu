@@ -28,9 +28,11 @@
 // Every wait is bounded in wall-clock time; after a failed wait the kernel records an error code,
 // stops issuing, drains and returns.
 //
-// Measured (us; floor by operations at 1910 TFLOP/s): 8192 tokens of 32 heads 412 to 422 (360), 1.65
-// PFLOP/s; three ragged chunks of up to 999 tokens of 16 heads behind up to 12001 132 (61); 16 tokens of 16
-// heads behind 16000 39 (4.5).  A tile of keys takes 2850 clocks for both tiles of tokens, 2710 of them the
+// Measured, calls back to back (us; floor by operations at 1910 TFLOP/s, by bytes at 6788 GB/s where that is
+// more): 8192 tokens of 32 heads 455 (360), 1.51 PFLOP/s at the 1755 MHz that the power limit leaves, 417 for a
+// call alone; of 128 heads 1804 (1439), 1640 alone; three ragged chunks of up to 999 tokens of 16 heads behind
+// up to 12001 135 to 140 (61); 16 tokens of 16 heads behind 16000 40 (19.7 by bytes).
+// A tile of keys takes 2850 clocks for both tiles of tokens, 2710 of them the
 // tensor unit's (68 for M = N = 128, 36 for M = 128, N = 64 with P in tensor memory).  The ragged chunks
 // lose 6000 clocks between two pieces of a CTA (Q, whose room is in use until the last scores, then
 // its first scores) and 10 us in the join.
